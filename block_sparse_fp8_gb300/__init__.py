@@ -4,6 +4,8 @@ A thin ctypes binding over the C ABI in include/bsa_fp8.h: it marshals PyTorch C
 (device pointers) and the current stream into ``bsa_fp8_prefill`` / ``bsa_fp8_compact_tiles``
 and the quantise step ``bsa_fp8_quantize_rows`` / ``bsa_fp8_append_kv``; ``prefill_host``
 marshals CPU tensors into ``bsa_fp8_prefill_host``, which copies them in and the results out.
+``decode`` / ``gather_kv`` / ``merge_states`` serve from the same cache: the next token's
+attention, the cache read back, and the join of attention results over parts of a cache.
 Every step of the computation runs in the library's CUDA kernels; there is no CPU path.
 The library must have been built (``block_sparse_fp8_gb300._build.build()``); importing the
 binding on a machine without it raises immediately.
@@ -20,7 +22,9 @@ __all__ = ["Dims", "AppendDims", "Tensors", "TENSOR_NAMES", "Q_TND", "Q_NTD", "K
            "KV_NHD", "prefill", "prefill_host", "compact_tiles", "quantize_rows", "append_kv",
            "workspace_size", "status_string", "set_wait_limit_ns", "lib",
            "SCALE_PER_TENSOR", "SCALE_PER_TOKEN_HEAD", "SCALE_PER_HEAD", "BsaError",
-           "DESCALE_AMAX", "DESCALE_UE8M0",
+           "DESCALE_AMAX", "DESCALE_UE8M0", "DecodeDims", "GatherDims", "make_decode_dims",
+           "decode", "decode_workspace_size", "gather_kv", "merge_states", "QTYPE_BF16",
+           "QTYPE_E4M3", "OUT_BF16", "OUT_FP32", "MAX_MERGE",
            "DEV_BAD_INDEX", "DEV_BAD_PAGE", "DEV_BAD_SEQLEN", "DEV_TIMEOUT"]
 
 SCALE_PER_TENSOR = 0
@@ -35,7 +39,8 @@ DEV_TIMEOUT = 8
 EXPORTED = ("bsa_fp8_prefill", "bsa_fp8_prefill_workspace_size", "bsa_fp8_compact_tiles",
             "bsa_fp8_prefill_noalloc", "bsa_fp8_prefill_host", "bsa_fp8_quantize_rows",
             "bsa_fp8_quantize_rows_ue8m0", "bsa_fp8_append_kv", "bsa_fp8_set_wait_limit_ns",
-            "bsa_status_string")
+            "bsa_fp8_decode", "bsa_fp8_decode_workspace_size", "bsa_fp8_gather_kv",
+            "bsa_fp8_merge_states", "bsa_status_string")
 
 # descale rules of the quantise step
 DESCALE_AMAX = 0    # amax / 448
@@ -75,6 +80,24 @@ class AppendDims(ctypes.Structure):
         "k_scale_kind", "v_scale_kind", "kv_layout", "k_descale_rule")]
 
 
+# decode's query types, gather_kv's output types, most parts of one merge_states call
+QTYPE_BF16, QTYPE_E4M3 = 0, 1
+OUT_BF16, OUT_FP32 = 0, 1
+MAX_MERGE = 8
+
+
+class DecodeDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in (
+        "B", "N1", "N2", "D", "page_size", "max_kv_len", "num_pages", "max_pages_per_seq",
+        "k_scale_kind", "v_scale_kind", "kv_layout", "q_type", "q_stride", "sparse")]
+
+
+class GatherDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in (
+        "B", "N2", "D", "page_size", "num_pages", "max_pages_per_seq", "total", "k_scale_kind",
+        "v_scale_kind", "kv_layout", "out_type")]
+
+
 _lib = None
 
 
@@ -108,6 +131,15 @@ def lib():
         L.bsa_fp8_append_kv.argtypes = [ctypes.POINTER(AppendDims)] + [vp] * 12
         L.bsa_fp8_set_wait_limit_ns.restype = i32
         L.bsa_fp8_set_wait_limit_ns.argtypes = [ctypes.c_ulonglong]
+        L.bsa_fp8_decode.restype = i32
+        L.bsa_fp8_decode.argtypes = [ctypes.POINTER(DecodeDims)] + [vp] * 11 + [f32, vp, vp, vp,
+                                                                                sz, vp, vp]
+        L.bsa_fp8_decode_workspace_size.restype = sz
+        L.bsa_fp8_decode_workspace_size.argtypes = [ctypes.POINTER(DecodeDims)]
+        L.bsa_fp8_gather_kv.restype = i32
+        L.bsa_fp8_gather_kv.argtypes = [ctypes.POINTER(GatherDims)] + [vp] * 11
+        L.bsa_fp8_merge_states.restype = i32
+        L.bsa_fp8_merge_states.argtypes = [i32, vp, vp, i32, i32, vp, vp, vp]
         L.bsa_status_string.restype = ctypes.c_char_p
         L.bsa_status_string.argtypes = [i32]
         _lib = L
@@ -302,3 +334,254 @@ def append_kv(k_new, v_new, cu_seqlens_new, cache_seqlens, block_table, k_pages,
     if st != 0:
         raise BsaError(st, "bsa_fp8_append_kv")
     return k_pages, v_pages, k_descale
+
+
+# ---------------------------------------------------------------------------------------------
+# serving: decode, gather_kv, merge_states
+# ---------------------------------------------------------------------------------------------
+
+def _check(name, t, dtypes, shape, device):
+    """Raises ValueError unless `t` is a contiguous tensor of one of `dtypes` and of `shape` on
+    `device`."""
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, q or the cache on {device}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _check_status(dev_status, device):
+    import torch
+
+    if dev_status is not None and (dev_status.device != device or dev_status.numel() < 1 or
+                                   dev_status.dtype != torch.int32):
+        raise ValueError(f"dev_status must be an int32 tensor on {device}")
+
+
+def _launch(device, stream, what, call):
+    """call(stream handle) with `device` current; raises BsaError on a status other than 0."""
+    import torch
+
+    if device.type != "cuda":
+        raise ValueError(f"{what}: tensors must be on a CUDA device, not {device}")
+    if stream is not None and stream.device != device:
+        raise ValueError(f"{what}: the stream is on {stream.device}, the tensors on {device}")
+    if torch.cuda.current_device() == device.index:
+        st = call((torch.cuda.current_stream() if stream is None else stream).cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            st = call((torch.cuda.current_stream() if stream is None else stream).cuda_stream)
+    if st != 0:
+        raise BsaError(st, what)
+
+
+def _codes(torch):
+    return (torch.uint8, torch.float8_e4m3fn)
+
+
+def _pool(pages, kv_layout):
+    """(pages, KV heads, page size, head dim) of a page pool."""
+    if pages.dim() != 4:
+        raise ValueError(f"pages have shape {tuple(pages.shape)}, expected four dimensions")
+    P, a, b, D = pages.shape
+    return (P, b, a, D) if kv_layout == KV_NHD else (P, a, b, D)
+
+
+def make_decode_dims(q, k_pages, block_table, max_kv_len, k_scale_kind, v_scale_kind,
+                     kv_layout=KV_HND, sparse=False) -> DecodeDims:
+    B, N1, D = q.shape
+    P, N2, ps, _ = _pool(k_pages, kv_layout)
+    return DecodeDims(B=B, N1=N1, N2=N2, D=D, page_size=ps, max_kv_len=int(max_kv_len),
+                      num_pages=P, max_pages_per_seq=block_table.shape[1],
+                      k_scale_kind=int(k_scale_kind), v_scale_kind=int(v_scale_kind),
+                      kv_layout=int(kv_layout),
+                      q_type=QTYPE_E4M3 if q.element_size() == 1 else QTYPE_BF16,
+                      q_stride=q.stride(0) if B > 1 else N1 * D, sparse=int(bool(sparse)))
+
+
+def decode_workspace_size(dims: DecodeDims) -> int:
+    """Bytes of workspace decode() needs for `dims` on the current device."""
+    return int(lib().bsa_fp8_decode_workspace_size(ctypes.byref(dims)))
+
+
+def decode(q, k_pages, v_pages, k_descale, v_descale, seqused_kv, block_table, max_kv_len: int,
+           q_descale=None, block_mask=None, sparse_indices=None, sparse_seq_len=None,
+           softmax_scale: float | None = None, out=None, lse=None, return_lse: bool = True,
+           dev_status=None, workspace=None, stream=None, k_scale_kind: int | None = None,
+           v_scale_kind: int | None = None, kv_layout: int = KV_HND):
+    """Attention of one new token per sequence over the paged cache (whose seqused_kv counts the
+    new token, appended beforehand).  q bf16 [B, N1, 128], or uint8/float8_e4m3fn with q_descale
+    f32 [B, N1]; its rows may lie further apart than N1 * 128 (a slice of a wider projection).
+    Pages, descales, block_table and scale kinds as in prefill(); seqused_kv i32 [B];
+    block_mask u8 [B, N1, Kb] or sparse_indices i32 [B, N1, Kb] + sparse_seq_len i32 [B, N1]
+    select 128-token tiles for each query head, Kb = ceil(max_kv_len / 128).
+    Returns (out bf16 [B, N1, 128], lse f32 [N1, B] or None); a sequence without tokens, or a head
+    without an enabled tile, gives 0 and -FLT_MAX.  `workspace` (decode_workspace_size bytes)
+    must not be shared by calls in flight at once."""
+    import torch
+
+    if q.dim() != 3:
+        raise ValueError(f"q has shape {tuple(q.shape)}, expected [B, N1, 128]")
+    B, N1, D = q.shape
+    dev = q.device
+    P, N2, ps, _ = _pool(k_pages, kv_layout)
+    if q.dtype != torch.bfloat16 and q.dtype not in _codes(torch):
+        raise ValueError(f"q has dtype {q.dtype}, expected bf16 or e4m3 codes")
+    if q.stride(2) != 1 or (N1 > 1 and q.stride(1) != D):
+        raise ValueError("q must be contiguous within a sequence's row")
+    if block_table.dim() != 2:
+        raise ValueError(f"block_table has shape {tuple(block_table.shape)}, expected [B, L]")
+    f32, i32 = (torch.float32,), (torch.int32,)
+    codes = _codes(torch)
+    _check("k_pages", k_pages, codes, k_pages.shape, dev)
+    _check("v_pages", v_pages, codes, k_pages.shape, dev)
+    k_kind = k_scale_kind if k_scale_kind is not None else (
+        SCALE_PER_TOKEN_HEAD if k_descale.dim() == 3 else SCALE_PER_TENSOR)
+    v_kind = v_scale_kind if v_scale_kind is not None else (
+        SCALE_PER_HEAD if v_descale.numel() == N2 else SCALE_PER_TENSOR)
+    _check("k_descale", k_descale, f32,
+           (P, N2, ps) if k_kind == SCALE_PER_TOKEN_HEAD else (1,), dev)
+    _check("v_descale", v_descale, f32, (N2,) if v_kind == SCALE_PER_HEAD else (1,), dev)
+    _check("seqused_kv", seqused_kv, i32, (B,), dev)
+    _check("block_table", block_table, i32, (B, block_table.shape[1]), dev)
+    if q_descale is not None:
+        _check("q_descale", q_descale, f32, (B, N1), dev)
+    sparse = block_mask is not None or sparse_indices is not None
+    if sparse:
+        Kb = -(-int(max_kv_len) // 128)
+        if block_mask is not None:
+            _check("block_mask", block_mask, (torch.uint8, torch.bool), (B, N1, Kb), dev)
+        if sparse_indices is not None:
+            _check("sparse_indices", sparse_indices, i32, (B, N1, Kb), dev)
+        if sparse_seq_len is not None:
+            _check("sparse_seq_len", sparse_seq_len, i32, (B, N1), dev)
+    dims = make_decode_dims(q, k_pages, block_table, max_kv_len, k_kind, v_kind, kv_layout, sparse)
+    if out is None:
+        out = torch.empty((B, N1, D), dtype=torch.bfloat16, device=dev)
+    else:
+        _check("out", out, (torch.bfloat16,), (B, N1, D), dev)
+    if lse is not None:
+        _check("lse", lse, f32, (N1, B), dev)
+    elif return_lse:
+        lse = torch.empty((N1, B), dtype=torch.float32, device=dev)
+    if softmax_scale is None:
+        softmax_scale = 1.0 / math.sqrt(D)
+    _check_status(dev_status, dev)
+    if workspace is not None and (workspace.device != dev or not workspace.is_contiguous()):
+        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+
+    def call(handle):
+        ws = workspace
+        if ws is None:
+            ws = torch.empty(decode_workspace_size(dims), dtype=torch.uint8, device=dev)
+        return lib().bsa_fp8_decode(
+            ctypes.byref(dims), _p(q), _p(q_descale), _p(k_pages), _p(v_pages), _p(k_descale),
+            _p(v_descale), _p(seqused_kv), _p(block_table), _p(block_mask), _p(sparse_indices),
+            _p(sparse_seq_len), float(softmax_scale), _p(out), _p(lse), _p(ws), ws.nbytes,
+            _p(dev_status), handle)
+
+    _launch(dev, stream, "bsa_fp8_decode", call)
+    return out, lse
+
+
+def gather_kv(k_pages, v_pages, k_descale, v_descale, cu_seqlens, block_table, total: int,
+              cache_starts=None, k_out=None, v_out=None, out_dtype=None, dev_status=None,
+              stream=None, k_scale_kind: int | None = None, v_scale_kind: int | None = None,
+              kv_layout: int = KV_HND):
+    """Reads tokens back from the paged cache: row cu_seqlens[b] + i of the returned k, v
+    [total, N2, 128] is the token at position cache_starts[b] + i (0 + i without it) of sequence
+    b, code * descale.  out_dtype bf16 (default) or float32, or that of k_out / v_out when given;
+    rows from cu_seqlens[B] on are left as they were.  k_pages = None or v_pages = None leaves
+    that side out (returned as None)."""
+    import torch
+
+    pages = k_pages if k_pages is not None else v_pages
+    if pages is None:
+        raise ValueError("k_pages and v_pages are both None")
+    dev = pages.device
+    P, N2, ps, D = _pool(pages, kv_layout)
+    f32, i32 = (torch.float32,), (torch.int32,)
+    given = k_out if k_out is not None else v_out
+    if out_dtype is None:
+        out_dtype = given.dtype if given is not None else torch.bfloat16
+    if out_dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"out_dtype {out_dtype}: bf16 or float32")
+    if block_table.dim() != 2:
+        raise ValueError(f"block_table has shape {tuple(block_table.shape)}, expected [B, L]")
+    B, L = block_table.shape
+    _check("block_table", block_table, i32, (B, L), dev)
+    _check("cu_seqlens", cu_seqlens, i32, (B + 1,), dev)
+    if cache_starts is not None:
+        _check("cache_starts", cache_starts, i32, (B,), dev)
+    k_kind, v_kind = SCALE_PER_TENSOR, SCALE_PER_TENSOR
+    shape = (int(total), N2, D)
+
+    def rows(name, t):
+        if t is None:
+            return torch.empty(shape, dtype=out_dtype, device=dev)
+        _check(name, t, (out_dtype,), shape, dev)
+        return t
+
+    if k_pages is not None:
+        _check("k_pages", k_pages, _codes(torch), pages.shape, dev)
+        k_kind = k_scale_kind if k_scale_kind is not None else (
+            SCALE_PER_TOKEN_HEAD if k_descale.dim() == 3 else SCALE_PER_TENSOR)
+        _check("k_descale", k_descale, f32,
+               (P, N2, ps) if k_kind == SCALE_PER_TOKEN_HEAD else (1,), dev)
+        k_out = rows("k_out", k_out)
+    elif k_out is not None:
+        raise ValueError("k_out given without k_pages")
+    if v_pages is not None:
+        _check("v_pages", v_pages, _codes(torch), pages.shape, dev)
+        v_kind = v_scale_kind if v_scale_kind is not None else (
+            SCALE_PER_HEAD if v_descale.numel() == N2 else SCALE_PER_TENSOR)
+        _check("v_descale", v_descale, f32, (N2,) if v_kind == SCALE_PER_HEAD else (1,), dev)
+        v_out = rows("v_out", v_out)
+    elif v_out is not None:
+        raise ValueError("v_out given without v_pages")
+    _check_status(dev_status, dev)
+    dims = GatherDims(B=B, N2=N2, D=D, page_size=ps, num_pages=P, max_pages_per_seq=L,
+                      total=int(total), k_scale_kind=int(k_kind), v_scale_kind=int(v_kind),
+                      kv_layout=int(kv_layout),
+                      out_type=OUT_FP32 if out_dtype == torch.float32 else OUT_BF16)
+    _launch(dev, stream, "bsa_fp8_gather_kv", lambda handle: lib().bsa_fp8_gather_kv(
+        ctypes.byref(dims), _p(k_pages), _p(v_pages), _p(k_descale), _p(v_descale),
+        _p(cu_seqlens), _p(cache_starts), _p(block_table), _p(k_out), _p(v_out), _p(dev_status),
+        handle))
+    return k_out, v_out
+
+
+def merge_states(outs, lses, out=None, lse=None, return_lse: bool = True, stream=None):
+    """Joins attention results over disjoint sets of keys: outs are 1 to MAX_MERGE bf16 tensors
+    [T, N1, 128] and lses their fp32 LSEs [N1, T], as prefill() and decode() return them (for
+    decode T = B).  Returns (out, lse) over the union of the keys.  `out` may be one of `outs`
+    and `lse` one of `lses`."""
+    import torch
+
+    n = len(outs)
+    if n < 1 or n > MAX_MERGE or len(lses) != n:
+        raise ValueError(f"{n} outs and {len(lses)} lses: 1 to {MAX_MERGE} of each")
+    if outs[0].dim() != 3 or outs[0].shape[2] != 128:
+        raise ValueError(f"outs[0] has shape {tuple(outs[0].shape)}, expected [T, N1, 128]")
+    T, N1, D = outs[0].shape
+    dev = outs[0].device
+    bf16, f32 = (torch.bfloat16,), (torch.float32,)
+    for i in range(n):
+        _check(f"outs[{i}]", outs[i], bf16, (T, N1, D), dev)
+        _check(f"lses[{i}]", lses[i], f32, (N1, T), dev)
+    if out is None:
+        out = torch.empty((T, N1, D), dtype=torch.bfloat16, device=dev)
+    else:
+        _check("out", out, bf16, (T, N1, D), dev)
+    if lse is not None:
+        _check("lse", lse, f32, (N1, T), dev)
+    elif return_lse:
+        lse = torch.empty((N1, T), dtype=torch.float32, device=dev)
+    po = (ctypes.c_void_p * n)(*(o.data_ptr() for o in outs))
+    pl = (ctypes.c_void_p * n)(*(x.data_ptr() for x in lses))
+    _launch(dev, stream, "bsa_fp8_merge_states", lambda handle: lib().bsa_fp8_merge_states(
+        n, po, pl, T, N1, _p(out), _p(lse), handle))
+    return out, lse

@@ -7,6 +7,8 @@
 //   * attn::bsa_attention_kernel (bsa_attention.cuh) -- the persistent prefill kernel.
 //   * quant::quantize_rows_kernel / quant::append_kv_kernel (bsa_quant.cuh) -- the quantise
 //     step that produces the prefill's e4m3 inputs.
+//   * decode (bsa_decode.cuh), gather (bsa_gather.cuh), merge (bsa_merge.cuh) -- serving: the next
+//     token's attention over the cache, the cache read back, the join of attention results.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -22,7 +24,10 @@
 #include "bsa_attention.cuh"
 #include "bsa_attention_wide.cuh"
 #include "bsa_common.cuh"
+#include "bsa_decode.cuh"
 #include "bsa_fp8.h"
+#include "bsa_gather.cuh"
+#include "bsa_merge.cuh"
 #include "bsa_quant.cuh"
 #include "ptx_sm103.cuh"
 
@@ -694,4 +699,202 @@ extern "C" bsa_status_t bsa_fp8_prefill_noalloc(
                       seqused_kv, block_table, block_mask, sparse_indices, sparse_seq_len,
                       softmax_scale, p_scale, out_bf16, lse_f32, nullptr, 0, dev_status, stream,
                       true);
+}
+
+// ------------------------------------------------------------------------------------------
+// serving: decode, cache read-back, merge
+// ------------------------------------------------------------------------------------------
+
+namespace {
+
+// byte strides of a page, a KV head and a slot inside the page pool
+void pool_strides(int kv_layout, int N2, int page_size, long long *page, long long *head,
+                  long long *slot) {
+  *page = (long long)N2 * page_size * HEAD_DIM;
+  *head = kv_layout == BSA_KV_NHD ? HEAD_DIM : (long long)page_size * HEAD_DIM;
+  *slot = kv_layout == BSA_KV_NHD ? (long long)N2 * HEAD_DIM : HEAD_DIM;
+}
+
+bsa_status_t validate_decode(const bsa_fp8_decode_dims_t *d) {
+  if (!d || d->D != HEAD_DIM || (d->page_size != 32 && d->page_size != 64))
+    return BSA_ERR_INVALID_ARGUMENT;
+  if (d->B < 0 || d->N1 < 1 || d->N2 < 1 || d->N1 % d->N2 != 0 || d->N1 / d->N2 > 16)
+    return BSA_ERR_INVALID_ARGUMENT;
+  if (d->max_kv_len < 0 || d->num_pages < 0 || d->max_pages_per_seq < 0)
+    return BSA_ERR_INVALID_ARGUMENT;
+  if ((long long)d->max_pages_per_seq * d->page_size < d->max_kv_len)
+    return BSA_ERR_INVALID_ARGUMENT;
+  if (d->k_scale_kind != BSA_SCALE_PER_TENSOR && d->k_scale_kind != BSA_SCALE_PER_TOKEN_HEAD)
+    return BSA_ERR_INVALID_ARGUMENT;
+  if (d->v_scale_kind != BSA_SCALE_PER_TENSOR && d->v_scale_kind != BSA_SCALE_PER_HEAD)
+    return BSA_ERR_INVALID_ARGUMENT;
+  if (d->kv_layout != BSA_KV_HND && d->kv_layout != BSA_KV_NHD) return BSA_ERR_INVALID_ARGUMENT;
+  if (d->q_type != BSA_QTYPE_BF16 && d->q_type != BSA_QTYPE_E4M3) return BSA_ERR_INVALID_ARGUMENT;
+  if (d->q_stride < (long long)d->N1 * HEAD_DIM ||
+      d->q_stride % (d->q_type == BSA_QTYPE_E4M3 ? 16 : 8) != 0)
+    return BSA_ERR_INVALID_ARGUMENT;
+  if (d->sparse != 0 && d->sparse != 1) return BSA_ERR_INVALID_ARGUMENT;
+  const long long kb = cdiv(d->max_kv_len, TILE);
+  if (kb > KB_MAX) return BSA_ERR_UNSUPPORTED;
+  // tile counts and grid sizes are int
+  if ((long long)d->B * d->N1 > (1LL << 30) || (long long)d->B * d->N2 * (kb + 1) > (1LL << 30))
+    return BSA_ERR_UNSUPPORTED;
+  return BSA_OK;
+}
+
+}  // namespace
+
+extern "C" size_t bsa_fp8_decode_workspace_size(const bsa_fp8_decode_dims_t *dims) {
+  if (validate_decode(dims) != BSA_OK) return 0;
+  return WORKSPACE_BYTES;
+}
+
+extern "C" bsa_status_t bsa_fp8_decode(const bsa_fp8_decode_dims_t *d, const void *q,
+                                       const float *q_descale, const void *k_pages,
+                                       const void *v_pages, const float *k_descale,
+                                       const float *v_descale, const int *seqused_kv,
+                                       const int *block_table, const uint8_t *block_mask,
+                                       const int *sparse_indices, const int *sparse_seq_len,
+                                       float softmax_scale, void *out_bf16, float *lse_f32,
+                                       void *workspace, size_t workspace_bytes, int *dev_status,
+                                       void *stream) {
+  bsa_status_t st = validate_decode(d);
+  if (st != BSA_OK) return st;
+  if (block_mask && sparse_indices) return BSA_ERR_INVALID_ARGUMENT;
+  if (sparse_indices && !sparse_seq_len) return BSA_ERR_INVALID_ARGUMENT;
+  if (!std::isfinite(softmax_scale)) return BSA_ERR_INVALID_ARGUMENT;
+  if (d->B == 0) return BSA_OK;
+  // a batch of empty sequences only (max_kv_len = 0) has no cache and no tiles to name
+  const bool none = d->max_kv_len == 0;
+  if (!none && (d->sparse != 0) != (block_mask || sparse_indices)) return BSA_ERR_INVALID_ARGUMENT;
+  const bool k_tok = d->k_scale_kind == BSA_SCALE_PER_TOKEN_HEAD;
+  const bool e4m3 = d->q_type == BSA_QTYPE_E4M3;
+  if (!q || !seqused_kv || !out_bf16 || e4m3 != (q_descale != nullptr))
+    return BSA_ERR_INVALID_ARGUMENT;
+  if (!none && (!k_pages || !v_pages || !k_descale || !v_descale || !block_table ||
+                d->num_pages < 1))
+    return BSA_ERR_INVALID_ARGUMENT;
+  if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) ||
+      (k_tok && !aligned16(k_descale)) || !aligned16(out_bf16) ||
+      (reinterpret_cast<uintptr_t>(lse_f32) & 3u) != 0)
+    return BSA_ERR_INVALID_ARGUMENT;
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+    return BSA_ERR_WORKSPACE;
+  int num_sms = 0;
+  st = check_device(0, &num_sms);
+  if (st != BSA_OK) return st;
+  if (workspace_bytes < WORKSPACE_BYTES) return BSA_ERR_WORKSPACE;
+  decode::Params p;
+  memset(&p, 0, sizeof(p));
+  p.q = q;
+  p.q_descale = q_descale;
+  p.k_pages = static_cast<const uint8_t *>(k_pages);
+  p.v_pages = static_cast<const uint8_t *>(v_pages);
+  p.k_descale = k_descale;
+  p.v_descale = v_descale;
+  p.seqused_kv = seqused_kv;
+  p.block_table = block_table;
+  p.block_mask = block_mask;
+  p.sparse_indices = sparse_indices;
+  p.sparse_seq_len = sparse_seq_len;
+  p.out = static_cast<__nv_bfloat16 *>(out_bf16);
+  p.lse = lse_f32;
+  p.dev_status = dev_status;
+  p.q_stride = d->q_stride;
+  pool_strides(d->kv_layout, d->N2, d->page_size, &p.page_bytes, &p.head_bytes, &p.slot_bytes);
+  p.B = d->B;
+  p.N1 = d->N1;
+  p.N2 = d->N2;
+  p.G = d->N1 / d->N2;
+  p.ps = d->page_size;
+  p.num_pages = d->num_pages;
+  p.L = d->max_pages_per_seq;
+  p.Kb = cdiv(d->max_kv_len, TILE);
+  p.max_kv_len = d->max_kv_len;
+  p.q_e4m3 = e4m3;
+  p.k_per_token = k_tok;
+  p.v_per_head = d->v_scale_kind == BSA_SCALE_PER_HEAD;
+  p.scale = softmax_scale;
+  decode::decode_kernel<<<(unsigned)(d->B * d->N1), decode::THREADS, 0, (cudaStream_t)stream>>>(p);
+  return cudaGetLastError() == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
+}
+
+extern "C" bsa_status_t bsa_fp8_gather_kv(const bsa_fp8_gather_dims_t *d, const void *k_pages,
+                                          const void *v_pages, const float *k_descale,
+                                          const float *v_descale, const int *cu_seqlens,
+                                          const int *cache_starts, const int *block_table,
+                                          void *k_out, void *v_out, int *dev_status,
+                                          void *stream) {
+  if (!d || d->D != HEAD_DIM || (d->page_size != 32 && d->page_size != 64) || d->B < 0 ||
+      d->N2 < 1 || d->num_pages < 0 || d->max_pages_per_seq < 0 || d->total < 0)
+    return BSA_ERR_INVALID_ARGUMENT;
+  if (d->k_scale_kind != BSA_SCALE_PER_TOKEN_HEAD && d->k_scale_kind != BSA_SCALE_PER_TENSOR)
+    return BSA_ERR_INVALID_ARGUMENT;
+  if (d->v_scale_kind != BSA_SCALE_PER_HEAD && d->v_scale_kind != BSA_SCALE_PER_TENSOR)
+    return BSA_ERR_INVALID_ARGUMENT;
+  if (d->kv_layout != BSA_KV_HND && d->kv_layout != BSA_KV_NHD) return BSA_ERR_INVALID_ARGUMENT;
+  if (d->out_type != BSA_OUT_BF16 && d->out_type != BSA_OUT_FP32) return BSA_ERR_INVALID_ARGUMENT;
+  if (d->total == 0 || d->B == 0) return BSA_OK;
+  if ((!k_out && !v_out) || !cu_seqlens || !block_table) return BSA_ERR_INVALID_ARGUMENT;
+  if ((k_out && (!k_pages || !k_descale)) || (v_out && (!v_pages || !v_descale)))
+    return BSA_ERR_INVALID_ARGUMENT;
+  if (!aligned16(k_out) || !aligned16(v_out) || !aligned16(k_pages) || !aligned16(v_pages))
+    return BSA_ERR_INVALID_ARGUMENT;
+  const bsa_status_t st = check_device(0, nullptr);
+  if (st != BSA_OK) return st;
+  gather::Params p;
+  memset(&p, 0, sizeof(p));
+  p.k_pages = static_cast<const uint8_t *>(k_pages);
+  p.v_pages = static_cast<const uint8_t *>(v_pages);
+  p.k_descale = k_descale;
+  p.v_descale = v_descale;
+  p.cu_seqlens = cu_seqlens;
+  p.cache_starts = cache_starts;
+  p.block_table = block_table;
+  p.k_out = k_out;
+  p.v_out = v_out;
+  p.dev_status = dev_status;
+  pool_strides(d->kv_layout, d->N2, d->page_size, &p.page_bytes, &p.head_bytes, &p.slot_bytes);
+  p.B = d->B;
+  p.N2 = d->N2;
+  p.ps = d->page_size;
+  p.num_pages = d->num_pages;
+  p.L = d->max_pages_per_seq;
+  p.total = d->total;
+  p.k_per_token = d->k_scale_kind == BSA_SCALE_PER_TOKEN_HEAD;
+  p.v_per_head = d->v_scale_kind == BSA_SCALE_PER_HEAD;
+  if (d->out_type == BSA_OUT_FP32)
+    gather::gather_kernel<float><<<d->total, gather::THREADS, 0, (cudaStream_t)stream>>>(p);
+  else
+    gather::gather_kernel<__nv_bfloat16><<<d->total, gather::THREADS, 0, (cudaStream_t)stream>>>(p);
+  return cudaGetLastError() == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
+}
+
+extern "C" bsa_status_t bsa_fp8_merge_states(int count, const void *const *outs,
+                                             const float *const *lses, int T, int N1,
+                                             void *out_bf16, float *lse_f32, void *stream) {
+  if (count < 1 || count > BSA_MAX_MERGE || !outs || !lses || T < 0 || N1 < 1 ||
+      (long long)T * N1 > 0x7fffffffLL)
+    return BSA_ERR_INVALID_ARGUMENT;
+  if (T == 0) return BSA_OK;
+  if (!out_bf16 || !aligned16(out_bf16) || (reinterpret_cast<uintptr_t>(lse_f32) & 3u) != 0)
+    return BSA_ERR_INVALID_ARGUMENT;
+  merge::Params p;
+  memset(&p, 0, sizeof(p));
+  for (int i = 0; i < count; ++i) {
+    if (!outs[i] || !lses[i] || !aligned16(outs[i]) ||
+        (reinterpret_cast<uintptr_t>(lses[i]) & 3u) != 0)
+      return BSA_ERR_INVALID_ARGUMENT;
+    p.outs[i] = static_cast<const __nv_bfloat16 *>(outs[i]);
+    p.lses[i] = lses[i];
+  }
+  const bsa_status_t st = check_device(0, nullptr);
+  if (st != BSA_OK) return st;
+  p.out = static_cast<__nv_bfloat16 *>(out_bf16);
+  p.lse = lse_f32;
+  p.count = count;
+  p.T = T;
+  p.N1 = N1;
+  merge::merge_kernel<<<(unsigned)(T * N1), merge::THREADS, 0, (cudaStream_t)stream>>>(p);
+  return cudaGetLastError() == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
 }

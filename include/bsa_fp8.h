@@ -322,6 +322,119 @@ bsa_status_t bsa_fp8_append_kv(const bsa_fp8_append_dims_t *dims, const void *k_
                                const float *k_scale, const float *v_scale, void *k_pages,
                                void *v_pages, float *k_descale, int *dev_status, void *stream);
 
+/* ------------------------------------------------------------------------------------------
+ * Serving beside the prefill: the next token's attention over the cache, the cache read back,
+ * and the join of attention results over parts of a cache.  No counterpart in the pages; the
+ * cache formats, scales, selection rules, LSE convention and error reporting are the prefill's.
+ * ------------------------------------------------------------------------------------------ */
+
+#define BSA_QTYPE_BF16 0 /* bf16 queries, no q_descale */
+#define BSA_QTYPE_E4M3 1 /* e4m3 queries with q_descale [B, N1], as bsa_fp8_quantize_rows writes */
+
+typedef struct {
+  int B;                 /* sequences, one query token each, >= 0 */
+  int N1;                /* query heads, >= 1 */
+  int N2;                /* KV heads, N1 % N2 == 0, 1 <= N1/N2 <= 16 */
+  int D;                 /* head dim, must be 128 */
+  int page_size;         /* 32 or 64 */
+  int max_kv_len;        /* >= every kv_len (sets Kb = ceil(max_kv_len/128)); Kb <= 4096 */
+  int num_pages;         /* physical pages in k/v pages */
+  int max_pages_per_seq; /* L, columns of block_table; L * page_size >= max_kv_len */
+  int k_scale_kind;      /* BSA_SCALE_PER_TENSOR or BSA_SCALE_PER_TOKEN_HEAD */
+  int v_scale_kind;      /* BSA_SCALE_PER_TENSOR or BSA_SCALE_PER_HEAD */
+  int kv_layout;         /* BSA_KV_HND (0) or BSA_KV_NHD (1) */
+  int q_type;            /* BSA_QTYPE_BF16 (0) or BSA_QTYPE_E4M3 (1) */
+  int q_stride;          /* elements from one sequence's query row to the next's, >= N1 * 128 and
+                            a multiple of 16 bytes (a slice of a wider projection's output) */
+  int sparse;            /* 1: block_mask or sparse_indices is given; 0: neither (dense) */
+} bsa_fp8_decode_dims_t;
+
+/* Bytes of device workspace bsa_fp8_decode needs for `dims` on the current device: the partial
+ * results of cut sequences (at most two per resident CTA) and, with dims->sparse, the tile lists
+ * of every (sequence, KV head).  0 for invalid dims; bsa_fp8_decode reports those. */
+size_t bsa_fp8_decode_workspace_size(const bsa_fp8_decode_dims_t *dims);
+
+/* Attention of one new token per sequence over the paged cache (the new token's own K and V
+ * appended beforehand, so that seqused_kv counts it).
+ *
+ *   O[b,h]   = sum_j softmax_j( q[b,h] . K^_j * softmax_scale ) V^_j,   LSE its natural log-sum-exp
+ *
+ * over the tokens j < seqused_kv[b] of the 128-token tiles enabled for (b, h).
+ *   q               bf16 or e4m3 (dims->q_type) [B, N1, 128], rows dims->q_stride elements apart,
+ *                   16-byte aligned
+ *   q_descale       fp32 [B, N1] for e4m3 queries; NULL for bf16
+ *   k/v pages, k_descale, v_descale, block_table   as in bsa_fp8_prefill, except that slots
+ *                   past a sequence's end may hold anything
+ *   seqused_kv      int32 [B], required
+ *   block_mask      uint8 [B, N1, Kb], nonzero = compute; or NULL
+ *   sparse_indices  int32 [B, N1, Kb] with sparse_seq_len int32 [B, N1]; or NULL (the prefill's
+ *                   forms with one Q tile).  Query heads of one KV head may enable different
+ *                   tiles: a tile is read once for the heads that share it.
+ *   softmax_scale   finite
+ *   out_bf16        bf16 [B, N1, 128], 16-byte aligned
+ *   lse_f32         fp32 [N1, B]; or NULL
+ *   workspace       device buffer of at least bsa_fp8_decode_workspace_size(dims) bytes, 256-byte
+ *                   aligned (BSA_ERR_WORKSPACE otherwise), written before it is read by every
+ *                   call; calls in flight at once must not share one
+ * A row with no visible key (an idle sequence among them) gets O = 0 and LSE = -FLT_MAX.  Bad
+ * device data is reported and skipped as in the prefill: a sequence of a bad length counts as
+ * empty, a bad page reads as zeros.  Scores, softmax statistics and sums are fp32; the
+ * probabilities are rounded to fp16 for the product with V. */
+bsa_status_t bsa_fp8_decode(const bsa_fp8_decode_dims_t *dims, const void *q,
+                            const float *q_descale, const void *k_pages, const void *v_pages,
+                            const float *k_descale, const float *v_descale,
+                            const int *seqused_kv, const int *block_table,
+                            const uint8_t *block_mask, const int *sparse_indices,
+                            const int *sparse_seq_len, float softmax_scale, void *out_bf16,
+                            float *lse_f32, void *workspace, size_t workspace_bytes,
+                            int *dev_status, void *stream);
+
+#define BSA_OUT_BF16 0
+#define BSA_OUT_FP32 1
+
+typedef struct {
+  int B;                 /* sequences, >= 0 */
+  int N2;                /* KV heads, >= 1 */
+  int D;                 /* head dim, must be 128 */
+  int page_size;         /* 32 or 64 */
+  int num_pages;         /* physical pages */
+  int max_pages_per_seq; /* L, columns of block_table */
+  int total;             /* rows of k_out / v_out, >= cu_seqlens[B] */
+  int k_scale_kind;      /* BSA_SCALE_PER_TENSOR or BSA_SCALE_PER_TOKEN_HEAD */
+  int v_scale_kind;      /* BSA_SCALE_PER_TENSOR or BSA_SCALE_PER_HEAD */
+  int kv_layout;         /* BSA_KV_HND (0) or BSA_KV_NHD (1) */
+  int out_type;          /* BSA_OUT_BF16 (0) or BSA_OUT_FP32 (1) */
+} bsa_fp8_gather_dims_t;
+
+/* Reads tokens back from the paged cache, the inverse of bsa_fp8_append_kv: row cu_seqlens[b] + i
+ * of k_out / v_out [total, N2, 128] is the token at logical position cache_starts[b] + i of
+ * sequence b, value = code * descale (one fp32 product, rounded once more for bf16).
+ *   cu_seqlens    int32 [B + 1], cu_seqlens[0] = 0, non-decreasing; rows from cu_seqlens[B] up to
+ *                 `total` are left as they were
+ *   cache_starts  int32 [B], or NULL (0)
+ *   k_out, v_out  16-byte aligned; one of them may be NULL: that side is not read (its pages and
+ *                 descale may then be NULL too)
+ * A token whose page is missing (a position below 0 or beyond L pages, an entry outside
+ * [0, num_pages)) reads as zeros and BSA_DEV_BAD_PAGE is OR-ed into *dev_status (if given). */
+bsa_status_t bsa_fp8_gather_kv(const bsa_fp8_gather_dims_t *dims, const void *k_pages,
+                               const void *v_pages, const float *k_descale,
+                               const float *v_descale, const int *cu_seqlens,
+                               const int *cache_starts, const int *block_table, void *k_out,
+                               void *v_out, int *dev_status, void *stream);
+
+#define BSA_MAX_MERGE 8
+
+/* Joins attention results over disjoint sets of keys (a shared prefix and each sequence's own
+ * suffix, the chunks of a long context) into the result over their union:
+ *   LSE = ln sum_i exp(LSE_i),   O = sum_i exp(LSE_i - LSE) O_i
+ * for `count` parts (1 .. BSA_MAX_MERGE).  outs / lses are HOST arrays of device pointers: bf16
+ * [T, N1, 128], 16-byte aligned, and fp32 [N1, T], in the prefill's and the decode's layouts.  A
+ * part whose LSE is -FLT_MAX (or -inf) saw no key: its O is not used, whatever it holds; a row
+ * with no other part gets O = 0 and LSE = -FLT_MAX.  out_bf16 may be one of `outs` and lse_f32
+ * (or NULL) one of `lses`; otherwise they must not overlap the inputs.  T * N1 <= 2^31 - 1. */
+bsa_status_t bsa_fp8_merge_states(int count, const void *const *outs, const float *const *lses,
+                                  int T, int N1, void *out_bf16, float *lse_f32, void *stream);
+
 /* Sets the limit of every bounded wait inside the prefill kernel for launches that follow, in
  * nanoseconds, for the whole process; 0 restores the default of 2 s.  A wait that runs out
  * sets BSA_DEV_TIMEOUT in *dev_status, every role of the CTA stops, waits (with the default
