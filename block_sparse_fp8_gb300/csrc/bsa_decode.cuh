@@ -1,24 +1,59 @@
 // Attention of one new token per sequence over the paged e4m3 cache.
 //
-//   s_j = (q . k_j) * qd * kd_j * softmax_scale,  O = vd * sum_j 2^(s_j - m) v_j / l
+//   s_j = (q . k_j) * qd * kd_j * softmax_scale * log2(e),  O = vd * sum_j 2^(s_j - m) v_j / l
 //
-// The simplest form: one CTA per (sequence, query head) walks the enabled tiles with a running
-// maximum m and sum l; a thread owns one token's score, then one dimension of O.
+// Bound by HBM: a KV head's token is 256 bytes of codes for 4 * 128 flop per query head, 16 flop
+// per byte at eight query heads, a tenth of the ridge.  So everything serves a steady stream of
+// loads:
+//
+//   * Work is cut evenly whatever the batch's lengths are.  Every (sequence, KV head) is a task of
+//     128-token tiles; the grid's CTAs (two per SM, resident at once) take equal runs of the
+//     batch's tiles in task order, each finding its run by a scan of the lengths.  A task that
+//     lies inside one run is finished there; a task cut by run borders leaves one partial (m, l,
+//     O in fp32) per run, which the join kernel combines.  No atomics: results do not depend on
+//     timing.
+//   * Within a tile each of the CTA's four warps owns 32 tokens and keeps its own (m, l, O), so
+//     warps never wait for one another inside a task.  A warp copies its own K and V rows with
+//     16-byte cp.async, STAGES deep; rows past the sequence's end and rows of a bad page are
+//     zero-filled by the copy itself, so nothing there can reach the result.
+//   * The products run on mma.sync m16n8k16 with tokens (K) or dimensions (V) as the 16 rows and
+//     up to eight query heads as the 8 columns: with one token per sequence there is no
+//     128-row operand for tcgen05.mma to work on, and the tensor pipe is far from its limit.
+//     e4m3 codes convert to fp16 exactly; queries are scaled to fp16 by a power of two per
+//     row, P is rounded to fp16 (2^-11 relative, against the result's bf16 2^-8), accumulation,
+//     maxima and sums are fp32.
+//   * Shared memory rows keep their 16-byte chunks XOR-swizzled by the row number, so the
+//     fragment reads of K (a thread: 32 dimensions of one token) and V (16 dimensions of one
+//     token) are free of bank conflicts.
 #pragma once
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
-#include <cuda_fp8.h>
 
 #include <cfloat>
 #include <cstdint>
 
 #include "bsa_common.cuh"
+#include "ptx_sm103.cuh"
 
 namespace bsa {
 namespace decode {
 
-constexpr int THREADS = 128;
+constexpr int WARPS = 4;
+constexpr int THREADS = WARPS * 32;
+constexpr int TOK = TILE / WARPS;  // tokens of a tile that one warp owns: one mma row block pair
+constexpr int STAGES = 3;
+constexpr int CTAS_PER_SM = 2;
+// one warp's stage: K rows, V rows, the tokens' K descales, {head mask, tokens left, last tile}
+constexpr int OFF_V = TOK * HEAD_DIM;
+constexpr int OFF_KD = 2 * TOK * HEAD_DIM;
+constexpr int OFF_META = OFF_KD + TOK * 4;
+constexpr int STAGE_BYTES = OFF_META + 16;
+constexpr int SMEM_BYTES = WARPS * STAGES * STAGE_BYTES;
+// fp16 probabilities are kept as 2^(s - m + P_SHIFT): the largest, 2^15, fits, and weights down to
+// 2^-29 of it keep full precision
+constexpr float P_SHIFT = 15.f;
+constexpr int MAX_G = 16;
 
 struct Params {
   const void *q;
@@ -31,100 +66,671 @@ struct Params {
   __nv_bfloat16 *out;
   float *lse;
   int *dev_status;
+  // workspace: per main CTA {task, partials, first slot} of the cut task it begins; per slot (two
+  // per CTA) and head of the group (m, l) and O; with lists, per task the count of its tiles and
+  // the tiles, ascending, with the heads that enable them in the upper half
+  int4 *desc;
+  float2 *part_ml;
+  float *part_o;
+  int *counts;
+  uint32_t *tiles;
   long long q_stride;                            // elements
   long long page_bytes, head_bytes, slot_bytes;  // strides inside the page pool
-  int B, N1, N2, G, ps, num_pages, L, Kb, max_kv_len;
+  int B, N1, N2, G, ps, ps_shift, num_pages, L, Kb, max_kv_len;
   int q_e4m3, k_per_token, v_per_head;
-  float scale;
+  float scale_log2;  // softmax_scale * log2(e)
 };
 
 __device__ __forceinline__ void report(const Params &p, int bits) {
   if (p.dev_status) atomicOr(p.dev_status, bits);
 }
 
-__device__ __forceinline__ float e4m3_value(uint8_t c) {
-  __nv_fp8_e4m3 x;
-  x.__x = c;
-  return static_cast<float>(x);
+// Tokens of sequence b; a bad length counts as none.
+__device__ __forceinline__ int seq_len(const Params &p, int b) {
+  const int kv = p.seqused_kv[b];
+  if (kv >= 0 && kv <= p.max_kv_len) return kv;  // max_kv_len <= L * ps is checked on the host
+  report(p, BSA_DEV_BAD_SEQLEN);
+  return 0;
 }
 
-__global__ void __launch_bounds__(THREADS) decode_kernel(const Params p) {
-  __shared__ float qs[HEAD_DIM], ps[TILE], red[THREADS / 32];
-  __shared__ uint32_t on[KB_MAX / 32];
-  __shared__ long long base[TILE];
-  const int b = blockIdx.x / p.N1, h = blockIdx.x % p.N1, kvh = h / p.G, tid = threadIdx.x;
-  int kv = p.seqused_kv[b];
-  if (kv < 0 || kv > p.max_kv_len || (long long)kv > (long long)p.L * p.ps) {
-    if (tid == 0) report(p, BSA_DEV_BAD_SEQLEN);
-    kv = 0;
-  }
-  qs[tid] = p.q_e4m3
-                ? e4m3_value(static_cast<const uint8_t *>(p.q)[b * p.q_stride + h * HEAD_DIM + tid]) *
-                      p.q_descale[b * p.N1 + h]
-                : __bfloat162float(static_cast<const __nv_bfloat16 *>(
-                      p.q)[b * p.q_stride + h * HEAD_DIM + tid]);
-  const size_t row = ((size_t)b * p.N1 + h) * p.Kb;
-  const int nt = (kv + TILE - 1) / TILE;
-  if (p.sparse_indices) {
-    for (int w = tid; w < KB_MAX / 32; w += THREADS) on[w] = 0;
-    __syncthreads();
-    int len = p.sparse_seq_len[(size_t)b * p.N1 + h];
-    if (len < 0 || len > p.Kb) {
-      if (tid == 0) report(p, BSA_DEV_BAD_INDEX);
-      len = len < 0 ? 0 : p.Kb;
-    }
-    for (int e = tid; e < len; e += THREADS) {
-      const int t = p.sparse_indices[row + e];
-      if (t < 0 || t >= p.Kb)
-        report(p, BSA_DEV_BAD_INDEX);
-      else
-        atomicOr(&on[t >> 5], 1u << (t & 31));
-    }
+// Tiles of a task that takes no part still number one, so that a CTA comes by and writes its
+// empty result.
+__device__ __forceinline__ int dense_tiles(int kv) { return max((kv + TILE - 1) / TILE, 1); }
+
+__device__ __forceinline__ void pdl_launch_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void pdl_wait() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// `bytes` (0 or SIZE) bytes from src, the rest of the SIZE bytes zero.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src, uint32_t bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a)
+               : "memory");
+  return v;
+}
+
+// Four e4m3 codes -> two f16 pairs, exactly.
+__device__ __forceinline__ void f16_of_e4m3x4(uint32_t w, uint32_t &lo, uint32_t &hi) {
+  asm("{\n\t.reg .b16 a, b;\n\t"
+      "mov.b32 {a, b}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+}
+
+__device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// The 8 x 8 matrix of 16-bit elements held across the warp, transposed.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// ------------------------------------------------------------------------------------------
+// Tile lists of the sparse forms: one CTA per (sequence, KV head) forms the union of its query
+// heads' tiles below the sequence's end, each with a mask of the heads that enable it.
+// ------------------------------------------------------------------------------------------
+__global__ void __launch_bounds__(THREADS) plan_kernel(const Params p) {
+  extern __shared__ uint32_t heads[];  // [Kb]
+  __shared__ int warp_n[WARPS];
+  pdl_launch_dependents();
+  const int task = blockIdx.x, b = task / p.N2, kvh = task % p.N2;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int kend = (seq_len(p, b) + TILE - 1) / TILE;
+  const size_t first = (size_t)b * p.N1 + (size_t)kvh * p.G;  // the group's first (b, h)
+  for (int t = tid; t < kend; t += THREADS) {
+    uint32_t on = 0;
+    if (p.block_mask)
+      for (int g = 0; g < p.G; ++g)
+        on |= p.block_mask[(first + g) * p.Kb + t] != 0 ? 1u << g : 0u;
+    heads[t] = on;
   }
   __syncthreads();
-  float m = -INFINITY, l = 0.f, acc = 0.f;
-  for (int t = 0; t < nt; ++t) {
-    if (p.block_mask && p.block_mask[row + t] == 0) continue;
-    if (p.sparse_indices && !((on[t >> 5] >> (t & 31)) & 1u)) continue;
-    const int pos = t * TILE + tid;
-    float s = -INFINITY;
-    long long at = -1;
-    if (pos < kv) {
-      const int pg = p.block_table[(size_t)b * p.L + pos / p.ps];
-      const int slot = pos % p.ps;
-      s = 0.f;
-      if (pg < 0 || pg >= p.num_pages) {
-        report(p, BSA_DEV_BAD_PAGE);
-      } else {
-        at = pg * p.page_bytes + kvh * p.head_bytes + slot * p.slot_bytes;
-        for (int d = 0; d < HEAD_DIM; ++d) s += qs[d] * e4m3_value(p.k_pages[at + d]);
-        s *= p.k_per_token ? p.k_descale[((size_t)pg * p.N2 + kvh) * p.ps + slot] : p.k_descale[0];
-        s *= p.scale;
+  if (p.sparse_indices) {
+    for (int g = 0; g < p.G; ++g) {
+      int len = p.sparse_seq_len[first + g];
+      if (len < 0 || len > p.Kb) {
+        if (tid == 0) report(p, BSA_DEV_BAD_INDEX);
+        len = len < 0 ? 0 : p.Kb;
       }
-    }
-    base[tid] = at;
-    float mx = s;
-    for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    if ((tid & 31) == 0) red[tid >> 5] = mx;
-    __syncthreads();
-    mx = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-    const float mn = fmaxf(m, mx), ms = mn == -INFINITY ? 0.f : mn;
-    ps[tid] = pos < kv ? expf(s - ms) : 0.f;
-    __syncthreads();
-    const float alpha = expf(m - ms);
-    acc *= alpha;
-    l *= alpha;
-    m = mn;
-    for (int j = 0; j < TILE && t * TILE + j < kv; ++j) {
-      l += ps[j];
-      if (base[j] >= 0) acc += ps[j] * e4m3_value(p.v_pages[base[j] + tid]);
+      for (int e = tid; e < len; e += THREADS) {
+        const int t = p.sparse_indices[(first + g) * p.Kb + e];
+        if (t < 0 || t >= p.Kb)
+          report(p, BSA_DEV_BAD_INDEX);
+        else if (t < kend)
+          atomicOr(&heads[t], 1u << g);
+      }
     }
     __syncthreads();
   }
-  const bool some = l != 0.f;
-  const float o = some ? acc / l * (p.v_per_head ? p.v_descale[kvh] : p.v_descale[0]) : 0.f;
-  p.out[((size_t)b * p.N1 + h) * HEAD_DIM + tid] = __float2bfloat16(o);
-  if (tid == 0 && p.lse) p.lse[(size_t)h * p.B + b] = some ? m + logf(l) : -FLT_MAX;
+  uint32_t *list = p.tiles + (size_t)task * p.Kb;
+  int n = 0;
+  for (int base = 0; base < kend; base += THREADS) {
+    const int t = base + tid;
+    const uint32_t on = t < kend ? heads[t] : 0u;
+    const unsigned bal = __ballot_sync(0xffffffffu, on != 0);
+    if (lane == 0) warp_n[warp] = __popc(bal);
+    __syncthreads();
+    int at = n + __popc(bal & ((1u << lane) - 1u));
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+      if (w < warp) at += warp_n[w];
+      n += warp_n[w];
+    }
+    if (on) list[at] = (uint32_t)t | on << 16;
+    __syncthreads();
+  }
+  if (tid == 0) p.counts[task] = n;
+}
+
+// ------------------------------------------------------------------------------------------
+// The attention kernel.
+// ------------------------------------------------------------------------------------------
+
+// A position in the batch's run of tiles, moved along by the copying side of a warp.
+template <bool SPARSE>
+struct Cursor {
+  int b, kvh, idx, n, kv;  // task, tile position in it, its tiles, the sequence's tokens
+  int pos, heads, page;    // of the current tile: the warp's first token, heads, physical page
+
+  __device__ __forceinline__ void enter(const Params &p) {  // a task's own numbers
+    if (SPARSE) {
+      n = max(p.counts[b * p.N2 + kvh], 1);
+    } else {
+      n = dense_tiles(kv);
+    }
+  }
+  // The current tile's entry and page (the page still unchecked; -1: nothing to read).
+  __device__ __forceinline__ void look(const Params &p, int warp) {
+    int tile = idx;
+    heads = 0xffff;
+    if (SPARSE) {
+      const size_t task = (size_t)b * p.N2 + kvh;
+      const uint32_t e = p.counts[task] > 0 ? p.tiles[task * p.Kb + idx] : 0u;
+      tile = e & 0xffffu;
+      heads = e >> 16;
+    }
+    pos = tile * TILE + warp * TOK;
+    page = pos < kv && heads != 0 ? p.block_table[(size_t)b * p.L + (pos >> p.ps_shift)] : -1;
+  }
+  __device__ __forceinline__ void next(const Params &p, int warp) {
+    if (++idx == n) {
+      idx = 0;
+      if (++kvh == p.N2) {
+        kvh = 0;
+        kv = seq_len(p, ++b);
+      }
+      enter(p);
+    }
+    look(p, warp);
+  }
+};
+
+template <int NT, bool SPARSE>  // NT: blocks of eight query heads per KV head
+__global__ void __launch_bounds__(THREADS, CTAS_PER_SM) decode_kernel(const Params p) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ float2 s_ml[WARPS][MAX_G];
+  __shared__ int s_sum[WARPS], s_item, s_off;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int r = lane >> 2, q4 = lane & 3;  // mma fragment coordinates
+  pdl_launch_dependents();
+  if (SPARSE) pdl_wait();  // the tile lists
+
+  // ---- this CTA's run [x0, x1) of the batch's tiles.  Items: sequences (all of whose KV heads
+  // have the same tiles), or tasks when every task has a list of its own.
+  const int items = SPARSE ? p.B * p.N2 : p.B;
+  const auto weight = [&](int i) {
+    return SPARSE ? max(p.counts[i], 1) : p.N2 * dense_tiles(seq_len(p, i));
+  };
+  const int per = (items + THREADS - 1) / THREADS, i0 = min(tid * per, items),
+            i1 = min(i0 + per, items);
+  int sum = 0;
+  for (int i = i0; i < i1; ++i) sum += weight(i);
+  int incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) s_sum[warp] = incl;
+  __syncthreads();
+  int total = 0;
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) {
+    if (w < warp) incl += s_sum[w];
+    total += s_sum[w];
+  }
+  const int runs = min((int)gridDim.x, total), cta = blockIdx.x;
+  if (cta >= runs) {
+    if (tid == 0) p.desc[cta] = make_int4(0, 0, 0, 0);
+    return;
+  }
+  const int x0 = (int)((long long)cta * total / runs);
+  const int x1 = (int)((long long)(cta + 1) * total / runs);
+  int before = incl - sum;
+  if (x0 >= before && x0 < incl) {
+    int i = i0;
+    for (int w = weight(i); x0 >= before + w && i + 1 < i1; w = weight(i)) {
+      before += w;
+      ++i;
+    }
+    s_item = i;
+    s_off = x0 - before;
+  }
+  __syncthreads();
+
+  Cursor<SPARSE> cur;
+  if (SPARSE) {
+    cur.b = s_item / p.N2;
+    cur.kvh = s_item % p.N2;
+    cur.idx = s_off;
+    cur.kv = seq_len(p, cur.b);
+    cur.enter(p);
+  } else {
+    cur.b = s_item;
+    cur.kv = seq_len(p, cur.b);
+    cur.enter(p);
+    cur.kvh = s_off / cur.n;
+    cur.idx = s_off % cur.n;
+  }
+  int b = cur.b, kvh = cur.kvh;      // the computing side's task
+  bool from_start = cur.idx == 0;    // the segment begins its task
+  int seg_n = cur.n, seg_x = x0;
+  cur.look(p, warp);
+
+  const uint32_t ring = ptx::smem_u32(smem) + warp * STAGES * STAGE_BYTES;
+  const int lrow = lane >> 3, lchunk = lane & 7;  // copy coordinates: 4 rows of 8 chunks at once
+  int to_issue = x1 - x0;
+
+  const auto issue = [&](int stage) {
+    if (to_issue > 0) {
+      const uint32_t dst = ring + stage * STAGE_BYTES;
+      const int left = cur.heads != 0 ? cur.kv - cur.pos : 0;
+      int page = cur.page;
+      if (page < 0 || page >= p.num_pages) {
+        if (left > 0 && lane == 0) report(p, BSA_DEV_BAD_PAGE);
+        page = -1;
+      }
+      const int rows = page >= 0 ? min(left, TOK) : 0;
+      const int slot = cur.pos & (p.ps - 1);
+      const long long off = page >= 0 ? page * p.page_bytes + cur.kvh * p.head_bytes +
+                                            (slot + lrow) * p.slot_bytes + lchunk * 16
+                                      : 0;
+      const uint8_t *ks = p.k_pages + off, *vs = p.v_pages + off;
+      if (left > 0) {
+#pragma unroll
+        for (int it = 0; it < TOK / 4; ++it) {
+          const int row = it * 4 + lrow;
+          const bool ok = row < rows;
+          const uint32_t d = dst + row * HEAD_DIM + ((lchunk ^ (row & 7)) << 4);
+          const long long o = ok ? it * 4 * p.slot_bytes : 0;
+          cp_async16(d, ok ? ks + o : p.k_pages, ok ? 16 : 0);
+          cp_async16(d + OFF_V, ok ? vs + o : p.v_pages, ok ? 16 : 0);
+        }
+        if (p.k_per_token) {
+          const bool ok = lane < rows;
+          const size_t at = ok ? ((size_t)page * p.N2 + cur.kvh) * p.ps + slot + lane : 0;
+          cp_async4(dst + OFF_KD + lane * 4, p.k_descale + at, ok ? 4 : 0);
+        }
+      }
+      if (lane == 0) {
+        const int last = cur.idx + 1 == cur.n;
+        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst + OFF_META),
+                     "r"(cur.heads), "r"(left), "r"(last), "r"(0)
+                     : "memory");
+      }
+      if (--to_issue > 0) cur.next(p, warp);
+    }
+    cp_async_commit();
+  };
+
+#pragma unroll
+  for (int s = 0; s < STAGES - 1; ++s) issue(s);
+
+  // ---- the group's queries as B fragments: column r is head r, a thread's 32 dimensions
+  // 32 q4 .. 32 q4 + 31 in steps of four (the order of K's reads below)
+  uint32_t qf[NT][16];
+  float fac[NT][2];  // score factors of the thread's columns 2 q4, 2 q4 + 1
+  const auto load_q = [&]() {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int g = nt * 8 + r;
+      const bool live = g < p.G;
+      const size_t at = (size_t)b * p.q_stride + (size_t)(kvh * p.G + (live ? g : 0)) * HEAD_DIM +
+                        q4 * 32;
+      float f = p.scale_log2;
+      if (p.q_e4m3) {
+        const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(p.q) + at);
+        const uint4 w0 = src[0], w1 = src[1];
+        const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f16_of_e4m3x4(w[i], qf[nt][2 * i], qf[nt][2 * i + 1]);
+        f *= p.q_descale[(size_t)b * p.N1 + kvh * p.G + (live ? g : 0)];
+      } else {
+        const uint4 *src =
+            reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.q) + at);
+        float amax = 0.f;
+        uint32_t w[16];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint4 v = src[i];
+          w[4 * i] = v.x;
+          w[4 * i + 1] = v.y;
+          w[4 * i + 2] = v.z;
+          w[4 * i + 3] = v.w;
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[i] << 16)),
+                                   fabsf(__uint_as_float(w[i] & 0xffff0000u))));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        // times 2^(14 - e), e the exponent of the row's largest value: it lands in
+        // [2^14, 2^15), and only values below 2^-28 of it lose bits to fp16's subnormals
+        const int e = max((int)(__float_as_uint(amax) >> 23) - 127, -110);
+        const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
+        f *= __uint_as_float((uint32_t)(127 + e - 14) << 23);
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          qf[nt][i] = f16x2(__uint_as_float(w[i] << 16) * up,
+                            __uint_as_float(w[i] & 0xffff0000u) * up);
+      }
+      if (!live) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) qf[nt][i] = 0u;
+      }
+      fac[nt][0] = __shfl_sync(0xffffffffu, f, 8 * q4);
+      fac[nt][1] = __shfl_sync(0xffffffffu, f, 8 * q4 + 4);
+    }
+  };
+
+  float m[NT][2], l[NT][2], acc[NT][8][4];
+  const auto reset = [&]() {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      m[nt][0] = m[nt][1] = -INFINITY;
+      l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) acc[nt][i][c] = 0.f;
+    }
+  };
+
+  // ---- one warp's 32 tokens of a tile
+  const float kd_all = p.k_per_token || !p.k_descale ? 1.f : p.k_descale[0];
+  const int group = (1 << p.G) - 1;
+  const auto compute = [&](uint32_t st, int heads, int left) {
+    float s[NT][2][4];  // [head block][16 tokens][token r | r + 8, head 2 q4 | + 1]
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) s[nt][mt][c] = 0.f;
+      const uint32_t row = st + (mt * 16 + r) * HEAD_DIM;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t chunk = ((2 * q4 + i) ^ r) << 4;
+        const uint4 a = lds128(row + chunk), c = lds128(row + 8 * HEAD_DIM + chunk);
+        const uint32_t wa[4] = {a.x, a.y, a.z, a.w}, wc[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          uint32_t a0, a1, a2, a3;
+          f16_of_e4m3x4(wa[w], a0, a2);
+          f16_of_e4m3x4(wc[w], a1, a3);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            mma16816(s[nt][mt], a0, a1, a2, a3, qf[nt][2 * (4 * i + w)],
+                     qf[nt][2 * (4 * i + w) + 1]);
+        }
+      }
+    }
+    // scores, masked; a masked value is replaced, never multiplied
+    const bool whole = left >= TOK && (!SPARSE || heads == group);
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt) {
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int t = mt * 16 + half * 8 + r;
+        float kd = kd_all;
+        if (p.k_per_token)
+          asm volatile("ld.shared.f32 %0, [%1];" : "=f"(kd) : "r"(st + OFF_KD + t * 4) : "memory");
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float &x = s[nt][mt][2 * half + c];
+            x *= kd * fac[nt][c];
+            if (!whole && (t >= left || (SPARSE && !((heads >> (nt * 8 + 2 * q4 + c)) & 1))))
+              x = -INFINITY;
+          }
+      }
+    }
+    uint32_t pf[NT][2][2];  // P as B fragments: [16 tokens][tokens 2 q4 | 2 q4 + 8, head r]
+    bool moved = false;
+    float alpha[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float ref[2];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float mx = fmaxf(fmaxf(s[nt][0][c], s[nt][0][2 + c]), fmaxf(s[nt][1][c], s[nt][1][2 + c]));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+        const float mn = fmaxf(m[nt][c], mx);
+        const float base = mn == -INFINITY ? 0.f : mn;
+        alpha[nt][c] = ptx::ex2_approx(m[nt][c] - base);
+        moved |= mn != m[nt][c];
+        m[nt][c] = mn;
+        ref[c] = base - P_SHIFT;
+      }
+      float sum0 = 0.f, sum1 = 0.f;
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt) {
+        float e[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) e[c] = ptx::ex2_approx(s[nt][mt][c] - ref[c & 1]);
+        sum0 += e[0] + e[2];
+        sum1 += e[1] + e[3];
+        pf[nt][mt][0] = transpose8x8(f16x2(e[0], e[1]));
+        pf[nt][mt][1] = transpose8x8(f16x2(e[2], e[3]));
+      }
+      l[nt][0] = l[nt][0] * alpha[nt][0] + sum0;
+      l[nt][1] = l[nt][1] * alpha[nt][1] + sum1;
+    }
+    if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) acc[nt][i][c] *= alpha[nt][c & 1];
+    }
+    const auto pv = [&]() {
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt) {
+        // tokens 2 q4, 2 q4 + 1 and those + 8, dimensions 16 r .. 16 r + 15
+        const uint32_t t0 = st + OFF_V + (mt * 16 + 2 * q4) * HEAD_DIM;
+        const uint32_t c0 = (r ^ (2 * q4)) << 4, c1 = (r ^ (2 * q4 + 1)) << 4;
+        const uint4 x0 = lds128(t0 + c0), x1 = lds128(t0 + HEAD_DIM + c1);
+        const uint4 y0 = lds128(t0 + 8 * HEAD_DIM + c0), y1 = lds128(t0 + 9 * HEAD_DIM + c1);
+        const uint32_t wx0[4] = {x0.x, x0.y, x0.z, x0.w}, wx1[4] = {x1.x, x1.y, x1.z, x1.w};
+        const uint32_t wy0[4] = {y0.x, y0.y, y0.z, y0.w}, wy1[4] = {y1.x, y1.y, y1.z, y1.w};
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          // bytes of the two tokens interleaved: a fragment pairs tokens within a dimension
+          uint32_t a[2][4];
+          f16_of_e4m3x4(__byte_perm(wx0[w], wx1[w], 0x5140), a[0][0], a[0][1]);
+          f16_of_e4m3x4(__byte_perm(wx0[w], wx1[w], 0x7362), a[1][0], a[1][1]);
+          f16_of_e4m3x4(__byte_perm(wy0[w], wy1[w], 0x5140), a[0][2], a[0][3]);
+          f16_of_e4m3x4(__byte_perm(wy0[w], wy1[w], 0x7362), a[1][2], a[1][3]);
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma16816(acc[nt][2 * w + i], a[i][0], a[i][1], a[i][2], a[i][3], pf[nt][mt][0],
+                       pf[nt][mt][1]);
+        }
+      }
+    };
+    if (!SPARSE || heads == group) {
+      pv();
+    } else {
+      // A tile that some heads mask: their weights are zero, but zero times a NaN of the tile's V
+      // would reach them through the shared product, so their columns are put back.
+      float kept[NT][8][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) kept[nt][i][c] = acc[nt][i][c];
+      pv();
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (!((heads >> (nt * 8 + 2 * q4 + (c & 1))) & 1)) acc[nt][i][c] = kept[nt][i][c];
+    }
+  };
+
+  // ---- the end of a segment: the four warps' states combined; written out when the segment is
+  // its whole task, left as a partial otherwise.  O goes through the stage just consumed, the one
+  // that the next copy will overwrite.
+  bool first_segment = true;
+  const auto flush = [&](int stage, bool to_end, int x) {
+    const uint32_t buf = ring + stage * STAGE_BYTES;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float t = l[nt][c];
+        t += __shfl_xor_sync(0xffffffffu, t, 4);
+        t += __shfl_xor_sync(0xffffffffu, t, 8);
+        t += __shfl_xor_sync(0xffffffffu, t, 16);
+        const int g = nt * 8 + 2 * q4 + c;
+        if (r == 0) s_ml[warp][g] = make_float2(m[nt][c], t);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(
+                           buf + g * (HEAD_DIM * 4) + (((4 * r + k) ^ q4) << 4)),
+                       "f"(acc[nt][2 * k][c]), "f"(acc[nt][2 * k][2 + c]),
+                       "f"(acc[nt][2 * k + 1][c]), "f"(acc[nt][2 * k + 1][2 + c])
+                       : "memory");
+      }
+    __syncthreads();
+    const bool complete = from_start && to_end;
+    const int slot = 2 * cta + (first_segment ? 0 : 1);
+    const uint8_t *o0 = smem + stage * STAGE_BYTES;
+    const float vd = !p.v_descale ? 0.f : p.v_per_head ? p.v_descale[kvh] : p.v_descale[0];
+    for (int g = 0; g < p.G; ++g) {
+      float2 ml[WARPS];
+      float mm = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) {
+        ml[w] = s_ml[w][g];
+        mm = fmaxf(mm, ml[w].x);
+      }
+      const float base = mm == -INFINITY ? 0.f : mm;
+      float ll = 0.f, o = 0.f;
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) {
+        const float f = ptx::ex2_approx(ml[w].x - base);
+        ll += f * ml[w].y;
+        o += f * *reinterpret_cast<const float *>(o0 + w * STAGES * STAGE_BYTES +
+                                                  g * (HEAD_DIM * 4) +
+                                                  (((tid >> 2) ^ ((g >> 1) & 3)) << 4) +
+                                                  (tid & 3) * 4);
+      }
+      if (complete) {
+        const int h = kvh * p.G + g;
+        const bool some = ll != 0.f;
+        p.out[((size_t)b * p.N1 + h) * HEAD_DIM + tid] =
+            __float2bfloat16(some ? o / ll * vd : 0.f);
+        if (tid == 0 && p.lse)
+          p.lse[(size_t)h * p.B + b] =
+              some ? (mm + log2f(ll) - P_SHIFT) * 0.6931471805599453f : -FLT_MAX;
+      } else {
+        if (tid == 0) p.part_ml[(size_t)slot * MAX_G + g] = make_float2(mm, ll);
+        p.part_o[((size_t)slot * p.G + g) * HEAD_DIM + tid] = o;
+      }
+    }
+    if (tid == 0 && x == x1) {
+      // the cut task that begins here, if one does: its partials are this slot and the first
+      // slots of the CTAs that follow, up to the run that holds its last tile
+      int4 d = make_int4(0, 0, 0, 0);
+      if (from_start && !to_end) {
+        const long long end = (long long)seg_x + seg_n;
+        d = make_int4(b * p.N2 + kvh, (int)((end * runs - 1) / total) - cta + 1, slot, 0);
+      }
+      p.desc[cta] = d;
+    }
+    __syncthreads();
+  };
+
+  load_q();
+  reset();
+  int stage = 0;
+  for (int x = x0; x < x1;) {
+    cp_async_wait<STAGES - 2>();
+    __syncwarp();  // the stage is filled for every lane, and the one before it read by every lane
+    const uint32_t st = ring + stage * STAGE_BYTES;
+    issue(stage == 0 ? STAGES - 1 : stage - 1);
+    uint32_t heads, left, last, unused;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(heads), "=r"(left), "=r"(last), "=r"(unused)
+                 : "r"(st + OFF_META)
+                 : "memory");
+    if ((int)left > 0) compute(st, (int)heads, (int)left);
+    ++x;
+    if (last || x == x1) {
+      flush(stage, last, x);
+      if (x < x1) {
+        first_segment = false;
+        from_start = true;
+        seg_x = x;
+        if (++kvh == p.N2) {
+          kvh = 0;
+          ++b;
+        }
+        seg_n = SPARSE ? max(p.counts[b * p.N2 + kvh], 1) : dense_tiles(seq_len(p, b));
+        load_q();
+        reset();
+      }
+    }
+    stage = stage == STAGES - 1 ? 0 : stage + 1;
+  }
+}
+
+// ------------------------------------------------------------------------------------------
+// The join: block (c, g) combines head g of the cut task that run c begins, if it begins one.
+// Launched beside the attention kernel's end (its blocks wait for that kernel's writes).
+// ------------------------------------------------------------------------------------------
+__global__ void __launch_bounds__(HEAD_DIM) join_kernel(const Params p) {
+  pdl_wait();
+  const int cta = blockIdx.x, g = blockIdx.y, d = threadIdx.x;
+  const int4 w = p.desc[cta];
+  const int n = w.y;
+  if (n == 0) return;
+  const auto slot = [&](int j) { return j == 0 ? w.z : 2 * (cta + j); };
+  float mm = -INFINITY;
+  for (int j = 0; j < n; ++j) mm = fmaxf(mm, p.part_ml[(size_t)slot(j) * MAX_G + g].x);
+  const float base = mm == -INFINITY ? 0.f : mm;
+  float ll = 0.f, o = 0.f;
+#pragma unroll 4
+  for (int j = 0; j < n; ++j) {
+    const float2 ml = p.part_ml[(size_t)slot(j) * MAX_G + g];
+    const float f = ptx::ex2_approx(ml.x - base);
+    ll += f * ml.y;
+    o += f * p.part_o[((size_t)slot(j) * p.G + g) * HEAD_DIM + d];
+  }
+  const int b = w.x / p.N2, kvh = w.x % p.N2, h = kvh * p.G + g;
+  const bool some = ll != 0.f;
+  const float vd = p.v_per_head ? p.v_descale[kvh] : p.v_descale[0];
+  p.out[((size_t)b * p.N1 + h) * HEAD_DIM + d] =
+      __float2bfloat16(some ? o / ll * vd : 0.f);
+  if (d == 0 && p.lse)
+    p.lse[(size_t)h * p.B + b] =
+        some ? (mm + log2f(ll) - P_SHIFT) * 0.6931471805599453f : -FLT_MAX;
 }
 
 }  // namespace decode

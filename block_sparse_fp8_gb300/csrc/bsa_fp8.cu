@@ -110,6 +110,7 @@ struct DeviceInfo {
   int smem_reserved = 0;      // shared memory the system reserves per resident block
   size_t smem_attr = 0;  // dynamic shared memory the attention kernel is enabled for
   size_t smem_attr_wide = 0;  // ... and the 256-wide macro-block kernel
+  bool decode_attr = false;   // the decode kernels' shared memory is enabled
 };
 
 static DeviceInfo g_devices[64];
@@ -744,9 +745,75 @@ bsa_status_t validate_decode(const bsa_fp8_decode_dims_t *d) {
 
 }  // namespace
 
+namespace {
+
+// Grid of the decode kernel and where its workspace arrays lie.  The grid depends on the SM count
+// and an upper bound of the tiles only: the host does not know the lengths.
+struct DecodePlan {
+  int grid = 0;
+  size_t off_ml = 0, off_o = 0, off_counts = 0, off_tiles = 0, bytes = 0;
+};
+
+DecodePlan plan_decode(const bsa_fp8_decode_dims_t *d, int num_sms) {
+  DecodePlan plan;
+  const long long tasks = (long long)d->B * d->N2, kb = cdiv(d->max_kv_len, TILE);
+  plan.grid = (int)std::max<long long>(
+      1, std::min<long long>((long long)decode::CTAS_PER_SM * std::max(num_sms, 1),
+                             tasks * std::max<long long>(kb, 1)));
+  const size_t slots = 2 * (size_t)plan.grid;
+  plan.off_ml = round256((size_t)plan.grid * sizeof(int4));
+  plan.off_o = plan.off_ml + round256(slots * decode::MAX_G * sizeof(float2));
+  plan.off_counts = plan.off_o + slots * (size_t)(d->N1 / d->N2) * HEAD_DIM * sizeof(float);
+  plan.off_tiles = plan.off_counts + (d->sparse ? round256((size_t)tasks * sizeof(int)) : 0);
+  plan.bytes = plan.off_tiles + (d->sparse ? (size_t)tasks * (size_t)kb * sizeof(uint32_t) : 0);
+  return plan;
+}
+
+// Enables the decode kernels' dynamic shared memory on the current device, once.
+bsa_status_t enable_decode() {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return BSA_ERR_CUDA;
+  std::lock_guard<std::mutex> lock(g_devices_mu);
+  DeviceInfo &di = g_devices[dev];  // check_device has bounded dev
+  if (di.decode_attr) return BSA_OK;
+  const auto enable = [](const void *kernel) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                decode::SMEM_BYTES) == cudaSuccess;
+  };
+  if (!enable((const void *)decode::decode_kernel<1, false>) ||
+      !enable((const void *)decode::decode_kernel<2, false>) ||
+      !enable((const void *)decode::decode_kernel<1, true>) ||
+      !enable((const void *)decode::decode_kernel<2, true>))
+    return BSA_ERR_CUDA;
+  di.decode_attr = true;
+  return BSA_OK;
+}
+
+// A launch that may begin while the kernel before it on the stream runs; it waits for that
+// kernel's writes itself (griddepcontrol.wait).
+template <typename... Args>
+bool launch_dependent(void (*kernel)(Args...), dim3 grid, int threads, size_t smem, void *stream,
+                      const Args &...args) {
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = (cudaStream_t)stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess;
+}
+
+}  // namespace
+
 extern "C" size_t bsa_fp8_decode_workspace_size(const bsa_fp8_decode_dims_t *dims) {
   if (validate_decode(dims) != BSA_OK) return 0;
-  return WORKSPACE_BYTES;
+  int num_sms = 0;
+  if (check_device(0, &num_sms) != BSA_OK) return WORKSPACE_BYTES;
+  return plan_decode(dims, num_sms).bytes;
 }
 
 extern "C" bsa_status_t bsa_fp8_decode(const bsa_fp8_decode_dims_t *d, const void *q,
@@ -783,7 +850,11 @@ extern "C" bsa_status_t bsa_fp8_decode(const bsa_fp8_decode_dims_t *d, const voi
   int num_sms = 0;
   st = check_device(0, &num_sms);
   if (st != BSA_OK) return st;
-  if (workspace_bytes < WORKSPACE_BYTES) return BSA_ERR_WORKSPACE;
+  const DecodePlan plan = plan_decode(d, num_sms);
+  if (workspace_bytes < plan.bytes) return BSA_ERR_WORKSPACE;
+  st = enable_decode();
+  if (st != BSA_OK) return st;
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
   decode::Params p;
   memset(&p, 0, sizeof(p));
   p.q = q;
@@ -814,9 +885,33 @@ extern "C" bsa_status_t bsa_fp8_decode(const bsa_fp8_decode_dims_t *d, const voi
   p.q_e4m3 = e4m3;
   p.k_per_token = k_tok;
   p.v_per_head = d->v_scale_kind == BSA_SCALE_PER_HEAD;
-  p.scale = softmax_scale;
-  decode::decode_kernel<<<(unsigned)(d->B * d->N1), decode::THREADS, 0, (cudaStream_t)stream>>>(p);
-  return cudaGetLastError() == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
+  p.scale_log2 = (float)((double)softmax_scale * 1.4426950408889634);
+  p.ps_shift = d->page_size == 64 ? 6 : 5;
+  p.desc = reinterpret_cast<int4 *>(ws);
+  p.part_ml = reinterpret_cast<float2 *>(ws + plan.off_ml);
+  p.part_o = reinterpret_cast<float *>(ws + plan.off_o);
+  p.counts = reinterpret_cast<int *>(ws + plan.off_counts);
+  p.tiles = reinterpret_cast<uint32_t *>(ws + plan.off_tiles);
+  const cudaStream_t s = (cudaStream_t)stream;
+  const bool wide = p.G > 8;  // two blocks of eight query heads per KV head
+  if (d->sparse && !none) {
+    decode::plan_kernel<<<(unsigned)(d->B * d->N2), decode::THREADS,
+                          (size_t)p.Kb * sizeof(uint32_t), s>>>(p);
+    if (cudaGetLastError() != cudaSuccess) return BSA_ERR_CUDA;
+    if (!launch_dependent(wide ? decode::decode_kernel<2, true> : decode::decode_kernel<1, true>,
+                          dim3((unsigned)plan.grid), decode::THREADS, decode::SMEM_BYTES, stream,
+                          p))
+      return BSA_ERR_CUDA;
+  } else {
+    const auto kernel = wide ? decode::decode_kernel<2, false> : decode::decode_kernel<1, false>;
+    kernel<<<(unsigned)plan.grid, decode::THREADS, decode::SMEM_BYTES, s>>>(p);
+    if (cudaGetLastError() != cudaSuccess) return BSA_ERR_CUDA;
+  }
+  // tasks of one tile are never cut
+  if (p.Kb > 1 && !launch_dependent(decode::join_kernel, dim3((unsigned)plan.grid, (unsigned)p.G),
+                                    HEAD_DIM, 0, stream, p))
+    return BSA_ERR_CUDA;
+  return BSA_OK;
 }
 
 extern "C" bsa_status_t bsa_fp8_gather_kv(const bsa_fp8_gather_dims_t *d, const void *k_pages,
