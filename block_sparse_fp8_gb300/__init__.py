@@ -340,46 +340,54 @@ def append_kv(k_new, v_new, cu_seqlens_new, cache_seqlens, block_table, k_pages,
 # serving: decode, gather_kv, merge_states
 # ---------------------------------------------------------------------------------------------
 
-def _check(name, t, dtypes, shape, device):
-    """Raises ValueError unless `t` is a contiguous tensor of one of `dtypes` and of `shape` on
-    `device`."""
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, q or the cache on {device}")
+# A serving loop makes these calls once a layer and token, so their checks are kept to a few plain
+# comparisons a tensor (a refusal works out its message afterwards).
+
+def _refuse(name, t, dtypes, shape, dev):
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, q or the cache on another device")
     if t.dtype not in dtypes:
         raise ValueError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _check_status(dev_status, device):
+def _check(name, t, dtypes, shape, dev):
+    """Raises ValueError unless `t` is a contiguous tensor of one of `dtypes` and of `shape` on
+    the CUDA device of index `dev` (-1: not a CUDA device, which _call refuses)."""
+    if (t.dtype not in dtypes or t.shape != shape or t.get_device() != dev
+            or not t.is_contiguous()):
+        _refuse(name, t, dtypes, shape, dev)
+
+
+def _call(fn, args, dev, stream, what):
+    """fn(*args, stream handle) with device `dev` current; raises BsaError on a status but 0."""
     import torch
 
-    if dev_status is not None and (dev_status.device != device or dev_status.numel() < 1 or
-                                   dev_status.dtype != torch.int32):
-        raise ValueError(f"dev_status must be an int32 tensor on {device}")
-
-
-def _launch(device, stream, what, call):
-    """call(stream handle) with `device` current; raises BsaError on a status other than 0."""
-    import torch
-
-    if device.type != "cuda":
-        raise ValueError(f"{what}: tensors must be on a CUDA device, not {device}")
-    if stream is not None and stream.device != device:
-        raise ValueError(f"{what}: the stream is on {stream.device}, the tensors on {device}")
-    if torch.cuda.current_device() == device.index:
-        st = call((torch.cuda.current_stream() if stream is None else stream).cuda_stream)
+    if dev < 0:
+        raise ValueError(f"{what}: tensors must be on a CUDA device")
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(dev)
+    elif stream.device.index != dev:
+        raise ValueError(f"{what}: the stream is on {stream.device}, the tensors on cuda:{dev}")
     else:
-        with torch.cuda.device(device):
-            st = call((torch.cuda.current_stream() if stream is None else stream).cuda_stream)
+        handle = stream.cuda_stream
+    if torch.cuda.current_device() == dev:
+        st = fn(*args, handle)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, handle)
     if st != 0:
         raise BsaError(st, what)
 
 
-def _codes(torch):
-    return (torch.uint8, torch.float8_e4m3fn)
+def _check_status(dev_status, dev):
+    import torch
+
+    if (dev_status.dtype is not torch.int32 or dev_status.numel() < 1
+            or dev_status.get_device() != dev):
+        raise ValueError("dev_status must be an int32 tensor on the device of the others")
 
 
 def _pool(pages, kv_layout):
@@ -394,12 +402,11 @@ def make_decode_dims(q, k_pages, block_table, max_kv_len, k_scale_kind, v_scale_
                      kv_layout=KV_HND, sparse=False) -> DecodeDims:
     B, N1, D = q.shape
     P, N2, ps, _ = _pool(k_pages, kv_layout)
-    return DecodeDims(B=B, N1=N1, N2=N2, D=D, page_size=ps, max_kv_len=int(max_kv_len),
-                      num_pages=P, max_pages_per_seq=block_table.shape[1],
-                      k_scale_kind=int(k_scale_kind), v_scale_kind=int(v_scale_kind),
-                      kv_layout=int(kv_layout),
-                      q_type=QTYPE_E4M3 if q.element_size() == 1 else QTYPE_BF16,
-                      q_stride=q.stride(0) if B > 1 else N1 * D, sparse=int(bool(sparse)))
+    # in the order of DecodeDims' fields
+    return DecodeDims(B, N1, N2, D, ps, max_kv_len, P, block_table.shape[1], k_scale_kind,
+                      v_scale_kind, kv_layout,
+                      QTYPE_E4M3 if q.element_size() == 1 else QTYPE_BF16,
+                      q.stride(0) if B > 1 else N1 * D, 1 if sparse else 0)
 
 
 def decode_workspace_size(dims: DecodeDims) -> int:
@@ -423,30 +430,31 @@ def decode(q, k_pages, v_pages, k_descale, v_descale, seqused_kv, block_table, m
     must not be shared by calls in flight at once."""
     import torch
 
+    bf16, f32, i32 = (torch.bfloat16,), (torch.float32,), (torch.int32,)
+    codes = (torch.uint8, torch.float8_e4m3fn)
+    dev = q.get_device()
     if q.dim() != 3:
         raise ValueError(f"q has shape {tuple(q.shape)}, expected [B, N1, 128]")
     B, N1, D = q.shape
-    dev = q.device
-    P, N2, ps, _ = _pool(k_pages, kv_layout)
-    if q.dtype != torch.bfloat16 and q.dtype not in _codes(torch):
+    if q.dtype not in bf16 and q.dtype not in codes:
         raise ValueError(f"q has dtype {q.dtype}, expected bf16 or e4m3 codes")
-    if q.stride(2) != 1 or (N1 > 1 and q.stride(1) != D):
+    if not q.is_contiguous() and (q.stride(2) != 1 or (N1 > 1 and q.stride(1) != D)):
         raise ValueError("q must be contiguous within a sequence's row")
+    P, N2, ps, _ = _pool(k_pages, kv_layout)
     if block_table.dim() != 2:
         raise ValueError(f"block_table has shape {tuple(block_table.shape)}, expected [B, L]")
-    f32, i32 = (torch.float32,), (torch.int32,)
-    codes = _codes(torch)
-    _check("k_pages", k_pages, codes, k_pages.shape, dev)
-    _check("v_pages", v_pages, codes, k_pages.shape, dev)
     k_kind = k_scale_kind if k_scale_kind is not None else (
         SCALE_PER_TOKEN_HEAD if k_descale.dim() == 3 else SCALE_PER_TENSOR)
     v_kind = v_scale_kind if v_scale_kind is not None else (
         SCALE_PER_HEAD if v_descale.numel() == N2 else SCALE_PER_TENSOR)
+    _check("k_pages", k_pages, codes, k_pages.shape, dev)
+    _check("v_pages", v_pages, codes, k_pages.shape, dev)
     _check("k_descale", k_descale, f32,
            (P, N2, ps) if k_kind == SCALE_PER_TOKEN_HEAD else (1,), dev)
     _check("v_descale", v_descale, f32, (N2,) if v_kind == SCALE_PER_HEAD else (1,), dev)
     _check("seqused_kv", seqused_kv, i32, (B,), dev)
-    _check("block_table", block_table, i32, (B, block_table.shape[1]), dev)
+    L = block_table.shape[1]
+    _check("block_table", block_table, i32, (B, L), dev)
     if q_descale is not None:
         _check("q_descale", q_descale, f32, (B, N1), dev)
     sparse = block_mask is not None or sparse_indices is not None
@@ -458,33 +466,46 @@ def decode(q, k_pages, v_pages, k_descale, v_descale, seqused_kv, block_table, m
             _check("sparse_indices", sparse_indices, i32, (B, N1, Kb), dev)
         if sparse_seq_len is not None:
             _check("sparse_seq_len", sparse_seq_len, i32, (B, N1), dev)
-    dims = make_decode_dims(q, k_pages, block_table, max_kv_len, k_kind, v_kind, kv_layout, sparse)
     if out is None:
-        out = torch.empty((B, N1, D), dtype=torch.bfloat16, device=dev)
+        out = torch.empty((B, N1, D), dtype=torch.bfloat16, device=q.device)
     else:
-        _check("out", out, (torch.bfloat16,), (B, N1, D), dev)
+        _check("out", out, bf16, (B, N1, D), dev)
     if lse is not None:
         _check("lse", lse, f32, (N1, B), dev)
     elif return_lse:
-        lse = torch.empty((N1, B), dtype=torch.float32, device=dev)
+        lse = torch.empty((N1, B), dtype=torch.float32, device=q.device)
+    if dev_status is not None:
+        _check_status(dev_status, dev)
+    # in the order of DecodeDims' fields, as make_decode_dims
+    dims = DecodeDims(B, N1, N2, D, ps, max_kv_len, P, L, k_kind, v_kind, kv_layout,
+                      QTYPE_BF16 if q.dtype in bf16 else QTYPE_E4M3,
+                      q.stride(0) if B > 1 else N1 * D, sparse)
+    if workspace is None:
+        if dev < 0:
+            raise ValueError("decode: tensors must be on a CUDA device")
+        with torch.cuda.device(dev):
+            nbytes = decode_workspace_size(dims)
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on q's device")
     if softmax_scale is None:
         softmax_scale = 1.0 / math.sqrt(D)
-    _check_status(dev_status, dev)
-    if workspace is not None and (workspace.device != dev or not workspace.is_contiguous()):
-        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
-
-    def call(handle):
-        ws = workspace
-        if ws is None:
-            ws = torch.empty(decode_workspace_size(dims), dtype=torch.uint8, device=dev)
-        return lib().bsa_fp8_decode(
-            ctypes.byref(dims), _p(q), _p(q_descale), _p(k_pages), _p(v_pages), _p(k_descale),
-            _p(v_descale), _p(seqused_kv), _p(block_table), _p(block_mask), _p(sparse_indices),
-            _p(sparse_seq_len), float(softmax_scale), _p(out), _p(lse), _p(ws), ws.nbytes,
-            _p(dev_status), handle)
-
-    _launch(dev, stream, "bsa_fp8_decode", call)
+    _call(lib().bsa_fp8_decode,
+          (ctypes.byref(dims), q.data_ptr(), _p(q_descale), k_pages.data_ptr(),
+           v_pages.data_ptr(), k_descale.data_ptr(), v_descale.data_ptr(), seqused_kv.data_ptr(),
+           block_table.data_ptr(), _p(block_mask), _p(sparse_indices), _p(sparse_seq_len),
+           softmax_scale, out.data_ptr(), _p(lse), workspace.data_ptr(), workspace.nbytes,
+           _p(dev_status)), dev, stream, "bsa_fp8_decode")
     return out, lse
+
+
+def _gather_rows(name, t, dtype, shape, pages):
+    import torch
+
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=pages.device)
+    _check(name, t, (dtype,), shape, pages.get_device())
+    return t
 
 
 def gather_kv(k_pages, v_pages, k_descale, v_descale, cu_seqlens, block_table, total: int,
@@ -498,12 +519,13 @@ def gather_kv(k_pages, v_pages, k_descale, v_descale, cu_seqlens, block_table, t
     that side out (returned as None)."""
     import torch
 
+    f32, i32 = (torch.float32,), (torch.int32,)
+    codes = (torch.uint8, torch.float8_e4m3fn)
     pages = k_pages if k_pages is not None else v_pages
     if pages is None:
         raise ValueError("k_pages and v_pages are both None")
-    dev = pages.device
+    dev = pages.get_device()
     P, N2, ps, D = _pool(pages, kv_layout)
-    f32, i32 = (torch.float32,), (torch.int32,)
     given = k_out if k_out is not None else v_out
     if out_dtype is None:
         out_dtype = given.dtype if given is not None else torch.bfloat16
@@ -516,41 +538,35 @@ def gather_kv(k_pages, v_pages, k_descale, v_descale, cu_seqlens, block_table, t
     _check("cu_seqlens", cu_seqlens, i32, (B + 1,), dev)
     if cache_starts is not None:
         _check("cache_starts", cache_starts, i32, (B,), dev)
-    k_kind, v_kind = SCALE_PER_TENSOR, SCALE_PER_TENSOR
-    shape = (int(total), N2, D)
-
-    def rows(name, t):
-        if t is None:
-            return torch.empty(shape, dtype=out_dtype, device=dev)
-        _check(name, t, (out_dtype,), shape, dev)
-        return t
-
+    if dev_status is not None:
+        _check_status(dev_status, dev)
+    total = int(total)
+    k_kind = v_kind = SCALE_PER_TENSOR
+    shape = (total, N2, D)
     if k_pages is not None:
-        _check("k_pages", k_pages, _codes(torch), pages.shape, dev)
         k_kind = k_scale_kind if k_scale_kind is not None else (
             SCALE_PER_TOKEN_HEAD if k_descale.dim() == 3 else SCALE_PER_TENSOR)
+        _check("k_pages", k_pages, codes, pages.shape, dev)
         _check("k_descale", k_descale, f32,
                (P, N2, ps) if k_kind == SCALE_PER_TOKEN_HEAD else (1,), dev)
-        k_out = rows("k_out", k_out)
+        k_out = _gather_rows("k_out", k_out, out_dtype, shape, pages)
     elif k_out is not None:
         raise ValueError("k_out given without k_pages")
     if v_pages is not None:
-        _check("v_pages", v_pages, _codes(torch), pages.shape, dev)
         v_kind = v_scale_kind if v_scale_kind is not None else (
             SCALE_PER_HEAD if v_descale.numel() == N2 else SCALE_PER_TENSOR)
+        _check("v_pages", v_pages, codes, pages.shape, dev)
         _check("v_descale", v_descale, f32, (N2,) if v_kind == SCALE_PER_HEAD else (1,), dev)
-        v_out = rows("v_out", v_out)
+        v_out = _gather_rows("v_out", v_out, out_dtype, shape, pages)
     elif v_out is not None:
         raise ValueError("v_out given without v_pages")
-    _check_status(dev_status, dev)
-    dims = GatherDims(B=B, N2=N2, D=D, page_size=ps, num_pages=P, max_pages_per_seq=L,
-                      total=int(total), k_scale_kind=int(k_kind), v_scale_kind=int(v_kind),
-                      kv_layout=int(kv_layout),
-                      out_type=OUT_FP32 if out_dtype == torch.float32 else OUT_BF16)
-    _launch(dev, stream, "bsa_fp8_gather_kv", lambda handle: lib().bsa_fp8_gather_kv(
-        ctypes.byref(dims), _p(k_pages), _p(v_pages), _p(k_descale), _p(v_descale),
-        _p(cu_seqlens), _p(cache_starts), _p(block_table), _p(k_out), _p(v_out), _p(dev_status),
-        handle))
+    # in the order of GatherDims' fields
+    dims = GatherDims(B, N2, D, ps, P, L, total, k_kind, v_kind, kv_layout,
+                      OUT_FP32 if out_dtype is torch.float32 else OUT_BF16)
+    _call(lib().bsa_fp8_gather_kv,
+          (ctypes.byref(dims), _p(k_pages), _p(v_pages), _p(k_descale), _p(v_descale),
+           cu_seqlens.data_ptr(), _p(cache_starts), block_table.data_ptr(), _p(k_out), _p(v_out),
+           _p(dev_status)), dev, stream, "bsa_fp8_gather_kv")
     return k_out, v_out
 
 
@@ -561,27 +577,30 @@ def merge_states(outs, lses, out=None, lse=None, return_lse: bool = True, stream
     and `lse` one of `lses`."""
     import torch
 
+    bf16, f32 = (torch.bfloat16,), (torch.float32,)
     n = len(outs)
     if n < 1 or n > MAX_MERGE or len(lses) != n:
         raise ValueError(f"{n} outs and {len(lses)} lses: 1 to {MAX_MERGE} of each")
-    if outs[0].dim() != 3 or outs[0].shape[2] != 128:
-        raise ValueError(f"outs[0] has shape {tuple(outs[0].shape)}, expected [T, N1, 128]")
-    T, N1, D = outs[0].shape
-    dev = outs[0].device
-    bf16, f32 = (torch.bfloat16,), (torch.float32,)
-    for i in range(n):
-        _check(f"outs[{i}]", outs[i], bf16, (T, N1, D), dev)
-        _check(f"lses[{i}]", lses[i], f32, (N1, T), dev)
+    first = outs[0]
+    dev = first.get_device()
+    if first.dim() != 3 or first.shape[2] != 128:
+        raise ValueError(f"outs[0] has shape {tuple(first.shape)}, expected [T, N1, 128]")
+    shape = first.shape
+    T, N1, _ = shape
+    for o in outs:
+        _check("outs", o, bf16, shape, dev)
+    for x in lses:
+        _check("lses", x, f32, (N1, T), dev)
     if out is None:
-        out = torch.empty((T, N1, D), dtype=torch.bfloat16, device=dev)
+        out = torch.empty(shape, dtype=torch.bfloat16, device=first.device)
     else:
-        _check("out", out, bf16, (T, N1, D), dev)
+        _check("out", out, bf16, shape, dev)
     if lse is not None:
         _check("lse", lse, f32, (N1, T), dev)
     elif return_lse:
-        lse = torch.empty((N1, T), dtype=torch.float32, device=dev)
-    po = (ctypes.c_void_p * n)(*(o.data_ptr() for o in outs))
-    pl = (ctypes.c_void_p * n)(*(x.data_ptr() for x in lses))
-    _launch(dev, stream, "bsa_fp8_merge_states", lambda handle: lib().bsa_fp8_merge_states(
-        n, po, pl, T, N1, _p(out), _p(lse), handle))
+        lse = torch.empty((N1, T), dtype=torch.float32, device=first.device)
+    ptrs = ctypes.c_void_p * n
+    _call(lib().bsa_fp8_merge_states,
+          (n, ptrs(*[o.data_ptr() for o in outs]), ptrs(*[x.data_ptr() for x in lses]), T, N1,
+           out.data_ptr(), _p(lse)), dev, stream, "bsa_fp8_merge_states")
     return out, lse

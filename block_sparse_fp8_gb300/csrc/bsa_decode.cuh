@@ -42,7 +42,7 @@ namespace decode {
 constexpr int WARPS = 4;
 constexpr int THREADS = WARPS * 32;
 constexpr int TOK = TILE / WARPS;  // tokens of a tile that one warp owns: one mma row block pair
-constexpr int STAGES = 3;
+constexpr int STAGES = 2;
 constexpr int CTAS_PER_SM = 2;
 // one warp's stage: K rows, V rows, the tokens' K descales, {head mask, tokens left, last tile}
 constexpr int OFF_V = TOK * HEAD_DIM;
@@ -66,10 +66,9 @@ struct Params {
   __nv_bfloat16 *out;
   float *lse;
   int *dev_status;
-  // workspace: per main CTA {task, partials, first slot} of the cut task it begins; per slot (two
-  // per CTA) and head of the group (m, l) and O; with lists, per task the count of its tiles and
-  // the tiles, ascending, with the heads that enable them in the upper half
-  int4 *desc;
+  // workspace: per slot (two per CTA) and head of the group a partial (m, l) and O; with lists, per
+  // task the count of its tiles and the tiles, ascending, the heads that enable them in the upper
+  // half
   float2 *part_ml;
   float *part_o;
   int *counts;
@@ -161,6 +160,18 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// Thread d's element of head g of (b, kvh)'s result, and the row's LSE.
+__device__ __forceinline__ void write_row(const Params &p, int b, int kvh, int g, int d, float m,
+                                          float l, float o) {
+  const int h = kvh * p.G + g;
+  const bool some = l != 0.f;  // a NaN sum is a result, not an empty row
+  const float vd = some ? (p.v_per_head ? p.v_descale[kvh] : p.v_descale[0]) : 0.f;
+  p.out[((size_t)b * p.N1 + h) * HEAD_DIM + d] = __float2bfloat16(some ? o / l * vd : 0.f);
+  if (d == 0 && p.lse)
+    p.lse[(size_t)h * p.B + b] =
+        some ? (m + log2f(l) - P_SHIFT) * 0.6931471805599453f : -FLT_MAX;
+}
+
 // ------------------------------------------------------------------------------------------
 // Tile lists of the sparse forms: one CTA per (sequence, KV head) forms the union of its query
 // heads' tiles below the sequence's end, each with a mask of the heads that enable it.
@@ -222,6 +233,63 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(const Params p) {
 // The attention kernel.
 // ------------------------------------------------------------------------------------------
 
+// Run `index` of the batch's tiles cut into `grid` runs (as many as there are tiles, if those are
+// fewer): tiles [x0, x1), and where tile x0 (with `last`: tile x1 - 1) lies: item and offset in it.
+// Items are sequences, all of whose KV heads have the same tiles, or tasks when every task has a
+// list of its own.  Called by all of a CTA's W warps.
+struct Run {
+  int x0, x1, total, runs, item, off;
+};
+
+template <bool SPARSE, int W>
+__device__ __forceinline__ Run find_run(const Params &p, int grid, int index, bool last) {
+  __shared__ int s_sum[W], s_item, s_off;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int items = SPARSE ? p.B * p.N2 : p.B;
+  const auto weight = [&](int i) {
+    return SPARSE ? max(__ldcg(p.counts + i), 1) : p.N2 * dense_tiles(seq_len(p, i));
+  };
+  const int per = (items + W * 32 - 1) / (W * 32), i0 = min(tid * per, items),
+            i1 = min(i0 + per, items);
+  int sum = 0;
+  for (int i = i0; i < i1; ++i) sum += weight(i);
+  int incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) s_sum[warp] = incl;
+  __syncthreads();
+  Run run;
+  run.total = 0;
+#pragma unroll
+  for (int w = 0; w < W; ++w) {
+    if (w < warp) incl += s_sum[w];
+    run.total += s_sum[w];
+  }
+  run.runs = min(grid, run.total);
+  run.x0 = run.x1 = run.item = run.off = 0;
+  if (index >= run.runs) return run;
+  run.x0 = (int)((long long)index * run.total / run.runs);
+  run.x1 = (int)((long long)(index + 1) * run.total / run.runs);
+  const int x = last ? run.x1 - 1 : run.x0;
+  int before = incl - sum;
+  if (x >= before && x < incl) {
+    int i = i0;
+    for (int w = weight(i); x >= before + w && i + 1 < i1; w = weight(i)) {
+      before += w;
+      ++i;
+    }
+    s_item = i;
+    s_off = x - before;
+  }
+  __syncthreads();
+  run.item = s_item;
+  run.off = s_off;
+  return run;
+}
+
 // A position in the batch's run of tiles, moved along by the copying side of a warp.
 template <bool SPARSE>
 struct Cursor {
@@ -265,72 +333,31 @@ template <int NT, bool SPARSE>  // NT: blocks of eight query heads per KV head
 __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) decode_kernel(const Params p) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float2 s_ml[WARPS][MAX_G];
-  __shared__ int s_sum[WARPS], s_item, s_off;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int r = lane >> 2, q4 = lane & 3;  // mma fragment coordinates
-  pdl_launch_dependents();
-  if (SPARSE) pdl_wait();  // the tile lists
+  if (SPARSE) pdl_wait();   // the tile lists
+  pdl_launch_dependents();  // the join, which may read the lists' counts too: only now
 
-  // ---- this CTA's run [x0, x1) of the batch's tiles.  Items: sequences (all of whose KV heads
-  // have the same tiles), or tasks when every task has a list of its own.
-  const int items = SPARSE ? p.B * p.N2 : p.B;
-  const auto weight = [&](int i) {
-    return SPARSE ? max(p.counts[i], 1) : p.N2 * dense_tiles(seq_len(p, i));
-  };
-  const int per = (items + THREADS - 1) / THREADS, i0 = min(tid * per, items),
-            i1 = min(i0 + per, items);
-  int sum = 0;
-  for (int i = i0; i < i1; ++i) sum += weight(i);
-  int incl = sum;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += v;
-  }
-  if (lane == 31) s_sum[warp] = incl;
-  __syncthreads();
-  int total = 0;
-#pragma unroll
-  for (int w = 0; w < WARPS; ++w) {
-    if (w < warp) incl += s_sum[w];
-    total += s_sum[w];
-  }
-  const int runs = min((int)gridDim.x, total), cta = blockIdx.x;
-  if (cta >= runs) {
-    if (tid == 0) p.desc[cta] = make_int4(0, 0, 0, 0);
-    return;
-  }
-  const int x0 = (int)((long long)cta * total / runs);
-  const int x1 = (int)((long long)(cta + 1) * total / runs);
-  int before = incl - sum;
-  if (x0 >= before && x0 < incl) {
-    int i = i0;
-    for (int w = weight(i); x0 >= before + w && i + 1 < i1; w = weight(i)) {
-      before += w;
-      ++i;
-    }
-    s_item = i;
-    s_off = x0 - before;
-  }
-  __syncthreads();
+  const Run run = find_run<SPARSE, WARPS>(p, (int)gridDim.x, (int)blockIdx.x, false);
+  if (run.x0 >= run.x1) return;
+  const int cta = blockIdx.x, x0 = run.x0, x1 = run.x1;
 
   Cursor<SPARSE> cur;
   if (SPARSE) {
-    cur.b = s_item / p.N2;
-    cur.kvh = s_item % p.N2;
-    cur.idx = s_off;
+    cur.b = run.item / p.N2;
+    cur.kvh = run.item % p.N2;
+    cur.idx = run.off;
     cur.kv = seq_len(p, cur.b);
     cur.enter(p);
   } else {
-    cur.b = s_item;
+    cur.b = run.item;
     cur.kv = seq_len(p, cur.b);
     cur.enter(p);
-    cur.kvh = s_off / cur.n;
-    cur.idx = s_off % cur.n;
+    cur.kvh = run.off / cur.n;
+    cur.idx = run.off % cur.n;
   }
   int b = cur.b, kvh = cur.kvh;      // the computing side's task
   bool from_start = cur.idx == 0;    // the segment begins its task
-  int seg_n = cur.n, seg_x = x0;
   cur.look(p, warp);
 
   const uint32_t ring = ptx::smem_u32(smem) + warp * STAGES * STAGE_BYTES;
@@ -597,7 +624,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) decode_kernel(const Para
   // its whole task, left as a partial otherwise.  O goes through the stage just consumed, the one
   // that the next copy will overwrite.
   bool first_segment = true;
-  const auto flush = [&](int stage, bool to_end, int x) {
+  const auto flush = [&](int stage, bool to_end) {
     const uint32_t buf = ring + stage * STAGE_BYTES;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -621,7 +648,6 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) decode_kernel(const Para
     const bool complete = from_start && to_end;
     const int slot = 2 * cta + (first_segment ? 0 : 1);
     const uint8_t *o0 = smem + stage * STAGE_BYTES;
-    const float vd = !p.v_descale ? 0.f : p.v_per_head ? p.v_descale[kvh] : p.v_descale[0];
     for (int g = 0; g < p.G; ++g) {
       float2 ml[WARPS];
       float mm = -INFINITY;
@@ -642,27 +668,11 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) decode_kernel(const Para
                                                   (tid & 3) * 4);
       }
       if (complete) {
-        const int h = kvh * p.G + g;
-        const bool some = ll != 0.f;
-        p.out[((size_t)b * p.N1 + h) * HEAD_DIM + tid] =
-            __float2bfloat16(some ? o / ll * vd : 0.f);
-        if (tid == 0 && p.lse)
-          p.lse[(size_t)h * p.B + b] =
-              some ? (mm + log2f(ll) - P_SHIFT) * 0.6931471805599453f : -FLT_MAX;
+        write_row(p, b, kvh, g, tid, mm, ll, o);
       } else {
         if (tid == 0) p.part_ml[(size_t)slot * MAX_G + g] = make_float2(mm, ll);
         p.part_o[((size_t)slot * p.G + g) * HEAD_DIM + tid] = o;
       }
-    }
-    if (tid == 0 && x == x1) {
-      // the cut task that begins here, if one does: its partials are this slot and the first
-      // slots of the CTAs that follow, up to the run that holds its last tile
-      int4 d = make_int4(0, 0, 0, 0);
-      if (from_start && !to_end) {
-        const long long end = (long long)seg_x + seg_n;
-        d = make_int4(b * p.N2 + kvh, (int)((end * runs - 1) / total) - cta + 1, slot, 0);
-      }
-      p.desc[cta] = d;
     }
     __syncthreads();
   };
@@ -683,16 +693,14 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) decode_kernel(const Para
     if ((int)left > 0) compute(st, (int)heads, (int)left);
     ++x;
     if (last || x == x1) {
-      flush(stage, last, x);
+      flush(stage, last);
       if (x < x1) {
         first_segment = false;
         from_start = true;
-        seg_x = x;
         if (++kvh == p.N2) {
           kvh = 0;
           ++b;
         }
-        seg_n = SPARSE ? max(p.counts[b * p.N2 + kvh], 1) : dense_tiles(seq_len(p, b));
         load_q();
         reset();
       }
@@ -702,35 +710,93 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) decode_kernel(const Para
 }
 
 // ------------------------------------------------------------------------------------------
-// The join: block (c, g) combines head g of the cut task that run c begins, if it begins one.
-// Launched beside the attention kernel's end (its blocks wait for that kernel's writes).
+// The join: block (c, g) combines head g of the cut task that run c begins, if it begins one: run c's
+// last slot and the first slots of the runs that follow, up to the one that holds the task's last
+// tile.  Launched while the attention kernel runs: a block finds its runs in that kernel's shadow
+// and then waits for its writes.  The eight warps share the partials out, a lane holding four
+// dimensions.
 // ------------------------------------------------------------------------------------------
-__global__ void __launch_bounds__(HEAD_DIM) join_kernel(const Params p) {
-  pdl_wait();
-  const int cta = blockIdx.x, g = blockIdx.y, d = threadIdx.x;
-  const int4 w = p.desc[cta];
-  const int n = w.y;
-  if (n == 0) return;
-  const auto slot = [&](int j) { return j == 0 ? w.z : 2 * (cta + j); };
-  float mm = -INFINITY;
-  for (int j = 0; j < n; ++j) mm = fmaxf(mm, p.part_ml[(size_t)slot(j) * MAX_G + g].x);
-  const float base = mm == -INFINITY ? 0.f : mm;
-  float ll = 0.f, o = 0.f;
-#pragma unroll 4
-  for (int j = 0; j < n; ++j) {
-    const float2 ml = p.part_ml[(size_t)slot(j) * MAX_G + g];
-    const float f = ptx::ex2_approx(ml.x - base);
-    ll += f * ml.y;
-    o += f * p.part_o[((size_t)slot(j) * p.G + g) * HEAD_DIM + d];
+constexpr int JOIN_WARPS = 8;
+constexpr int JOIN_THREADS = JOIN_WARPS * 32;
+constexpr int JOIN_AHEAD = 4;  // partials in flight per warp
+
+template <bool SPARSE>
+__global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const Params p) {
+  __shared__ float2 s_ml[JOIN_WARPS];
+  __shared__ float4 s_o[JOIN_WARPS][32];
+  const int c = blockIdx.x, g = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // one block always waits, so that the join never ends before the kernel it belongs to
+  if (c == 0 && g == 0) pdl_wait();
+  const Run run = find_run<SPARSE, JOIN_WARPS>(p, (int)gridDim.x, c, true);
+  if (run.x0 >= run.x1) return;
+  int task, n, idx;  // the run's last tile is tile idx of a task of n
+  if (SPARSE) {
+    task = run.item;
+    n = max(__ldcg(p.counts + task), 1);
+    idx = run.off;
+  } else {
+    n = dense_tiles(seq_len(p, run.item));
+    task = run.item * p.N2 + run.off / n;
+    idx = run.off % n;
   }
-  const int b = w.x / p.N2, kvh = w.x % p.N2, h = kvh * p.G + g;
-  const bool some = ll != 0.f;
-  const float vd = p.v_per_head ? p.v_descale[kvh] : p.v_descale[0];
-  p.out[((size_t)b * p.N1 + h) * HEAD_DIM + d] =
-      __float2bfloat16(some ? o / ll * vd : 0.f);
-  if (d == 0 && p.lse)
-    p.lse[(size_t)h * p.B + b] =
-        some ? (mm + log2f(ll) - P_SHIFT) * 0.6931471805599453f : -FLT_MAX;
+  // the task's first tile lies in an earlier run, or its last one in this: not cut, or not here
+  const int t0 = run.x1 - 1 - idx;
+  if (t0 < run.x0 || idx == n - 1) return;
+  const int parts = (int)(((long long)(t0 + n) * run.runs - 1) / run.total) - c + 1;
+  const int first = 2 * c + (t0 > run.x0 ? 1 : 0);  // after a finished segment: the second slot
+  pdl_wait();
+
+  float m = -INFINITY, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int j0 = warp; j0 < parts; j0 += JOIN_WARPS * JOIN_AHEAD) {
+    float2 ml[JOIN_AHEAD];
+    float4 v[JOIN_AHEAD];
+#pragma unroll
+    for (int u = 0; u < JOIN_AHEAD; ++u) {
+      const int j = j0 + u * JOIN_WARPS;
+      ml[u] = make_float2(-INFINITY, 0.f);
+      v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (j < parts) {
+        const size_t slot = j == 0 ? first : 2 * (size_t)(c + j);
+        ml[u] = p.part_ml[slot * MAX_G + g];
+        v[u] = reinterpret_cast<const float4 *>(p.part_o)[(slot * p.G + g) * 32 + lane];
+      }
+    }
+    float mn = m;
+#pragma unroll
+    for (int u = 0; u < JOIN_AHEAD; ++u) mn = fmaxf(mn, ml[u].x);
+    const float base = mn == -INFINITY ? 0.f : mn;
+    const float a = ptx::ex2_approx(m - base);
+    l *= a;
+    o = make_float4(o.x * a, o.y * a, o.z * a, o.w * a);
+    m = mn;
+#pragma unroll
+    for (int u = 0; u < JOIN_AHEAD; ++u) {
+      const float f = ptx::ex2_approx(ml[u].x - base);
+      l += f * ml[u].y;
+      o.x += f * v[u].x;
+      o.y += f * v[u].y;
+      o.z += f * v[u].z;
+      o.w += f * v[u].w;
+    }
+  }
+  s_o[warp][lane] = o;
+  if (lane == 0) s_ml[warp] = make_float2(m, l);
+  __syncthreads();
+  if (tid >= HEAD_DIM) return;
+  float mm = -INFINITY;
+#pragma unroll
+  for (int w = 0; w < JOIN_WARPS; ++w) mm = fmaxf(mm, s_ml[w].x);
+  const float base = mm == -INFINITY ? 0.f : mm;
+  float ll = 0.f, oo = 0.f;
+#pragma unroll
+  for (int w = 0; w < JOIN_WARPS; ++w) {
+    const float f = ptx::ex2_approx(s_ml[w].x - base);
+    ll += f * s_ml[w].y;
+    oo += f * reinterpret_cast<const float *>(s_o[w])[tid];
+  }
+  const int b = task / p.N2, kvh = task % p.N2;
+  write_row(p, b, kvh, g, tid, mm, ll, oo);
 }
 
 }  // namespace decode

@@ -761,7 +761,7 @@ DecodePlan plan_decode(const bsa_fp8_decode_dims_t *d, int num_sms) {
       1, std::min<long long>((long long)decode::CTAS_PER_SM * std::max(num_sms, 1),
                              tasks * std::max<long long>(kb, 1)));
   const size_t slots = 2 * (size_t)plan.grid;
-  plan.off_ml = round256((size_t)plan.grid * sizeof(int4));
+  plan.off_ml = 0;
   plan.off_o = plan.off_ml + round256(slots * decode::MAX_G * sizeof(float2));
   plan.off_counts = plan.off_o + slots * (size_t)(d->N1 / d->N2) * HEAD_DIM * sizeof(float);
   plan.off_tiles = plan.off_counts + (d->sparse ? round256((size_t)tasks * sizeof(int)) : 0);
@@ -887,7 +887,6 @@ extern "C" bsa_status_t bsa_fp8_decode(const bsa_fp8_decode_dims_t *d, const voi
   p.v_per_head = d->v_scale_kind == BSA_SCALE_PER_HEAD;
   p.scale_log2 = (float)((double)softmax_scale * 1.4426950408889634);
   p.ps_shift = d->page_size == 64 ? 6 : 5;
-  p.desc = reinterpret_cast<int4 *>(ws);
   p.part_ml = reinterpret_cast<float2 *>(ws + plan.off_ml);
   p.part_o = reinterpret_cast<float *>(ws + plan.off_o);
   p.counts = reinterpret_cast<int *>(ws + plan.off_counts);
@@ -908,8 +907,11 @@ extern "C" bsa_status_t bsa_fp8_decode(const bsa_fp8_decode_dims_t *d, const voi
     if (cudaGetLastError() != cudaSuccess) return BSA_ERR_CUDA;
   }
   // tasks of one tile are never cut
-  if (p.Kb > 1 && !launch_dependent(decode::join_kernel, dim3((unsigned)plan.grid, (unsigned)p.G),
-                                    HEAD_DIM, 0, stream, p))
+  const bool lists = d->sparse && !none;
+  if (p.Kb > 1 &&
+      !launch_dependent(lists ? decode::join_kernel<true> : decode::join_kernel<false>,
+                        dim3((unsigned)plan.grid, (unsigned)p.G), decode::JOIN_THREADS, 0, stream,
+                        p))
     return BSA_ERR_CUDA;
   return BSA_OK;
 }
@@ -935,7 +937,8 @@ extern "C" bsa_status_t bsa_fp8_gather_kv(const bsa_fp8_gather_dims_t *d, const 
     return BSA_ERR_INVALID_ARGUMENT;
   if (!aligned16(k_out) || !aligned16(v_out) || !aligned16(k_pages) || !aligned16(v_pages))
     return BSA_ERR_INVALID_ARGUMENT;
-  const bsa_status_t st = check_device(0, nullptr);
+  int num_sms = 0;
+  const bsa_status_t st = check_device(0, &num_sms);
   if (st != BSA_OK) return st;
   gather::Params p;
   memset(&p, 0, sizeof(p));
@@ -958,10 +961,15 @@ extern "C" bsa_status_t bsa_fp8_gather_kv(const bsa_fp8_gather_dims_t *d, const 
   p.total = d->total;
   p.k_per_token = d->k_scale_kind == BSA_SCALE_PER_TOKEN_HEAD;
   p.v_per_head = d->v_scale_kind == BSA_SCALE_PER_HEAD;
+  // a block's tokens: as many as leave every SM a few blocks, so that a lookup serves many rows of
+  // a long read and a short read still spreads over the GPU
+  p.tokens = gather::MAX_TOKENS;
+  while (p.tokens > 1 && cdiv(d->total, p.tokens) < 8 * num_sms) p.tokens /= 2;
+  const unsigned grid = (unsigned)cdiv(d->total, p.tokens);
   if (d->out_type == BSA_OUT_FP32)
-    gather::gather_kernel<float><<<d->total, gather::THREADS, 0, (cudaStream_t)stream>>>(p);
+    gather::gather_kernel<true><<<grid, gather::THREADS, 0, (cudaStream_t)stream>>>(p);
   else
-    gather::gather_kernel<__nv_bfloat16><<<d->total, gather::THREADS, 0, (cudaStream_t)stream>>>(p);
+    gather::gather_kernel<false><<<grid, gather::THREADS, 0, (cudaStream_t)stream>>>(p);
   return cudaGetLastError() == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
 }
 
@@ -983,13 +991,26 @@ extern "C" bsa_status_t bsa_fp8_merge_states(int count, const void *const *outs,
     p.outs[i] = static_cast<const __nv_bfloat16 *>(outs[i]);
     p.lses[i] = lses[i];
   }
-  const bsa_status_t st = check_device(0, nullptr);
+  int num_sms = 0;
+  const bsa_status_t st = check_device(0, &num_sms);
   if (st != BSA_OK) return st;
   p.out = static_cast<__nv_bfloat16 *>(out_bf16);
   p.lse = lse_f32;
   p.count = count;
   p.T = T;
   p.N1 = N1;
-  merge::merge_kernel<<<(unsigned)(T * N1), merge::THREADS, 0, (cudaStream_t)stream>>>(p);
+  // tiles of up to 32 heads and 256 rows, smaller ones while they do not give every SM a few
+  p.head_shift = 0;
+  while (p.head_shift < 5 && (1 << p.head_shift) < N1) ++p.head_shift;
+  int rows = merge::MAX_ROWS;
+  while (rows > 32 && (long long)T * N1 / rows < 8 * num_sms) rows /= 2;
+  p.tok_shift = 0;
+  while ((1 << (p.tok_shift + p.head_shift)) < rows) ++p.tok_shift;
+  p.head_tiles = cdiv(N1, 1 << p.head_shift);
+  const unsigned grid = (unsigned)((long long)cdiv(T, 1 << p.tok_shift) * p.head_tiles);
+  const auto kernel = count <= 2   ? merge::merge_kernel<2>
+                      : count <= 4 ? merge::merge_kernel<4>
+                                   : merge::merge_kernel<8>;
+  kernel<<<grid, merge::THREADS, 0, (cudaStream_t)stream>>>(p);
   return cudaGetLastError() == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
 }

@@ -159,8 +159,7 @@ def _decode_args():
     ("q_descale", torch.zeros(8, 2), "shape"),
     ("out", torch.zeros(2, 8, 128), "dtype"), ("lse", torch.zeros(2, 8), "shape"),
     ("dev_status", torch.zeros(1, dtype=torch.int64), "int32"),
-    ("workspace", torch.zeros(64, 2, dtype=torch.uint8)[:, 0], "contiguous"),
-    ("seqused_kv", torch.zeros(2, dtype=torch.int32, device="meta"), "meta")])
+    ("workspace", torch.zeros(64, 2, dtype=torch.uint8)[:, 0], "contiguous")])
 def test_decode_binding_refuses(name, value, match):
     a = _decode_args()
     a[name] = value
