@@ -160,58 +160,84 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Thread d's element of head g of (b, kvh)'s result, and the row's LSE.
-__device__ __forceinline__ void write_row(const Params &p, int b, int kvh, int g, int d, float m,
-                                          float l, float o) {
+// Head g of (b, kvh)'s result from a warp's (m, l, O), four dimensions a lane, and its LSE.
+__device__ __forceinline__ void write_row(const Params &p, int b, int kvh, int g, int lane, float m,
+                                          float l, float4 o) {
   const int h = kvh * p.G + g;
   const bool some = l != 0.f;  // a NaN sum is a result, not an empty row
-  const float vd = some ? (p.v_per_head ? p.v_descale[kvh] : p.v_descale[0]) : 0.f;
-  p.out[((size_t)b * p.N1 + h) * HEAD_DIM + d] = __float2bfloat16(some ? o / l * vd : 0.f);
-  if (d == 0 && p.lse)
+  const float f = some ? (p.v_per_head ? p.v_descale[kvh] : p.v_descale[0]) / l : 0.f;
+  const __nv_bfloat162 lo = __floats2bfloat162_rn(some ? o.x * f : 0.f, some ? o.y * f : 0.f);
+  const __nv_bfloat162 hi = __floats2bfloat162_rn(some ? o.z * f : 0.f, some ? o.w * f : 0.f);
+  uint2 w;
+  memcpy(&w.x, &lo, 4);
+  memcpy(&w.y, &hi, 4);
+  reinterpret_cast<uint2 *>(p.out)[((size_t)b * p.N1 + h) * 32 + lane] = w;
+  if (lane == 0 && p.lse)
     p.lse[(size_t)h * p.B + b] =
         some ? (m + log2f(l) - P_SHIFT) * 0.6931471805599453f : -FLT_MAX;
+}
+
+// (m, l, O) += a partial of its own maximum.
+__device__ __forceinline__ void add_part(float &m, float &l, float4 &o, float2 ml, float4 v) {
+  const float mn = fmaxf(m, ml.x), base = mn == -INFINITY ? 0.f : mn;
+  const float a = ptx::ex2_approx(m - base), f = ptx::ex2_approx(ml.x - base);
+  m = mn;
+  l = l * a + f * ml.y;
+  o = make_float4(o.x * a + f * v.x, o.y * a + f * v.y, o.z * a + f * v.z, o.w * a + f * v.w);
 }
 
 // ------------------------------------------------------------------------------------------
 // Tile lists of the sparse forms: one CTA per (sequence, KV head) forms the union of its query
 // heads' tiles below the sequence's end, each with a mask of the heads that enable it.
 // ------------------------------------------------------------------------------------------
-__global__ void __launch_bounds__(THREADS) plan_kernel(const Params p) {
+constexpr int PLAN_WARPS = 16;  // a warp per query head of the group
+constexpr int PLAN_THREADS = PLAN_WARPS * 32;
+constexpr int PLAN_AHEAD = 8;   // list entries in flight per lane
+
+__global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const Params p) {
   extern __shared__ uint32_t heads[];  // [Kb]
-  __shared__ int warp_n[WARPS];
+  __shared__ int warp_n[PLAN_WARPS];
+  pdl_wait();
   pdl_launch_dependents();
   const int task = blockIdx.x, b = task / p.N2, kvh = task % p.N2;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int kend = (seq_len(p, b) + TILE - 1) / TILE;
   const size_t first = (size_t)b * p.N1 + (size_t)kvh * p.G;  // the group's first (b, h)
-  for (int t = tid; t < kend; t += THREADS) {
+  int len = p.sparse_indices && warp < p.G ? p.sparse_seq_len[first + warp] : 0;
+  const int kend = (seq_len(p, b) + TILE - 1) / TILE;
+  for (int t = tid; t < kend; t += PLAN_THREADS) {
     uint32_t on = 0;
-    if (p.block_mask)
+    if (p.block_mask) {
+#pragma unroll 4
       for (int g = 0; g < p.G; ++g)
         on |= p.block_mask[(first + g) * p.Kb + t] != 0 ? 1u << g : 0u;
+    }
     heads[t] = on;
   }
   __syncthreads();
   if (p.sparse_indices) {
-    for (int g = 0; g < p.G; ++g) {
-      int len = p.sparse_seq_len[first + g];
-      if (len < 0 || len > p.Kb) {
-        if (tid == 0) report(p, BSA_DEV_BAD_INDEX);
-        len = len < 0 ? 0 : p.Kb;
-      }
-      for (int e = tid; e < len; e += THREADS) {
-        const int t = p.sparse_indices[(first + g) * p.Kb + e];
-        if (t < 0 || t >= p.Kb)
+    if (len < 0 || len > p.Kb) {
+      if (lane == 0) report(p, BSA_DEV_BAD_INDEX);
+      len = len < 0 ? 0 : p.Kb;
+    }
+    const int *list = p.sparse_indices + (first + warp) * p.Kb;
+    for (int e0 = lane; e0 < len; e0 += 32 * PLAN_AHEAD) {
+      int t[PLAN_AHEAD];
+#pragma unroll
+      for (int u = 0; u < PLAN_AHEAD; ++u) t[u] = e0 + 32 * u < len ? list[e0 + 32 * u] : kend;
+#pragma unroll
+      for (int u = 0; u < PLAN_AHEAD; ++u) {
+        if (e0 + 32 * u >= len) continue;
+        if (t[u] < 0 || t[u] >= p.Kb)
           report(p, BSA_DEV_BAD_INDEX);
-        else if (t < kend)
-          atomicOr(&heads[t], 1u << g);
+        else if (t[u] < kend)
+          atomicOr(&heads[t[u]], 1u << warp);
       }
     }
     __syncthreads();
   }
   uint32_t *list = p.tiles + (size_t)task * p.Kb;
   int n = 0;
-  for (int base = 0; base < kend; base += THREADS) {
+  for (int base = 0; base < kend; base += PLAN_THREADS) {
     const int t = base + tid;
     const uint32_t on = t < kend ? heads[t] : 0u;
     const unsigned bal = __ballot_sync(0xffffffffu, on != 0);
@@ -219,7 +245,7 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(const Params p) {
     __syncthreads();
     int at = n + __popc(bal & ((1u << lane) - 1u));
 #pragma unroll
-    for (int w = 0; w < WARPS; ++w) {
+    for (int w = 0; w < PLAN_WARPS; ++w) {
       if (w < warp) at += warp_n[w];
       n += warp_n[w];
     }
@@ -229,30 +255,42 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(const Params p) {
   if (tid == 0) p.counts[task] = n;
 }
 
-// ------------------------------------------------------------------------------------------
-// The attention kernel.
-// ------------------------------------------------------------------------------------------
-
-// Run `index` of the batch's tiles cut into `grid` runs (as many as there are tiles, if those are
-// fewer): tiles [x0, x1), and where tile x0 (with `last`: tile x1 - 1) lies: item and offset in it.
-// Items are sequences, all of whose KV heads have the same tiles, or tasks when every task has a
-// list of its own.  Called by all of a CTA's W warps.
-struct Run {
-  int x0, x1, total, runs, item, off;
+// The batch's tiles, in task order, cut into even runs for `grid` CTAs (as many runs as there are
+// tiles, if those are fewer).
+struct Cut {
+  int runs, size, larger;  // runs have `size` tiles, the first `larger` of them one more
+  __device__ __forceinline__ int begin(int i) const { return i * size + min(i, larger); }
+  __device__ __forceinline__ int of(int x) const {  // the run that holds tile x
+    const int edge = larger * (size + 1);
+    return x < edge ? x / (size + 1) : larger + (x - edge) / size;
+  }
 };
 
-template <bool SPARSE, int W>
-__device__ __forceinline__ Run find_run(const Params &p, int grid, int index, bool last) {
-  __shared__ int s_sum[W], s_item, s_off;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+// Finds the cut, and the item in which a wanted tile lies.  Items are sequences, all of whose KV heads
+// have the same tiles, or tasks when every task has a list of its own.  want(cut) names the tile, or
+// is negative: none wanted, the item is -1.  With by_item the item is given instead and its first
+// tile is returned.  Called by all of a CTA's warps; every thread sums a stretch of the items.
+struct Found {
+  int item, off;  // the item, the wanted tile's offset in it (by_item: the item's first tile)
+};
+
+constexpr int MAX_WARPS = 8;
+
+template <bool SPARSE>
+__device__ __forceinline__ int item_tiles(const Params &p, int i) {
+  return SPARSE ? max(__ldcg(p.counts + i), 1) : p.N2 * dense_tiles(seq_len(p, i));
+}
+
+template <bool SPARSE, typename Want>
+__device__ __forceinline__ Found find_tile(const Params &p, int grid, Cut &cut, bool by_item,
+                                           Want &&want) {
+  __shared__ int s_sum[MAX_WARPS], s_item, s_off;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x;
   const int items = SPARSE ? p.B * p.N2 : p.B;
-  const auto weight = [&](int i) {
-    return SPARSE ? max(__ldcg(p.counts + i), 1) : p.N2 * dense_tiles(seq_len(p, i));
-  };
-  const int per = (items + W * 32 - 1) / (W * 32), i0 = min(tid * per, items),
+  const int per = (items + threads - 1) / threads, i0 = min(tid * per, items),
             i1 = min(i0 + per, items);
   int sum = 0;
-  for (int i = i0; i < i1; ++i) sum += weight(i);
+  for (int i = i0; i < i1; ++i) sum += item_tiles<SPARSE>(p, i);
   int incl = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -261,33 +299,29 @@ __device__ __forceinline__ Run find_run(const Params &p, int grid, int index, bo
   }
   if (lane == 31) s_sum[warp] = incl;
   __syncthreads();
-  Run run;
-  run.total = 0;
-#pragma unroll
-  for (int w = 0; w < W; ++w) {
+  int total = 0;
+  for (int w = 0; w < threads / 32; ++w) {
     if (w < warp) incl += s_sum[w];
-    run.total += s_sum[w];
+    total += s_sum[w];
   }
-  run.runs = min(grid, run.total);
-  run.x0 = run.x1 = run.item = run.off = 0;
-  if (index >= run.runs) return run;
-  run.x0 = (int)((long long)index * run.total / run.runs);
-  run.x1 = (int)((long long)(index + 1) * run.total / run.runs);
-  const int x = last ? run.x1 - 1 : run.x0;
-  int before = incl - sum;
-  if (x >= before && x < incl) {
-    int i = i0;
-    for (int w = weight(i); x >= before + w && i + 1 < i1; w = weight(i)) {
+  cut.runs = min(grid, total);
+  cut.size = total / cut.runs;
+  cut.larger = total - cut.runs * cut.size;
+  const int x = want(cut);
+  if (x < 0) return Found{-1, 0};
+  int before = incl - sum, i = i0;
+  if (by_item ? x >= i0 && x < i1 : x >= before && x < incl) {
+    for (; i + 1 < i1; ++i) {
+      if (by_item && i == x) break;
+      const int w = item_tiles<SPARSE>(p, i);
+      if (!by_item && x < before + w) break;
       before += w;
-      ++i;
     }
     s_item = i;
-    s_off = x - before;
+    s_off = by_item ? before : x - before;
   }
   __syncthreads();
-  run.item = s_item;
-  run.off = s_off;
-  return run;
+  return Found{s_item, s_off};
 }
 
 // A position in the batch's run of tiles, moved along by the copying side of a warp.
@@ -335,29 +369,99 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) decode_kernel(const Para
   __shared__ float2 s_ml[WARPS][MAX_G];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int r = lane >> 2, q4 = lane & 3;  // mma fragment coordinates
-  if (SPARSE) pdl_wait();   // the tile lists
-  pdl_launch_dependents();  // the join, which may read the lists' counts too: only now
+  pdl_wait();               // what the stream ran before: the tile lists among it
+  pdl_launch_dependents();  // the join, which reads the lengths and counts as well: only now
 
-  const Run run = find_run<SPARSE, WARPS>(p, (int)gridDim.x, (int)blockIdx.x, false);
-  if (run.x0 >= run.x1) return;
-  const int cta = blockIdx.x, x0 = run.x0, x1 = run.x1;
+  const int cta = blockIdx.x;
+  Cut cut;
+  const Found at = find_tile<SPARSE>(p, (int)gridDim.x, cut, false, [&](const Cut &c) {
+    return cta < c.runs ? c.begin(cta) : -1;
+  });
+  if (at.item < 0) return;
+  const int x0 = cut.begin(cta), x1 = cut.begin(cta + 1);
 
   Cursor<SPARSE> cur;
   if (SPARSE) {
-    cur.b = run.item / p.N2;
-    cur.kvh = run.item % p.N2;
-    cur.idx = run.off;
+    cur.b = at.item / p.N2;
+    cur.kvh = at.item % p.N2;
+    cur.idx = at.off;
     cur.kv = seq_len(p, cur.b);
     cur.enter(p);
   } else {
-    cur.b = run.item;
+    cur.b = at.item;
     cur.kv = seq_len(p, cur.b);
     cur.enter(p);
-    cur.kvh = run.off / cur.n;
-    cur.idx = run.off % cur.n;
+    cur.kvh = at.off / cur.n;
+    cur.idx = at.off % cur.n;
   }
   int b = cur.b, kvh = cur.kvh;      // the computing side's task
   bool from_start = cur.idx == 0;    // the segment begins its task
+  // ---- the group's queries as B fragments: column r is head r, a thread's 32 dimensions
+  // 32 q4 .. 32 q4 + 31 in steps of four (the order of K's reads below).  Fetched raw first (16
+  // words of bf16, or 8 of e4m3), converted once the copies in flight are on their way.
+  uint32_t qf[NT][16];
+  float fac[NT][2];  // score factors of the thread's columns 2 q4, 2 q4 + 1
+  float qd[NT];
+  const auto fetch_q = [&](int qb, int qh) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int g = nt * 8 + r;
+      qd[nt] = 1.f;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) qf[nt][i] = 0u;
+      if (g >= p.G) continue;
+      const size_t at = (size_t)qb * p.q_stride + (size_t)(qh * p.G + g) * HEAD_DIM + q4 * 32;
+      const uint4 *src = p.q_e4m3 ? reinterpret_cast<const uint4 *>(
+                                        static_cast<const uint8_t *>(p.q) + at)
+                                  : reinterpret_cast<const uint4 *>(
+                                        static_cast<const __nv_bfloat16 *>(p.q) + at);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (i >= 2 && p.q_e4m3) break;
+        const uint4 v = src[i];
+        qf[nt][4 * i] = v.x;
+        qf[nt][4 * i + 1] = v.y;
+        qf[nt][4 * i + 2] = v.z;
+        qf[nt][4 * i + 3] = v.w;
+      }
+      if (p.q_e4m3) qd[nt] = p.q_descale[(size_t)qb * p.N1 + qh * p.G + g];
+    }
+  };
+  const auto convert_q = [&]() {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float f = p.scale_log2;
+      if (p.q_e4m3) {
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = qf[nt][i];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f16_of_e4m3x4(w[i], qf[nt][2 * i], qf[nt][2 * i + 1]);
+        f *= qd[nt];
+      } else {
+        float amax = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(qf[nt][i] << 16)),
+                                   fabsf(__uint_as_float(qf[nt][i] & 0xffff0000u))));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        // times 2^(14 - e), e the exponent of the row's largest value: it lands in
+        // [2^14, 2^15), and only values below 2^-28 of it lose bits to fp16's subnormals
+        const int e = max((int)(__float_as_uint(amax) >> 23) - 127, -110);
+        const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
+        f *= __uint_as_float((uint32_t)(127 + e - 14) << 23);
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          qf[nt][i] = f16x2(__uint_as_float(qf[nt][i] << 16) * up,
+                            __uint_as_float(qf[nt][i] & 0xffff0000u) * up);
+      }
+      fac[nt][0] = __shfl_sync(0xffffffffu, f, 8 * q4);
+      fac[nt][1] = __shfl_sync(0xffffffffu, f, 8 * q4 + 4);
+    }
+  };
+
+  fetch_q(b, kvh);
   cur.look(p, warp);
 
   const uint32_t ring = ptx::smem_u32(smem) + warp * STAGES * STAGE_BYTES;
@@ -408,63 +512,6 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) decode_kernel(const Para
 
 #pragma unroll
   for (int s = 0; s < STAGES - 1; ++s) issue(s);
-
-  // ---- the group's queries as B fragments: column r is head r, a thread's 32 dimensions
-  // 32 q4 .. 32 q4 + 31 in steps of four (the order of K's reads below)
-  uint32_t qf[NT][16];
-  float fac[NT][2];  // score factors of the thread's columns 2 q4, 2 q4 + 1
-  const auto load_q = [&]() {
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int g = nt * 8 + r;
-      const bool live = g < p.G;
-      const size_t at = (size_t)b * p.q_stride + (size_t)(kvh * p.G + (live ? g : 0)) * HEAD_DIM +
-                        q4 * 32;
-      float f = p.scale_log2;
-      if (p.q_e4m3) {
-        const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(p.q) + at);
-        const uint4 w0 = src[0], w1 = src[1];
-        const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f16_of_e4m3x4(w[i], qf[nt][2 * i], qf[nt][2 * i + 1]);
-        f *= p.q_descale[(size_t)b * p.N1 + kvh * p.G + (live ? g : 0)];
-      } else {
-        const uint4 *src =
-            reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.q) + at);
-        float amax = 0.f;
-        uint32_t w[16];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint4 v = src[i];
-          w[4 * i] = v.x;
-          w[4 * i + 1] = v.y;
-          w[4 * i + 2] = v.z;
-          w[4 * i + 3] = v.w;
-        }
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[i] << 16)),
-                                   fabsf(__uint_as_float(w[i] & 0xffff0000u))));
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-        // times 2^(14 - e), e the exponent of the row's largest value: it lands in
-        // [2^14, 2^15), and only values below 2^-28 of it lose bits to fp16's subnormals
-        const int e = max((int)(__float_as_uint(amax) >> 23) - 127, -110);
-        const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
-        f *= __uint_as_float((uint32_t)(127 + e - 14) << 23);
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          qf[nt][i] = f16x2(__uint_as_float(w[i] << 16) * up,
-                            __uint_as_float(w[i] & 0xffff0000u) * up);
-      }
-      if (!live) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) qf[nt][i] = 0u;
-      }
-      fac[nt][0] = __shfl_sync(0xffffffffu, f, 8 * q4);
-      fac[nt][1] = __shfl_sync(0xffffffffu, f, 8 * q4 + 4);
-    }
-  };
 
   float m[NT][2], l[NT][2], acc[NT][8][4];
   const auto reset = [&]() {
@@ -646,38 +693,29 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) decode_kernel(const Para
       }
     __syncthreads();
     const bool complete = from_start && to_end;
-    const int slot = 2 * cta + (first_segment ? 0 : 1);
+    const size_t slot = 2 * (size_t)cta + (first_segment ? 0 : 1);
     const uint8_t *o0 = smem + stage * STAGE_BYTES;
-    for (int g = 0; g < p.G; ++g) {
-      float2 ml[WARPS];
-      float mm = -INFINITY;
+#pragma unroll 2
+    for (int g = warp; g < p.G; g += WARPS) {  // a head a warp, four dimensions a lane
+      float mm = -INFINITY, ll = 0.f;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int w = 0; w < WARPS; ++w) {
-        ml[w] = s_ml[w][g];
-        mm = fmaxf(mm, ml[w].x);
-      }
-      const float base = mm == -INFINITY ? 0.f : mm;
-      float ll = 0.f, o = 0.f;
-#pragma unroll
-      for (int w = 0; w < WARPS; ++w) {
-        const float f = ptx::ex2_approx(ml[w].x - base);
-        ll += f * ml[w].y;
-        o += f * *reinterpret_cast<const float *>(o0 + w * STAGES * STAGE_BYTES +
-                                                  g * (HEAD_DIM * 4) +
-                                                  (((tid >> 2) ^ ((g >> 1) & 3)) << 4) +
-                                                  (tid & 3) * 4);
-      }
+      for (int w = 0; w < WARPS; ++w)
+        add_part(mm, ll, o, s_ml[w][g],
+                 *reinterpret_cast<const float4 *>(o0 + w * STAGES * STAGE_BYTES +
+                                                   g * (HEAD_DIM * 4) +
+                                                   ((lane ^ ((g >> 1) & 3)) << 4)));
       if (complete) {
-        write_row(p, b, kvh, g, tid, mm, ll, o);
+        write_row(p, b, kvh, g, lane, mm, ll, o);
       } else {
-        if (tid == 0) p.part_ml[(size_t)slot * MAX_G + g] = make_float2(mm, ll);
-        p.part_o[((size_t)slot * p.G + g) * HEAD_DIM + tid] = o;
+        if (lane == 0) p.part_ml[slot * MAX_G + g] = make_float2(mm, ll);
+        reinterpret_cast<float4 *>(p.part_o)[(slot * p.G + g) * 32 + lane] = o;
       }
     }
     __syncthreads();
   };
 
-  load_q();
+  convert_q();
   reset();
   int stage = 0;
   for (int x = x0; x < x1;) {
@@ -701,7 +739,8 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) decode_kernel(const Para
           kvh = 0;
           ++b;
         }
-        load_q();
+        fetch_q(b, kvh);
+        convert_q();
         reset();
       }
     }
@@ -710,93 +749,78 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) decode_kernel(const Para
 }
 
 // ------------------------------------------------------------------------------------------
-// The join: block (c, g) combines head g of the cut task that run c begins, if it begins one: run c's
-// last slot and the first slots of the runs that follow, up to the one that holds the task's last
-// tile.  Launched while the attention kernel runs: a block finds its runs in that kernel's shadow
-// and then waits for its writes.  The eight warps share the partials out, a lane holding four
-// dimensions.
+// The join of the cut tasks.  A task's partials are its first run's last slot and the first slots of
+// the runs that follow, up to the one that holds its last tile.  Launched while the attention kernel
+// runs: the blocks find their partials in that kernel's shadow, in the registers it leaves
+// free, and then wait for its writes.  With fewer tasks than runs (`by_task`) a task has many
+// partials: a block joins one head of one task, its warps sharing the partials out.  Otherwise a
+// task has two or three: a block joins the task that its run begins and leaves unfinished, if it
+// does, a head a warp.
 // ------------------------------------------------------------------------------------------
-constexpr int JOIN_WARPS = 8;
-constexpr int JOIN_THREADS = JOIN_WARPS * 32;
-constexpr int JOIN_AHEAD = 4;  // partials in flight per warp
+constexpr int JOIN_AHEAD = 5;  // partials in flight per warp
 
 template <bool SPARSE>
-__global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const Params p) {
-  __shared__ float2 s_ml[JOIN_WARPS];
-  __shared__ float4 s_o[JOIN_WARPS][32];
-  const int c = blockIdx.x, g = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  // one block always waits, so that the join never ends before the kernel it belongs to
-  if (c == 0 && g == 0) pdl_wait();
-  const Run run = find_run<SPARSE, JOIN_WARPS>(p, (int)gridDim.x, c, true);
-  if (run.x0 >= run.x1) return;
-  int task, n, idx;  // the run's last tile is tile idx of a task of n
-  if (SPARSE) {
-    task = run.item;
-    n = max(__ldcg(p.counts + task), 1);
-    idx = run.off;
+__global__ void __launch_bounds__(MAX_WARPS * 32) join_kernel(const Params p, bool by_task,
+                                                              int grid) {
+  __shared__ float2 s_ml[MAX_WARPS];
+  __shared__ float4 s_o[MAX_WARPS][32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
+  const int index = blockIdx.x;
+  Cut cut;
+  const Found at = find_tile<SPARSE>(p, grid, cut, by_task, [&](const Cut &c) {
+    return by_task ? (SPARSE ? index : index / p.N2) : index < c.runs ? c.begin(index + 1) - 1 : -1;
+  });
+  if (at.item < 0) return;  // (never block 0)
+  const int n = SPARSE ? item_tiles<SPARSE>(p, at.item) : dense_tiles(seq_len(p, at.item));
+  int task, t0;  // the task and its first tile
+  if (by_task) {
+    task = index;
+    t0 = at.off + (SPARSE ? 0 : index % p.N2 * n);
   } else {
-    n = dense_tiles(seq_len(p, run.item));
-    task = run.item * p.N2 + run.off / n;
-    idx = run.off % n;
+    task = SPARSE ? at.item : at.item * p.N2 + at.off / n;
+    t0 = cut.begin(index + 1) - 1 - at.off % n;
   }
-  // the task's first tile lies in an earlier run, or its last one in this: not cut, or not here
-  const int t0 = run.x1 - 1 - idx;
-  if (t0 < run.x0 || idx == n - 1) return;
-  const int parts = (int)(((long long)(t0 + n) * run.runs - 1) / run.total) - c + 1;
-  const int first = 2 * c + (t0 > run.x0 ? 1 : 0);  // after a finished segment: the second slot
+  const int c = cut.of(t0), parts = cut.of(t0 + n - 1) - c + 1;
+  if (parts == 1 || (!by_task && c != index)) {  // not cut, or another block's
+    // one block always waits, so that the join never ends before the kernel it belongs to
+    if (index == 0 && blockIdx.y == 0) pdl_wait();
+    return;
+  }
+  const int first = 2 * c + (t0 > cut.begin(c) ? 1 : 0);  // after a finished segment: the second slot
+  const int b = task / p.N2, kvh = task % p.N2;
   pdl_wait();
 
-  float m = -INFINITY, l = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int j0 = warp; j0 < parts; j0 += JOIN_WARPS * JOIN_AHEAD) {
-    float2 ml[JOIN_AHEAD];
-    float4 v[JOIN_AHEAD];
+  const int g0 = by_task ? (int)blockIdx.y : warp, g1 = by_task ? g0 + 1 : p.G;
+  const int j0 = by_task ? warp : 0, step = by_task ? warps : 1;
+  for (int g = g0; g < g1; g += warps) {
+    float m = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int j = j0; j < parts; j += step * JOIN_AHEAD) {
+      float2 ml[JOIN_AHEAD];
+      float4 v[JOIN_AHEAD];
 #pragma unroll
-    for (int u = 0; u < JOIN_AHEAD; ++u) {
-      const int j = j0 + u * JOIN_WARPS;
-      ml[u] = make_float2(-INFINITY, 0.f);
-      v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (j < parts) {
-        const size_t slot = j == 0 ? first : 2 * (size_t)(c + j);
-        ml[u] = p.part_ml[slot * MAX_G + g];
-        v[u] = reinterpret_cast<const float4 *>(p.part_o)[(slot * p.G + g) * 32 + lane];
+      for (int u = 0; u < JOIN_AHEAD; ++u) {
+        const int ju = j + u * step;
+        ml[u] = make_float2(-INFINITY, 0.f);
+        v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (ju < parts) {
+          const size_t slot = ju == 0 ? first : 2 * (size_t)(c + ju);
+          ml[u] = p.part_ml[slot * MAX_G + g];
+          v[u] = reinterpret_cast<const float4 *>(p.part_o)[(slot * p.G + g) * 32 + lane];
+        }
       }
+#pragma unroll
+      for (int u = 0; u < JOIN_AHEAD; ++u) add_part(m, l, o, ml[u], v[u]);
     }
-    float mn = m;
-#pragma unroll
-    for (int u = 0; u < JOIN_AHEAD; ++u) mn = fmaxf(mn, ml[u].x);
-    const float base = mn == -INFINITY ? 0.f : mn;
-    const float a = ptx::ex2_approx(m - base);
-    l *= a;
-    o = make_float4(o.x * a, o.y * a, o.z * a, o.w * a);
-    m = mn;
-#pragma unroll
-    for (int u = 0; u < JOIN_AHEAD; ++u) {
-      const float f = ptx::ex2_approx(ml[u].x - base);
-      l += f * ml[u].y;
-      o.x += f * v[u].x;
-      o.y += f * v[u].y;
-      o.z += f * v[u].z;
-      o.w += f * v[u].w;
+    if (by_task) {
+      s_o[warp][lane] = o;
+      if (lane == 0) s_ml[warp] = make_float2(m, l);
+      __syncthreads();
+      if (warp > 0) return;
+      for (int w = 1; w < warps; ++w) add_part(m, l, o, s_ml[w], s_o[w][lane]);
     }
+    write_row(p, b, kvh, g, lane, m, l, o);
   }
-  s_o[warp][lane] = o;
-  if (lane == 0) s_ml[warp] = make_float2(m, l);
-  __syncthreads();
-  if (tid >= HEAD_DIM) return;
-  float mm = -INFINITY;
-#pragma unroll
-  for (int w = 0; w < JOIN_WARPS; ++w) mm = fmaxf(mm, s_ml[w].x);
-  const float base = mm == -INFINITY ? 0.f : mm;
-  float ll = 0.f, oo = 0.f;
-#pragma unroll
-  for (int w = 0; w < JOIN_WARPS; ++w) {
-    const float f = ptx::ex2_approx(s_ml[w].x - base);
-    ll += f * s_ml[w].y;
-    oo += f * reinterpret_cast<const float *>(s_o[w])[tid];
-  }
-  const int b = task / p.N2, kvh = task % p.N2;
-  write_row(p, b, kvh, g, tid, mm, ll, oo);
 }
 
 }  // namespace decode

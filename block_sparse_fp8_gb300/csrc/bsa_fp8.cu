@@ -891,27 +891,27 @@ extern "C" bsa_status_t bsa_fp8_decode(const bsa_fp8_decode_dims_t *d, const voi
   p.part_o = reinterpret_cast<float *>(ws + plan.off_o);
   p.counts = reinterpret_cast<int *>(ws + plan.off_counts);
   p.tiles = reinterpret_cast<uint32_t *>(ws + plan.off_tiles);
-  const cudaStream_t s = (cudaStream_t)stream;
   const bool wide = p.G > 8;  // two blocks of eight query heads per KV head
-  if (d->sparse && !none) {
-    decode::plan_kernel<<<(unsigned)(d->B * d->N2), decode::THREADS,
-                          (size_t)p.Kb * sizeof(uint32_t), s>>>(p);
-    if (cudaGetLastError() != cudaSuccess) return BSA_ERR_CUDA;
-    if (!launch_dependent(wide ? decode::decode_kernel<2, true> : decode::decode_kernel<1, true>,
-                          dim3((unsigned)plan.grid), decode::THREADS, decode::SMEM_BYTES, stream,
-                          p))
-      return BSA_ERR_CUDA;
-  } else {
-    const auto kernel = wide ? decode::decode_kernel<2, false> : decode::decode_kernel<1, false>;
-    kernel<<<(unsigned)plan.grid, decode::THREADS, decode::SMEM_BYTES, s>>>(p);
-    if (cudaGetLastError() != cudaSuccess) return BSA_ERR_CUDA;
-  }
-  // tasks of one tile are never cut
   const bool lists = d->sparse && !none;
-  if (p.Kb > 1 &&
-      !launch_dependent(lists ? decode::join_kernel<true> : decode::join_kernel<false>,
-                        dim3((unsigned)plan.grid, (unsigned)p.G), decode::JOIN_THREADS, 0, stream,
-                        p))
+  if (lists && !launch_dependent(decode::plan_kernel, dim3((unsigned)(d->B * d->N2)),
+                                 decode::PLAN_THREADS, (size_t)p.Kb * sizeof(uint32_t), stream, p))
+    return BSA_ERR_CUDA;
+  const auto kernel = lists ? (wide ? decode::decode_kernel<2, true> : decode::decode_kernel<1, true>)
+                            : (wide ? decode::decode_kernel<2, false>
+                                    : decode::decode_kernel<1, false>);
+  if (!launch_dependent(kernel, dim3((unsigned)plan.grid), decode::THREADS, decode::SMEM_BYTES,
+                        stream, p))
+    return BSA_ERR_CUDA;
+  if (p.Kb <= 1) return BSA_OK;  // tasks of one tile are never cut
+  // The join.  Beside two attention CTAs an SM has registers for one block of eight warps, two
+  // of four or five of two: the most warps a task's head with which every block is resident
+  // before the attention kernel ends.
+  const long long tasks = (long long)d->B * d->N2;
+  const bool by_task = tasks < plan.grid;
+  const int warps = !by_task ? 4 : tasks * p.G <= num_sms ? 8 : tasks * p.G <= 2 * num_sms ? 4 : 2;
+  if (!launch_dependent(lists ? decode::join_kernel<true> : decode::join_kernel<false>,
+                        by_task ? dim3((unsigned)tasks, (unsigned)p.G) : dim3((unsigned)plan.grid),
+                        warps * 32, 0, stream, p, by_task, plan.grid))
     return BSA_ERR_CUDA;
   return BSA_OK;
 }
