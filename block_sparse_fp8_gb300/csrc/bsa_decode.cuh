@@ -13,20 +13,23 @@
 //     O in fp32) per run, which the join kernel combines.  No atomics: results do not depend on
 //     timing.
 //   * Within a tile each of the CTA's four warps owns 32 tokens and keeps its own (m, l, O), so
-//     warps never wait for one another inside a task.  A warp copies its own K and V rows with
-//     16-byte cp.async, STAGES deep; rows past the sequence's end and rows of a bad page are
-//     zero-filled by the copy itself, so nothing there can reach the result.
+//     warps never wait for one another inside a task.  A warp fetches its own K and V rows, 32 slots
+//     of a page each, by TMA (one lane, one instruction each; 16-byte cp.async by all lanes
+//     took a fifth of the kernel's instructions) into a ring STAGES deep.  A bad page is fetched
+//     from beyond the pool, which reads as zeros; what lies past a sequence's end is replaced
+//     before it is used, so nothing there can reach the result.
 //   * The products run on mma.sync m16n8k16 with tokens (K) or dimensions (V) as the 16 rows and
 //     up to eight query heads as the 8 columns: with one token per sequence there is no
 //     128-row operand for tcgen05.mma to work on, and the tensor pipe is far from its limit.
 //     e4m3 codes convert to fp16 exactly; queries are scaled to fp16 by a power of two per
 //     row, P is rounded to fp16 (2^-11 relative, against the result's bf16 2^-8), accumulation,
 //     maxima and sums are fp32.
-//   * Shared memory rows keep their 16-byte chunks XOR-swizzled by the row number, so the
-//     fragment reads of K (a thread: 32 dimensions of one token) and V (16 dimensions of one
-//     token) are free of bank conflicts.
+//   * The 128-byte swizzle (a row's 16-byte chunks XORed with the row number) keeps the fragment
+//     reads of K (a thread: 32 dimensions of one token) and V (16 dimensions of one token) free of
+//     bank conflicts.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -44,12 +47,11 @@ constexpr int THREADS = WARPS * 32;
 constexpr int TOK = TILE / WARPS;  // tokens of a tile that one warp owns: one mma row block pair
 constexpr int STAGES = 2;
 constexpr int CTAS_PER_SM = 2;
-// one warp's stage: K rows, V rows, the tokens' K descales, {head mask, tokens left, last tile}
+// one warp's stage: K rows, V rows (1024-byte aligned, as the swizzle wants)
 constexpr int OFF_V = TOK * HEAD_DIM;
-constexpr int OFF_KD = 2 * TOK * HEAD_DIM;
-constexpr int OFF_META = OFF_KD + TOK * 4;
-constexpr int STAGE_BYTES = OFF_META + 16;
-constexpr int SMEM_BYTES = WARPS * STAGES * STAGE_BYTES;
+constexpr int STAGE_BYTES = 2 * TOK * HEAD_DIM;
+constexpr int SMEM_ALIGN = 1024;
+constexpr int SMEM_BYTES = WARPS * STAGES * STAGE_BYTES + SMEM_ALIGN;
 // fp16 probabilities are kept as 2^(s - m + P_SHIFT): the largest, 2^15, fits, and weights down to
 // 2^-29 of it keep full precision
 constexpr float P_SHIFT = 15.f;
@@ -73,11 +75,12 @@ struct Params {
   float *part_o;
   int *counts;
   uint32_t *tiles;
-  long long q_stride;                            // elements
-  long long page_bytes, head_bytes, slot_bytes;  // strides inside the page pool
+  long long q_stride;  // elements
   int B, N1, N2, G, ps, ps_shift, num_pages, L, Kb, max_kv_len;
   int q_e4m3, k_per_token, v_per_head;
+  int kv_nhd;
   float scale_log2;  // softmax_scale * log2(e)
+  unsigned long long wait_limit_ns;
 };
 
 __device__ __forceinline__ void report(const Params &p, int bits) {
@@ -103,21 +106,13 @@ __device__ __forceinline__ void pdl_wait() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
-// `bytes` (0 or SIZE) bytes from src, the rest of the SIZE bytes zero.
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, uint32_t bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
-               : "memory");
-}
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src, uint32_t bytes) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes)
-               : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() {
-  asm volatile("cp.async.commit_group;" ::: "memory");
-}
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+// Waits for a phase of a barrier, at most limit_ns; false when that runs out.
+__device__ __noinline__ bool wait_more(uint64_t *bar, uint32_t parity, unsigned long long limit_ns) {
+  const unsigned long long t0 = ptx::globaltimer_ns();
+  const uint32_t hint = (uint32_t)min(limit_ns, (unsigned long long)WAIT_LIMIT_NS);
+  while (!ptx::mbar_try_wait_hint(bar, parity, hint))
+    if (ptx::globaltimer_ns() - t0 > limit_ns) return false;
+  return true;
 }
 
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
@@ -364,9 +359,16 @@ struct Cursor {
 };
 
 template <int NT, bool SPARSE>  // NT: blocks of eight query heads per KV head
-__global__ void __launch_bounds__(THREADS, CTAS_PER_SM) decode_kernel(const Params p) {
-  extern __shared__ __align__(128) uint8_t smem[];
+__global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
+    decode_kernel(const Params p, const __grid_constant__ CUtensorMap tk,
+                  const __grid_constant__ CUtensorMap tv) {
+  extern __shared__ uint8_t smem_raw[];
   __shared__ float2 s_ml[WARPS][MAX_G];
+  __shared__ __align__(16) float s_kd[WARPS][STAGES][TOK];
+  // {heads, tokens left, last tile of its task, page bad}
+  __shared__ __align__(16) int4 s_meta[WARPS][STAGES];
+  __shared__ uint64_t s_full[WARPS][STAGES];
+  uint8_t *const smem = smem_raw + (-ptx::smem_u32(smem_raw) & (SMEM_ALIGN - 1));
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int r = lane >> 2, q4 = lane & 3;  // mma fragment coordinates
   pdl_wait();               // what the stream ran before: the tile lists among it
@@ -465,49 +467,38 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) decode_kernel(const Para
   cur.look(p, warp);
 
   const uint32_t ring = ptx::smem_u32(smem) + warp * STAGES * STAGE_BYTES;
-  const int lrow = lane >> 3, lchunk = lane & 7;  // copy coordinates: 4 rows of 8 chunks at once
+  if (lane == 0) {
+    for (int i = 0; i < STAGES; ++i) ptx::mbar_init(&s_full[warp][i], 1);
+    ptx::fence_mbarrier_init();
+  }
+  __syncwarp();
   int to_issue = x1 - x0;
+  uint32_t phases = 0, in_flight = 0;  // a bit a stage
 
   const auto issue = [&](int stage) {
-    if (to_issue > 0) {
-      const uint32_t dst = ring + stage * STAGE_BYTES;
-      const int left = cur.heads != 0 ? cur.kv - cur.pos : 0;
-      int page = cur.page;
-      if (page < 0 || page >= p.num_pages) {
-        if (left > 0 && lane == 0) report(p, BSA_DEV_BAD_PAGE);
-        page = -1;
-      }
-      const int rows = page >= 0 ? min(left, TOK) : 0;
-      const int slot = cur.pos & (p.ps - 1);
-      const long long off = page >= 0 ? page * p.page_bytes + cur.kvh * p.head_bytes +
-                                            (slot + lrow) * p.slot_bytes + lchunk * 16
-                                      : 0;
-      const uint8_t *ks = p.k_pages + off, *vs = p.v_pages + off;
+    if (to_issue == 0) return;
+    const int left = cur.heads != 0 ? cur.kv - cur.pos : 0;
+    const bool bad = cur.page < 0 || cur.page >= p.num_pages;
+    if (left > 0) in_flight |= 1u << stage;
+    if (lane == 0) {
+      s_meta[warp][stage] = make_int4(cur.heads, left, cur.idx + 1 == cur.n, bad);
       if (left > 0) {
-#pragma unroll
-        for (int it = 0; it < TOK / 4; ++it) {
-          const int row = it * 4 + lrow;
-          const bool ok = row < rows;
-          const uint32_t d = dst + row * HEAD_DIM + ((lchunk ^ (row & 7)) << 4);
-          const long long o = ok ? it * 4 * p.slot_bytes : 0;
-          cp_async16(d, ok ? ks + o : p.k_pages, ok ? 16 : 0);
-          cp_async16(d + OFF_V, ok ? vs + o : p.v_pages, ok ? 16 : 0);
-        }
-        if (p.k_per_token) {
-          const bool ok = lane < rows;
-          const size_t at = ok ? ((size_t)page * p.N2 + cur.kvh) * p.ps + slot + lane : 0;
-          cp_async4(dst + OFF_KD + lane * 4, p.k_descale + at, ok ? 4 : 0);
-        }
+        if (bad) report(p, BSA_DEV_BAD_PAGE);
+        const int page = bad ? p.num_pages : cur.page, slot = cur.pos & (p.ps - 1);
+        const int c1 = p.kv_nhd ? cur.kvh : slot, c2 = p.kv_nhd ? slot : cur.kvh;
+        const bool kd = p.k_per_token && !bad;
+        uint64_t *bar = &s_full[warp][stage];
+        uint8_t *dst = smem + (warp * STAGES + stage) * STAGE_BYTES;
+        ptx::mbar_arrive_expect_tx(bar, STAGE_BYTES + (kd ? TOK * 4 : 0));
+        ptx::tma_load_4d(dst, &tk, bar, 0, c1, c2, page);
+        ptx::tma_load_4d(dst + OFF_V, &tv, bar, 0, c1, c2, page);
+        if (kd)
+          ptx::bulk_load(s_kd[warp][stage],
+                         p.k_descale + ((size_t)page * p.N2 + cur.kvh) * p.ps + slot, TOK * 4,
+                         bar);
       }
-      if (lane == 0) {
-        const int last = cur.idx + 1 == cur.n;
-        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst + OFF_META),
-                     "r"(cur.heads), "r"(left), "r"(last), "r"(0)
-                     : "memory");
-      }
-      if (--to_issue > 0) cur.next(p, warp);
     }
-    cp_async_commit();
+    if (--to_issue > 0) cur.next(p, warp);
   };
 
 #pragma unroll
@@ -529,7 +520,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) decode_kernel(const Para
   // ---- one warp's 32 tokens of a tile
   const float kd_all = p.k_per_token || !p.k_descale ? 1.f : p.k_descale[0];
   const int group = (1 << p.G) - 1;
-  const auto compute = [&](uint32_t st, int heads, int left) {
+  const auto compute = [&](uint32_t st, const float *kds, int heads, int left, bool bad) {
     float s[NT][2][4];  // [head block][16 tokens][token r | r + 8, head 2 q4 | + 1]
 #pragma unroll
     for (int mt = 0; mt < 2; ++mt) {
@@ -556,23 +547,23 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) decode_kernel(const Para
       }
     }
     // scores, masked; a masked value is replaced, never multiplied
-    const bool whole = left >= TOK && (!SPARSE || heads == group);
+    const bool whole = left >= TOK && (!SPARSE || heads == group) && !bad;
 #pragma unroll
     for (int mt = 0; mt < 2; ++mt) {
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         const int t = mt * 16 + half * 8 + r;
-        float kd = kd_all;
-        if (p.k_per_token)
-          asm volatile("ld.shared.f32 %0, [%1];" : "=f"(kd) : "r"(st + OFF_KD + t * 4) : "memory");
+        const float kd = p.k_per_token ? kds[t] : kd_all;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             float &x = s[nt][mt][2 * half + c];
             x *= kd * fac[nt][c];
-            if (!whole && (t >= left || (SPARSE && !((heads >> (nt * 8 + 2 * q4 + c)) & 1))))
-              x = -INFINITY;
+            if (!whole) {
+              if (bad) x = 0.f;  // no descale was fetched
+              if (t >= left || (SPARSE && !((heads >> (nt * 8 + 2 * q4 + c)) & 1))) x = -INFINITY;
+            }
           }
       }
     }
@@ -623,8 +614,16 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) decode_kernel(const Para
         // tokens 2 q4, 2 q4 + 1 and those + 8, dimensions 16 r .. 16 r + 15
         const uint32_t t0 = st + OFF_V + (mt * 16 + 2 * q4) * HEAD_DIM;
         const uint32_t c0 = (r ^ (2 * q4)) << 4, c1 = (r ^ (2 * q4 + 1)) << 4;
-        const uint4 x0 = lds128(t0 + c0), x1 = lds128(t0 + HEAD_DIM + c1);
-        const uint4 y0 = lds128(t0 + 8 * HEAD_DIM + c0), y1 = lds128(t0 + 9 * HEAD_DIM + c1);
+        uint4 x0 = lds128(t0 + c0), x1 = lds128(t0 + HEAD_DIM + c1);
+        uint4 y0 = lds128(t0 + 8 * HEAD_DIM + c0), y1 = lds128(t0 + 9 * HEAD_DIM + c1);
+        if (left < TOK) {  // whatever lies past the end, NaN codes too, counts as zero
+          const int t = mt * 16 + 2 * q4;
+          const uint4 zero = make_uint4(0, 0, 0, 0);
+          if (t >= left) x0 = zero;
+          if (t + 1 >= left) x1 = zero;
+          if (t + 8 >= left) y0 = zero;
+          if (t + 9 >= left) y1 = zero;
+        }
         const uint32_t wx0[4] = {x0.x, x0.y, x0.z, x0.w}, wx1[4] = {x1.x, x1.y, x1.z, x1.w};
         const uint32_t wy0[4] = {y0.x, y0.y, y0.z, y0.w}, wy1[4] = {y1.x, y1.y, y1.z, y1.w};
 #pragma unroll
@@ -712,6 +711,8 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) decode_kernel(const Para
         reinterpret_cast<float4 *>(p.part_o)[(slot * p.G + g) * 32 + lane] = o;
       }
     }
+    // the stage's next contents come through the async proxy
+    ptx::fence_proxy_async_smem();
     __syncthreads();
   };
 
@@ -719,16 +720,28 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) decode_kernel(const Para
   reset();
   int stage = 0;
   for (int x = x0; x < x1;) {
-    cp_async_wait<STAGES - 2>();
-    __syncwarp();  // the stage is filled for every lane, and the one before it read by every lane
-    const uint32_t st = ring + stage * STAGE_BYTES;
+    __syncwarp();  // the stage before this one has been read by every lane, and is refilled
     issue(stage == 0 ? STAGES - 1 : stage - 1);
-    uint32_t heads, left, last, unused;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(heads), "=r"(left), "=r"(last), "=r"(unused)
-                 : "r"(st + OFF_META)
-                 : "memory");
-    if ((int)left > 0) compute(st, (int)heads, (int)left);
+    const int4 meta = s_meta[warp][stage];
+    const int heads = meta.x, left = meta.y;
+    const bool last = meta.z != 0;
+    if (left > 0) {
+      uint64_t *bar = &s_full[warp][stage];
+      const uint32_t parity = (phases >> stage) & 1u;
+      bool ok = __all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity));
+      if (!ok) ok = __all_sync(0xffffffffu, wait_more(bar, parity, p.wait_limit_ns));
+      if (!ok) {
+        // out of time: report, see the copies in flight land (with the default limit), leave
+        if (lane == 0) report(p, BSA_DEV_TIMEOUT);
+        for (int i = 0; i < STAGES; ++i)
+          if ((in_flight >> i) & 1u)
+            wait_more(&s_full[warp][i], (phases >> i) & 1u, WAIT_LIMIT_NS);
+        return;
+      }
+      phases ^= 1u << stage;
+      in_flight &= ~(1u << stage);
+      compute(ring + stage * STAGE_BYTES, s_kd[warp][stage], heads, left, meta.w != 0);
+    }
     ++x;
     if (last || x == x1) {
       flush(stage, last);

@@ -872,7 +872,9 @@ extern "C" bsa_status_t bsa_fp8_decode(const bsa_fp8_decode_dims_t *d, const voi
   p.lse = lse_f32;
   p.dev_status = dev_status;
   p.q_stride = d->q_stride;
-  pool_strides(d->kv_layout, d->N2, d->page_size, &p.page_bytes, &p.head_bytes, &p.slot_bytes);
+  p.kv_nhd = d->kv_layout == BSA_KV_NHD;
+  const unsigned long long lim = g_wait_limit_ns.load(std::memory_order_relaxed);
+  p.wait_limit_ns = lim ? lim : WAIT_LIMIT_NS;
   p.B = d->B;
   p.N1 = d->N1;
   p.N2 = d->N2;
@@ -892,6 +894,21 @@ extern "C" bsa_status_t bsa_fp8_decode(const bsa_fp8_decode_dims_t *d, const voi
   p.counts = reinterpret_cast<int *>(ws + plan.off_counts);
   p.tiles = reinterpret_cast<uint32_t *>(ws + plan.off_tiles);
   const bool wide = p.G > 8;  // two blocks of eight query heads per KV head
+  // Tensor maps of the pools: a box is a warp's 32 slots of one page and head, in shared memory
+  // consecutive 128-byte rows in either layout.
+  CUtensorMap tk, tv;
+  memset(&tk, 0, sizeof(tk));
+  memset(&tv, 0, sizeof(tv));
+  if (!none) {
+    const cuuint64_t H = (cuuint64_t)d->N2, S = (cuuint64_t)d->page_size;
+    const bool nhd = p.kv_nhd != 0;
+    const cuuint64_t gd[4] = {HEAD_DIM, nhd ? H : S, nhd ? S : H, (cuuint64_t)d->num_pages};
+    const cuuint64_t gs[3] = {HEAD_DIM, gd[1] * HEAD_DIM, H * S * HEAD_DIM};
+    const cuuint32_t box[4] = {HEAD_DIM, nhd ? 1u : (cuuint32_t)decode::TOK,
+                               nhd ? (cuuint32_t)decode::TOK : 1u, 1};
+    if (!encode_map(&tk, k_pages, 4, gd, gs, box) || !encode_map(&tv, v_pages, 4, gd, gs, box))
+      return BSA_ERR_CUDA;
+  }
   const bool lists = d->sparse && !none;
   if (lists && !launch_dependent(decode::plan_kernel, dim3((unsigned)(d->B * d->N2)),
                                  decode::PLAN_THREADS, (size_t)p.Kb * sizeof(uint32_t), stream, p))
@@ -900,7 +917,7 @@ extern "C" bsa_status_t bsa_fp8_decode(const bsa_fp8_decode_dims_t *d, const voi
                             : (wide ? decode::decode_kernel<2, false>
                                     : decode::decode_kernel<1, false>);
   if (!launch_dependent(kernel, dim3((unsigned)plan.grid), decode::THREADS, decode::SMEM_BYTES,
-                        stream, p))
+                        stream, p, tk, tv))
     return BSA_ERR_CUDA;
   if (p.Kb <= 1) return BSA_OK;  // tasks of one tile are never cut
   // The join.  Beside two attention CTAs an SM has registers for one block of eight warps, two
