@@ -341,30 +341,42 @@ def append_kv(k_new, v_new, cu_seqlens_new, cache_seqlens, block_table, k_pages,
 # ---------------------------------------------------------------------------------------------
 
 # A serving loop makes these calls once a layer and token, so their checks are kept to a few plain
-# comparisons a tensor (a refusal works out its message afterwards).
+# comparisons a tensor (a refusal works out its message afterwards), and the names they need are
+# looked up once.
 
-def _refuse(name, t, dtypes, shape, dev):
+_names = None
+
+
+def _torch_names():
+    """(torch, bf16, fp32, int32, the dtypes of e4m3 codes)."""
+    global _names
+    if _names is None:
+        import torch
+
+        _names = (torch, torch.bfloat16, torch.float32, torch.int32,
+                  (torch.uint8, torch.float8_e4m3fn))
+    return _names
+
+
+def _check(name, t, dtype, shape, dev):
+    """Raises ValueError unless `t` is a contiguous tensor of `dtype` (or of one of a tuple of them)
+    and of `shape` on the CUDA device of index `dev` (-1: no CUDA device, which _call refuses)."""
+    if (t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous()):
+        return
+    dtypes = dtype if type(dtype) is tuple else (dtype,)
     if t.get_device() != dev:
         raise ValueError(f"{name} is on {t.device}, q or the cache on another device")
     if t.dtype not in dtypes:
         raise ValueError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    raise ValueError(f"{name} must be contiguous")
-
-
-def _check(name, t, dtypes, shape, dev):
-    """Raises ValueError unless `t` is a contiguous tensor of one of `dtypes` and of `shape` on
-    the CUDA device of index `dev` (-1: not a CUDA device, which _call refuses)."""
-    if (t.dtype not in dtypes or t.shape != shape or t.get_device() != dev
-            or not t.is_contiguous()):
-        _refuse(name, t, dtypes, shape, dev)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
 
 
 def _call(fn, args, dev, stream, what):
     """fn(*args, stream handle) with device `dev` current; raises BsaError on a status but 0."""
-    import torch
-
+    torch = _torch_names()[0]
     if dev < 0:
         raise ValueError(f"{what}: tensors must be on a CUDA device")
     if stream is None:
@@ -383,9 +395,7 @@ def _call(fn, args, dev, stream, what):
 
 
 def _check_status(dev_status, dev):
-    import torch
-
-    if (dev_status.dtype is not torch.int32 or dev_status.numel() < 1
+    if (dev_status.dtype is not _torch_names()[3] or dev_status.numel() < 1
             or dev_status.get_device() != dev):
         raise ValueError("dev_status must be an int32 tensor on the device of the others")
 
@@ -428,15 +438,13 @@ def decode(q, k_pages, v_pages, k_descale, v_descale, seqused_kv, block_table, m
     Returns (out bf16 [B, N1, 128], lse f32 [N1, B] or None); a sequence without tokens, or a head
     without an enabled tile, gives 0 and -FLT_MAX.  `workspace` (decode_workspace_size bytes)
     must not be shared by calls in flight at once."""
-    import torch
-
-    bf16, f32, i32 = (torch.bfloat16,), (torch.float32,), (torch.int32,)
-    codes = (torch.uint8, torch.float8_e4m3fn)
+    torch, bf16, f32, i32, codes = _torch_names()
     dev = q.get_device()
     if q.dim() != 3:
         raise ValueError(f"q has shape {tuple(q.shape)}, expected [B, N1, 128]")
     B, N1, D = q.shape
-    if q.dtype not in bf16 and q.dtype not in codes:
+    is_bf16 = q.dtype is bf16
+    if not is_bf16 and q.dtype not in codes:
         raise ValueError(f"q has dtype {q.dtype}, expected bf16 or e4m3 codes")
     if not q.is_contiguous() and (q.stride(2) != 1 or (N1 > 1 and q.stride(1) != D)):
         raise ValueError("q must be contiguous within a sequence's row")
@@ -447,8 +455,9 @@ def decode(q, k_pages, v_pages, k_descale, v_descale, seqused_kv, block_table, m
         SCALE_PER_TOKEN_HEAD if k_descale.dim() == 3 else SCALE_PER_TENSOR)
     v_kind = v_scale_kind if v_scale_kind is not None else (
         SCALE_PER_HEAD if v_descale.numel() == N2 else SCALE_PER_TENSOR)
-    _check("k_pages", k_pages, codes, k_pages.shape, dev)
-    _check("v_pages", v_pages, codes, k_pages.shape, dev)
+    pool = k_pages.shape
+    _check("k_pages", k_pages, k_pages.dtype if k_pages.dtype in codes else codes, pool, dev)
+    _check("v_pages", v_pages, v_pages.dtype if v_pages.dtype in codes else codes, pool, dev)
     _check("k_descale", k_descale, f32,
            (P, N2, ps) if k_kind == SCALE_PER_TOKEN_HEAD else (1,), dev)
     _check("v_descale", v_descale, f32, (N2,) if v_kind == SCALE_PER_HEAD else (1,), dev)
@@ -461,7 +470,8 @@ def decode(q, k_pages, v_pages, k_descale, v_descale, seqused_kv, block_table, m
     if sparse:
         Kb = -(-int(max_kv_len) // 128)
         if block_mask is not None:
-            _check("block_mask", block_mask, (torch.uint8, torch.bool), (B, N1, Kb), dev)
+            _check("block_mask", block_mask,
+                   torch.bool if block_mask.dtype is torch.bool else torch.uint8, (B, N1, Kb), dev)
         if sparse_indices is not None:
             _check("sparse_indices", sparse_indices, i32, (B, N1, Kb), dev)
         if sparse_seq_len is not None:
@@ -478,7 +488,7 @@ def decode(q, k_pages, v_pages, k_descale, v_descale, seqused_kv, block_table, m
         _check_status(dev_status, dev)
     # in the order of DecodeDims' fields, as make_decode_dims
     dims = DecodeDims(B, N1, N2, D, ps, max_kv_len, P, L, k_kind, v_kind, kv_layout,
-                      QTYPE_BF16 if q.dtype in bf16 else QTYPE_E4M3,
+                      QTYPE_BF16 if is_bf16 else QTYPE_E4M3,
                       q.stride(0) if B > 1 else N1 * D, sparse)
     if workspace is None:
         if dev < 0:
@@ -500,11 +510,9 @@ def decode(q, k_pages, v_pages, k_descale, v_descale, seqused_kv, block_table, m
 
 
 def _gather_rows(name, t, dtype, shape, pages):
-    import torch
-
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=pages.device)
-    _check(name, t, (dtype,), shape, pages.get_device())
+        return _torch_names()[0].empty(shape, dtype=dtype, device=pages.device)
+    _check(name, t, dtype, shape, pages.get_device())
     return t
 
 
@@ -517,10 +525,7 @@ def gather_kv(k_pages, v_pages, k_descale, v_descale, cu_seqlens, block_table, t
     b, code * descale.  out_dtype bf16 (default) or float32, or that of k_out / v_out when given;
     rows from cu_seqlens[B] on are left as they were.  k_pages = None or v_pages = None leaves
     that side out (returned as None)."""
-    import torch
-
-    f32, i32 = (torch.float32,), (torch.int32,)
-    codes = (torch.uint8, torch.float8_e4m3fn)
+    torch, _, f32, i32, codes = _torch_names()
     pages = k_pages if k_pages is not None else v_pages
     if pages is None:
         raise ValueError("k_pages and v_pages are both None")
@@ -546,7 +551,8 @@ def gather_kv(k_pages, v_pages, k_descale, v_descale, cu_seqlens, block_table, t
     if k_pages is not None:
         k_kind = k_scale_kind if k_scale_kind is not None else (
             SCALE_PER_TOKEN_HEAD if k_descale.dim() == 3 else SCALE_PER_TENSOR)
-        _check("k_pages", k_pages, codes, pages.shape, dev)
+        _check("k_pages", k_pages, k_pages.dtype if k_pages.dtype in codes else codes, pages.shape,
+               dev)
         _check("k_descale", k_descale, f32,
                (P, N2, ps) if k_kind == SCALE_PER_TOKEN_HEAD else (1,), dev)
         k_out = _gather_rows("k_out", k_out, out_dtype, shape, pages)
@@ -555,7 +561,8 @@ def gather_kv(k_pages, v_pages, k_descale, v_descale, cu_seqlens, block_table, t
     if v_pages is not None:
         v_kind = v_scale_kind if v_scale_kind is not None else (
             SCALE_PER_HEAD if v_descale.numel() == N2 else SCALE_PER_TENSOR)
-        _check("v_pages", v_pages, codes, pages.shape, dev)
+        _check("v_pages", v_pages, v_pages.dtype if v_pages.dtype in codes else codes, pages.shape,
+               dev)
         _check("v_descale", v_descale, f32, (N2,) if v_kind == SCALE_PER_HEAD else (1,), dev)
         v_out = _gather_rows("v_out", v_out, out_dtype, shape, pages)
     elif v_out is not None:
@@ -575,9 +582,7 @@ def merge_states(outs, lses, out=None, lse=None, return_lse: bool = True, stream
     [T, N1, 128] and lses their fp32 LSEs [N1, T], as prefill() and decode() return them (for
     decode T = B).  Returns (out, lse) over the union of the keys.  `out` may be one of `outs`
     and `lse` one of `lses`."""
-    import torch
-
-    bf16, f32 = (torch.bfloat16,), (torch.float32,)
+    torch, bf16, f32, _, _ = _torch_names()
     n = len(outs)
     if n < 1 or n > MAX_MERGE or len(lses) != n:
         raise ValueError(f"{n} outs and {len(lses)} lses: 1 to {MAX_MERGE} of each")

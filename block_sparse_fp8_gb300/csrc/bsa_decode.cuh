@@ -11,7 +11,8 @@
 //     batch's tiles in task order, each finding its run by a scan of the lengths.  A task that
 //     lies inside one run is finished there; a task cut by run borders leaves one partial (m, l,
 //     O in fp32) per run, which the join kernel combines.  No atomics: results do not depend on
-//     timing.
+//     timing.  Where no sequence has more than WHOLE_TILES tiles and there is a CTA for every
+//     task, the runs are whole tasks instead, with nothing to scan and nothing to join.
 //   * Within a tile each of the CTA's four warps owns 32 tokens and keeps its own (m, l, O), so
 //     warps never wait for one another inside a task.  A warp fetches its own K and V rows, 32 slots
 //     of a page each, by TMA (one lane, one instruction each; 16-byte cp.async by all lanes
@@ -56,6 +57,7 @@ constexpr int SMEM_BYTES = WARPS * STAGES * STAGE_BYTES + SMEM_ALIGN;
 // 2^-29 of it keep full precision
 constexpr float P_SHIFT = 15.f;
 constexpr int MAX_G = 16;
+constexpr int WHOLE_TILES = 4;
 
 struct Params {
   const void *q;
@@ -79,6 +81,7 @@ struct Params {
   int B, N1, N2, G, ps, ps_shift, num_pages, L, Kb, max_kv_len;
   int q_e4m3, k_per_token, v_per_head;
   int kv_nhd;
+  int whole;  // the batch is cut between tasks only
   float scale_log2;  // softmax_scale * log2(e)
   unsigned long long wait_limit_ns;
 };
@@ -122,6 +125,10 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
                : "r"(a)
                : "memory");
   return v;
+}
+
+__device__ __forceinline__ void prefetch_l1(const void *a) {
+  asm volatile("prefetch.global.L1 [%0];" ::"l"(a));
 }
 
 // Four e4m3 codes -> two f16 pairs, exactly.
@@ -277,10 +284,10 @@ __device__ __forceinline__ int item_tiles(const Params &p, int i) {
 }
 
 template <bool SPARSE, typename Want>
-__device__ __forceinline__ Found find_tile(const Params &p, int grid, Cut &cut, bool by_item,
-                                           Want &&want) {
+__device__ __forceinline__ Found find_tile(const Params &p, int grid, int threads, Cut &cut,
+                                           bool by_item, Want &&want) {
   __shared__ int s_sum[MAX_WARPS], s_item, s_off;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int items = SPARSE ? p.B * p.N2 : p.B;
   const int per = (items + threads - 1) / threads, i0 = min(tid * per, items),
             i1 = min(i0 + per, items);
@@ -295,7 +302,9 @@ __device__ __forceinline__ Found find_tile(const Params &p, int grid, Cut &cut, 
   if (lane == 31) s_sum[warp] = incl;
   __syncthreads();
   int total = 0;
-  for (int w = 0; w < threads / 32; ++w) {
+#pragma unroll
+  for (int w = 0; w < MAX_WARPS; ++w) {
+    if (w >= threads / 32) break;
     if (w < warp) incl += s_sum[w];
     total += s_sum[w];
   }
@@ -365,36 +374,51 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
   extern __shared__ uint8_t smem_raw[];
   __shared__ float2 s_ml[WARPS][MAX_G];
   __shared__ __align__(16) float s_kd[WARPS][STAGES][TOK];
-  // {heads, tokens left, last tile of its task, page bad}
+  // {heads, tokens left, last tile of its task (1) and of the run (2), page bad}
   __shared__ __align__(16) int4 s_meta[WARPS][STAGES];
   __shared__ uint64_t s_full[WARPS][STAGES];
   uint8_t *const smem = smem_raw + (-ptx::smem_u32(smem_raw) & (SMEM_ALIGN - 1));
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int r = lane >> 2, q4 = lane & 3;  // mma fragment coordinates
+  if (lane == 0) {
+    for (int i = 0; i < STAGES; ++i) ptx::mbar_init(&s_full[warp][i], 1);
+    ptx::fence_mbarrier_init();
+    if (warp == 0 && p.Kb > 0) {
+      ptx::prefetch_tmap(&tk);
+      ptx::prefetch_tmap(&tv);
+    }
+  }
+  __syncwarp();
   pdl_wait();               // what the stream ran before: the tile lists among it
   pdl_launch_dependents();  // the join, which reads the lengths and counts as well: only now
 
+  // this CTA's run: its first tile's place, and its length in tiles (`whole`: in tasks)
   const int cta = blockIdx.x;
-  Cut cut;
-  const Found at = find_tile<SPARSE>(p, (int)gridDim.x, cut, false, [&](const Cut &c) {
-    return cta < c.runs ? c.begin(cta) : -1;
-  });
-  if (at.item < 0) return;
-  const int x0 = cut.begin(cta), x1 = cut.begin(cta + 1);
-
+  int units;
   Cursor<SPARSE> cur;
-  if (SPARSE) {
-    cur.b = at.item / p.N2;
-    cur.kvh = at.item % p.N2;
-    cur.idx = at.off;
+  if (p.whole) {
+    const int tasks = p.B * p.N2, runs = min((int)gridDim.x, tasks);
+    const Cut cut = {runs, tasks / runs, tasks % runs};
+    const int t0 = cut.begin(cta);
+    units = cut.begin(cta + 1) - t0;  // the grid is no larger than the tasks
+    cur.b = t0 / p.N2;
+    cur.kvh = t0 % p.N2;
+    cur.idx = 0;
     cur.kv = seq_len(p, cur.b);
     cur.enter(p);
   } else {
-    cur.b = at.item;
+    Cut cut;
+    const Found at = find_tile<SPARSE>(p, (int)gridDim.x, THREADS, cut, false, [&](const Cut &c) {
+      return cta < c.runs ? c.begin(cta) : -1;
+    });
+    if (at.item < 0) return;
+    units = cut.begin(cta + 1) - cut.begin(cta);
+    cur.b = SPARSE ? at.item / p.N2 : at.item;
     cur.kv = seq_len(p, cur.b);
+    if (SPARSE) cur.kvh = at.item % p.N2;
     cur.enter(p);
-    cur.kvh = at.off / cur.n;
-    cur.idx = at.off % cur.n;
+    if (!SPARSE) cur.kvh = at.off / cur.n;
+    cur.idx = SPARSE ? at.off : at.off % cur.n;
   }
   int b = cur.b, kvh = cur.kvh;      // the computing side's task
   bool from_start = cur.idx == 0;    // the segment begins its task
@@ -467,21 +491,23 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
   cur.look(p, warp);
 
   const uint32_t ring = ptx::smem_u32(smem) + warp * STAGES * STAGE_BYTES;
-  if (lane == 0) {
-    for (int i = 0; i < STAGES; ++i) ptx::mbar_init(&s_full[warp][i], 1);
-    ptx::fence_mbarrier_init();
-  }
-  __syncwarp();
-  int to_issue = x1 - x0;
   uint32_t phases = 0, in_flight = 0;  // a bit a stage
 
+  const int q_size = p.q_e4m3 ? 1 : 2, q_lines = p.G * q_size;  // 128-byte lines of a group
+  const auto q_row = [&](int qb, int qh) {
+    return static_cast<const uint8_t *>(p.q) +
+           ((size_t)qb * p.q_stride + (size_t)qh * p.G * HEAD_DIM) * q_size;
+  };
+
   const auto issue = [&](int stage) {
-    if (to_issue == 0) return;
+    if (units == 0) return;
     const int left = cur.heads != 0 ? cur.kv - cur.pos : 0;
     const bool bad = cur.page < 0 || cur.page >= p.num_pages;
+    const bool last = cur.idx + 1 == cur.n, counts = !p.whole || last;
+    const bool end = counts && units == 1;
     if (left > 0) in_flight |= 1u << stage;
     if (lane == 0) {
-      s_meta[warp][stage] = make_int4(cur.heads, left, cur.idx + 1 == cur.n, bad);
+      s_meta[warp][stage] = make_int4(cur.heads, left, (last ? 1 : 0) | (end ? 2 : 0), bad);
       if (left > 0) {
         if (bad) report(p, BSA_DEV_BAD_PAGE);
         const int page = bad ? p.num_pages : cur.page, slot = cur.pos & (p.ps - 1);
@@ -498,7 +524,12 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
                          bar);
       }
     }
-    if (--to_issue > 0) cur.next(p, warp);
+    if (counts) --units;
+    if (!end) {
+      cur.next(p, warp);
+      // the next task's queries, wanted when the computing side gets there
+      if (cur.idx == 0 && lane < q_lines) prefetch_l1(q_row(cur.b, cur.kvh) + lane * 128);
+    }
   };
 
 #pragma unroll
@@ -719,12 +750,12 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
   convert_q();
   reset();
   int stage = 0;
-  for (int x = x0; x < x1;) {
+  for (;;) {
     __syncwarp();  // the stage before this one has been read by every lane, and is refilled
     issue(stage == 0 ? STAGES - 1 : stage - 1);
     const int4 meta = s_meta[warp][stage];
     const int heads = meta.x, left = meta.y;
-    const bool last = meta.z != 0;
+    const bool last = meta.z & 1, end = meta.z & 2;
     if (left > 0) {
       uint64_t *bar = &s_full[warp][stage];
       const uint32_t parity = (phases >> stage) & 1u;
@@ -742,20 +773,18 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
       in_flight &= ~(1u << stage);
       compute(ring + stage * STAGE_BYTES, s_kd[warp][stage], heads, left, meta.w != 0);
     }
-    ++x;
-    if (last || x == x1) {
+    if (last || end) {
       flush(stage, last);
-      if (x < x1) {
-        first_segment = false;
-        from_start = true;
-        if (++kvh == p.N2) {
-          kvh = 0;
-          ++b;
-        }
-        fetch_q(b, kvh);
-        convert_q();
-        reset();
+      if (end) return;
+      first_segment = false;
+      from_start = true;
+      if (++kvh == p.N2) {
+        kvh = 0;
+        ++b;
       }
+      fetch_q(b, kvh);
+      convert_q();
+      reset();
     }
     stage = stage == STAGES - 1 ? 0 : stage + 1;
   }
@@ -780,7 +809,7 @@ __global__ void __launch_bounds__(MAX_WARPS * 32) join_kernel(const Params p, bo
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
   const int index = blockIdx.x;
   Cut cut;
-  const Found at = find_tile<SPARSE>(p, grid, cut, by_task, [&](const Cut &c) {
+  const Found at = find_tile<SPARSE>(p, grid, (int)blockDim.x, cut, by_task, [&](const Cut &c) {
     return by_task ? (SPARSE ? index : index / p.N2) : index < c.runs ? c.begin(index + 1) - 1 : -1;
   });
   if (at.item < 0) return;  // (never block 0)
