@@ -147,8 +147,8 @@ def lib():
 
 
 def set_wait_limit_ns(ns: int) -> None:
-    """Limit of every bounded wait inside the prefill kernel for later launches (0: the
-    default, 2 s).  A wait that runs out sets DEV_TIMEOUT in the device status word."""
+    """Limit of every bounded wait inside the prefill and decode kernels for later launches (0:
+    the default, 2 s).  A wait that runs out sets DEV_TIMEOUT in the device status word."""
     lib().bsa_fp8_set_wait_limit_ns(int(ns))
 
 
@@ -374,8 +374,9 @@ def _check(name, t, dtype, shape, dev):
         raise ValueError(f"{name} must be contiguous")
 
 
-def _call(fn, args, dev, stream, what):
-    """fn(*args, stream handle) with device `dev` current; raises BsaError on a status but 0."""
+def _call(fn, args, dev, stream, what, made=()):
+    """fn(*args, stream handle) with device `dev` current; raises BsaError on a status but 0.
+    `made`: tensors of this call's own, which live on the current stream."""
     torch = _torch_names()[0]
     if dev < 0:
         raise ValueError(f"{what}: tensors must be on a CUDA device")
@@ -392,6 +393,9 @@ def _call(fn, args, dev, stream, what):
             st = fn(*args, handle)
     if st != 0:
         raise BsaError(st, what)
+    if stream is not None:
+        for t in made:
+            t.record_stream(stream)
 
 
 def _check_status(dev_status, dev):
@@ -476,26 +480,32 @@ def decode(q, k_pages, v_pages, k_descale, v_descale, seqused_kv, block_table, m
             _check("sparse_indices", sparse_indices, i32, (B, N1, Kb), dev)
         if sparse_seq_len is not None:
             _check("sparse_seq_len", sparse_seq_len, i32, (B, N1), dev)
+    made = []
     if out is None:
         out = torch.empty((B, N1, D), dtype=torch.bfloat16, device=q.device)
+        made.append(out)
     else:
         _check("out", out, bf16, (B, N1, D), dev)
     if lse is not None:
         _check("lse", lse, f32, (N1, B), dev)
     elif return_lse:
         lse = torch.empty((N1, B), dtype=torch.float32, device=q.device)
+        made.append(lse)
     if dev_status is not None:
         _check_status(dev_status, dev)
     # in the order of DecodeDims' fields, as make_decode_dims
-    dims = DecodeDims(B, N1, N2, D, ps, max_kv_len, P, L, k_kind, v_kind, kv_layout,
-                      QTYPE_BF16 if is_bf16 else QTYPE_E4M3,
-                      q.stride(0) if B > 1 else N1 * D, sparse)
+    q_stride = q.stride(0) if B > 1 else N1 * D
+    if q_stride >= 1 << 31:
+        raise ValueError(f"q's rows lie {q_stride} elements apart: 2^31 - 1 at most")
+    dims = DecodeDims(B, N1, N2, D, ps, int(max_kv_len), P, L, k_kind, v_kind, kv_layout,
+                      QTYPE_BF16 if is_bf16 else QTYPE_E4M3, q_stride, sparse)
     if workspace is None:
         if dev < 0:
             raise ValueError("decode: tensors must be on a CUDA device")
         with torch.cuda.device(dev):
             nbytes = decode_workspace_size(dims)
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+        made.append(workspace)
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on q's device")
     if softmax_scale is None:
@@ -505,14 +515,16 @@ def decode(q, k_pages, v_pages, k_descale, v_descale, seqused_kv, block_table, m
            v_pages.data_ptr(), k_descale.data_ptr(), v_descale.data_ptr(), seqused_kv.data_ptr(),
            block_table.data_ptr(), _p(block_mask), _p(sparse_indices), _p(sparse_seq_len),
            softmax_scale, out.data_ptr(), _p(lse), workspace.data_ptr(), workspace.nbytes,
-           _p(dev_status)), dev, stream, "bsa_fp8_decode")
+           _p(dev_status)), dev, stream, "bsa_fp8_decode", made)
     return out, lse
 
 
-def _gather_rows(name, t, dtype, shape, pages):
+def _gather_rows(name, t, dtype, shape, pages, made):
     if t is None:
-        return _torch_names()[0].empty(shape, dtype=dtype, device=pages.device)
-    _check(name, t, dtype, shape, pages.get_device())
+        t = _torch_names()[0].empty(shape, dtype=dtype, device=pages.device)
+        made.append(t)
+    else:
+        _check(name, t, dtype, shape, pages.get_device())
     return t
 
 
@@ -548,6 +560,7 @@ def gather_kv(k_pages, v_pages, k_descale, v_descale, cu_seqlens, block_table, t
     total = int(total)
     k_kind = v_kind = SCALE_PER_TENSOR
     shape = (total, N2, D)
+    made = []
     if k_pages is not None:
         k_kind = k_scale_kind if k_scale_kind is not None else (
             SCALE_PER_TOKEN_HEAD if k_descale.dim() == 3 else SCALE_PER_TENSOR)
@@ -555,7 +568,7 @@ def gather_kv(k_pages, v_pages, k_descale, v_descale, cu_seqlens, block_table, t
                dev)
         _check("k_descale", k_descale, f32,
                (P, N2, ps) if k_kind == SCALE_PER_TOKEN_HEAD else (1,), dev)
-        k_out = _gather_rows("k_out", k_out, out_dtype, shape, pages)
+        k_out = _gather_rows("k_out", k_out, out_dtype, shape, pages, made)
     elif k_out is not None:
         raise ValueError("k_out given without k_pages")
     if v_pages is not None:
@@ -564,7 +577,7 @@ def gather_kv(k_pages, v_pages, k_descale, v_descale, cu_seqlens, block_table, t
         _check("v_pages", v_pages, v_pages.dtype if v_pages.dtype in codes else codes, pages.shape,
                dev)
         _check("v_descale", v_descale, f32, (N2,) if v_kind == SCALE_PER_HEAD else (1,), dev)
-        v_out = _gather_rows("v_out", v_out, out_dtype, shape, pages)
+        v_out = _gather_rows("v_out", v_out, out_dtype, shape, pages, made)
     elif v_out is not None:
         raise ValueError("v_out given without v_pages")
     # in the order of GatherDims' fields
@@ -573,7 +586,7 @@ def gather_kv(k_pages, v_pages, k_descale, v_descale, cu_seqlens, block_table, t
     _call(lib().bsa_fp8_gather_kv,
           (ctypes.byref(dims), _p(k_pages), _p(v_pages), _p(k_descale), _p(v_descale),
            cu_seqlens.data_ptr(), _p(cache_starts), block_table.data_ptr(), _p(k_out), _p(v_out),
-           _p(dev_status)), dev, stream, "bsa_fp8_gather_kv")
+           _p(dev_status)), dev, stream, "bsa_fp8_gather_kv", made)
     return k_out, v_out
 
 
@@ -596,16 +609,19 @@ def merge_states(outs, lses, out=None, lse=None, return_lse: bool = True, stream
         _check("outs", o, bf16, shape, dev)
     for x in lses:
         _check("lses", x, f32, (N1, T), dev)
+    made = []
     if out is None:
         out = torch.empty(shape, dtype=torch.bfloat16, device=first.device)
+        made.append(out)
     else:
         _check("out", out, bf16, shape, dev)
     if lse is not None:
         _check("lse", lse, f32, (N1, T), dev)
     elif return_lse:
         lse = torch.empty((N1, T), dtype=torch.float32, device=first.device)
+        made.append(lse)
     ptrs = ctypes.c_void_p * n
     _call(lib().bsa_fp8_merge_states,
           (n, ptrs(*[o.data_ptr() for o in outs]), ptrs(*[x.data_ptr() for x in lses]), T, N1,
-           out.data_ptr(), _p(lse)), dev, stream, "bsa_fp8_merge_states")
+           out.data_ptr(), _p(lse)), dev, stream, "bsa_fp8_merge_states", made)
     return out, lse

@@ -90,9 +90,10 @@ __device__ __forceinline__ void report(const Params &p, int bits) {
   if (p.dev_status) atomicOr(p.dev_status, bits);
 }
 
-// Tokens of sequence b; a bad length counts as none.
+// Tokens of sequence b; a bad length counts as none.  Read past L1: the join looks before it has
+// waited for the kernel that it joins.
 __device__ __forceinline__ int seq_len(const Params &p, int b) {
-  const int kv = p.seqused_kv[b];
+  const int kv = __ldcg(p.seqused_kv + b);
   if (kv >= 0 && kv <= p.max_kv_len) return kv;  // max_kv_len <= L * ps is checked on the host
   report(p, BSA_DEV_BAD_SEQLEN);
   return 0;
@@ -109,11 +110,20 @@ __device__ __forceinline__ void pdl_wait() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
-// Waits for a phase of a barrier, at most limit_ns; false when that runs out.
+// The first probe of a barrier: the thread is suspended, up to the limit, while the phase is
+// incomplete.  A suspension outlasts a limit of some microseconds, so such a one is polled for.
+__device__ __forceinline__ bool wait_first(uint64_t *bar, uint32_t parity,
+                                           unsigned long long limit_ns) {
+  if (limit_ns < 20000) return ptx::mbar_test_wait(bar, parity);
+  return ptx::mbar_try_wait_hint(bar, parity,
+                                 (uint32_t)min(limit_ns, (unsigned long long)WAIT_LIMIT_NS));
+}
+
+// Polls for a phase that the first probe did not see complete, at most limit_ns; false when that
+// runs out.
 __device__ __noinline__ bool wait_more(uint64_t *bar, uint32_t parity, unsigned long long limit_ns) {
   const unsigned long long t0 = ptx::globaltimer_ns();
-  const uint32_t hint = (uint32_t)min(limit_ns, (unsigned long long)WAIT_LIMIT_NS);
-  while (!ptx::mbar_try_wait_hint(bar, parity, hint))
+  while (!ptx::mbar_test_wait(bar, parity))
     if (ptx::globaltimer_ns() - t0 > limit_ns) return false;
   return true;
 }
@@ -759,7 +769,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
     if (left > 0) {
       uint64_t *bar = &s_full[warp][stage];
       const uint32_t parity = (phases >> stage) & 1u;
-      bool ok = __all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity));
+      bool ok = __all_sync(0xffffffffu, wait_first(bar, parity, p.wait_limit_ns));
       if (!ok) ok = __all_sync(0xffffffffu, wait_more(bar, parity, p.wait_limit_ns));
       if (!ok) {
         // out of time: report, see the copies in flight land (with the default limit), leave

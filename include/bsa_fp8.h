@@ -435,8 +435,8 @@ bsa_status_t bsa_fp8_gather_kv(const bsa_fp8_gather_dims_t *dims, const void *k_
 bsa_status_t bsa_fp8_merge_states(int count, const void *const *outs, const float *const *lses,
                                   int T, int N1, void *out_bf16, float *lse_f32, void *stream);
 
-/* Sets the limit of every bounded wait inside the prefill kernel for launches that follow, in
- * nanoseconds, for the whole process; 0 restores the default of 2 s.  A wait that runs out
+/* Sets the limit of every bounded wait inside the prefill and decode kernels for launches that
+ * follow, in nanoseconds, for the whole process; 0 restores the default of 2 s.  A wait that runs out
  * sets BSA_DEV_TIMEOUT in *dev_status, every role of the CTA stops, waits (with the default
  * limit) for the copies and tensor-core operations it has issued, frees its tensor memory and
  * exits; the results of that launch are then undefined, the CUDA context stays usable.  A

@@ -71,6 +71,8 @@ DENSE = [
     ([640, 5, 1290], 32, 2, 64, True, False, True, False),
     ([77], 48, 3, 32, False, True, True, True),
     ([2048], 5, 5, 64, False, True, True, False),
+    ([512, 3, 400], 10, 2, 32, False, True, True, False),
+    ([200] * 80, 8, 4, 64, True, True, True, False),
     ([9001, 130], 10, 2, 32, False, True, True, False),
     ([20000], 16, 1, 64, True, True, True, True),
 ]
@@ -117,23 +119,24 @@ def test_decode_sparse(form, lens, N1, N2, keep):
 
 
 @pytest.mark.parametrize("form", ["mask", "index"])
-def test_decode_nan_in_a_tile_one_head_masks(form):
-    """Heads 0 and 2 mask a tile that holds NaN in K and V; heads 1 and 3 of the same KV head
-    read it and get NaN, the first two are untouched by it."""
+@pytest.mark.parametrize("N1", [4, 12])
+def test_decode_nan_in_a_tile_one_head_masks(N1, form):
+    """Every other head masks a tile that holds NaN in K and V; the others of the same KV head read
+    it and get NaN, the first are untouched by it."""
     cache = S.Cache(4, [500], 1, 32)
-    q, qd, q64 = S.queries(5, 1, 4, False)
-    on = np.ones((1, 4, 4), dtype=bool)
-    on[0, 0, 1] = on[0, 2, 1] = False
+    q, qd, q64 = S.queries(5, 1, N1, False)
+    keep, hit = list(range(0, N1, 2)), list(range(1, N1, 2))
+    on = np.ones((1, N1, 4), dtype=bool)
+    on[0, keep, 1] = False
     d = cache.device()
     pg = int(cache.table[0, 5])                          # tokens 160 .. 191 lie in tile 1
     d["k_pages"][pg, 0, 3] = 0x7f
     d["v_pages"][pg, 0, 4] = 0xff
     out, lse = _decode(cache, q, qd, on, form, dev=d)
     O, Z, E, F = S.reference(cache, q64, on)
-    keep = [0, 2]
     S.within(out[:, keep], O[:, keep], E[:, keep], "masking heads O")
     S.within(lse[keep], Z[keep], F[keep], "masking heads LSE")
-    assert torch.isnan(out[:, [1, 3]].float()).all()
+    assert torch.isnan(out[:, hit].float()).all()
 
 
 @pytest.mark.parametrize("scale", [0.0, -0.3, 4.0])
@@ -325,6 +328,99 @@ def test_decode_on_two_streams_at_once():
     torch.cuda.synchronize()
     for (cache, _, _, q64, _), g in zip(jobs, got):
         _compare(cache, q64, g, what="two streams")
+
+
+def test_decode_and_merge_on_a_given_stream():
+    """stream= names the stream; what the call allocates itself stays its own until that stream is
+    through with it."""
+    import block_sparse_fp8_gb300 as bsa
+
+    cache = S.Cache(65, [9000, 3000], 2, 64)
+    q, _, q64 = S.queries(66, 2, 8, False)
+    d, q = cache.device(), q.cuda()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)                    # the call waits behind this
+    got = bsa.decode(q, d["k_pages"], d["v_pages"], d["k_descale"], d["v_descale"],
+                     d["seqused_kv"], d["block_table"], 9000, stream=side, **d["kinds"])
+    both = bsa.merge_states([got[0]], [got[1]], stream=side)
+    for _ in range(8):                                   # would take a freed workspace's place
+        torch.full((4 << 20,), float("nan"), device="cuda")
+    side.synchronize()
+    _compare(cache, q64, got, what="given stream")
+    _compare(cache, q64, both, what="merge of one")
+
+
+def test_decode_first_call_inside_a_capture():
+    """A fresh process whose first call of the library is captured into a graph."""
+    import os
+    import subprocess
+    import sys
+
+    code = """
+import numpy as np, torch
+import serving_helpers as S
+import block_sparse_fp8_gb300 as bsa
+cache = S.Cache(75, [3000, 200], 2, 32)
+d = cache.device()
+q, _, q64 = S.queries(76, 2, 8, False)
+q = q.cuda()
+out = torch.empty(2, 8, 128, dtype=torch.bfloat16, device="cuda")
+lse = torch.empty(8, 2, device="cuda")
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    bsa.decode(q, d["k_pages"], d["v_pages"], d["k_descale"], d["v_descale"], d["seqused_kv"],
+               d["block_table"], 3000, out=out, lse=lse, **d["kinds"])
+g.replay()
+torch.cuda.synchronize()
+O, Z, E, F = S.reference(cache, q64)
+S.within(out, O, E, "O")
+S.within(lse, Z, F, "LSE")
+print("captured first")
+"""
+    here = os.path.dirname(os.path.abspath(__file__))
+    env = dict(os.environ, PYTHONPATH=os.pathsep.join([os.path.dirname(here), here]))
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, env=env,
+                       timeout=300)
+    assert r.returncode == 0 and "captured first" in r.stdout, r.stderr[-2000:]
+
+
+def test_decode_watchdog():
+    """A batch that waits for memory (537 MB).  With a limit below those waits its launches stop
+    early and say so; the launch after them, at the default limit, gives the bits of the one
+    before them."""
+    import block_sparse_fp8_gb300 as bsa
+
+    g = torch.Generator(device="cuda").manual_seed(1)
+    B, N1, N2, ps, n = 64, 32, 8, 64, 4096
+    P = B * n // ps
+    kp, vp = (torch.randint(0, 0x78, (P, N2, ps, 128), dtype=torch.uint8, device="cuda",
+                            generator=g) for _ in range(2))
+    kd = torch.rand(P, N2, ps, device="cuda", generator=g) * 0.01
+    vd = torch.full((N2,), 0.01, device="cuda")
+    used = torch.full((B,), n, dtype=torch.int32, device="cuda")
+    table = torch.randperm(P, device="cuda", generator=g).int().view(B, -1)
+    q = torch.randn(B, N1, 128, device="cuda", generator=g).bfloat16()
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    call = lambda: bsa.decode(q, kp, vp, kd, vd, used, table, n, dev_status=st)
+    before = call()
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0 and torch.isfinite(before[0].float()).all()
+    try:
+        bsa.set_wait_limit_ns(1)
+        for _ in range(3):
+            st.zero_()
+            call()
+            torch.cuda.synchronize()
+            assert int(st.item()) == bsa.DEV_TIMEOUT
+    finally:
+        bsa.set_wait_limit_ns(0)
+    st.zero_()
+    after = call()
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0
+    assert torch.equal(after[0], before[0]) and torch.equal(after[1], before[1])
 
 
 def test_decode_is_deterministic():
