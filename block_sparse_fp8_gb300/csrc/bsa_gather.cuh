@@ -5,8 +5,13 @@
 // takes a run of tokens.  Its first threads look the tokens up -- the sequence by binary search over
 // cu_seqlens, then the block table -- and leave page and slot in shared memory, so that the
 // dependent reads are paid once a token and not once a row.  Then a row of 128 values belongs to
-// 16 lanes (bf16) or 32 (fp32), each of which turns 8 or 4 codes into one 16-byte store; a thread has
-// the K and V codes of ROWS rows in flight.
+// 16 lanes, each of which turns 8 codes into one 16-byte store (bf16: 8 neighbours) or two (fp32: 4
+// neighbours of each half, so that either store covers 256 bytes in a row); a thread has the K and
+// V codes of ROWS rows in flight.
+//
+// Measured (mean of back-to-back calls): 4 x 64K tokens x 8 heads to bf16 (1619 MB) 244 us, 6.63
+// TB/s, 98% of the measured copy rate (two rows in flight: 247; one block a row, the first form: 1044);
+// 22K tokens x 8 heads to fp32 (224 MB) 35 us, 94%.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -55,37 +60,34 @@ __device__ __forceinline__ uint32_t bf16x2(float a, float b) {
   return r;
 }
 
+constexpr int LANES = 16;                // of a row
+constexpr int STEP = THREADS / LANES;    // rows of a block's pass
+
+// Lane li's 8 codes of the row at p.
 template <bool F32>
-struct Codes;  // a thread's share of a row
-template <>
-struct Codes<false> {
-  uint2 c;
-  __device__ __forceinline__ void load(const uint8_t *p) { c = *reinterpret_cast<const uint2 *>(p); }
-  __device__ __forceinline__ void zero() { c = make_uint2(0, 0); }
-  __device__ __forceinline__ uint4 scaled(float s) const {
-    const float2 a = values2(c.x), b = values2(c.x >> 16), d = values2(c.y), e = values2(c.y >> 16);
-    return make_uint4(bf16x2(a.x * s, a.y * s), bf16x2(b.x * s, b.y * s), bf16x2(d.x * s, d.y * s),
-                      bf16x2(e.x * s, e.y * s));
+__device__ __forceinline__ uint2 load_codes(const uint8_t *p, int li) {
+  if (!F32) return reinterpret_cast<const uint2 *>(p)[li];
+  return make_uint2(reinterpret_cast<const uint32_t *>(p)[li],
+                    reinterpret_cast<const uint32_t *>(p)[li + 16]);
+}
+
+// ... and their values, into the row at out.
+template <bool F32>
+__device__ __forceinline__ void store_values(void *out, size_t row, int li, uint2 c, float s) {
+  const float2 a = values2(c.x), b = values2(c.x >> 16), d = values2(c.y), e = values2(c.y >> 16);
+  if (F32) {
+    float4 *o = static_cast<float4 *>(out) + row * (HEAD_DIM / 4) + li;
+    __stcs(o, make_float4(a.x * s, a.y * s, b.x * s, b.y * s));
+    __stcs(o + 16, make_float4(d.x * s, d.y * s, e.x * s, e.y * s));
+  } else {
+    __stcs(static_cast<uint4 *>(out) + row * (HEAD_DIM / 8) + li,
+           make_uint4(bf16x2(a.x * s, a.y * s), bf16x2(b.x * s, b.y * s),
+                      bf16x2(d.x * s, d.y * s), bf16x2(e.x * s, e.y * s)));
   }
-};
-template <>
-struct Codes<true> {
-  uint32_t c;
-  __device__ __forceinline__ void load(const uint8_t *p) {
-    c = *reinterpret_cast<const uint32_t *>(p);
-  }
-  __device__ __forceinline__ void zero() { c = 0; }
-  __device__ __forceinline__ uint4 scaled(float s) const {
-    const float2 a = values2(c), b = values2(c >> 16);
-    return make_uint4(__float_as_uint(a.x * s), __float_as_uint(a.y * s), __float_as_uint(b.x * s),
-                      __float_as_uint(b.y * s));
-  }
-};
+}
 
 template <bool F32>
 __global__ void __launch_bounds__(THREADS) gather_kernel(const Params p) {
-  constexpr int LANES = F32 ? 32 : 16;  // of a row
-  constexpr int STEP = THREADS / LANES;
   __shared__ int s_page[MAX_TOKENS], s_slot[MAX_TOKENS];
   const int tid = threadIdx.x, t0 = blockIdx.x * p.tokens;
   if (tid < p.tokens) {
@@ -111,45 +113,49 @@ __global__ void __launch_bounds__(THREADS) gather_kernel(const Params p) {
     s_slot[tid] = slot;
   }
   __syncthreads();
-  const int li = tid % LANES, rows = p.tokens * p.N2;
-  for (int r0 = tid / LANES; r0 < rows; r0 += STEP * ROWS) {
-    Codes<F32> k[ROWS], v[ROWS];
+  // The block's rows (token, head), token-major: a thread's next row lies STEP rows on.
+  const int li = tid % LANES, dt = STEP / p.N2, dg = STEP % p.N2;
+  const float k_all = p.k_per_token || !p.k_out ? 0.f : p.k_descale[0];
+  const float v_all = p.v_per_head || !p.v_out ? 0.f : p.v_descale[0];
+  int t = tid / LANES / p.N2, g = tid / LANES - t * p.N2;
+  while (t < p.tokens) {
+    uint2 k[ROWS], v[ROWS];
     float ks[ROWS], vs[ROWS];
     int page[ROWS];
-    size_t at[ROWS];
+    size_t row[ROWS];
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
-      const int r = r0 + i * STEP, t = r / p.N2, g = r - t * p.N2;
-      page[i] = r < rows ? s_page[t] : -2;
-      at[i] = ((size_t)(t0 + t) * p.N2 + g) * HEAD_DIM + li * (HEAD_DIM / LANES);
-      k[i].zero();
-      v[i].zero();
-      ks[i] = vs[i] = 0.f;
+      page[i] = t < p.tokens ? s_page[t] : -2;
+      row[i] = (size_t)(t0 + t) * p.N2 + g;
+      k[i] = v[i] = make_uint2(0, 0);
+      ks[i] = k_all;
+      vs[i] = v_all;
       if (page[i] >= 0) {
         const int slot = s_slot[t];
-        const long long off = page[i] * p.page_bytes + g * p.head_bytes + slot * p.slot_bytes +
-                              li * (HEAD_DIM / LANES);
+        const long long off = page[i] * p.page_bytes + g * p.head_bytes + slot * p.slot_bytes;
         if (p.k_out) {
-          k[i].load(p.k_pages + off);
-          ks[i] = p.k_per_token ? p.k_descale[((size_t)page[i] * p.N2 + g) * p.ps + slot]
-                                : p.k_descale[0];
+          k[i] = load_codes<F32>(p.k_pages + off, li);
+          if (p.k_per_token) ks[i] = p.k_descale[((size_t)page[i] * p.N2 + g) * p.ps + slot];
         }
         if (p.v_out) {
-          v[i].load(p.v_pages + off);
-          vs[i] = p.v_per_head ? p.v_descale[g] : p.v_descale[0];
+          v[i] = load_codes<F32>(p.v_pages + off, li);
+          if (p.v_per_head) vs[i] = p.v_descale[g];
         }
+      }
+      t += dt;
+      g += dg;
+      if (g >= p.N2) {
+        g -= p.N2;
+        ++t;
       }
     }
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
       if (page[i] == -2) continue;
-      constexpr int SIZE = F32 ? 4 : 2;
-      if (p.k_out)
-        __stcs(reinterpret_cast<uint4 *>(static_cast<uint8_t *>(p.k_out) + at[i] * SIZE),
-               k[i].scaled(ks[i]));
-      if (p.v_out)
-        __stcs(reinterpret_cast<uint4 *>(static_cast<uint8_t *>(p.v_out) + at[i] * SIZE),
-               v[i].scaled(vs[i]));
+      // a missing page's codes are zero: so are its values, whatever the descale
+      const bool none = page[i] < 0;
+      if (p.k_out) store_values<F32>(p.k_out, row[i], li, k[i], none ? 0.f : ks[i]);
+      if (p.v_out) store_values<F32>(p.v_out, row[i], li, v[i], none ? 0.f : vs[i]);
     }
   }
 }

@@ -7,6 +7,10 @@
 // lanes to a row stream the parts, a thread's 16 bytes of every part of two rows in flight at once.
 // out may be one of the parts and lse one of their LSEs: whoever writes an element has read all of
 // its sources before.
+//
+// Measured (mean of back-to-back calls): five parts of 16K tokens x 64 heads (1636 MB) 254 us, 6.45
+// TB/s, 95% of the measured copy rate (one block a row, the first form: 1232); two of 8K x 32
+// (204 MB) 34 us, 89%, the rest launch and ramp.
 #pragma once
 
 #include <cuda_bf16.h>
