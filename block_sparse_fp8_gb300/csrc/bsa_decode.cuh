@@ -137,6 +137,9 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
   return v;
 }
 
+__device__ __forceinline__ void prefetch_l2(const void *a) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(a));
+}
 __device__ __forceinline__ void prefetch_l1(const void *a) {
   asm volatile("prefetch.global.L1 [%0];" ::"l"(a));
 }
@@ -200,13 +203,16 @@ __device__ __forceinline__ void add_part(float &m, float &l, float4 &o, float2 m
 
 // ------------------------------------------------------------------------------------------
 // Tile lists of the sparse forms: one CTA per (sequence, KV head) forms the union of its query
-// heads' tiles below the sequence's end, each with a mask of the heads that enable it.
+// heads' tiles below the sequence's end, each with a mask of the heads that enable it.  Nothing but
+// latency: the lengths, a mask's bytes of all heads and the first entries of all lists are read at
+// once (what lies past the end is in the row all the same, and dropped after the length is known).
 // ------------------------------------------------------------------------------------------
 constexpr int PLAN_WARPS = 16;  // a warp per query head of the group
 constexpr int PLAN_THREADS = PLAN_WARPS * 32;
 constexpr int PLAN_AHEAD = 8;   // list entries in flight per lane
 
-__global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const Params p) {
+template <bool MASK>  // block_mask, or sparse_indices
+__global__ void __launch_bounds__(PLAN_THREADS, 2) plan_kernel(const Params p) {
   extern __shared__ uint32_t heads[];  // [Kb]
   __shared__ int warp_n[PLAN_WARPS];
   pdl_wait();
@@ -214,28 +220,38 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const Params p) {
   const int task = blockIdx.x, b = task / p.N2, kvh = task % p.N2;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const size_t first = (size_t)b * p.N1 + (size_t)kvh * p.G;  // the group's first (b, h)
-  int len = p.sparse_indices && warp < p.G ? p.sparse_seq_len[first + warp] : 0;
-  const int kend = (seq_len(p, b) + TILE - 1) / TILE;
-  for (int t = tid; t < kend; t += PLAN_THREADS) {
+  const bool lists = !MASK && warp < p.G;
+  const int *row = p.sparse_indices + (first + warp) * p.Kb;
+  int len = lists ? p.sparse_seq_len[first + warp] : 0;
+  const int kv = seq_len(p, b);
+  int t[PLAN_AHEAD];
+#pragma unroll
+  for (int u = 0; u < PLAN_AHEAD; ++u)
+    t[u] = lists && lane + 32 * u < p.Kb ? row[lane + 32 * u] : 0;
+  for (int i = tid; i < p.Kb; i += PLAN_THREADS) {
     uint32_t on = 0;
-    if (p.block_mask) {
-#pragma unroll 4
-      for (int g = 0; g < p.G; ++g)
-        on |= p.block_mask[(first + g) * p.Kb + t] != 0 ? 1u << g : 0u;
+    if (MASK) {
+      const uint8_t *col = p.block_mask + first * p.Kb + i;
+      uint8_t byte[MAX_G];
+#pragma unroll
+      for (int g = 0; g < MAX_G; ++g) byte[g] = g < p.G ? col[g * p.Kb] : 0;  // below 2^16 bytes
+#pragma unroll
+      for (int g = 0; g < MAX_G; ++g) on |= byte[g] != 0 ? 1u << g : 0u;
     }
-    heads[t] = on;
+    heads[i] = on;
   }
+  const int kend = (kv + TILE - 1) / TILE;
   __syncthreads();
-  if (p.sparse_indices) {
+  if (!MASK) {
     if (len < 0 || len > p.Kb) {
       if (lane == 0) report(p, BSA_DEV_BAD_INDEX);
       len = len < 0 ? 0 : p.Kb;
     }
-    const int *list = p.sparse_indices + (first + warp) * p.Kb;
     for (int e0 = lane; e0 < len; e0 += 32 * PLAN_AHEAD) {
-      int t[PLAN_AHEAD];
+      if (e0 >= 32 * PLAN_AHEAD) {
 #pragma unroll
-      for (int u = 0; u < PLAN_AHEAD; ++u) t[u] = e0 + 32 * u < len ? list[e0 + 32 * u] : kend;
+        for (int u = 0; u < PLAN_AHEAD; ++u) t[u] = e0 + 32 * u < len ? row[e0 + 32 * u] : 0;
+      }
 #pragma unroll
       for (int u = 0; u < PLAN_AHEAD; ++u) {
         if (e0 + 32 * u >= len) continue;
@@ -399,6 +415,14 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
     }
   }
   __syncwarp();
+  if (SPARSE) {
+    // while the lists are being made: the queries and the block table into L2, a line a thread
+    const size_t line = ((size_t)blockIdx.x * THREADS + tid) * 128;
+    if (line < (size_t)p.B * p.q_stride * (p.q_e4m3 ? 1 : 2))
+      prefetch_l2(static_cast<const uint8_t *>(p.q) + line);
+    if (line < (size_t)p.B * p.L * 4)
+      prefetch_l2(reinterpret_cast<const uint8_t *>(p.block_table) + line);
+  }
   pdl_wait();               // what the stream ran before: the tile lists among it
   pdl_launch_dependents();  // the join, which reads the lengths and counts as well: only now
 

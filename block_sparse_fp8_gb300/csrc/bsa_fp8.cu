@@ -917,7 +917,9 @@ extern "C" bsa_status_t bsa_fp8_decode(const bsa_fp8_decode_dims_t *d, const voi
       return BSA_ERR_CUDA;
   }
   const bool lists = d->sparse && !none;
-  if (lists && !launch_dependent(decode::plan_kernel, dim3((unsigned)(d->B * d->N2)),
+  if (lists && !launch_dependent(block_mask ? decode::plan_kernel<true>
+                                            : decode::plan_kernel<false>,
+                                 dim3((unsigned)(d->B * d->N2)),
                                  decode::PLAN_THREADS, (size_t)p.Kb * sizeof(uint32_t), stream, p))
     return BSA_ERR_CUDA;
   const auto kernel = lists ? (wide ? decode::decode_kernel<2, true> : decode::decode_kernel<1, true>)
