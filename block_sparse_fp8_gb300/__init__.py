@@ -386,7 +386,7 @@ def _call(fn, args, dev, stream, what, made=()):
         raise ValueError(f"{what}: the stream is on {stream.device}, the tensors on cuda:{dev}")
     else:
         handle = stream.cuda_stream
-    if torch.cuda.current_device() == dev:
+    if torch._C._cuda_getDevice() == dev:
         st = fn(*args, handle)
     else:
         with torch.cuda.device(dev):
@@ -406,9 +406,10 @@ def _check_status(dev_status, dev):
 
 def _pool(pages, kv_layout):
     """(pages, KV heads, page size, head dim) of a page pool."""
-    if pages.dim() != 4:
-        raise ValueError(f"pages have shape {tuple(pages.shape)}, expected four dimensions")
-    P, a, b, D = pages.shape
+    shape = pages.shape
+    if len(shape) != 4:
+        raise ValueError(f"pages have shape {tuple(shape)}, expected four dimensions")
+    P, a, b, D = shape
     return (P, b, a, D) if kv_layout == KV_NHD else (P, a, b, D)
 
 
@@ -444,17 +445,25 @@ def decode(q, k_pages, v_pages, k_descale, v_descale, seqused_kv, block_table, m
     must not be shared by calls in flight at once."""
     torch, bf16, f32, i32, codes = _torch_names()
     dev = q.get_device()
-    if q.dim() != 3:
-        raise ValueError(f"q has shape {tuple(q.shape)}, expected [B, N1, 128]")
-    B, N1, D = q.shape
+    shape = q.shape
+    if len(shape) != 3:
+        raise ValueError(f"q has shape {tuple(shape)}, expected [B, N1, 128]")
+    B, N1, D = shape
     is_bf16 = q.dtype is bf16
     if not is_bf16 and q.dtype not in codes:
         raise ValueError(f"q has dtype {q.dtype}, expected bf16 or e4m3 codes")
-    if not q.is_contiguous() and (q.stride(2) != 1 or (N1 > 1 and q.stride(1) != D)):
-        raise ValueError("q must be contiguous within a sequence's row")
+    q_stride = N1 * D
+    if not q.is_contiguous():
+        if q.stride(2) != 1 or (N1 > 1 and q.stride(1) != D):
+            raise ValueError("q must be contiguous within a sequence's row")
+        if B > 1:
+            q_stride = q.stride(0)
+            if q_stride >= 1 << 31:
+                raise ValueError(f"q's rows lie {q_stride} elements apart: 2^31 - 1 at most")
     P, N2, ps, _ = _pool(k_pages, kv_layout)
-    if block_table.dim() != 2:
-        raise ValueError(f"block_table has shape {tuple(block_table.shape)}, expected [B, L]")
+    table = block_table.shape
+    if len(table) != 2:
+        raise ValueError(f"block_table has shape {tuple(table)}, expected [B, L]")
     k_kind = k_scale_kind if k_scale_kind is not None else (
         SCALE_PER_TOKEN_HEAD if k_descale.dim() == 3 else SCALE_PER_TENSOR)
     v_kind = v_scale_kind if v_scale_kind is not None else (
@@ -466,7 +475,7 @@ def decode(q, k_pages, v_pages, k_descale, v_descale, seqused_kv, block_table, m
            (P, N2, ps) if k_kind == SCALE_PER_TOKEN_HEAD else (1,), dev)
     _check("v_descale", v_descale, f32, (N2,) if v_kind == SCALE_PER_HEAD else (1,), dev)
     _check("seqused_kv", seqused_kv, i32, (B,), dev)
-    L = block_table.shape[1]
+    L = table[1]
     _check("block_table", block_table, i32, (B, L), dev)
     if q_descale is not None:
         _check("q_descale", q_descale, f32, (B, N1), dev)
@@ -485,7 +494,7 @@ def decode(q, k_pages, v_pages, k_descale, v_descale, seqused_kv, block_table, m
         out = torch.empty((B, N1, D), dtype=torch.bfloat16, device=q.device)
         made.append(out)
     else:
-        _check("out", out, bf16, (B, N1, D), dev)
+        _check("out", out, bf16, shape, dev)
     if lse is not None:
         _check("lse", lse, f32, (N1, B), dev)
     elif return_lse:
@@ -494,9 +503,6 @@ def decode(q, k_pages, v_pages, k_descale, v_descale, seqused_kv, block_table, m
     if dev_status is not None:
         _check_status(dev_status, dev)
     # in the order of DecodeDims' fields, as make_decode_dims
-    q_stride = q.stride(0) if B > 1 else N1 * D
-    if q_stride >= 1 << 31:
-        raise ValueError(f"q's rows lie {q_stride} elements apart: 2^31 - 1 at most")
     dims = DecodeDims(B, N1, N2, D, ps, int(max_kv_len), P, L, k_kind, v_kind, kv_layout,
                       QTYPE_BF16 if is_bf16 else QTYPE_E4M3, q_stride, sparse)
     if workspace is None:

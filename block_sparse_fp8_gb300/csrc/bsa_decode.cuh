@@ -418,8 +418,8 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
   if (SPARSE) {
     // while the lists are being made: the queries and the block table into L2, a line a thread
     const size_t line = ((size_t)blockIdx.x * THREADS + tid) * 128;
-    if (line < (size_t)p.B * p.q_stride * (p.q_e4m3 ? 1 : 2))
-      prefetch_l2(static_cast<const uint8_t *>(p.q) + line);
+    const size_t q_end = (size_t)(p.B - 1) * p.q_stride + (size_t)p.N1 * HEAD_DIM;  // elements
+    if (line < q_end * (p.q_e4m3 ? 1 : 2)) prefetch_l2(static_cast<const uint8_t *>(p.q) + line);
     if (line < (size_t)p.B * p.L * 4)
       prefetch_l2(reinterpret_cast<const uint8_t *>(p.block_table) + line);
   }
