@@ -460,7 +460,9 @@ def decode(q, k_pages, v_pages, k_descale, v_descale, seqused_kv, block_table, m
             q_stride = q.stride(0)
             if q_stride >= 1 << 31:
                 raise ValueError(f"q's rows lie {q_stride} elements apart: 2^31 - 1 at most")
-    P, N2, ps, _ = _pool(k_pages, kv_layout)
+    P, N2, ps, pool_d = _pool(k_pages, kv_layout)
+    if pool_d != D:
+        raise ValueError(f"k_pages has shape {tuple(k_pages.shape)}, q a head dim of {D}")
     table = block_table.shape
     if len(table) != 2:
         raise ValueError(f"block_table has shape {tuple(table)}, expected [B, L]")
@@ -520,7 +522,7 @@ def decode(q, k_pages, v_pages, k_descale, v_descale, seqused_kv, block_table, m
           (ctypes.byref(dims), q.data_ptr(), _p(q_descale), k_pages.data_ptr(),
            v_pages.data_ptr(), k_descale.data_ptr(), v_descale.data_ptr(), seqused_kv.data_ptr(),
            block_table.data_ptr(), _p(block_mask), _p(sparse_indices), _p(sparse_seq_len),
-           softmax_scale, out.data_ptr(), _p(lse), workspace.data_ptr(), workspace.nbytes,
+           float(softmax_scale), out.data_ptr(), _p(lse), workspace.data_ptr(), workspace.nbytes,
            _p(dev_status)), dev, stream, "bsa_fp8_decode", made)
     return out, lse
 

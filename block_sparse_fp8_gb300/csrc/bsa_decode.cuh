@@ -283,6 +283,13 @@ __global__ void __launch_bounds__(PLAN_THREADS, 2) plan_kernel(const Params p) {
   if (tid == 0) p.counts[task] = n;
 }
 
+// Tiles that task's list holds (one for an empty list, as above).  Bounded by the list's room, as the
+// walks below are by the batch: lengths that someone changes under a running call spoil its
+// results, but lead it nowhere outside its tensors.
+__device__ __forceinline__ int listed_tiles(const Params &p, int task) {
+  return min(max(__ldcg(p.counts + task), 1), p.Kb);
+}
+
 // The batch's tiles, in task order, cut into even runs for `grid` CTAs (as many runs as there are
 // tiles, if those are fewer).
 struct Cut {
@@ -306,7 +313,7 @@ constexpr int MAX_WARPS = 8;
 
 template <bool SPARSE>
 __device__ __forceinline__ int item_tiles(const Params &p, int i) {
-  return SPARSE ? max(__ldcg(p.counts + i), 1) : p.N2 * dense_tiles(seq_len(p, i));
+  return SPARSE ? listed_tiles(p, i) : p.N2 * dense_tiles(seq_len(p, i));
 }
 
 template <bool SPARSE, typename Want>
@@ -361,11 +368,7 @@ struct Cursor {
   int pos, heads, page;    // of the current tile: the warp's first token, heads, physical page
 
   __device__ __forceinline__ void enter(const Params &p) {  // a task's own numbers
-    if (SPARSE) {
-      n = max(p.counts[b * p.N2 + kvh], 1);
-    } else {
-      n = dense_tiles(kv);
-    }
+    n = SPARSE ? listed_tiles(p, b * p.N2 + kvh) : dense_tiles(kv);
   }
   // The current tile's entry and page (the page still unchecked; -1: nothing to read).
   __device__ __forceinline__ void look(const Params &p, int warp) {
@@ -385,7 +388,8 @@ struct Cursor {
       idx = 0;
       if (++kvh == p.N2) {
         kvh = 0;
-        kv = seq_len(p, ++b);
+        b = min(b + 1, p.B - 1);
+        kv = seq_len(p, b);
       }
       enter(p);
     }
@@ -451,8 +455,8 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
     cur.kv = seq_len(p, cur.b);
     if (SPARSE) cur.kvh = at.item % p.N2;
     cur.enter(p);
-    if (!SPARSE) cur.kvh = at.off / cur.n;
-    cur.idx = SPARSE ? at.off : at.off % cur.n;
+    if (!SPARSE) cur.kvh = min(at.off / cur.n, p.N2 - 1);
+    cur.idx = SPARSE ? min(at.off, cur.n - 1) : at.off % cur.n;
   }
   int b = cur.b, kvh = cur.kvh;      // the computing side's task
   bool from_start = cur.idx == 0;    // the segment begins its task
@@ -814,7 +818,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
       from_start = true;
       if (++kvh == p.N2) {
         kvh = 0;
-        ++b;
+        b = min(b + 1, p.B - 1);
       }
       fetch_q(b, kvh);
       convert_q();
@@ -853,11 +857,12 @@ __global__ void __launch_bounds__(MAX_WARPS * 32) join_kernel(const Params p, bo
     task = index;
     t0 = at.off + (SPARSE ? 0 : index % p.N2 * n);
   } else {
-    task = SPARSE ? at.item : at.item * p.N2 + at.off / n;
-    t0 = cut.begin(index + 1) - 1 - at.off % n;
+    task = SPARSE ? at.item : at.item * p.N2 + min(at.off / n, p.N2 - 1);
+    t0 = cut.begin(index + 1) - 1 - (SPARSE ? min(at.off, n - 1) : at.off % n);
   }
-  const int c = cut.of(t0), parts = cut.of(t0 + n - 1) - c + 1;
-  if (parts == 1 || (!by_task && c != index)) {  // not cut, or another block's
+  const int c = min(cut.of(t0), cut.runs - 1);
+  const int parts = min(cut.of(t0 + n - 1), cut.runs - 1) - c + 1;
+  if (parts <= 1 || (!by_task && c != index)) {  // not cut, or another block's
     // one block always waits, so that the join never ends before the kernel it belongs to
     if (index == 0 && blockIdx.y == 0) pdl_wait();
     return;

@@ -789,8 +789,10 @@ bsa_status_t enable_decode() {
   if (!enable((const void *)decode::decode_kernel<1, false>) ||
       !enable((const void *)decode::decode_kernel<2, false>) ||
       !enable((const void *)decode::decode_kernel<1, true>) ||
-      !enable((const void *)decode::decode_kernel<2, true>))
+      !enable((const void *)decode::decode_kernel<2, true>)) {
+    (void)cudaGetLastError();  // leave no pending error behind
     return BSA_ERR_CUDA;
+  }
   di.decode_attr = true;
   return BSA_OK;
 }
@@ -810,7 +812,9 @@ bool launch_dependent(void (*kernel)(Args...), dim3 grid, int threads, size_t sm
   cfg.stream = (cudaStream_t)stream;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess;
+  if (cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess) return true;
+  (void)cudaGetLastError();  // leave no pending error behind
+  return false;
 }
 
 }  // namespace

@@ -94,6 +94,63 @@ def test_decode_many_short_sequences():
     _compare(cache, q64, _decode(cache, q, qd), what="many")
 
 
+def test_decode_thousands_of_tokens_of_one():
+    """Far more sequences than CTAs: 5000 of one to three tokens."""
+    rng = np.random.default_rng(6)
+    lens = [int(x) for x in rng.integers(1, 4, 5000)]
+    cache = S.Cache(12, lens, 1, 32)
+    q, qd, q64 = S.queries(13, len(lens), 2, True)
+    _compare(cache, q64, _decode(cache, q, qd), what="thousands")
+
+
+@pytest.mark.parametrize("form", [None, "mask", "index"])
+def test_decode_longest_capacity(form):
+    """max_kv_len at the supported limit, as a graph for any length would be captured, over short
+    sequences and over one that fills it."""
+    cap = 4096 * 128
+    for lens in ([70, 0, 4000], [cap]):
+        cache = S.Cache(14, lens, 1, 64, spare_cols=0)
+        full = np.full((len(lens), cap // 64), 0x7fffffff, dtype=np.int32)
+        full[:, :cache.L] = cache.table
+        cache.table, cache.L = full, cap // 64
+        on = None
+        if form:
+            on = np.random.default_rng(2).random((len(lens), 3, 4096)) < 0.02
+        q, qd, q64 = S.queries(15, len(lens), 3, False)
+        _compare(cache, q64, _decode(cache, q, qd, on, form, max_kv_len=cap), on, str(lens))
+
+
+def test_decode_shared_pages():
+    """Two sequences whose tables name the same pages, one twice in a row."""
+    cache = S.Cache(16, [96, 96], 2, 32)
+    cache.table[1, 0] = cache.table[1, 2] = cache.table[0, 1]
+    for x in (cache.k, cache.v, cache.kd):
+        x[1] = x[1].copy()
+        x[1][:, :32] = x[1][:, 64:96] = x[0][:, 32:64]
+    q, qd, q64 = S.queries(17, 2, 4, False)
+    _compare(cache, q64, _decode(cache, q, qd), what="shared")
+
+
+def test_decode_refuses_a_small_workspace():
+    import block_sparse_fp8_gb300 as bsa
+
+    cache = S.Cache(18, [5000], 1, 32)
+    d = cache.device()
+    q = S.queries(19, 1, 8, False)[0].cuda()
+    dims = bsa.make_decode_dims(q, d["k_pages"], d["block_table"], 5000, 1, 2)
+    need = bsa.decode_workspace_size(dims)
+    for ws in (torch.empty(need - 1, dtype=torch.uint8, device="cuda"),
+               torch.empty(need + 64, dtype=torch.uint8, device="cuda")[64:]):
+        with pytest.raises(bsa.BsaError) as e:
+            _decode_call(bsa, cache, d, q, None, None, ws)
+        assert e.value.status == 4
+    with pytest.raises(ValueError, match="device"):
+        _decode_call(bsa, cache, dict(d, seqused_kv=d["seqused_kv"].cpu()), q, None, None, None)
+    with pytest.raises(bsa.BsaError):                    # bf16 queries take no q_descale
+        _decode_call(bsa, cache, d, q, None, None, None,
+                     q_descale=torch.ones(1, 8, device="cuda"))
+
+
 def test_decode_all_idle():
     cache = S.Cache(1, [0, 0, 0], 2, 64)
     q, qd, q64 = S.queries(2, 3, 6, False)
@@ -467,6 +524,21 @@ def test_gather_exact(lens, starts, N2, ps, k_tok, v_head, dtype, nhd):
         want = np.concatenate([p[which].transpose(1, 0, 2) for p in parts]).astype(np.float32)
         want = torch.from_numpy(want).to(dtype)
         assert torch.equal(got[:T].cpu(), want)
+
+
+def test_gather_fewer_rows_than_tokens():
+    """total below cu_seqlens[B]: the rows there are, and nothing behind them."""
+    import block_sparse_fp8_gb300 as bsa
+
+    cache = S.Cache(81, [50, 60], 2, 32)
+    d = cache.device()
+    cu = torch.tensor([0, 50, 110], dtype=torch.int32, device="cuda")
+    k = torch.full((90, 2, 128), 5.0, device="cuda")
+    bsa.gather_kv(d["k_pages"], None, d["k_descale"], None, cu, d["block_table"], 73,
+                  k_out=k[:73])
+    want = np.concatenate([cache.rows(b)[0].transpose(1, 0, 2) for b in range(2)])
+    assert np.array_equal(k[:73].cpu().numpy(), want[:73].astype(np.float32))
+    assert (k[73:] == 5).all()
 
 
 def test_gather_one_side_and_missing_pages():

@@ -147,6 +147,8 @@ def _decode_args():
     ("v_pages", torch.zeros(6, 2, 64, 128, dtype=torch.uint8), "shape"),
     ("k_pages", torch.zeros(6, 32, 2, 128, dtype=torch.uint8).transpose(1, 2), "contiguous"),
     ("k_pages", torch.zeros(6, 2, 32, 128, dtype=torch.float16), "dtype"),
+    ("k_pages", torch.zeros(6, 2, 32, 64, dtype=torch.uint8), "head dim"),
+    ("k_pages", torch.zeros(6, 2, 32 * 128, dtype=torch.uint8), "shape"),
     ("k_descale", torch.zeros(6, 2, 31), "shape"), ("k_descale", torch.zeros(2), "shape"),
     ("v_descale", torch.zeros(3), "shape"), ("v_descale", torch.zeros(2).double(), "dtype"),
     ("seqused_kv", torch.zeros(2, dtype=torch.int64), "dtype"),
