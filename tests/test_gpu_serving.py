@@ -367,6 +367,58 @@ def test_decode_two_graphs_share_a_workspace(sparse):
     _compare(cache, q64, (out, lse), on, "shorter")
 
 
+@pytest.mark.parametrize("sparse", [False, True])
+def test_decode_step_captured_with_its_length_update(sparse):
+    """A captured step that lengthens the sequences, appends and decodes, replayed: every replay sees
+    the lengths and rows that its own step wrote (bit for bit an eager decode's result)."""
+    import block_sparse_fp8_gb300 as bsa
+
+    g = torch.Generator(device="cuda").manual_seed(4)
+    B, N1, N2, ps, L = 4, 16, 2, 32, 96
+    rand = lambda *s: torch.randn(*s, device="cuda", generator=g).bfloat16()
+    kp, vp = (torch.zeros(B * L, N2, ps, 128, dtype=torch.uint8, device="cuda") for _ in range(2))
+    kd = torch.ones(B * L, N2, ps, device="cuda")
+    vs = torch.full((N2,), 0.012, device="cuda")
+    table = torch.randperm(B * L, device="cuda", generator=g).int().view(B, L)
+    used = torch.tensor([2500, 10, 127, 1023], dtype=torch.int32, device="cuda")
+    cu = torch.cat([torch.zeros(1, dtype=torch.int32, device="cuda"), used.cumsum(0).int()])
+    T = int(cu[-1])
+    bsa.append_kv(rand(T, N2, 128), rand(T, N2, 128), cu, torch.zeros_like(used), table, kp, vp,
+                  k_descale=kd, v_scale=vs)
+    k1, v1, q = rand(B, N2, 128), rand(B, N2, 128), rand(B, N1, 128)
+    one = torch.arange(B + 1, dtype=torch.int32, device="cuda")
+    cap = L * ps
+    kw = {}
+    if sparse:
+        kw["block_mask"] = (torch.rand(B, N1, cap // 128, device="cuda", generator=g) < 0.5).byte()
+        kw["block_mask"][:, :, 0] = 1
+    out = torch.empty(B, N1, 128, dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty(N1, B, device="cuda")
+    ws = torch.empty(32 << 20, dtype=torch.uint8, device="cuda")
+
+    def decode(**o):
+        return bsa.decode(q, kp, vp, kd, vs, used, table, cap, **o, **kw)
+
+    def step():
+        bsa.append_kv(k1, v1, one, used, table, kp, vp, k_descale=kd, v_scale=vs)
+        used.add_(1)
+        decode(out=out, lse=lse, workspace=ws)
+        k1.mul_(-1.01)                                   # the next step's rows
+        q.copy_(q.roll(1, 2))
+
+    step()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for i in range(40):
+        graph.replay()
+        q.copy_(q.roll(-1, 2))                           # this replay's queries again
+        want = decode()
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1]), i
+        q.copy_(q.roll(1, 2))
+    assert int(used[1]) == 10 + 41
+
+
 def test_decode_on_two_streams_at_once():
     import block_sparse_fp8_gb300 as bsa
 
