@@ -78,11 +78,11 @@ struct Params {
   float *lse;
   int *dev_status;
   // workspace: per slot (two per CTA) and head of the group a partial (m, l) and O; with lists, per
-  // task the count of its tiles and the tiles, ascending, the heads that enable them in the upper
-  // half
+  // task {the count of its tiles, the sequence's tokens} and the tiles, ascending, the heads that
+  // enable them in the upper half
   float2 *part_ml;
   float *part_o;
-  int *counts;
+  int2 *counts;
   uint32_t *tiles;
   long long q_stride;  // elements
   int B, N1, N2, G, ps, ps_shift, num_pages, L, Kb, max_kv_len;
@@ -287,14 +287,16 @@ __global__ void __launch_bounds__(PLAN_THREADS, 2) plan_kernel(const Params p) {
     if (on) list[at] = (uint32_t)t | on << 16;
     __syncthreads();
   }
-  if (tid == 0) p.counts[task] = n;
+  if (tid == 0) p.counts[task] = make_int2(n, kv);
 }
 
 // Tiles that task's list holds (one for an empty list, as above).  Bounded by the list's room, as the
 // walks below are by the batch: lengths that someone changes under a running call spoil its
 // results, but lead it nowhere outside its tensors.
-__device__ __forceinline__ int listed_tiles(const Params &p, int task) {
-  return min(max(__ldcg(p.counts + task), 1), p.Kb);
+__device__ __forceinline__ int listed_tiles(const Params &p, int task, int &kv) {
+  const int2 c = __ldcg(p.counts + task);
+  kv = c.y;
+  return min(max(c.x, 1), p.Kb);
 }
 
 // The batch's tiles, in task order, cut into even runs for `grid` CTAs (as many runs as there are
@@ -314,25 +316,27 @@ struct Cut {
 // tile is returned.  Called by all of a CTA's warps; every thread sums a stretch of the items.
 struct Found {
   int item, off;  // the item, the wanted tile's offset in it (by_item: the item's first tile)
+  int kv;         // the tokens of the item's sequence
 };
 
 constexpr int MAX_WARPS = 8;
 
-template <bool SPARSE>
-__device__ __forceinline__ int item_tiles(const Params &p, int i) {
-  return SPARSE ? listed_tiles(p, i) : p.N2 * dense_tiles(seq_len(p, i));
-}
-
 template <bool SPARSE, typename Want>
 __device__ __forceinline__ Found find_tile(const Params &p, int grid, int threads, Cut &cut,
                                            bool by_item, Want &&want) {
-  __shared__ int s_sum[MAX_WARPS], s_item, s_off;
+  __shared__ int s_sum[MAX_WARPS], s_item, s_off, s_kv;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int items = SPARSE ? p.B * p.N2 : p.B;
   const int per = (items + threads - 1) / threads, i0 = min(tid * per, items),
             i1 = min(i0 + per, items);
+  int kv = 0;  // of the item looked at last
+  const auto tiles = [&](int i) {
+    if (SPARSE) return listed_tiles(p, i, kv);
+    kv = seq_len(p, i);
+    return p.N2 * dense_tiles(kv);
+  };
   int sum = 0;
-  for (int i = i0; i < i1; ++i) sum += item_tiles<SPARSE>(p, i);
+  for (int i = i0; i < i1; ++i) sum += tiles(i);
   int incl = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -352,20 +356,22 @@ __device__ __forceinline__ Found find_tile(const Params &p, int grid, int thread
   cut.size = total / cut.runs;
   cut.larger = total - cut.runs * cut.size;
   const int x = want(cut);
-  if (x < 0) return Found{-1, 0};
+  if (x < 0) return Found{-1, 0, 0};
   int before = incl - sum, i = i0;
   if (by_item ? x >= i0 && x < i1 : x >= before && x < incl) {
-    for (; i + 1 < i1; ++i) {
-      if (by_item && i == x) break;
-      const int w = item_tiles<SPARSE>(p, i);
-      if (!by_item && x < before + w) break;
-      before += w;
+    if (per > 1) {  // (a single item has just been looked at)
+      for (;; ++i) {
+        const int w = tiles(i);
+        if (i + 1 >= i1 || (by_item ? i == x : x < before + w)) break;
+        before += w;
+      }
     }
     s_item = i;
     s_off = by_item ? before : x - before;
+    s_kv = kv;
   }
   __syncthreads();
-  return Found{s_item, s_off};
+  return Found{s_item, s_off, s_kv};
 }
 
 // A position in the batch's run of tiles, moved along by the copying side of a warp.
@@ -374,16 +380,13 @@ struct Cursor {
   int b, kvh, idx, n, kv;  // task, tile position in it, its tiles, the sequence's tokens
   int pos, heads, page;    // of the current tile: the warp's first token, heads, physical page
 
-  __device__ __forceinline__ void enter(const Params &p) {  // a task's own numbers
-    n = SPARSE ? listed_tiles(p, b * p.N2 + kvh) : dense_tiles(kv);
-  }
   // The current tile's entry and page (the page still unchecked; -1: nothing to read).
   __device__ __forceinline__ void look(const Params &p, int warp) {
     int tile = idx;
     heads = 0xffff;
     if (SPARSE) {
       const size_t task = (size_t)b * p.N2 + kvh;
-      const uint32_t e = p.counts[task] > 0 ? p.tiles[task * p.Kb + idx] : 0u;
+      const uint32_t e = p.counts[task].x > 0 ? p.tiles[task * p.Kb + idx] : 0u;
       tile = e & 0xffffu;
       heads = e >> 16;
     }
@@ -396,9 +399,9 @@ struct Cursor {
       if (++kvh == p.N2) {
         kvh = 0;
         b = min(b + 1, p.B - 1);
-        kv = seq_len(p, b);
+        if (!SPARSE) kv = seq_len(p, b);
       }
-      enter(p);
+      n = SPARSE ? listed_tiles(p, b * p.N2 + kvh, kv) : dense_tiles(kv);
     }
     look(p, warp);
   }
@@ -449,8 +452,8 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
     cur.b = t0 / p.N2;
     cur.kvh = t0 % p.N2;
     cur.idx = 0;
-    cur.kv = seq_len(p, cur.b);
-    cur.enter(p);
+    if (!SPARSE) cur.kv = seq_len(p, cur.b);
+    cur.n = SPARSE ? listed_tiles(p, t0, cur.kv) : dense_tiles(cur.kv);
   } else {
     Cut cut;
     const Found at = find_tile<SPARSE>(p, (int)gridDim.x, THREADS, cut, false, [&](const Cut &c) {
@@ -459,9 +462,9 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
     if (at.item < 0) return;
     units = cut.begin(cta + 1) - cut.begin(cta);
     cur.b = SPARSE ? at.item / p.N2 : at.item;
-    cur.kv = seq_len(p, cur.b);
+    cur.kv = at.kv;
     if (SPARSE) cur.kvh = at.item % p.N2;
-    cur.enter(p);
+    cur.n = SPARSE ? listed_tiles(p, at.item, cur.kv) : dense_tiles(cur.kv);
     if (!SPARSE) cur.kvh = min(at.off / cur.n, p.N2 - 1);
     cur.idx = SPARSE ? min(at.off, cur.n - 1) : at.off % cur.n;
   }
@@ -858,7 +861,8 @@ __global__ void __launch_bounds__(MAX_WARPS * 32) join_kernel(const Params p, bo
     return by_task ? (SPARSE ? index : index / p.N2) : index < c.runs ? c.begin(index + 1) - 1 : -1;
   });
   if (at.item < 0) return;  // (never block 0)
-  const int n = SPARSE ? item_tiles<SPARSE>(p, at.item) : dense_tiles(seq_len(p, at.item));
+  int kv = at.kv;
+  const int n = SPARSE ? listed_tiles(p, at.item, kv) : dense_tiles(kv);
   int task, t0;  // the task and its first tile
   if (by_task) {
     task = index;

@@ -769,7 +769,7 @@ DecodePlan plan_decode(const bsa_fp8_decode_dims_t *d, int num_sms) {
   const size_t slots = plan.whole ? 0 : 2 * (size_t)plan.grid;
   plan.off_o = round256(slots * decode::MAX_G * sizeof(float2));
   plan.off_counts = plan.off_o + slots * (size_t)(d->N1 / d->N2) * HEAD_DIM * sizeof(float);
-  plan.off_tiles = plan.off_counts + (d->sparse ? round256((size_t)tasks * sizeof(int)) : 0);
+  plan.off_tiles = plan.off_counts + (d->sparse ? round256((size_t)tasks * sizeof(int2)) : 0);
   plan.bytes = std::max(WORKSPACE_BYTES, plan.off_tiles + (d->sparse ? (size_t)tasks * (size_t)kb *
                                                                            sizeof(uint32_t)
                                                                      : 0));
@@ -903,7 +903,7 @@ extern "C" bsa_status_t bsa_fp8_decode(const bsa_fp8_decode_dims_t *d, const voi
   p.ps_shift = d->page_size == 64 ? 6 : 5;
   p.part_ml = reinterpret_cast<float2 *>(ws);
   p.part_o = reinterpret_cast<float *>(ws + plan.off_o);
-  p.counts = reinterpret_cast<int *>(ws + plan.off_counts);
+  p.counts = reinterpret_cast<int2 *>(ws + plan.off_counts);
   p.tiles = reinterpret_cast<uint32_t *>(ws + plan.off_tiles);
   const bool wide = p.G > 8;  // two blocks of eight query heads per KV head
   // Tensor maps of the pools: a box is a warp's 32 slots of one page and head, in shared memory
