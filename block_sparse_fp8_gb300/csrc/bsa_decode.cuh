@@ -88,7 +88,7 @@ struct Params {
   int B, N1, N2, G, ps, ps_shift, num_pages, L, Kb, max_kv_len;
   int q_e4m3, k_per_token, v_per_head;
   int kv_nhd;
-  int whole;  // the batch is cut between tasks only
+  int whole;  // a run is a task, whatever its length
   float scale_log2;  // softmax_scale * log2(e)
   unsigned long long wait_limit_ns;
 };
@@ -440,27 +440,24 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
   pdl_wait();               // what the stream ran before: the tile lists among it
   pdl_launch_dependents();  // the join, which reads the lengths and counts as well: only now
 
-  // this CTA's run: its first tile's place, and its length in tiles (`whole`: in tasks)
+  // this CTA's run: its first tile's place, and the tiles left of it
   const int cta = blockIdx.x;
-  int units;
+  int tiles_left;
   Cursor<SPARSE> cur;
-  if (p.whole) {
-    const int tasks = p.B * p.N2, runs = min((int)gridDim.x, tasks);
-    const Cut cut = {runs, tasks / runs, tasks % runs};
-    const int t0 = cut.begin(cta);
-    units = cut.begin(cta + 1) - t0;  // the grid is no larger than the tasks
-    cur.b = t0 / p.N2;
-    cur.kvh = t0 % p.N2;
+  if (p.whole) {  // the grid has a CTA for every task
+    cur.b = cta / p.N2;
+    cur.kvh = cta % p.N2;
     cur.idx = 0;
     if (!SPARSE) cur.kv = seq_len(p, cur.b);
-    cur.n = SPARSE ? listed_tiles(p, t0, cur.kv) : dense_tiles(cur.kv);
+    cur.n = SPARSE ? listed_tiles(p, cta, cur.kv) : dense_tiles(cur.kv);
+    tiles_left = cur.n;
   } else {
     Cut cut;
     const Found at = find_tile<SPARSE>(p, (int)gridDim.x, THREADS, cut, false, [&](const Cut &c) {
       return cta < c.runs ? c.begin(cta) : -1;
     });
     if (at.item < 0) return;
-    units = cut.begin(cta + 1) - cut.begin(cta);
+    tiles_left = cut.begin(cta + 1) - cut.begin(cta);
     cur.b = SPARSE ? at.item / p.N2 : at.item;
     cur.kv = at.kv;
     if (SPARSE) cur.kvh = at.item % p.N2;
@@ -548,11 +545,10 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
   };
 
   const auto issue = [&](int stage) {
-    if (units == 0) return;
+    if (tiles_left == 0) return;
     const int left = cur.heads != 0 ? cur.kv - cur.pos : 0;
     const bool bad = cur.page < 0 || cur.page >= p.num_pages;
-    const bool last = cur.idx + 1 == cur.n, counts = !p.whole || last;
-    const bool end = counts && units == 1;
+    const bool last = cur.idx + 1 == cur.n, end = tiles_left == 1;
     if (left > 0) in_flight |= 1u << stage;
     if (lane == 0) {
       s_meta[warp][stage] = make_int4(cur.heads, left, (last ? 1 : 0) | (end ? 2 : 0), bad);
@@ -572,8 +568,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
                          bar);
       }
     }
-    if (counts) --units;
-    if (!end) {
+    if (--tiles_left > 0) {
       cur.next(p, warp);
       // the next task's queries, wanted when the computing side gets there
       if (cur.idx == 0 && lane < q_lines) prefetch_l1(q_row(cur.b, cur.kvh) + lane * 128);
