@@ -21,9 +21,13 @@
 //   * The products run on mma.sync m16n8k16 with tokens (K) or dimensions (V) as the 16 rows and
 //     up to eight query heads as the 8 columns: with one token per sequence there is no
 //     128-row operand for tcgen05.mma to work on, and the tensor pipe is far from its limit.
-//     e4m3 codes convert to fp16 exactly; queries are scaled to fp16 by a power of two per
-//     row, P is rounded to fp16 (2^-11 relative, against the result's bf16 2^-8), accumulation,
-//     maxima and sums are fp32.
+//     e4m3 codes convert to fp16 exactly, and so do bf16 queries times a power of two per row
+//     (values below 2^-28 of the row's largest lose bits).  P goes in as two fp16 terms, the
+//     rounded value and what the rounding left, together 2^-22 relative or 2^-40 of the largest
+//     weight, whichever is more; one term alone moves one result in fifteen by a bf16 step.
+//     Accumulation, maxima and sums are fp32 (the products cut off what lies below a sum's last
+//     bit, about 2^-25 of it each: after 400 of them one result in 300 is a bf16 step off, sums
+//     taken outside leave one in 2000, at 2 to 8% of the time).
 //   * The 128-byte swizzle (a row's 16-byte chunks XORed with the row number) keeps the fragment
 //     reads of K (a thread: 32 dimensions of one token) and V (16 dimensions of one token) free of
 //     bank conflicts.
@@ -61,7 +65,7 @@ constexpr int STAGE_BYTES = 2 * TOK * HEAD_DIM;
 constexpr int SMEM_ALIGN = 1024;
 constexpr int SMEM_BYTES = WARPS * STAGES * STAGE_BYTES + SMEM_ALIGN;
 // fp16 probabilities are kept as 2^(s - m + P_SHIFT): the largest, 2^15, fits, and weights down to
-// 2^-29 of it keep full precision
+// 2^-29 of it are normal numbers
 constexpr float P_SHIFT = 15.f;
 constexpr int MAX_G = 16;
 constexpr int WHOLE_TILES = 4;
@@ -172,6 +176,13 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
   uint32_t r;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
   return r;
+}
+
+// The two fp16 values of a pair as fp32.
+__device__ __forceinline__ float2 f32x2(uint32_t v) {
+  __half2 h;
+  memcpy(&h, &v, 4);
+  return __half22float2(h);
 }
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -641,7 +652,8 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
           }
       }
     }
-    uint32_t pf[NT][2][2];  // P as B fragments: [16 tokens][tokens 2 q4 | 2 q4 + 8, head r]
+    // P as B fragments: [16 tokens][rounded, rest][tokens 2 q4 | 2 q4 + 8, head r]
+    uint32_t pf[NT][2][2][2];
     bool moved = false;
     float alpha[NT][2];
 #pragma unroll
@@ -668,8 +680,14 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
         for (int c = 0; c < 4; ++c) e[c] = ptx::ex2_approx(s[nt][mt][c] - ref[c & 1]);
         sum0 += e[0] + e[2];
         sum1 += e[1] + e[3];
-        pf[nt][mt][0] = transpose8x8(f16x2(e[0], e[1]));
-        pf[nt][mt][1] = transpose8x8(f16x2(e[2], e[3]));
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const uint32_t hi = f16x2(e[2 * half], e[2 * half + 1]);
+          const float2 x = f32x2(hi);
+          pf[nt][mt][0][half] = transpose8x8(hi);
+          pf[nt][mt][1][half] =
+              transpose8x8(f16x2(e[2 * half] - x.x, e[2 * half + 1] - x.y));
+        }
       }
       l[nt][0] = l[nt][0] * alpha[nt][0] + sum0;
       l[nt][1] = l[nt][1] * alpha[nt][1] + sum1;
@@ -682,7 +700,9 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
 #pragma unroll
           for (int c = 0; c < 4; ++c) acc[nt][i][c] *= alpha[nt][c & 1];
     }
-    const auto pv = [&]() {
+    // With `masked` the columns of heads that mask the tile keep their sums: their weights are zero,
+    // but zero times a NaN of the tile's V would reach them through the shared product.
+    const auto pv = [&](const bool masked) {
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt) {
         // tokens 2 q4, 2 q4 + 1 and those + 8, dimensions 16 r .. 16 r + 15
@@ -711,33 +731,26 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
 #pragma unroll
           for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              mma16816(acc[nt][2 * w + i], a[i][0], a[i][1], a[i][2], a[i][3], pf[nt][mt][0],
-                       pf[nt][mt][1]);
+            for (int nt = 0; nt < NT; ++nt) {
+              float o[4];
+#pragma unroll
+              for (int c = 0; c < 4; ++c) o[c] = acc[nt][2 * w + i][c];
+#pragma unroll
+              for (int part = 0; part < 2; ++part)
+                mma16816(o, a[i][0], a[i][1], a[i][2], a[i][3], pf[nt][mt][part][0],
+                         pf[nt][mt][part][1]);
+#pragma unroll
+              for (int c = 0; c < 4; ++c)
+                if (!masked || ((heads >> (nt * 8 + 2 * q4 + (c & 1))) & 1))
+                  acc[nt][2 * w + i][c] = o[c];
+            }
         }
       }
     };
-    if (!SPARSE || heads == group) {
-      pv();
-    } else {
-      // A tile that some heads mask: their weights are zero, but zero times a NaN of the tile's V
-      // would reach them through the shared product, so their columns are put back.
-      float kept[NT][8][4];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) kept[nt][i][c] = acc[nt][i][c];
-      pv();
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-            if (!((heads >> (nt * 8 + 2 * q4 + (c & 1))) & 1)) acc[nt][i][c] = kept[nt][i][c];
-    }
+    if (!SPARSE || heads == group)
+      pv(false);
+    else
+      pv(true);
   };
 
   // ---- the end of a segment: the four warps' states combined; written out when the segment is

@@ -379,7 +379,7 @@ size_t bsa_fp8_decode_workspace_size(const bsa_fp8_decode_dims_t *dims);
  * A row with no visible key (an idle sequence among them) gets O = 0 and LSE = -FLT_MAX.  Bad
  * device data is reported and skipped as in the prefill: a sequence of a bad length counts as
  * empty, a bad page reads as zeros.  Scores, softmax statistics and sums are fp32; the
- * probabilities are rounded to fp16 for the product with V. */
+ * probabilities go into the product with V as two fp16 terms, 22 bits together. */
 bsa_status_t bsa_fp8_decode(const bsa_fp8_decode_dims_t *dims, const void *q,
                             const float *q_descale, const void *k_pages, const void *v_pages,
                             const float *k_descale, const float *v_descale,
