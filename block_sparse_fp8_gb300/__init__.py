@@ -7,6 +7,8 @@ marshals CPU tensors into ``bsa_fp8_prefill_host``, which copies them in and the
 ``decode`` / ``gather_kv`` / ``merge_states`` serve from the same cache: the next token's
 attention, the cache read back, and the join of attention results over parts of a cache.
 Every step of the computation runs in the library's CUDA kernels; there is no CPU path.
+Every call takes ``stream=`` (default: the current one).  The caller sees to it that the inputs are
+ready there; outputs and workspaces that the call makes itself come from that stream's memory.
 The library must have been built (``block_sparse_fp8_gb300._build.build()``); importing the
 binding on a machine without it raises immediately.
 """
@@ -167,6 +169,23 @@ def _stream_handle(stream):
     return s.cuda_stream
 
 
+def _empty(shape, dtype, device, stream, result=True):
+    """A tensor that a call makes for itself, from the memory of the stream that the call runs on
+    (None: the current one): memory that was freed may still be in use by work queued before, and
+    the allocator orders such reuse within one stream only.  A result may be read on the
+    current stream, once that has waited for `stream`, and dropped there: its memory is kept from
+    `stream` until the current one is through with it."""
+    import torch
+
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if result and t.is_cuda:
+        t.record_stream(torch.cuda.current_stream(t.device))
+    return t
+
+
 def make_dims(q, k_pages, block_table, cu_seqlens_q, max_q_len, max_kv_len, k_scale_kind,
               v_scale_kind, causal=True, q_layout=Q_TND, kv_layout=KV_HND,
               tiles_per_step=1) -> Dims:
@@ -220,12 +239,12 @@ def prefill(q, k_pages, v_pages, q_descale, k_descale, v_descale, cu_seqlens_q, 
                      v_kind, causal, q_layout, kv_layout, tiles_per_step)
     T, N1, D = dims.total_q, dims.N1, dims.D
     if out is None:
-        out = torch.empty((T, N1, D), dtype=torch.bfloat16, device=q.device)
+        out = _empty((T, N1, D), torch.bfloat16, q.device, stream)
     if lse is None and return_lse:
-        lse = torch.empty((N1, T), dtype=torch.float32, device=q.device)
+        lse = _empty((N1, T), torch.float32, q.device, stream)
     ws_bytes = workspace_size(dims)
     if ws_bytes and workspace is None:
-        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
+        workspace = _empty(ws_bytes, torch.uint8, q.device, stream, result=False)
     if softmax_scale is None:
         softmax_scale = 1.0 / math.sqrt(D)
     st = lib().bsa_fp8_prefill(
@@ -261,7 +280,7 @@ def prefill_host(host: dict, dev: dict, max_q_len: int, max_kv_len: int,
                      max_kv_len, k_kind, v_kind, causal, q_layout, kv_layout, tiles_per_step)
     ws_bytes = workspace_size(dims)
     if ws_bytes and workspace is None:
-        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev["q"].device)
+        workspace = _empty(ws_bytes, torch.uint8, dev["q"].device, stream, result=False)
     if softmax_scale is None:
         softmax_scale = 1.0 / math.sqrt(dims.D)
     th = Tensors(*(_p(host.get(n)) for n in TENSOR_NAMES))
@@ -281,8 +300,8 @@ def compact_tiles(cu_seqlens_q, seqused_kv, dims: Dims, block_mask=None, sparse_
     Qb = -(-dims.max_q_len // 128)
     Kb = -(-dims.max_kv_len // 128)
     dev = cu_seqlens_q.device
-    lists = torch.empty((dims.B, dims.N1, Qb, Kb), dtype=torch.int32, device=dev)
-    counts = torch.empty((dims.B, dims.N1, Qb), dtype=torch.int32, device=dev)
+    lists = _empty((dims.B, dims.N1, Qb, Kb), torch.int32, dev, stream)
+    counts = _empty((dims.B, dims.N1, Qb), torch.int32, dev, stream)
     st = lib().bsa_fp8_compact_tiles(ctypes.byref(dims), _p(cu_seqlens_q), _p(seqused_kv),
                                      _p(block_mask), _p(sparse_indices), _p(sparse_seq_len),
                                      _p(lists), _p(counts), _p(dev_status),
@@ -301,9 +320,9 @@ def quantize_rows(x, codes=None, descale=None, stream=None, rule: int = DESCALE_
     if x.dtype != torch.bfloat16 or x.shape[-1] != 128 or not x.is_contiguous():
         raise ValueError("x must be a contiguous bf16 tensor [..., 128]")
     if codes is None:
-        codes = torch.empty(x.shape, dtype=torch.uint8, device=x.device)
+        codes = _empty(x.shape, torch.uint8, x.device, stream)
     if descale is None:
-        descale = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+        descale = _empty(x.shape[:-1], torch.float32, x.device, stream)
     fn = lib().bsa_fp8_quantize_rows_ue8m0 if rule == DESCALE_UE8M0 else lib().bsa_fp8_quantize_rows
     st = fn(_p(x), x.numel() // 128, _p(codes), _p(descale), _stream_handle(stream))
     if st != 0:
@@ -374,9 +393,8 @@ def _check(name, t, dtype, shape, dev):
         raise ValueError(f"{name} must be contiguous")
 
 
-def _call(fn, args, dev, stream, what, made=()):
-    """fn(*args, stream handle) with device `dev` current; raises BsaError on a status but 0.
-    `made`: tensors of this call's own, which live on the current stream."""
+def _call(fn, args, dev, stream, what):
+    """fn(*args, stream handle) with device `dev` current; raises BsaError on a status but 0."""
     torch = _torch_names()[0]
     if dev < 0:
         raise ValueError(f"{what}: tensors must be on a CUDA device")
@@ -393,9 +411,6 @@ def _call(fn, args, dev, stream, what, made=()):
             st = fn(*args, handle)
     if st != 0:
         raise BsaError(st, what)
-    if stream is not None:
-        for t in made:
-            t.record_stream(stream)
 
 
 def _check_status(dev_status, dev):
@@ -491,17 +506,14 @@ def decode(q, k_pages, v_pages, k_descale, v_descale, seqused_kv, block_table, m
             _check("sparse_indices", sparse_indices, i32, (B, N1, Kb), dev)
         if sparse_seq_len is not None:
             _check("sparse_seq_len", sparse_seq_len, i32, (B, N1), dev)
-    made = []
     if out is None:
-        out = torch.empty((B, N1, D), dtype=torch.bfloat16, device=q.device)
-        made.append(out)
+        out = _empty((B, N1, D), bf16, q.device, stream)
     else:
         _check("out", out, bf16, shape, dev)
     if lse is not None:
         _check("lse", lse, f32, (N1, B), dev)
     elif return_lse:
-        lse = torch.empty((N1, B), dtype=torch.float32, device=q.device)
-        made.append(lse)
+        lse = _empty((N1, B), f32, q.device, stream)
     if dev_status is not None:
         _check_status(dev_status, dev)
     # in the order of DecodeDims' fields, as make_decode_dims
@@ -512,8 +524,7 @@ def decode(q, k_pages, v_pages, k_descale, v_descale, seqused_kv, block_table, m
             raise ValueError("decode: tensors must be on a CUDA device")
         with torch.cuda.device(dev):
             nbytes = decode_workspace_size(dims)
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
-        made.append(workspace)
+        workspace = _empty(nbytes, torch.uint8, q.device, stream, result=False)
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on q's device")
     if softmax_scale is None:
@@ -523,16 +534,14 @@ def decode(q, k_pages, v_pages, k_descale, v_descale, seqused_kv, block_table, m
            v_pages.data_ptr(), k_descale.data_ptr(), v_descale.data_ptr(), seqused_kv.data_ptr(),
            block_table.data_ptr(), _p(block_mask), _p(sparse_indices), _p(sparse_seq_len),
            float(softmax_scale), out.data_ptr(), _p(lse), workspace.data_ptr(), workspace.nbytes,
-           _p(dev_status)), dev, stream, "bsa_fp8_decode", made)
+           _p(dev_status)), dev, stream, "bsa_fp8_decode")
     return out, lse
 
 
-def _gather_rows(name, t, dtype, shape, pages, made):
+def _gather_rows(name, t, dtype, shape, pages, stream):
     if t is None:
-        t = _torch_names()[0].empty(shape, dtype=dtype, device=pages.device)
-        made.append(t)
-    else:
-        _check(name, t, dtype, shape, pages.get_device())
+        return _empty(shape, dtype, pages.device, stream)
+    _check(name, t, dtype, shape, pages.get_device())
     return t
 
 
@@ -568,7 +577,6 @@ def gather_kv(k_pages, v_pages, k_descale, v_descale, cu_seqlens, block_table, t
     total = int(total)
     k_kind = v_kind = SCALE_PER_TENSOR
     shape = (total, N2, D)
-    made = []
     if k_pages is not None:
         k_kind = k_scale_kind if k_scale_kind is not None else (
             SCALE_PER_TOKEN_HEAD if k_descale.dim() == 3 else SCALE_PER_TENSOR)
@@ -576,7 +584,7 @@ def gather_kv(k_pages, v_pages, k_descale, v_descale, cu_seqlens, block_table, t
                dev)
         _check("k_descale", k_descale, f32,
                (P, N2, ps) if k_kind == SCALE_PER_TOKEN_HEAD else (1,), dev)
-        k_out = _gather_rows("k_out", k_out, out_dtype, shape, pages, made)
+        k_out = _gather_rows("k_out", k_out, out_dtype, shape, pages, stream)
     elif k_out is not None:
         raise ValueError("k_out given without k_pages")
     if v_pages is not None:
@@ -585,7 +593,7 @@ def gather_kv(k_pages, v_pages, k_descale, v_descale, cu_seqlens, block_table, t
         _check("v_pages", v_pages, v_pages.dtype if v_pages.dtype in codes else codes, pages.shape,
                dev)
         _check("v_descale", v_descale, f32, (N2,) if v_kind == SCALE_PER_HEAD else (1,), dev)
-        v_out = _gather_rows("v_out", v_out, out_dtype, shape, pages, made)
+        v_out = _gather_rows("v_out", v_out, out_dtype, shape, pages, stream)
     elif v_out is not None:
         raise ValueError("v_out given without v_pages")
     # in the order of GatherDims' fields
@@ -594,7 +602,7 @@ def gather_kv(k_pages, v_pages, k_descale, v_descale, cu_seqlens, block_table, t
     _call(lib().bsa_fp8_gather_kv,
           (ctypes.byref(dims), _p(k_pages), _p(v_pages), _p(k_descale), _p(v_descale),
            cu_seqlens.data_ptr(), _p(cache_starts), block_table.data_ptr(), _p(k_out), _p(v_out),
-           _p(dev_status)), dev, stream, "bsa_fp8_gather_kv", made)
+           _p(dev_status)), dev, stream, "bsa_fp8_gather_kv")
     return k_out, v_out
 
 
@@ -617,19 +625,16 @@ def merge_states(outs, lses, out=None, lse=None, return_lse: bool = True, stream
         _check("outs", o, bf16, shape, dev)
     for x in lses:
         _check("lses", x, f32, (N1, T), dev)
-    made = []
     if out is None:
-        out = torch.empty(shape, dtype=torch.bfloat16, device=first.device)
-        made.append(out)
+        out = _empty(shape, bf16, first.device, stream)
     else:
         _check("out", out, bf16, shape, dev)
     if lse is not None:
         _check("lse", lse, f32, (N1, T), dev)
     elif return_lse:
-        lse = torch.empty((N1, T), dtype=torch.float32, device=first.device)
-        made.append(lse)
+        lse = _empty((N1, T), f32, first.device, stream)
     ptrs = ctypes.c_void_p * n
     _call(lib().bsa_fp8_merge_states,
           (n, ptrs(*[o.data_ptr() for o in outs]), ptrs(*[x.data_ptr() for x in lses]), T, N1,
-           out.data_ptr(), _p(lse)), dev, stream, "bsa_fp8_merge_states", made)
+           out.data_ptr(), _p(lse)), dev, stream, "bsa_fp8_merge_states")
     return out, lse

@@ -72,3 +72,133 @@ def test_decode_probabilities_keep_their_bits(lens, N1, N2, form, q8):
             S.within(out[b, h], O, bound, f"O of {b}, {h}")
             z = s.max() + np.log(p.sum())
             assert abs(float(lse[h, b]) - z) <= 2.0 ** -16 + n * 2.0 ** -21 + 2.0 ** -22 * abs(z)
+
+
+# -------------------------------------------------------------------- streams and their memory
+
+def _stream_calls():
+    """name -> (call(**kw) on inputs that are ready, check of its result)."""
+    import block_sparse_fp8_gb300 as bsa
+
+    cache = S.Cache(3, [3000, 200], 2, 32)
+    d = cache.device()
+    q, _, q64 = S.queries(4, 2, 8, False)
+    q = q.cuda()
+    cu = torch.tensor([0, 3000, 3200], dtype=torch.int32, device="cuda")
+    rows = [np.concatenate([cache.rows(b)[i].transpose(1, 0, 2) for b in range(2)])
+            for i in range(2)]
+    g = torch.Generator().manual_seed(5)
+    o = [torch.randn(700, 8, 128, generator=g).bfloat16() for _ in range(2)]
+    l = [torch.randn(8, 700, generator=g) for _ in range(2)]
+    w = torch.softmax(torch.stack(l).double(), 0).transpose(1, 2)[..., None]
+    merged = sum(w[i] * o[i].double() for i in range(2)).numpy()
+    size = sum(w[i] * o[i].double().abs() for i in range(2)).numpy()
+    do, dl = [x.cuda() for x in o], [x.cuda() for x in l]
+    x = torch.randn(900, 4, 128, generator=g).bfloat16().cuda()
+    codes = tuple(t.cpu() for t in bsa.quantize_rows(x))
+    q8, qd = bsa.quantize_rows(torch.randn(300, 8, 128, generator=g).bfloat16().cuda())
+    cuq = torch.tensor([0, 200, 300], dtype=torch.int32, device="cuda")
+    # the prefill wants zeros in the slots past a sequence's end
+    kp, vp = (torch.where(d[n] & 0x7f == 0x7f, 0, d[n]) for n in ("k_pages", "v_pages"))
+    kd = d["k_descale"].nan_to_num()
+
+    def prefill(**kw):
+        return bsa.prefill(q8, kp, vp, qd, kd, d["v_descale"], cuq, d["seqused_kv"],
+                           d["block_table"], 200, 3000, **d["kinds"], **kw)
+
+    ahead = tuple(t.cpu() for t in prefill())
+
+    def same(want):
+        def check(got):
+            assert all(torch.equal(a.cpu(), b) for a, b in zip(got, want))
+        return check
+
+    return {
+        "decode": (lambda **kw: bsa.decode(
+            q, d["k_pages"], d["v_pages"], d["k_descale"], d["v_descale"], d["seqused_kv"],
+            d["block_table"], 3000, **d["kinds"], **kw),
+            lambda got: _compare(cache, q64, got, what="stream")),
+        "gather_kv": (lambda **kw: bsa.gather_kv(
+            d["k_pages"], d["v_pages"], d["k_descale"], d["v_descale"], cu, d["block_table"], 3200,
+            out_dtype=torch.float32, **d["kinds"], **kw),
+            same([torch.from_numpy(r.astype(np.float32)) for r in rows])),
+        "merge_states": (lambda **kw: bsa.merge_states(do, dl, **kw),
+                         lambda got: S.within(got[0], merged, 2.0 ** -8 * np.abs(merged) +
+                                              2.0 ** -15 * size, "merge")),
+        "quantize_rows": (lambda **kw: bsa.quantize_rows(x, **kw), same(codes)),
+        "prefill": (prefill, same(ahead)),
+    }
+
+
+STREAM_CALLS = ["decode", "gather_kv", "merge_states", "quantize_rows", "prefill"]
+
+
+@pytest.mark.parametrize("name", STREAM_CALLS)
+def test_call_beside_work_on_freed_memory(name):
+    """A call on a stream that does not wait for the current one, where work is still queued on
+    memory that has been freed: neither has the other's memory."""
+    call, check = _stream_calls()[name]
+    sizes = [t.nbytes for t in call()]
+    if name == "decode":
+        import block_sparse_fp8_gb300 as bsa
+
+        sizes.append(bsa.decode_workspace_size(bsa.DecodeDims(
+            2, 8, 2, 128, 32, 3000, 97, 95, 1, 2, 0, 0, 1024, 0)))
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    kept, freed = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in sizes], set()
+    torch.cuda._sleep(200_000_000)
+    for k in kept:
+        busy = torch.empty(k.numel(), dtype=torch.uint8, device="cuda")
+        freed.add(busy.data_ptr())
+        busy.fill_(7)
+        k.copy_(busy)
+        del busy
+    got = call(stream=side)
+    assert not freed & {t.data_ptr() for t in got}
+    side.synchronize()
+    check(got)
+    torch.cuda.synchronize()
+    check(got)
+    assert all((k == 7).all() for k in kept)
+
+
+@pytest.mark.parametrize("name", STREAM_CALLS)
+def test_result_dropped_while_the_current_stream_reads_it(name):
+    """A result of another stream, read on the current one and dropped: the other stream's next
+    call does not get its memory before that read is done."""
+    call, check = _stream_calls()[name]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = call(stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda._sleep(200_000_000)
+    copies = [t.clone() for t in got]
+    was = {t.data_ptr() for t in got}
+    del got
+    again = call(stream=side)
+    assert not was & {t.data_ptr() for t in again}
+    torch.cuda.synchronize()
+    check(copies)
+    check(again)
+
+
+@pytest.mark.parametrize("name", STREAM_CALLS)
+def test_captured_on_a_forked_stream(name):
+    """stream= names a stream that a capture has forked; outputs and workspace are the call's own."""
+    call, check = _stream_calls()[name]
+    call()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        got = call(stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+    for _ in range(2):
+        for t in got:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        check(got)
