@@ -764,8 +764,9 @@ DecodePlan plan_decode(const bsa_fp8_decode_dims_t *d, int num_sms) {
   // 300 tokens 5.2 us against 5.8, 16 of 512 6.2 against 8.9); with eight, or with more
   // tasks than CTAs, an even cut is faster (64 of 300 11.9 us against 12.4).
   plan.whole = kb <= decode::WHOLE_TILES && tasks <= resident;
+  // (a task without a tile is one piece of work all the same: 512 idle ones 5 us, on one CTA 700)
   plan.grid = (int)std::max<long long>(
-      1, std::min<long long>(resident, plan.whole ? tasks : tasks * kb));
+      1, std::min<long long>(resident, plan.whole ? tasks : tasks * std::max(kb, 1LL)));
   const size_t slots = plan.whole ? 0 : 2 * (size_t)plan.grid;
   plan.off_o = round256(slots * decode::MAX_G * sizeof(float2));
   plan.off_counts = plan.off_o + slots * (size_t)(d->N1 / d->N2) * HEAD_DIM * sizeof(float);

@@ -202,3 +202,18 @@ def test_captured_on_a_forked_stream(name):
         graph.replay()
         torch.cuda.synchronize()
         check(got)
+
+
+# ------------------------------------------------------------------------------ mixed batches
+
+def test_decode_large_idle_batch():
+    """max_kv_len = 0 with more (sequence, KV head) tasks than CTAs: the empty results are shared
+    out like those of sequences that could hold a token (the partials' room follows the grid)."""
+    import block_sparse_fp8_gb300 as bsa
+
+    cache = S.Cache(20, [0] * 90, 8, 32)
+    q, qd, q64 = S.queries(21, 90, 16, False)
+    _compare(cache, q64, _decode(cache, q, qd, max_kv_len=0), what="idle")
+    none, one = (bsa.decode_workspace_size(bsa.DecodeDims(90, 16, 8, 128, 32, n, 2, 1, 1, 2, 0, 0,
+                                                          2048, 0)) for n in (0, 1))
+    assert none == one
