@@ -851,9 +851,12 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
 // the runs that follow, up to the one that holds its last tile.  Launched while the attention kernel
 // runs: the blocks find their partials in that kernel's shadow, in the registers it leaves
 // free, and then wait for its writes.  With fewer tasks than runs (`by_task`) a task has many
-// partials: a block joins one head of one task, its warps sharing the partials out.  Otherwise a
-// task has two or three: a block joins the task that its run begins and leaves unfinished, if it
-// does, a head a warp.
+// partials: a block joins one head of one task, its warps sharing the partials out.  Otherwise most
+// cut tasks have two or three, but a long sequence among short ones may have one in every run, so a
+// task is joined by the blocks of the runs that it leaves unfinished, as many as there are heads:
+// they deal the heads out among them, a head a warp, or, with more partials than a warp reads at
+// once, a head a block, whose warps share the partials out (one sequence of 512K tokens among 319
+// of 500, one KV head, 8 query heads: 48 us, with all heads in the first run's block 92).
 // ------------------------------------------------------------------------------------------
 constexpr int JOIN_AHEAD = 5;  // partials in flight per warp
 
@@ -877,11 +880,15 @@ __global__ void __launch_bounds__(MAX_WARPS * 32) join_kernel(const Params p, bo
     t0 = at.off + (SPARSE ? 0 : index % p.N2 * n);
   } else {
     task = SPARSE ? at.item : at.item * p.N2 + min(at.off / n, p.N2 - 1);
-    t0 = cut.begin(index + 1) - 1 - (SPARSE ? min(at.off, n - 1) : at.off % n);
+    t0 = max(cut.begin(index + 1) - 1 - (SPARSE ? min(at.off, n - 1) : at.off % n), 0);
   }
   const int c = min(cut.of(t0), cut.runs - 1);
   const int parts = min(cut.of(t0 + n - 1), cut.runs - 1) - c + 1;
-  if (parts <= 1 || (!by_task && c != index)) {  // not cut, or another block's
+  // the blocks of one task, and this one's number among them; the run with the task's last tile is
+  // not asked: it may begin the next cut task
+  const int blocks = by_task ? p.G : min(parts - 1, p.G);
+  const int block = by_task ? (int)blockIdx.y : index - c;
+  if (parts <= 1 || block >= blocks) {  // not cut, or enough others
     // one block always waits, so that the join never ends before the kernel it belongs to
     if (index == 0 && blockIdx.y == 0) pdl_wait();
     return;
@@ -890,9 +897,9 @@ __global__ void __launch_bounds__(MAX_WARPS * 32) join_kernel(const Params p, bo
   const int b = task / p.N2, kvh = task % p.N2;
   pdl_wait();
 
-  const int g0 = by_task ? (int)blockIdx.y : warp, g1 = by_task ? g0 + 1 : p.G;
-  const int j0 = by_task ? warp : 0, step = by_task ? warps : 1;
-  for (int g = g0; g < g1; g += warps) {
+  const bool together = by_task || parts > JOIN_AHEAD;  // a block's warps share a head's partials
+  const int j0 = together ? warp : 0, step = together ? warps : 1;
+  for (int g = block + (together ? 0 : warp * blocks); g < p.G; g += blocks * (together ? 1 : warps)) {
     float m = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int j = j0; j < parts; j += step * JOIN_AHEAD) {
@@ -912,14 +919,15 @@ __global__ void __launch_bounds__(MAX_WARPS * 32) join_kernel(const Params p, bo
 #pragma unroll
       for (int u = 0; u < JOIN_AHEAD; ++u) add_part(m, l, o, ml[u], v[u]);
     }
-    if (by_task) {
+    if (together) {
       s_o[warp][lane] = o;
       if (lane == 0) s_ml[warp] = make_float2(m, l);
       __syncthreads();
-      if (warp > 0) return;
-      for (int w = 1; w < warps; ++w) add_part(m, l, o, s_ml[w], s_o[w][lane]);
+      if (warp == 0)
+        for (int w = 1; w < warps; ++w) add_part(m, l, o, s_ml[w], s_o[w][lane]);
     }
-    write_row(p, b, kvh, g, lane, m, l, o);
+    if (!together || warp == 0) write_row(p, b, kvh, g, lane, m, l, o);
+    if (together) __syncthreads();  // the next head's states go where these were
   }
 }
 

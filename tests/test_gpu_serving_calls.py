@@ -217,3 +217,65 @@ def test_decode_large_idle_batch():
     none, one = (bsa.decode_workspace_size(bsa.DecodeDims(90, 16, 8, 128, 32, n, 2, 1, 1, 2, 0, 0,
                                                           2048, 0)) for n in (0, 1))
     assert none == one
+
+
+@pytest.mark.parametrize("form", [None, "mask", "index"])
+@pytest.mark.parametrize("lens,N1,N2", [
+    ([90] * 200 + [40000] + [70] * 119, 8, 1),             # a partial in about every second run
+    ([1, 0, 128] * 55 + [30001], 24, 2),
+    ([150] * 60 + [1300] + [150] * 20 + [5000] + [150] * 20, 12, 4),    # four, and twenty
+    ([1000 + 3 * i for i in range(40)], 40, 8)])
+def test_decode_long_sequences_among_short_ones(lens, N1, N2, form):
+    """At least as many tasks as runs, some of them cut by many runs: their joins are shared out."""
+    cache = S.Cache(len(lens) + N1, lens, N2, 32)
+    on = None
+    if form:
+        rng = np.random.default_rng(N1)
+        on = rng.random((len(lens), N1, -(-max(lens) // 128))) < 0.6
+        on[:, :, 0] = True
+        on[3, 0] = False
+    q, qd, q64 = S.queries(N1 + 1, len(lens), N1, False)
+    _compare(cache, q64, _decode(cache, q, qd, on, form or "mask"), on, str(form))
+
+
+def _device_us(lens, N1, N2):
+    """Shortest device time of a captured decode over `lens`, in microseconds."""
+    import block_sparse_fp8_gb300 as bsa
+
+    g = torch.Generator(device="cuda").manual_seed(1)
+    per = [-(-n // 32) for n in lens]
+    P = sum(per)
+    kp, vp = (torch.randint(0, 0x78, (P, N2, 32, 128), dtype=torch.uint8, device="cuda",
+                            generator=g) for _ in range(2))
+    kd = torch.rand(P, N2, 32, device="cuda", generator=g) * 0.01
+    table = torch.zeros(len(lens), max(per), dtype=torch.int32)
+    at = 0
+    for b, n in enumerate(per):
+        table[b, :n] = torch.arange(at, at + n)
+        at += n
+    table, used = table.cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda")
+    q = torch.randn(len(lens), N1, 128, device="cuda", generator=g).bfloat16()
+    call = lambda: bsa.decode(q, kp, vp, kd, torch.ones(N2, device="cuda"), used, table, max(lens))
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(10):
+            call()
+    best = float("inf")
+    for _ in range(6):
+        a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        a.record()
+        graph.replay()
+        b.record()
+        torch.cuda.synchronize()
+        best = min(best, a.elapsed_time(b) * 100)
+    return best
+
+
+def test_decode_time_does_not_hang_on_the_mix():
+    """One sequence of 512K tokens among 319 of 500, against 320 of as many tokens in all: 60 us
+    against 50, where the join by the first run's block alone took the first to 150."""
+    mixed = _device_us([512 * 1024] + [500] * 319, 16, 1)
+    even = _device_us([2137] * 320, 16, 1)
+    assert mixed < 2 * even, (mixed, even)
