@@ -850,7 +850,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
 // The join of the cut tasks.  A task's partials are its first run's last slot and the first slots of
 // the runs that follow, up to the one that holds its last tile.  Launched while the attention kernel
 // runs: the blocks find their partials in that kernel's shadow, in the registers it leaves
-// free, and then wait for its writes.  With fewer tasks than runs (`by_task`) a task has many
+// free (up to eight heads per KV head; the kernels for more leave none), and then wait for its writes.  With fewer tasks than runs (`by_task`) a task has many
 // partials: a block joins one head of one task, its warps sharing the partials out.  Otherwise most
 // cut tasks have two or three, but a long sequence among short ones may have one in every run, so a
 // task is joined by the blocks of the runs that it leaves unfinished, as many as there are heads:

@@ -939,9 +939,11 @@ extern "C" bsa_status_t bsa_fp8_decode(const bsa_fp8_decode_dims_t *d, const voi
                         stream, p, tk, tv))
     return BSA_ERR_CUDA;
   if (plan.whole || p.Kb <= 1) return BSA_OK;  // no task is cut
-  // The join.  Beside two attention CTAs an SM has registers for one block of eight warps, two
-  // of four or five of two: the most warps a task's head with which every block is resident
-  // before the attention kernel ends.
+  // The join, 62 registers.  Beside two CTAs of the dense kernel for up to eight heads (184
+  // registers) an SM has room for one block of eight warps, two of four or four of two; beside
+  // the list kernel's (200) for one of four or three of two; the kernels for more heads (254)
+  // leave none, and there the join starts as their CTAs end.  Taken are the most warps a task's head
+  // with which nearly every block is resident beside the dense kernel.
   const long long tasks = (long long)d->B * d->N2;
   const bool by_task = tasks < plan.grid;
   const int warps = !by_task ? 4 : tasks * p.G <= num_sms ? 8 : tasks * p.G <= 2 * num_sms ? 4 : 2;
