@@ -610,7 +610,7 @@ def merge_states(outs, lses, out=None, lse=None, return_lse: bool = True, stream
     """Joins attention results over disjoint sets of keys: outs are 1 to MAX_MERGE bf16 tensors
     [T, N1, 128] and lses their fp32 LSEs [N1, T], as prefill() and decode() return them (for
     decode T = B).  Returns (out, lse) over the union of the keys.  `out` may be one of `outs`
-    and `lse` one of `lses`."""
+    and `lse` one of `lses`; memory that overlaps in part is refused."""
     torch, bf16, f32, _, _ = _torch_names()
     n = len(outs)
     if n < 1 or n > MAX_MERGE or len(lses) != n:

@@ -1012,6 +1012,11 @@ extern "C" bsa_status_t bsa_fp8_gather_kv(const bsa_fp8_gather_dims_t *d, const 
   return cudaGetLastError() == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
 }
 
+static bool overlap(const void *a, size_t na, const void *b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + nb && y < x + na;
+}
+
 extern "C" bsa_status_t bsa_fp8_merge_states(int count, const void *const *outs,
                                              const float *const *lses, int T, int N1,
                                              void *out_bf16, float *lse_f32, void *stream) {
@@ -1030,6 +1035,14 @@ extern "C" bsa_status_t bsa_fp8_merge_states(int count, const void *const *outs,
     p.outs[i] = static_cast<const __nv_bfloat16 *>(outs[i]);
     p.lses[i] = lses[i];
   }
+  // an element is written once its own sources have been read, not its neighbours'
+  const size_t nz = (size_t)T * N1 * 4, nl = lse_f32 ? nz : 0, no = (size_t)T * N1 * HEAD_DIM * 2;
+  if (overlap(out_bf16, no, lse_f32, nl)) return BSA_ERR_INVALID_ARGUMENT;
+  for (int i = 0; i < count; ++i)
+    if ((out_bf16 != outs[i] && overlap(out_bf16, no, outs[i], no)) ||
+        (lse_f32 != lses[i] && overlap(lse_f32, nl, lses[i], nz)) ||
+        overlap(out_bf16, no, lses[i], nz) || overlap(lse_f32, nl, outs[i], no))
+      return BSA_ERR_INVALID_ARGUMENT;
   int num_sms = 0;
   const bsa_status_t st = check_device(0, &num_sms);
   if (st != BSA_OK) return st;

@@ -431,7 +431,8 @@ bsa_status_t bsa_fp8_gather_kv(const bsa_fp8_gather_dims_t *dims, const void *k_
  * [T, N1, 128], 16-byte aligned, and fp32 [N1, T], in the prefill's and the decode's layouts.  A
  * part whose LSE is -FLT_MAX (or -inf) saw no key: its O is not used, whatever it holds; a row
  * with no other part gets O = 0 and LSE = -FLT_MAX.  out_bf16 may be one of `outs` and lse_f32
- * (or NULL) one of `lses`; otherwise they must not overlap the inputs.  T * N1 <= 2^31 - 1. */
+ * (or NULL) one of `lses`; any other overlap of them with the inputs or with each other is refused
+ * (BSA_ERR_INVALID_ARGUMENT).  T * N1 <= 2^31 - 1. */
 bsa_status_t bsa_fp8_merge_states(int count, const void *const *outs, const float *const *lses,
                                   int T, int N1, void *out_bf16, float *lse_f32, void *stream);
 

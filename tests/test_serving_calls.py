@@ -73,3 +73,30 @@ def test_tensors_come_from_the_stream_of_the_call(name, monkeypatch):
     with contextlib.suppress(ValueError):
         call(stream=side)
     assert a.seen == [side] * count
+
+
+def test_merge_refuses_memory_that_overlaps_in_part():
+    """Outputs may be one of the inputs; any other overlap is refused before CUDA is touched."""
+    import ctypes
+    import os
+    import shutil
+
+    from block_sparse_fp8_gb300 import _build
+
+    if _build.needs_build():
+        if shutil.which(_build.nvcc()) is None and not os.path.exists(_build.nvcc()):
+            pytest.skip("nvcc not available")
+        _build.build()
+    T, N1 = 4, 8
+    O, L = T * N1 * 256, T * N1 * 4                     # bytes of a part's O and LSE
+    a, b, la, lb, end = 1 << 20, 2 << 20, 3 << 20, 4 << 20, 5 << 20      # never dereferenced
+
+    def status(out, lse):
+        outs, lses = (ctypes.c_void_p * 2)(a, b), (ctypes.c_void_p * 2)(la, lb)
+        return bsa.lib().bsa_fp8_merge_states(2, outs, lses, T, N1, out, lse, None)
+
+    for out, lse in ((a + 256, end), (b - 16, end), (b + O - 16, end), (end, la + 4),
+                     (end, lb + L - 4), (end, lb - 4), (la, end), (lb - O + 16, end), (end, a),
+                     (end, b + O - 4), (end, end), (end, end + O - 4), (a, b), (a + 256, None),
+                     (a, la + 4)):
+        assert status(out, lse) == 1, (out, lse)
