@@ -371,7 +371,8 @@ size_t bsa_fp8_decode_workspace_size(const bsa_fp8_decode_dims_t *dims);
  *                   forms with one Q tile).  Query heads of one KV head may enable different
  *                   tiles: a tile is read once for the heads that share it.
  *   softmax_scale   finite
- *   out_bf16        bf16 [B, N1, 128], 16-byte aligned
+ *   out_bf16        bf16 [B, N1, 128], 16-byte aligned; may be q itself (bf16, dense rows), and
+ *                   must not overlap an input otherwise
  *   lse_f32         fp32 [N1, B]; or NULL
  *   workspace       device buffer of at least bsa_fp8_decode_workspace_size(dims) bytes, 256-byte
  *                   aligned (BSA_ERR_WORKSPACE otherwise), written before it is read by every

@@ -279,3 +279,189 @@ def test_decode_time_does_not_hang_on_the_mix():
     mixed = _device_us([512 * 1024] + [500] * 319, 16, 1)
     even = _device_us([2137] * 320, 16, 1)
     assert mixed < 2 * even, (mixed, even)
+
+
+@pytest.mark.parametrize("before", ["copy", "memset", "fork", "nothing"])
+@pytest.mark.parametrize("sparse", [False, True])
+def test_decode_captured_behind_other_nodes(before, sparse):
+    """The programmatic launches as a capture's first nodes, and behind a copy, a memset and a join
+    of two streams: every replay waits for what the queries come from."""
+    import block_sparse_fp8_gb300 as bsa
+
+    cache = S.Cache(75, [3000, 200], 2, 32)
+    d = cache.device()
+    q, _, q64 = S.queries(76, 2, 8, False)
+    q = q.cuda()
+    given = torch.zeros_like(q) if before in ("copy", "fork") else q
+    word = torch.zeros(1, dtype=torch.int32, device="cuda")
+    kw = {}
+    if sparse:
+        kw["block_mask"] = torch.ones(2, 8, 24, dtype=torch.uint8, device="cuda")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        if before == "copy":
+            given.copy_(q)
+        elif before == "memset":
+            word.zero_()
+        elif before == "fork":
+            side.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(side):
+                given.copy_(q)
+                given.add_(0)
+            word.add_(1)
+            torch.cuda.current_stream().wait_stream(side)
+        got = bsa.decode(given, d["k_pages"], d["v_pages"], d["k_descale"], d["v_descale"],
+                         d["seqused_kv"], d["block_table"], 3000, dev_status=word, **d["kinds"],
+                         **kw)
+    for _ in range(3):
+        if given is not q:
+            given.zero_()
+        got[0].zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        _compare(cache, q64, got, what=before)
+
+
+@pytest.mark.parametrize("form", [None, "mask"])
+@pytest.mark.parametrize("lens,N1,N2", [([100, 300], 8, 2), ([9000, 10, 700], 12, 1),
+                                        ([400] * 90, 16, 4)])
+def test_decode_over_its_queries(lens, N1, N2, form):
+    """out may be q: a row is written when all that reads its query has been read."""
+    import block_sparse_fp8_gb300 as bsa
+
+    cache = S.Cache(sum(lens), lens, N2, 32)
+    d = cache.device()
+    q, _, q64 = S.queries(N1, len(lens), N1, False)
+    kw, on = {}, None
+    if form:
+        on = np.random.default_rng(1).random((len(lens), N1, -(-max(lens) // 128))) < 0.7
+        kw["block_mask"] = torch.from_numpy(on).cuda()
+    q = q.cuda()
+    got = bsa.decode(q, d["k_pages"], d["v_pages"], d["k_descale"], d["v_descale"],
+                     d["seqused_kv"], d["block_table"], max(lens), out=q, **d["kinds"], **kw)
+    assert got[0] is q
+    _compare(cache, q64, got, on, "in place")
+
+
+# ----------------------------------------------------------------------- forms in combination
+
+@pytest.mark.parametrize("form", ["mask", "index"])
+@pytest.mark.parametrize("q8,k_tok,v_head,nhd", [
+    (True, True, True, False), (True, False, False, True), (False, False, True, False),
+    (True, True, False, True), (False, True, False, False)])
+@pytest.mark.parametrize("lens,N1,N2,ps", [([900, 0, 3000], 8, 1, 32), ([130, 2000], 36, 3, 64),
+                                           ([300] * 40, 16, 8, 32)])
+def test_decode_sparse_types_and_scales(lens, N1, N2, ps, q8, k_tok, v_head, nhd, form):
+    """Lists and masks with either type of query, either kind of either scale and either layout, up
+    to more tasks than runs."""
+    cache = S.Cache(sum(lens) + N1, lens, N2, ps, k_tok, v_head, nhd)
+    on = np.random.default_rng(N1).random((len(lens), N1, -(-max(lens) // 128))) < 0.4
+    on[0, 0] = False
+    q, qd, q64 = S.queries(N1, len(lens), N1, q8)
+    _compare(cache, q64, _decode(cache, q, qd, on, form), on, form)
+
+
+@pytest.mark.parametrize("N1", [12, 24, 28, 40, 48])
+@pytest.mark.parametrize("T,n", [(1, 2), (777, 3)])
+def test_merge_head_counts(N1, T, n):
+    """Head counts that are no power of two."""
+    import block_sparse_fp8_gb300 as bsa
+    from test_gpu_serving import _merge_reference, _parts
+
+    outs, lses = _parts(T + N1, n, T, N1, 0.2)
+    out, lse = bsa.merge_states([o.cuda() for o in outs], [x.cuda() for x in lses])
+    O, Z, E, F = _merge_reference(outs, lses)
+    S.within(out, O, E, "merge O")
+    S.within(lse, Z, F, "merge LSE")
+
+
+@pytest.mark.parametrize("cuts", [[320], [160, 320], [32, 256, 320]])
+def test_prefills_over_parts_of_a_context_merge(cuts):
+    """A prompt behind a cached prefix: the prefill over the prefix (in parts, none of them causal)
+    and the one over the prompt itself, joined, against the prefill over both; and the decode of
+    its last token the same way.  Keys differ in one dimension, by integers, and the softmax
+    scale is ln 2, so every probability is a power of two, which the prefill's e4m3 holds.  What
+    is left: half a bf16 step of each part, 2^-8 |O_i| with its weight, and of the result, and
+    2^-13 of A = sum_j p_j |v_j| for the sums over at most 520 tokens."""
+    import block_sparse_fp8_gb300 as bsa
+
+    ps, N1, N2, T, P = 32, 8, 2, 200, 320
+    rng = np.random.default_rng(len(cuts))
+    n = P + T
+    pages = -(-n // ps)
+    level = rng.integers(0, 4, (N2, n))
+    kp = np.zeros((pages, N2, ps, 128), dtype=np.uint8)
+    vp = np.zeros_like(kp)
+    v = S.finite_codes(rng, (N2, n, 128))
+    for t in range(n):
+        kp[t // ps, :, t % ps, 0] = np.array([0x00, 0x38, 0x40, 0x44])[level[:, t]]
+        vp[t // ps, :, t % ps] = v[:, t]
+    kp, vp = torch.from_numpy(kp).cuda(), torch.from_numpy(vp).cuda()
+    kd, vd = torch.ones(pages, N2, ps, device="cuda"), torch.full((N2,), 0.01, device="cuda")
+    q = torch.zeros(T, N1, 128, dtype=torch.uint8, device="cuda")
+    q[:, :, 0] = 0x38
+    qd = torch.ones(T, N1, device="cuda")
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    table, scale = torch.arange(pages, dtype=torch.int32, device="cuda"), float(np.log(2.0))
+
+    def part(lo, hi, causal):
+        return bsa.prefill(q, kp, vp, qd, kd, vd, i32([0, T]), i32([hi - lo]),
+                           table[lo // ps:-(-hi // ps)].view(1, -1).clone(), T, hi - lo,
+                           softmax_scale=scale, causal=causal)
+
+    def last(lo, hi):
+        return bsa.decode(q[-1:], kp, vp, kd, vd, i32([hi - lo]),
+                          table[lo // ps:-(-hi // ps)].view(1, -1).clone(), hi - lo,
+                          q_descale=qd[-1:], softmax_scale=scale)
+
+    ends = [0] + cuts
+    spans = list(zip(ends, ends[1:])) + [(P, n)]
+    parts = [part(a, b, b == n) for a, b in spans]
+    joined = bsa.merge_states([x[0] for x in parts], [x[1] for x in parts])
+    whole = part(0, n, True)
+    lasts = [last(a, b) for a, b in spans]
+    joined1 = bsa.merge_states([x[0] for x in lasts], [x[1] for x in lasts])
+    whole1 = last(0, n)
+    values = S.VAL[v] * np.float64(np.float32(0.01))
+    G = N1 // N2
+    O, A, R, Z = (np.zeros((T, N1, 128)), np.zeros((T, N1, 128)), np.zeros((T, N1, 128)),
+                  np.zeros((N1, T)))
+    for t in range(T):
+        for g in range(N2):
+            m = P + t + 1                                # the tokens that row t sees
+            p = 2.0 ** level[g, :m]
+            heads = slice(g * G, (g + 1) * G)
+            O[t, heads] = p @ values[g, :m] / p.sum()
+            A[t, heads] = p @ np.abs(values[g, :m]) / p.sum()
+            Z[heads, t] = np.log(p.sum())
+            for a, b in spans:                           # the parts' own results, with their weights
+                R[t, heads] += np.abs(p[a:b] @ values[g, a:min(b, m)]) / p.sum()
+    step, sums, lse = 2.0 ** -8, 2.0 ** -13 * A, np.full_like(Z, 2.0 ** -13)
+    S.within(whole[0], O, step * np.abs(O) + sums, "whole O")
+    S.within(whole[1], Z, lse, "whole LSE")
+    S.within(joined[0], O, step * (np.abs(O) + R) * (1 + 2.0 ** -8) + sums, "joined O")
+    S.within(joined[1], Z, lse, "joined LSE")
+    S.within(whole1[0], O[-1:], (step * np.abs(O) + sums)[-1:], "last O")
+    S.within(joined1[0], O[-1:], (step * (np.abs(O) + R) * (1 + 2.0 ** -8) + sums)[-1:],
+             "joined last O")
+    S.within(joined1[1], Z[:, -1:], lse[:, -1:], "joined last LSE")
+
+
+@pytest.mark.parametrize("nhd", [False, True])
+@pytest.mark.parametrize("f32", [False, True])
+def test_gather_one_head_many_blocks(f32, nhd):
+    """One KV head, rows enough for every size of a block's run of tokens."""
+    import block_sparse_fp8_gb300 as bsa
+
+    lens = [20000, 0, 1, 60000]
+    cache = S.Cache(9, lens, 1, 64, nhd=nhd)
+    d = cache.device()
+    cu = torch.tensor(np.cumsum([0] + lens), dtype=torch.int32, device="cuda")
+    k, v = bsa.gather_kv(d["k_pages"], d["v_pages"], d["k_descale"], d["v_descale"], cu,
+                         d["block_table"], sum(lens), **d["kinds"],
+                         out_dtype=torch.float32 if f32 else torch.bfloat16)
+    for got, i in ((k, 0), (v, 1)):
+        want = np.concatenate([cache.rows(b)[i].transpose(1, 0, 2) for b in range(4)])
+        assert torch.equal(got.cpu(), torch.from_numpy(want.astype(np.float32)).to(got.dtype))
