@@ -670,7 +670,9 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
         alpha[nt][c] = ptx::ex2_approx(m[nt][c] - base);
         moved |= mn != m[nt][c];
         m[nt][c] = mn;
-        ref[c] = base - P_SHIFT;
+        // rounded up: beyond 2^24 the nearest number may lie 16 below, where the largest weight,
+        // 2^16, is no fp16 number (the shift is then less than 15, scores are whole numbers)
+        ref[c] = __fadd_ru(base, -P_SHIFT);
       }
       float sum0 = 0.f, sum1 = 0.f;
 #pragma unroll

@@ -465,3 +465,35 @@ def test_gather_one_head_many_blocks(f32, nhd):
     for got, i in ((k, 0), (v, 1)):
         want = np.concatenate([cache.rows(b)[i].transpose(1, 0, 2) for b in range(4)])
         assert torch.equal(got.cpu(), torch.from_numpy(want.astype(np.float32)).to(got.dtype))
+
+
+# ------------------------------------------------------------------------------- wide ranges
+
+@pytest.mark.parametrize("power", [4, 16, 17, 18, 19, 20, 21, 22, 23, 24, 40, 100])
+@pytest.mark.parametrize("N1,form", [(8, None), (16, "mask")])
+def test_decode_large_scores(power, N1, form):
+    """Scores far above 2^24, where fp32 holds no odd numbers: integers below 2^7 times 2^power.
+    Scores that differ do so by at least 2^(power + 1) > 30, so a row is the mean of V over the
+    tokens of its largest score: half a bf16 step, 2^-12 of A for the rest (as above)."""
+    lens = [300, 37]
+    cache = S.Cache(power, lens, 1, 32)
+    _unit_keys(cache)
+    cache.kd_pages = np.where(np.isnan(cache.kd_pages), cache.kd_pages, 1.0).astype(np.float32)
+    rng = np.random.default_rng(power)
+    sign = rng.choice([-1.0, 1.0], (2, N1, 128))
+    q = torch.from_numpy(sign * 2.0 ** power).to(torch.bfloat16)
+    on = None
+    if form:
+        on = rng.random((2, N1, 3)) < 0.7
+        on[:, :, 0] = True
+    out, lse = _decode(cache, q, None, on, scale=1.0)
+    for b, n in enumerate(lens):
+        k, v = S.VAL[cache.k[b][0]], cache.rows(b)[1][0]
+        for h in range(N1):
+            take = np.ones(n, bool) if on is None else np.repeat(on[b, h], S.TILE)[:n]
+            s = np.where(take, k @ sign[b, h], -np.inf)
+            best = s == s.max()
+            O, A = v[best].mean(0), np.abs(v[best]).mean(0)
+            S.within(out[b, h], O, 2.0 ** -8 * np.abs(O) + 2.0 ** -12 * A, f"O of {b}, {h}")
+            z = s.max() * 2.0 ** power + np.log(best.sum())
+            assert abs(float(lse[h, b]) - z) <= 2.0 ** -21 * abs(z) + 2.0 ** -15
