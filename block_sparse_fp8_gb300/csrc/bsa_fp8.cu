@@ -939,7 +939,7 @@ extern "C" bsa_status_t bsa_fp8_decode(const bsa_fp8_decode_dims_t *d, const voi
                         stream, p, tk, tv))
     return BSA_ERR_CUDA;
   if (plan.whole || p.Kb <= 1) return BSA_OK;  // no task is cut
-  // The join, 62 registers.  Beside two CTAs of the dense kernel for up to eight heads (184
+  // The join, 64 registers.  Beside two CTAs of the dense kernel for up to eight heads (184
   // registers) an SM has room for one block of eight warps, two of four or four of two; beside
   // the list kernel's (200) for one of four or three of two; the kernels for more heads (254)
   // leave none, and there the join starts as their CTAs end.  Taken are the most warps a task's head

@@ -497,3 +497,13 @@ def test_decode_large_scores(power, N1, form):
             S.within(out[b, h], O, 2.0 ** -8 * np.abs(O) + 2.0 ** -12 * A, f"O of {b}, {h}")
             z = s.max() * 2.0 ** power + np.log(best.sum())
             assert abs(float(lse[h, b]) - z) <= 2.0 ** -21 * abs(z) + 2.0 ** -15
+
+
+@pytest.mark.parametrize("vd", [1e-37, 1e-30, 1e30])
+@pytest.mark.parametrize("lens", [[300], [20000, 40]])
+def test_decode_value_magnitudes(vd, lens):
+    """V descales near the ends of fp32's range."""
+    cache = S.Cache(7, lens, 2, 32)
+    cache.vd[:] = vd
+    q, qd, q64 = S.queries(8, len(lens), 8, False)
+    _compare(cache, q64, _decode(cache, q, qd), what="values")
