@@ -199,8 +199,8 @@ __device__ __forceinline__ void write_row(const Params &p, int b, int kvh, int g
   const int h = kvh * p.G + g;
   const bool some = l != 0.f;  // a NaN sum is a result, not an empty row
   // (the quotient first: a small descale over a large sum may leave fp32's normal numbers)
-  const float f = some ? 1.f / l : 0.f;
   const float vd = !some ? 0.f : p.v_per_head ? p.v_descale[kvh] : p.v_descale[0];
+  const float f = 1.f / (some ? l : 1.f);
   if (!some) o = make_float4(0.f, 0.f, 0.f, 0.f);
   const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x * f * vd, o.y * f * vd);
   const __nv_bfloat162 hi = __floats2bfloat162_rn(o.z * f * vd, o.w * f * vd);
