@@ -25,9 +25,9 @@
 //     (values below 2^-28 of the row's largest lose bits).  P goes in as two fp16 terms, the
 //     rounded value and what the rounding left, together 2^-22 relative or 2^-40 of the largest
 //     weight, whichever is more; one term alone moves one result in fifteen by a bf16 step.
-//     Accumulation, maxima and sums are fp32 (the products cut off what lies below a sum's last
-//     bit, about 2^-25 of it each: after 400 of them one result in 300 is a bf16 step off, sums
-//     taken outside leave one in 2000, at 2 to 8% of the time).
+//     Accumulation, maxima and sums are fp32.  A tile's products start from zero and are added to
+//     the sums outside: mma.sync cuts off what lies below its accumulator's last bit, some 2^-25
+//     of it each time, which pulled a run of 1000 products 2^-15 towards zero.
 //   * The 128-byte swizzle (a row's 16-byte chunks XORed with the row number) keeps the fragment
 //     reads of K (a thread: 32 dimensions of one token) and V (16 dimensions of one token) free of
 //     bank conflicts.
@@ -657,7 +657,6 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
     }
     // P as B fragments: [16 tokens][rounded, rest][tokens 2 q4 | 2 q4 + 8, head r]
     uint32_t pf[NT][2][2][2];
-    bool moved = false;
     float alpha[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -671,7 +670,6 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
         const float mn = fmaxf(m[nt][c], mx);
         const float base = mn == -INFINITY ? 0.f : mn;
         alpha[nt][c] = ptx::ex2_approx(m[nt][c] - base);
-        moved |= mn != m[nt][c];
         m[nt][c] = mn;
         // rounded up: beyond 2^24 the nearest number may lie 16 below, where the largest weight,
         // 2^16, is no fp16 number (the shift is then less than 15, scores are whole numbers)
@@ -697,59 +695,59 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
       l[nt][0] = l[nt][0] * alpha[nt][0] + sum0;
       l[nt][1] = l[nt][1] * alpha[nt][1] + sum1;
     }
-    if (__any_sync(0xffffffffu, moved)) {
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) acc[nt][i][c] *= alpha[nt][c & 1];
-    }
     // With `masked` the columns of heads that mask the tile keep their sums: their weights are zero,
     // but zero times a NaN of the tile's V would reach them through the shared product.
     const auto pv = [&](const bool masked) {
+      uint4 v[2][4];  // [16 tokens][tokens 2 q4, 2 q4 + 1 and those + 8], dimensions 16 r .. 16 r + 15
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt) {
-        // tokens 2 q4, 2 q4 + 1 and those + 8, dimensions 16 r .. 16 r + 15
         const uint32_t t0 = st + OFF_V + (mt * 16 + 2 * q4) * HEAD_DIM;
         const uint32_t c0 = (r ^ (2 * q4)) << 4, c1 = (r ^ (2 * q4 + 1)) << 4;
-        uint4 x0 = lds128(t0 + c0), x1 = lds128(t0 + HEAD_DIM + c1);
-        uint4 y0 = lds128(t0 + 8 * HEAD_DIM + c0), y1 = lds128(t0 + 9 * HEAD_DIM + c1);
+        v[mt][0] = lds128(t0 + c0);
+        v[mt][1] = lds128(t0 + HEAD_DIM + c1);
+        v[mt][2] = lds128(t0 + 8 * HEAD_DIM + c0);
+        v[mt][3] = lds128(t0 + 9 * HEAD_DIM + c1);
         if (left < TOK) {  // whatever lies past the end, NaN codes too, counts as zero
           const int t = mt * 16 + 2 * q4;
           const uint4 zero = make_uint4(0, 0, 0, 0);
-          if (t >= left) x0 = zero;
-          if (t + 1 >= left) x1 = zero;
-          if (t + 8 >= left) y0 = zero;
-          if (t + 9 >= left) y1 = zero;
+          if (t >= left) v[mt][0] = zero;
+          if (t + 1 >= left) v[mt][1] = zero;
+          if (t + 8 >= left) v[mt][2] = zero;
+          if (t + 9 >= left) v[mt][3] = zero;
         }
-        const uint32_t wx0[4] = {x0.x, x0.y, x0.z, x0.w}, wx1[4] = {x1.x, x1.y, x1.z, x1.w};
-        const uint32_t wy0[4] = {y0.x, y0.y, y0.z, y0.w}, wy1[4] = {y1.x, y1.y, y1.z, y1.w};
+      }
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          // bytes of the two tokens interleaved: a fragment pairs tokens within a dimension
+      for (int w = 0; w < 4; ++w) {
+        float o[2][NT][4] = {};
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt) {
+          uint32_t x[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            x[k] = w == 0 ? v[mt][k].x : w == 1 ? v[mt][k].y : w == 2 ? v[mt][k].z : v[mt][k].w;
+          // bytes of two tokens interleaved: a fragment pairs tokens within a dimension
           uint32_t a[2][4];
-          f16_of_e4m3x4(__byte_perm(wx0[w], wx1[w], 0x5140), a[0][0], a[0][1]);
-          f16_of_e4m3x4(__byte_perm(wx0[w], wx1[w], 0x7362), a[1][0], a[1][1]);
-          f16_of_e4m3x4(__byte_perm(wy0[w], wy1[w], 0x5140), a[0][2], a[0][3]);
-          f16_of_e4m3x4(__byte_perm(wy0[w], wy1[w], 0x7362), a[1][2], a[1][3]);
+          f16_of_e4m3x4(__byte_perm(x[0], x[1], 0x5140), a[0][0], a[0][1]);
+          f16_of_e4m3x4(__byte_perm(x[0], x[1], 0x7362), a[1][0], a[1][1]);
+          f16_of_e4m3x4(__byte_perm(x[2], x[3], 0x5140), a[0][2], a[0][3]);
+          f16_of_e4m3x4(__byte_perm(x[2], x[3], 0x7362), a[1][2], a[1][3]);
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
+          for (int part = 1; part >= 0; --part)
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              float o[4];
+            for (int i = 0; i < 2; ++i)
 #pragma unroll
-              for (int c = 0; c < 4; ++c) o[c] = acc[nt][2 * w + i][c];
-#pragma unroll
-              for (int part = 0; part < 2; ++part)
-                mma16816(o, a[i][0], a[i][1], a[i][2], a[i][3], pf[nt][mt][part][0],
+              for (int nt = 0; nt < NT; ++nt)
+                mma16816(o[i][nt], a[i][0], a[i][1], a[i][2], a[i][3], pf[nt][mt][part][0],
                          pf[nt][mt][part][1]);
-#pragma unroll
-              for (int c = 0; c < 4; ++c)
-                if (!masked || ((heads >> (nt * 8 + 2 * q4 + (c & 1))) & 1))
-                  acc[nt][2 * w + i][c] = o[c];
-            }
         }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              if (!masked || ((heads >> (nt * 8 + 2 * q4 + (c & 1))) & 1))
+                acc[nt][2 * w + i][c] = fmaf(acc[nt][2 * w + i][c], alpha[nt][c & 1], o[i][nt][c]);
       }
     };
     if (!SPARSE || heads == group)

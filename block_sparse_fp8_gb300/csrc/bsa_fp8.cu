@@ -939,11 +939,10 @@ extern "C" bsa_status_t bsa_fp8_decode(const bsa_fp8_decode_dims_t *d, const voi
                         stream, p, tk, tv))
     return BSA_ERR_CUDA;
   if (plan.whole || p.Kb <= 1) return BSA_OK;  // no task is cut
-  // The join, 64 registers.  Beside two CTAs of the dense kernel for up to eight heads (184
-  // registers) an SM has room for one block of eight warps, two of four or four of two; beside
-  // the list kernel's (200) for one of four or three of two; the kernels for more heads (254)
-  // leave none, and there the join starts as their CTAs end.  Taken are the most warps a task's head
-  // with which nearly every block is resident beside the dense kernel.
+  // The join, 64 registers.  Beside two CTAs of the kernels for up to eight heads (220 registers,
+  // with lists 214) an SM has room for one block of four warps or two of two; the kernels for more
+  // heads (255) leave none.  Blocks that find no room start as attention CTAs end.  The more heads and
+  // tasks there are, the fewer warps a block has.
   const long long tasks = (long long)d->B * d->N2;
   const bool by_task = tasks < plan.grid;
   const int warps = !by_task ? 4 : tasks * p.G <= num_sms ? 8 : tasks * p.G <= 2 * num_sms ? 4 : 2;
