@@ -456,8 +456,8 @@ def decode(q, k_pages, v_pages, k_descale, v_descale, seqused_kv, block_table, m
     block_mask u8 [B, N1, Kb] or sparse_indices i32 [B, N1, Kb] + sparse_seq_len i32 [B, N1]
     select 128-token tiles for each query head, Kb = ceil(max_kv_len / 128).
     Returns (out bf16 [B, N1, 128], lse f32 [N1, B] or None); a sequence without tokens, or a head
-    without an enabled tile, gives 0 and -FLT_MAX.  `out` may be q itself.  `workspace` (decode_workspace_size bytes)
-    must not be shared by calls in flight at once."""
+    without an enabled tile, gives 0 and -FLT_MAX.  `out` may be q itself.  `workspace`
+    (decode_workspace_size bytes) must not be shared by calls in flight at once."""
     torch, bf16, f32, i32, codes = _torch_names()
     dev = q.get_device()
     shape = q.shape

@@ -33,12 +33,16 @@
 //     bank conflicts.
 //
 // Measured (mean of back-to-back calls, inputs from HBM): 64 sequences of 8-16K tokens, 64/8 heads
-// (1655 MB) 245 us, 6.75 TB/s, 99% of the measured copy rate and what a bare copy loop of the same
-// access pattern reaches.  The alternatives there: 16-byte cp.async by all lanes 257 us, three stages
-// 266 us, three CTAs per SM 260 us, one CTA of four stages 316 us (more in flight spoils the DRAM's
-// pattern, less does not fill it).  2 x 128K tokens, 32/4 heads (268 MB) 47 us; 8 x 50-64K at a
-// quarter of the tiles (243 MB) 48 us; 16 ragged sequences (62 MB) 17.5 us; one of 300 tokens 5.2 us:
-// the first tile is done after 4 to 5 us (length, page, rows: a chain of reads), the join takes 2.5.
+// (1655 MB) 245 us, 6.75 TB/s, 99% of the measured copy rate; a bare loop of the same copies reaches
+// 6.99 TB/s, which would be 237 us.  The alternatives there, measured in an earlier form of 245 us:
+// 16-byte cp.async by all lanes 257 us, three stages 266 us, three CTAs per SM 260 us, one CTA of four
+// stages 316 us (more in flight spoils the DRAM's pattern, less does not fill it).  2 x 128K
+// tokens, 32/4 heads (268 MB) 47.5 us; 8 x 50-64K at a quarter of the tiles (243 MB) 49.5 us; 16
+// ragged sequences (62 MB) 18.4 us; one of 300 tokens 5.3 us: the first tile is done after 4 to 5 us
+// (length, page, rows: a chain of reads), the join takes 2.5.  That HBM is the bound holds up to eight
+// query heads per KV head.  Sixteen double the products and the softmax, on the same eight warps an SM:
+// 16 x 32K tokens, 64/4 heads (545 MB, 80 us at the copy rate) 113 us, 125 us under masks that leave
+// each head a quarter of the tiles (and all heads together nearly all): bound by issue and latency.
 #pragma once
 
 #include <cuda.h>
@@ -852,14 +856,15 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
 // ------------------------------------------------------------------------------------------
 // The join of the cut tasks.  A task's partials are its first run's last slot and the first slots of
 // the runs that follow, up to the one that holds its last tile.  Launched while the attention kernel
-// runs: the blocks find their partials in that kernel's shadow, in the registers it leaves
-// free (up to eight heads per KV head; the kernels for more leave none), and then wait for its writes.  With fewer tasks than runs (`by_task`) a task has many
-// partials: a block joins one head of one task, its warps sharing the partials out.  Otherwise most
-// cut tasks have two or three, but a long sequence among short ones may have one in every run, so a
-// task is joined by the blocks of the runs that it leaves unfinished, as many as there are heads:
-// they deal the heads out among them, a head a warp, or, with more partials than a warp reads at
-// once, a head a block, whose warps share the partials out (one sequence of 512K tokens among 319
-// of 500, one KV head, 8 query heads: 48 us, with all heads in the first run's block 92).
+// runs: the blocks find their partials in that kernel's shadow, in the registers it leaves free (up
+// to eight heads per KV head; the kernels for more leave none), and then wait for its writes.
+// With fewer tasks than runs (`by_task`) a task has many partials: a block joins one head of one task,
+// its warps sharing the partials out.  Otherwise most cut tasks have two or three, but a long
+// sequence among short ones may have one in every run, so a task is joined by the blocks of the
+// runs that it leaves unfinished, as many as there are heads: they deal the heads out among them, a
+// head a warp, or, with more partials than a warp reads at once, a head a block, whose warps
+// share the partials out (one sequence of 512K tokens among 319 of 500, one KV head, 8 query heads: 48
+// us, with all heads in the first run's block 92).
 // ------------------------------------------------------------------------------------------
 constexpr int JOIN_AHEAD = 5;  // partials in flight per warp
 

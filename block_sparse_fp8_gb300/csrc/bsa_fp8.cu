@@ -744,10 +744,6 @@ bsa_status_t validate_decode(const bsa_fp8_decode_dims_t *d) {
   return BSA_OK;
 }
 
-}  // namespace
-
-namespace {
-
 // Grid of the decode kernel and where its workspace arrays lie.  The grid depends on the SM count
 // and an upper bound of the tiles only: the host does not know the lengths.
 struct DecodePlan {
@@ -939,7 +935,7 @@ extern "C" bsa_status_t bsa_fp8_decode(const bsa_fp8_decode_dims_t *d, const voi
                         stream, p, tk, tv))
     return BSA_ERR_CUDA;
   if (plan.whole || p.Kb <= 1) return BSA_OK;  // no task is cut
-  // The join, 64 registers.  Beside two CTAs of the kernels for up to eight heads (220 registers,
+  // The join, 62 registers.  Beside two CTAs of the kernels for up to eight heads (220 registers,
   // with lists 214) an SM has room for one block of four warps or two of two; the kernels for more
   // heads (255) leave none.  Blocks that find no room start as attention CTAs end.  The more heads and
   // tasks there are, the fewer warps a block has.
