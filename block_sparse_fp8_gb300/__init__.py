@@ -6,6 +6,9 @@ and the quantise step ``bsa_fp8_quantize_rows`` / ``bsa_fp8_append_kv``; ``prefi
 marshals CPU tensors into ``bsa_fp8_prefill_host``, which copies them in and the results out.
 ``decode`` / ``gather_kv`` / ``merge_states`` serve from the same cache: the next token's
 attention, the cache read back, and the join of attention results over parts of a cache.
+Around them: ``rope`` / ``rope_quantize`` (rotary positions), ``assign_pages`` / ``release_pages``
+(block tables and slot maps from the requests' lengths), and a cache held in 4 bits:
+``append_kv_fp4`` / ``gather_kv_fp4`` / ``decode_fp4``.
 Every step of the computation runs in the library's CUDA kernels; there is no CPU path.
 Every call takes ``stream=`` (default: the current one).  The caller sees to it that the inputs are
 ready there; outputs and workspaces that the call makes itself come from that stream's memory.
@@ -27,7 +30,11 @@ __all__ = ["Dims", "AppendDims", "Tensors", "TENSOR_NAMES", "Q_TND", "Q_NTD", "K
            "DESCALE_AMAX", "DESCALE_UE8M0", "DecodeDims", "GatherDims", "make_decode_dims",
            "decode", "decode_workspace_size", "gather_kv", "merge_states", "QTYPE_BF16",
            "QTYPE_E4M3", "OUT_BF16", "OUT_FP32", "MAX_MERGE",
-           "DEV_BAD_INDEX", "DEV_BAD_PAGE", "DEV_BAD_SEQLEN", "DEV_TIMEOUT"]
+           "rope", "rope_quantize", "rope_frequencies", "ROPE_HALF", "ROPE_INTERLEAVED", "ROPE_NONE",
+           "ROPE_LINEAR", "ROPE_BASE", "ROPE_PARTS", "RopeDims", "assign_pages", "release_pages",
+           "PagesDims", "append_kv_fp4", "gather_kv_fp4", "decode_fp4",
+           "decode_fp4_workspace_size", "Fp4AppendDims",
+           "DEV_BAD_INDEX", "DEV_BAD_PAGE", "DEV_BAD_SEQLEN", "DEV_TIMEOUT", "DEV_NO_PAGES"]
 
 SCALE_PER_TENSOR = 0
 SCALE_PER_TOKEN_HEAD = 1
@@ -37,12 +44,15 @@ DEV_BAD_INDEX = 1
 DEV_BAD_PAGE = 2
 DEV_BAD_SEQLEN = 4
 DEV_TIMEOUT = 8
+DEV_NO_PAGES = 16
 
 EXPORTED = ("bsa_fp8_prefill", "bsa_fp8_prefill_workspace_size", "bsa_fp8_compact_tiles",
             "bsa_fp8_prefill_noalloc", "bsa_fp8_prefill_host", "bsa_fp8_quantize_rows",
             "bsa_fp8_quantize_rows_ue8m0", "bsa_fp8_append_kv", "bsa_fp8_set_wait_limit_ns",
             "bsa_fp8_decode", "bsa_fp8_decode_workspace_size", "bsa_fp8_gather_kv",
-            "bsa_fp8_merge_states", "bsa_status_string")
+            "bsa_fp8_merge_states", "bsa_rope_frequencies", "bsa_rope", "bsa_rope_quantize",
+            "bsa_assign_pages", "bsa_release_pages", "bsa_fp4_append_kv", "bsa_fp4_gather_kv",
+            "bsa_fp4_decode", "bsa_fp4_decode_workspace_size", "bsa_status_string")
 
 # descale rules of the quantise step
 DESCALE_AMAX = 0    # amax / 448
@@ -100,6 +110,27 @@ class GatherDims(ctypes.Structure):
         "v_scale_kind", "kv_layout", "out_type")]
 
 
+# pairs of a rotated head, and how frequencies are stretched
+ROPE_HALF, ROPE_INTERLEAVED = 0, 1
+ROPE_NONE, ROPE_LINEAR, ROPE_BASE, ROPE_PARTS = 0, 1, 2, 3
+
+
+class RopeDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("T", "N1", "N2", "D", "rotary_dim", "layout")] + [
+        (n, ctypes.c_longlong) for n in ("q_stride", "k_stride", "q_out_stride", "k_out_stride")]
+
+
+class PagesDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in (
+        "B", "page_size", "num_pages", "max_pages_per_seq", "total")]
+
+
+class Fp4AppendDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in (
+        "N2", "D", "page_size", "num_pages", "total_new", "k_scale_kind", "v_scale_kind",
+        "kv_layout")] + [(n, ctypes.c_longlong) for n in ("k_stride", "v_stride")]
+
+
 _lib = None
 
 
@@ -142,6 +173,26 @@ def lib():
         L.bsa_fp8_gather_kv.argtypes = [ctypes.POINTER(GatherDims)] + [vp] * 11
         L.bsa_fp8_merge_states.restype = i32
         L.bsa_fp8_merge_states.argtypes = [i32, vp, vp, i32, i32, vp, vp, vp]
+        f64 = ctypes.c_double
+        L.bsa_rope_frequencies.restype = i32
+        L.bsa_rope_frequencies.argtypes = [i32, i32, f64, f64, f64, f64, f64, vp, vp]
+        L.bsa_rope.restype = i32
+        L.bsa_rope.argtypes = [ctypes.POINTER(RopeDims)] + [vp] * 4 + [f32] + [vp] * 3
+        L.bsa_rope_quantize.restype = i32
+        L.bsa_rope_quantize.argtypes = [ctypes.POINTER(RopeDims)] + [vp] * 3 + [f32, i32] + [vp] * 3
+        L.bsa_assign_pages.restype = i32
+        L.bsa_assign_pages.argtypes = [ctypes.POINTER(PagesDims)] + [vp] * 11
+        L.bsa_release_pages.restype = i32
+        L.bsa_release_pages.argtypes = [ctypes.POINTER(PagesDims)] + [vp] * 8
+        L.bsa_fp4_append_kv.restype = i32
+        L.bsa_fp4_append_kv.argtypes = [ctypes.POINTER(Fp4AppendDims)] + [vp] * 11
+        L.bsa_fp4_gather_kv.restype = i32
+        L.bsa_fp4_gather_kv.argtypes = [ctypes.POINTER(GatherDims)] + [vp] * 13
+        L.bsa_fp4_decode.restype = i32
+        L.bsa_fp4_decode.argtypes = [ctypes.POINTER(DecodeDims)] + [vp] * 13 + [f32, vp, vp, vp,
+                                                                                sz, vp, vp]
+        L.bsa_fp4_decode_workspace_size.restype = sz
+        L.bsa_fp4_decode_workspace_size.argtypes = [ctypes.POINTER(DecodeDims)]
         L.bsa_status_string.restype = ctypes.c_char_p
         L.bsa_status_string.argtypes = [i32]
         _lib = L
@@ -419,6 +470,17 @@ def _check_status(dev_status, dev):
         raise ValueError("dev_status must be an int32 tensor on the device of the others")
 
 
+def _check_fp4(k_pages, v_pages, k_scales, v_scales, pool, scales, dev):
+    """The pages and block scales of a 4-bit cache; a side whose pages are None is not looked at."""
+    torch, codes = _torch_names()[0], _torch_names()[4]
+    for name, t, sc in (("k", k_pages, k_scales), ("v", v_pages, v_scales)):
+        if t is not None:
+            if sc is None:
+                raise ValueError(f"{name}_pages given without {name}_scales")
+            _check(name + "_pages", t, torch.uint8, pool, dev)
+            _check(name + "_scales", sc, sc.dtype if sc.dtype in codes else codes, scales, dev)
+
+
 def _pool(pages, kv_layout):
     """(pages, KV heads, page size, head dim) of a page pool."""
     shape = pages.shape
@@ -444,20 +506,11 @@ def decode_workspace_size(dims: DecodeDims) -> int:
     return int(lib().bsa_fp8_decode_workspace_size(ctypes.byref(dims)))
 
 
-def decode(q, k_pages, v_pages, k_descale, v_descale, seqused_kv, block_table, max_kv_len: int,
-           q_descale=None, block_mask=None, sparse_indices=None, sparse_seq_len=None,
-           softmax_scale: float | None = None, out=None, lse=None, return_lse: bool = True,
-           dev_status=None, workspace=None, stream=None, k_scale_kind: int | None = None,
-           v_scale_kind: int | None = None, kv_layout: int = KV_HND):
-    """Attention of one new token per sequence over the paged cache (whose seqused_kv counts the
-    new token, appended beforehand).  q bf16 [B, N1, 128], or uint8/float8_e4m3fn with q_descale
-    f32 [B, N1]; its rows may lie further apart than N1 * 128 (a slice of a wider projection).
-    Pages, descales, block_table and scale kinds as in prefill(); seqused_kv i32 [B];
-    block_mask u8 [B, N1, Kb] or sparse_indices i32 [B, N1, Kb] + sparse_seq_len i32 [B, N1]
-    select 128-token tiles for each query head, Kb = ceil(max_kv_len / 128).
-    Returns (out bf16 [B, N1, 128], lse f32 [N1, B] or None); a sequence without tokens, or a head
-    without an enabled tile, gives 0 and -FLT_MAX.  `out` may be q itself.  `workspace`
-    (decode_workspace_size bytes) must not be shared by calls in flight at once."""
+def _decode(fn, what, size, fp4, q, k_pages, v_pages, k_scales, v_scales, k_descale,
+            v_descale, seqused_kv, block_table, max_kv_len, q_descale, block_mask, sparse_indices,
+            sparse_seq_len, softmax_scale, out, lse, return_lse, dev_status, workspace, stream,
+            k_scale_kind, v_scale_kind, kv_layout):
+    """decode() and decode_fp4(), which gives block scales."""
     torch, bf16, f32, i32, codes = _torch_names()
     dev = q.get_device()
     shape = q.shape
@@ -476,20 +529,28 @@ def decode(q, k_pages, v_pages, k_descale, v_descale, seqused_kv, block_table, m
             if q_stride >= 1 << 31:
                 raise ValueError(f"q's rows lie {q_stride} elements apart: 2^31 - 1 at most")
     P, N2, ps, pool_d = _pool(k_pages, kv_layout)
-    if pool_d != D:
+    if pool_d != (D // 2 if fp4 else D):
         raise ValueError(f"k_pages has shape {tuple(k_pages.shape)}, q a head dim of {D}")
     table = block_table.shape
     if len(table) != 2:
         raise ValueError(f"block_table has shape {tuple(table)}, expected [B, L]")
-    k_kind = k_scale_kind if k_scale_kind is not None else (
-        SCALE_PER_TOKEN_HEAD if k_descale.dim() == 3 else SCALE_PER_TENSOR)
+    if k_scale_kind is not None:
+        k_kind = k_scale_kind
+    elif fp4:
+        k_kind = SCALE_PER_HEAD if k_descale.numel() == N2 else SCALE_PER_TENSOR
+    else:
+        k_kind = SCALE_PER_TOKEN_HEAD if k_descale.dim() == 3 else SCALE_PER_TENSOR
     v_kind = v_scale_kind if v_scale_kind is not None else (
         SCALE_PER_HEAD if v_descale.numel() == N2 else SCALE_PER_TENSOR)
     pool = k_pages.shape
-    _check("k_pages", k_pages, k_pages.dtype if k_pages.dtype in codes else codes, pool, dev)
-    _check("v_pages", v_pages, v_pages.dtype if v_pages.dtype in codes else codes, pool, dev)
+    if fp4:
+        _check_fp4(k_pages, v_pages, k_scales, v_scales, pool, (P, N2, ps, 8), dev)
+    else:
+        _check("k_pages", k_pages, k_pages.dtype if k_pages.dtype in codes else codes, pool, dev)
+        _check("v_pages", v_pages, v_pages.dtype if v_pages.dtype in codes else codes, pool, dev)
     _check("k_descale", k_descale, f32,
-           (P, N2, ps) if k_kind == SCALE_PER_TOKEN_HEAD else (1,), dev)
+           (P, N2, ps) if k_kind == SCALE_PER_TOKEN_HEAD else
+           (N2,) if k_kind == SCALE_PER_HEAD else (1,), dev)
     _check("v_descale", v_descale, f32, (N2,) if v_kind == SCALE_PER_HEAD else (1,), dev)
     _check("seqused_kv", seqused_kv, i32, (B,), dev)
     L = table[1]
@@ -523,19 +584,40 @@ def decode(q, k_pages, v_pages, k_descale, v_descale, seqused_kv, block_table, m
         if dev < 0:
             raise ValueError("decode: tensors must be on a CUDA device")
         with torch.cuda.device(dev):
-            nbytes = decode_workspace_size(dims)
+            nbytes = size(dims)
         workspace = _empty(nbytes, torch.uint8, q.device, stream, result=False)
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on q's device")
     if softmax_scale is None:
         softmax_scale = 1.0 / math.sqrt(D)
-    _call(lib().bsa_fp8_decode,
+    scales = (k_scales.data_ptr(), v_scales.data_ptr()) if fp4 else ()
+    _call(fn,
           (ctypes.byref(dims), q.data_ptr(), _p(q_descale), k_pages.data_ptr(),
-           v_pages.data_ptr(), k_descale.data_ptr(), v_descale.data_ptr(), seqused_kv.data_ptr(),
+           v_pages.data_ptr(), *scales, k_descale.data_ptr(), v_descale.data_ptr(), seqused_kv.data_ptr(),
            block_table.data_ptr(), _p(block_mask), _p(sparse_indices), _p(sparse_seq_len),
            float(softmax_scale), out.data_ptr(), _p(lse), workspace.data_ptr(), workspace.nbytes,
-           _p(dev_status)), dev, stream, "bsa_fp8_decode")
+           _p(dev_status)), dev, stream, what)
     return out, lse
+
+
+def decode(q, k_pages, v_pages, k_descale, v_descale, seqused_kv, block_table, max_kv_len: int,
+           q_descale=None, block_mask=None, sparse_indices=None, sparse_seq_len=None,
+           softmax_scale: float | None = None, out=None, lse=None, return_lse: bool = True,
+           dev_status=None, workspace=None, stream=None, k_scale_kind: int | None = None,
+           v_scale_kind: int | None = None, kv_layout: int = KV_HND):
+    """Attention of one new token per sequence over the paged cache (whose seqused_kv counts the
+    new token, appended beforehand).  q bf16 [B, N1, 128], or uint8/float8_e4m3fn with q_descale
+    f32 [B, N1]; its rows may lie further apart than N1 * 128 (a slice of a wider projection).
+    Pages, descales, block_table and scale kinds as in prefill(); seqused_kv i32 [B];
+    block_mask u8 [B, N1, Kb] or sparse_indices i32 [B, N1, Kb] + sparse_seq_len i32 [B, N1]
+    select 128-token tiles for each query head, Kb = ceil(max_kv_len / 128).
+    Returns (out bf16 [B, N1, 128], lse f32 [N1, B] or None); a sequence without tokens, or a head
+    without an enabled tile, gives 0 and -FLT_MAX.  `out` may be q itself.  `workspace`
+    (decode_workspace_size bytes) must not be shared by calls in flight at once."""
+    return _decode(lib().bsa_fp8_decode, "bsa_fp8_decode", decode_workspace_size, False, q, k_pages,
+                   v_pages, None, None, k_descale, v_descale, seqused_kv, block_table, max_kv_len, q_descale,
+                   block_mask, sparse_indices, sparse_seq_len, softmax_scale, out, lse, return_lse,
+                   dev_status, workspace, stream, k_scale_kind, v_scale_kind, kv_layout)
 
 
 def _gather_rows(name, t, dtype, shape, pages, stream):
@@ -545,21 +627,19 @@ def _gather_rows(name, t, dtype, shape, pages, stream):
     return t
 
 
-def gather_kv(k_pages, v_pages, k_descale, v_descale, cu_seqlens, block_table, total: int,
-              cache_starts=None, k_out=None, v_out=None, out_dtype=None, dev_status=None,
-              stream=None, k_scale_kind: int | None = None, v_scale_kind: int | None = None,
-              kv_layout: int = KV_HND):
-    """Reads tokens back from the paged cache: row cu_seqlens[b] + i of the returned k, v
-    [total, N2, 128] is the token at position cache_starts[b] + i (0 + i without it) of sequence
-    b, code * descale.  out_dtype bf16 (default) or float32, or that of k_out / v_out when given;
-    rows from cu_seqlens[B] on are left as they were.  k_pages = None or v_pages = None leaves
-    that side out (returned as None)."""
+def _gather(fn, what, fp4, k_pages, v_pages, k_scales, v_scales, k_descale, v_descale, cu_seqlens,
+            block_table, total, cache_starts, k_out, v_out, out_dtype, dev_status, stream,
+            k_scale_kind, v_scale_kind, kv_layout):
+    """gather_kv() and gather_kv_fp4()."""
     torch, _, f32, i32, codes = _torch_names()
     pages = k_pages if k_pages is not None else v_pages
     if pages is None:
         raise ValueError("k_pages and v_pages are both None")
     dev = pages.get_device()
     P, N2, ps, D = _pool(pages, kv_layout)
+    if fp4:
+        D *= 2
+        _check_fp4(k_pages, v_pages, k_scales, v_scales, pages.shape, (P, N2, ps, D // 16), dev)
     given = k_out if k_out is not None else v_out
     if out_dtype is None:
         out_dtype = given.dtype if given is not None else torch.bfloat16
@@ -578,20 +658,27 @@ def gather_kv(k_pages, v_pages, k_descale, v_descale, cu_seqlens, block_table, t
     k_kind = v_kind = SCALE_PER_TENSOR
     shape = (total, N2, D)
     if k_pages is not None:
-        k_kind = k_scale_kind if k_scale_kind is not None else (
-            SCALE_PER_TOKEN_HEAD if k_descale.dim() == 3 else SCALE_PER_TENSOR)
-        _check("k_pages", k_pages, k_pages.dtype if k_pages.dtype in codes else codes, pages.shape,
-               dev)
+        if k_scale_kind is not None:
+            k_kind = k_scale_kind
+        elif fp4:
+            k_kind = SCALE_PER_HEAD if k_descale.numel() == N2 else SCALE_PER_TENSOR
+        else:
+            k_kind = SCALE_PER_TOKEN_HEAD if k_descale.dim() == 3 else SCALE_PER_TENSOR
+        if not fp4:
+            _check("k_pages", k_pages, k_pages.dtype if k_pages.dtype in codes else codes,
+                   pages.shape, dev)
         _check("k_descale", k_descale, f32,
-               (P, N2, ps) if k_kind == SCALE_PER_TOKEN_HEAD else (1,), dev)
+               (P, N2, ps) if k_kind == SCALE_PER_TOKEN_HEAD else
+               (N2,) if k_kind == SCALE_PER_HEAD else (1,), dev)
         k_out = _gather_rows("k_out", k_out, out_dtype, shape, pages, stream)
     elif k_out is not None:
         raise ValueError("k_out given without k_pages")
     if v_pages is not None:
         v_kind = v_scale_kind if v_scale_kind is not None else (
             SCALE_PER_HEAD if v_descale.numel() == N2 else SCALE_PER_TENSOR)
-        _check("v_pages", v_pages, v_pages.dtype if v_pages.dtype in codes else codes, pages.shape,
-               dev)
+        if not fp4:
+            _check("v_pages", v_pages, v_pages.dtype if v_pages.dtype in codes else codes,
+                   pages.shape, dev)
         _check("v_descale", v_descale, f32, (N2,) if v_kind == SCALE_PER_HEAD else (1,), dev)
         v_out = _gather_rows("v_out", v_out, out_dtype, shape, pages, stream)
     elif v_out is not None:
@@ -599,11 +686,26 @@ def gather_kv(k_pages, v_pages, k_descale, v_descale, cu_seqlens, block_table, t
     # in the order of GatherDims' fields
     dims = GatherDims(B, N2, D, ps, P, L, total, k_kind, v_kind, kv_layout,
                       OUT_FP32 if out_dtype is torch.float32 else OUT_BF16)
-    _call(lib().bsa_fp8_gather_kv,
-          (ctypes.byref(dims), _p(k_pages), _p(v_pages), _p(k_descale), _p(v_descale),
+    scales = (_p(k_scales), _p(v_scales)) if fp4 else ()
+    _call(fn,
+          (ctypes.byref(dims), _p(k_pages), _p(v_pages), *scales, _p(k_descale), _p(v_descale),
            cu_seqlens.data_ptr(), _p(cache_starts), block_table.data_ptr(), _p(k_out), _p(v_out),
-           _p(dev_status)), dev, stream, "bsa_fp8_gather_kv")
+           _p(dev_status)), dev, stream, what)
     return k_out, v_out
+
+
+def gather_kv(k_pages, v_pages, k_descale, v_descale, cu_seqlens, block_table, total: int,
+              cache_starts=None, k_out=None, v_out=None, out_dtype=None, dev_status=None,
+              stream=None, k_scale_kind: int | None = None, v_scale_kind: int | None = None,
+              kv_layout: int = KV_HND):
+    """Reads tokens back from the paged cache: row cu_seqlens[b] + i of the returned k, v
+    [total, N2, 128] is the token at position cache_starts[b] + i (0 + i without it) of sequence
+    b, code * descale.  out_dtype bf16 (default) or float32, or that of k_out / v_out when given;
+    rows from cu_seqlens[B] on are left as they were.  k_pages = None or v_pages = None leaves
+    that side out (returned as None)."""
+    return _gather(lib().bsa_fp8_gather_kv, "bsa_fp8_gather_kv", False, k_pages, v_pages, None, None,
+                   k_descale, v_descale, cu_seqlens, block_table, total, cache_starts, k_out, v_out,
+                   out_dtype, dev_status, stream, k_scale_kind, v_scale_kind, kv_layout)
 
 
 def merge_states(outs, lses, out=None, lse=None, return_lse: bool = True, stream=None):
@@ -638,3 +740,270 @@ def merge_states(outs, lses, out=None, lse=None, return_lse: bool = True, stream
           (n, ptrs(*[o.data_ptr() for o in outs]), ptrs(*[x.data_ptr() for x in lses]), T, N1,
            out.data_ptr(), _p(lse)), dev, stream, "bsa_fp8_merge_states")
     return out, lse
+
+
+# ---------------------------------------------------------------------------------------------
+# around attention: rotary positions, pages, the 4-bit cache
+# ---------------------------------------------------------------------------------------------
+
+def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: int = ROPE_NONE,
+                     factor: float = 1.0, context: float = 0.0, slow: float = 1.0,
+                     fast: float = 32.0, inv_freq=None, device=None):
+    """The frequencies rope() takes: an int64 tensor [rotary_dim / 2] of turns per position times
+    2^64, modulo 2^64.  f_i = base^(-2i / rotary_dim) radians a position, stretched by `factor`:
+    ROPE_LINEAR f_i / factor; ROPE_BASE base * factor^(R / (R - 2)); ROPE_PARTS f_i where a dimension
+    turns more than `fast` times within `context` positions, f_i / factor where fewer than `slow`
+    times, a blend between.  inv_freq (rotary_dim / 2 numbers, radians a position) gives frequencies
+    of the caller's own instead.  Made on the host, once for a model."""
+    import torch
+
+    n = int(rotary_dim) // 2
+    out = (ctypes.c_uint64 * max(n, 1))()
+    own = None
+    if inv_freq is not None:
+        values = [float(x) for x in inv_freq]
+        if len(values) != n:
+            raise ValueError(f"{len(values)} frequencies, expected {n}")
+        own = (ctypes.c_double * n)(*values)
+    st = lib().bsa_rope_frequencies(int(rotary_dim), int(scaling), base, factor, context, slow, fast,
+                                    own, out)
+    if st != 0:
+        raise BsaError(st, "bsa_rope_frequencies")
+    signed = [x - (1 << 64) if x >> 63 else x for x in out]
+    return torch.tensor(signed, dtype=torch.int64, device=device)
+
+
+def _rows(name, t, T, dev):
+    """The strides from token to token of a bf16 tensor [T, heads, 128] whose tokens are each in one
+    piece."""
+    shape = t.shape
+    if t.dtype is not _torch_names()[1]:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected bf16")
+    if len(shape) != 3 or shape[2] != 128 or shape[0] != T:
+        raise ValueError(f"{name} has shape {tuple(shape)}, expected [{T}, heads, 128]")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, the others on another device")
+    if t.is_contiguous():
+        return shape[1] * 128
+    if t.stride(2) != 1 or (shape[1] > 1 and t.stride(1) != 128):
+        raise ValueError(f"{name} must be contiguous within a token")
+    return t.stride(0) if T > 1 else shape[1] * 128
+
+
+def _rope_common(q, positions, freqs):
+    torch, _, _, i32, _ = _torch_names()
+    if q.dim() != 3:
+        raise ValueError(f"q has shape {tuple(q.shape)}, expected [T, N1, 128]")
+    T, dev = q.shape[0], q.get_device()
+    _check("positions", positions, i32, (T,), dev)
+    if freqs.dim() != 1:
+        raise ValueError(f"freqs has shape {tuple(freqs.shape)}, expected [rotary_dim / 2]")
+    _check("freqs", freqs, torch.int64, freqs.shape, dev)
+    return T, dev, _rows("q", q, T, dev)
+
+
+def rope(q, positions, freqs, k=None, layout: int = ROPE_HALF, amplitude: float = 1.0, out=None,
+         k_out=None, stream=None):
+    """Rotary positions of q bf16 [T, N1, 128] and, in the same launch, k bf16 [T, N2, 128]: pairs of
+    the first 2 * len(freqs) values of every head (value i with i + len(freqs) under ROPE_HALF, 2i
+    with 2i + 1 under ROPE_INTERLEAVED) turned by position * frequency and multiplied by `amplitude`,
+    the rest of the head copied.  positions i32 [T]; freqs from rope_frequencies().  Tokens may lie
+    further apart than their heads fill (slices of a wider projection).  out / k_out may be q / k
+    themselves.  Returns (out, k_out), k_out None without k."""
+    bf16 = _torch_names()[1]
+    T, dev, q_stride = _rope_common(q, positions, freqs)
+    N1, N2 = q.shape[1], 0
+    k_stride = k_out_stride = 0
+    if out is None:
+        out = _empty(q.shape, bf16, q.device, stream)
+    q_out_stride = _rows("out", out, T, dev)
+    if out.shape != q.shape:
+        raise ValueError(f"out has shape {tuple(out.shape)}, expected {tuple(q.shape)}")
+    if k is not None:
+        k_stride = _rows("k", k, T, dev)
+        N2 = k.shape[1]
+        if k_out is None:
+            k_out = _empty(k.shape, bf16, k.device, stream)
+        k_out_stride = _rows("k_out", k_out, T, dev)
+        if k_out.shape != k.shape:
+            raise ValueError(f"k_out has shape {tuple(k_out.shape)}, expected {tuple(k.shape)}")
+    elif k_out is not None:
+        raise ValueError("k_out given without k")
+    # in the order of RopeDims' fields
+    dims = RopeDims(T, N1, N2, 128, 2 * freqs.shape[0], layout, q_stride, k_stride, q_out_stride,
+                    k_out_stride)
+    _call(lib().bsa_rope,
+          (ctypes.byref(dims), q.data_ptr(), _p(k), positions.data_ptr(), freqs.data_ptr(),
+           amplitude, out.data_ptr(), _p(k_out)), dev, stream, "bsa_rope")
+    return out, k_out
+
+
+def rope_quantize(q, positions, freqs, layout: int = ROPE_HALF, amplitude: float = 1.0, codes=None,
+                  descale=None, rule: int = DESCALE_AMAX, stream=None):
+    """rope() of q alone and quantize_rows() of the result in one, without rounding to bf16 in
+    between: (e4m3 codes uint8 [T, N1, 128], fp32 descale [T, N1]), as prefill() and decode() take
+    queries."""
+    torch, _, f32, _, kinds = _torch_names()
+    T, dev, q_stride = _rope_common(q, positions, freqs)
+    N1 = q.shape[1]
+    if codes is None:
+        codes = _empty(q.shape, torch.uint8, q.device, stream)
+    else:
+        _check("codes", codes, codes.dtype if codes.dtype in kinds else kinds, q.shape, dev)
+    if descale is None:
+        descale = _empty((T, N1), f32, q.device, stream)
+    else:
+        _check("descale", descale, f32, (T, N1), dev)
+    dims = RopeDims(T, N1, 0, 128, 2 * freqs.shape[0], layout, q_stride, 0, 0, 0)
+    _call(lib().bsa_rope_quantize,
+          (ctypes.byref(dims), q.data_ptr(), positions.data_ptr(), freqs.data_ptr(), amplitude,
+           int(rule), codes.data_ptr(), descale.data_ptr()), dev, stream, "bsa_rope_quantize")
+    return codes, descale
+
+
+def _check_pages(block_table, free_pages, free_count, B, dev):
+    i32 = _torch_names()[3]
+    if block_table.dim() != 2:
+        raise ValueError(f"block_table has shape {tuple(block_table.shape)}, expected [B, L]")
+    if free_pages.dim() != 1:
+        raise ValueError(f"free_pages has shape {tuple(free_pages.shape)}, expected [num_pages]")
+    L = block_table.shape[1]
+    _check("block_table", block_table, i32, (B, L), dev)
+    _check("free_pages", free_pages, i32, free_pages.shape, dev)
+    _check("free_count", free_count, i32, (1,), dev)
+    return L
+
+
+def assign_pages(new_lens, cache_seqlens, block_table, free_pages, free_count, page_size: int,
+                 total: int, cu_seqlens=None, seqused_kv=None, positions=None, slot_map=None,
+                 dev_status=None, stream=None):
+    """Gives every sequence the pages for its new_lens i32 [B] tokens behind the cache_seqlens i32
+    [B] that it holds, and says where those tokens go.  block_table i32 [B, L] gets the new pages;
+    free_pages i32 [num_pages] is a stack whose first free_count i32 [1] entries are free: pages are
+    taken from its top in the sequences' order.  Returns (cu_seqlens i32 [B + 1], seqused_kv i32
+    [B], positions i32 [total], slot_map i32 [total]): the new tokens' first rows, the lengths
+    afterwards, and each new token's position in its sequence and its slot (page * page_size +
+    slot), as prefill(), append_kv(), rope() and append_kv_fp4() take them; rows from
+    cu_seqlens[B] on get position 0 and slot -1.  A sequence whose pages are not there gets none:
+    slots -1, its length unchanged, DEV_NO_PAGES.  seqused_kv must not be cache_seqlens."""
+    i32 = _torch_names()[3]
+    if new_lens.dim() != 1:
+        raise ValueError(f"new_lens has shape {tuple(new_lens.shape)}, expected [B]")
+    B, dev, total = new_lens.shape[0], new_lens.get_device(), int(total)
+    _check("new_lens", new_lens, i32, (B,), dev)
+    _check("cache_seqlens", cache_seqlens, i32, (B,), dev)
+    L = _check_pages(block_table, free_pages, free_count, B, dev)
+    if dev_status is not None:
+        _check_status(dev_status, dev)
+    device = new_lens.device
+    outs = []
+    for name, t, n in (("cu_seqlens", cu_seqlens, B + 1), ("seqused_kv", seqused_kv, B),
+                       ("positions", positions, total), ("slot_map", slot_map, total)):
+        if t is None:
+            t = _empty((n,), i32, device, stream)
+        else:
+            _check(name, t, i32, (n,), dev)
+        outs.append(t)
+    dims = PagesDims(B, int(page_size), free_pages.shape[0], L, total)
+    _call(lib().bsa_assign_pages,
+          (ctypes.byref(dims), new_lens.data_ptr(), cache_seqlens.data_ptr(),
+           block_table.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(),
+           outs[0].data_ptr(), outs[1].data_ptr(), outs[2].data_ptr(), outs[3].data_ptr(),
+           _p(dev_status)), dev, stream, "bsa_assign_pages")
+    return tuple(outs)
+
+
+def release_pages(seq_lens, keep_lens, block_table, free_pages, free_count, page_size: int,
+                  out=None, dev_status=None, stream=None):
+    """Cuts every sequence down to its first keep_lens i32 [B] tokens (0: all of it goes) and puts the
+    pages that hold none of them back on the stack, so that a release undoes the assign_pages()
+    before it.  Returns the lengths afterwards (`out`, which may be seq_lens itself).  A page must be
+    held by one sequence only."""
+    i32 = _torch_names()[3]
+    if seq_lens.dim() != 1:
+        raise ValueError(f"seq_lens has shape {tuple(seq_lens.shape)}, expected [B]")
+    B, dev = seq_lens.shape[0], seq_lens.get_device()
+    _check("seq_lens", seq_lens, i32, (B,), dev)
+    _check("keep_lens", keep_lens, i32, (B,), dev)
+    L = _check_pages(block_table, free_pages, free_count, B, dev)
+    if dev_status is not None:
+        _check_status(dev_status, dev)
+    if out is None:
+        out = _empty((B,), i32, seq_lens.device, stream)
+    else:
+        _check("out", out, i32, (B,), dev)
+    dims = PagesDims(B, int(page_size), free_pages.shape[0], L, 0)
+    _call(lib().bsa_release_pages,
+          (ctypes.byref(dims), seq_lens.data_ptr(), keep_lens.data_ptr(), block_table.data_ptr(),
+           free_pages.data_ptr(), free_count.data_ptr(), out.data_ptr(), _p(dev_status)), dev,
+          stream, "bsa_release_pages")
+    return out
+
+
+def _fp4_kind(given, descale, N2):
+    if given is not None:
+        return given
+    return SCALE_PER_HEAD if descale.numel() == N2 else SCALE_PER_TENSOR
+
+
+def append_kv_fp4(k_new, v_new, slot_map, k_pages, v_pages, k_scales, v_scales, k_descale, v_descale,
+                  dev_status=None, stream=None, k_scale_kind: int | None = None,
+                  v_scale_kind: int | None = None, kv_layout: int = KV_HND):
+    """Writes bf16 K/V tokens [T_new, N2, 128] (tokens may lie further apart) into the 4-bit cache at
+    slot_map i32 [T_new] (page * page_size + slot, as assign_pages() gives it; negative: skipped),
+    in place.  Pages uint8 [P, N2, page_size, 64] (KV_HND) or [P, page_size, N2, 64] (KV_NHD) hold
+    e2m1 codes, two to a byte; k_scales / v_scales uint8 or float8_e4m3fn [P, N2, page_size, 8] a
+    scale for every 16 of them; k_descale / v_descale f32 [1] or [N2], chosen by the caller (the
+    largest value expected / 2688 uses the scales' whole range).  value = code * scale * descale."""
+    f32, i32 = _torch_names()[2:4]
+    T, dev = k_new.shape[0], k_new.get_device()
+    k_stride, v_stride = _rows("k_new", k_new, T, dev), _rows("v_new", v_new, T, dev)
+    P, N2, ps, half = _pool(k_pages, kv_layout)
+    if half != 64 or k_new.shape[1] != N2 or v_new.shape[1] != N2:
+        raise ValueError(f"pages of shape {tuple(k_pages.shape)} do not hold rows "
+                         f"{tuple(k_new.shape)} and {tuple(v_new.shape)} in 4 bits")
+    _check_fp4(k_pages, v_pages, k_scales, v_scales, k_pages.shape, (P, N2, ps, 8), dev)
+    k_kind, v_kind = _fp4_kind(k_scale_kind, k_descale, N2), _fp4_kind(v_scale_kind, v_descale, N2)
+    _check("k_descale", k_descale, f32, (N2,) if k_kind == SCALE_PER_HEAD else (1,), dev)
+    _check("v_descale", v_descale, f32, (N2,) if v_kind == SCALE_PER_HEAD else (1,), dev)
+    _check("slot_map", slot_map, i32, (T,), dev)
+    if dev_status is not None:
+        _check_status(dev_status, dev)
+    dims = Fp4AppendDims(N2, 128, ps, P, T, k_kind, v_kind, int(kv_layout), k_stride, v_stride)
+    _call(lib().bsa_fp4_append_kv,
+          (ctypes.byref(dims), k_new.data_ptr(), v_new.data_ptr(), slot_map.data_ptr(),
+           k_descale.data_ptr(), v_descale.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+           k_scales.data_ptr(), v_scales.data_ptr(), _p(dev_status)), dev, stream,
+          "bsa_fp4_append_kv")
+    return k_pages, v_pages, k_scales, v_scales
+
+
+def gather_kv_fp4(k_pages, v_pages, k_scales, v_scales, k_descale, v_descale, cu_seqlens,
+                  block_table, total: int, cache_starts=None, k_out=None, v_out=None,
+                  out_dtype=None, dev_status=None, stream=None, k_scale_kind: int | None = None,
+                  v_scale_kind: int | None = None, kv_layout: int = KV_HND):
+    """gather_kv() from a 4-bit cache (append_kv_fp4() says how it lies)."""
+    return _gather(lib().bsa_fp4_gather_kv, "bsa_fp4_gather_kv", True, k_pages, v_pages, k_scales,
+                   v_scales, k_descale, v_descale, cu_seqlens, block_table, total, cache_starts,
+                   k_out, v_out, out_dtype, dev_status, stream, k_scale_kind, v_scale_kind,
+                   kv_layout)
+
+
+def decode_fp4_workspace_size(dims: DecodeDims) -> int:
+    """Bytes of workspace decode_fp4() needs for `dims` on the current device."""
+    return int(lib().bsa_fp4_decode_workspace_size(ctypes.byref(dims)))
+
+
+def decode_fp4(q, k_pages, v_pages, k_scales, v_scales, k_descale, v_descale, seqused_kv, block_table,
+               max_kv_len: int, q_descale=None, block_mask=None, sparse_indices=None,
+               sparse_seq_len=None, softmax_scale: float | None = None, out=None, lse=None,
+               return_lse: bool = True, dev_status=None, workspace=None, stream=None,
+               k_scale_kind: int | None = None, v_scale_kind: int | None = None,
+               kv_layout: int = KV_HND):
+    """decode() over a 4-bit cache (append_kv_fp4() says how it lies): the same queries, selection of
+    tiles, outputs and rules; `workspace` has decode_fp4_workspace_size bytes."""
+    return _decode(lib().bsa_fp4_decode, "bsa_fp4_decode", decode_fp4_workspace_size, True, q, k_pages,
+                   v_pages, k_scales, v_scales, k_descale, v_descale, seqused_kv, block_table,
+                   max_kv_len, q_descale, block_mask, sparse_indices, sparse_seq_len, softmax_scale,
+                   out, lse, return_lse, dev_status, workspace, stream, k_scale_kind, v_scale_kind,
+                   kv_layout)

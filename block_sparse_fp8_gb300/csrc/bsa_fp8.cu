@@ -25,10 +25,13 @@
 #include "bsa_attention_wide.cuh"
 #include "bsa_common.cuh"
 #include "bsa_decode.cuh"
+#include "bsa_fp4.cuh"
 #include "bsa_fp8.h"
 #include "bsa_gather.cuh"
 #include "bsa_merge.cuh"
+#include "bsa_pages.cuh"
 #include "bsa_quant.cuh"
+#include "bsa_rope.cuh"
 #include "ptx_sm103.cuh"
 
 namespace bsa {
@@ -199,13 +202,14 @@ static Params make_params(const bsa_fp8_dims_t *d) {
 
 static bool encode_map(CUtensorMap *map, const void *base, int rank, const cuuint64_t *dims,
                        const cuuint64_t *strides, const cuuint32_t *box,
-                       CUtensorMapL2promotion promotion = CU_TENSOR_MAP_L2_PROMOTION_L2_256B) {
+                       CUtensorMapL2promotion promotion = CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                       CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
   auto fn = encode_fn();
   if (!fn) return false;
   cuuint32_t estr[4] = {1, 1, 1, 1};
   CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, (cuuint32_t)rank, const_cast<void *>(base),
                   dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  CU_TENSOR_MAP_SWIZZLE_128B, promotion,
+                  swizzle, promotion,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
@@ -710,14 +714,14 @@ extern "C" bsa_status_t bsa_fp8_prefill_noalloc(
 namespace {
 
 // byte strides of a page, a KV head and a slot inside the page pool
-void pool_strides(int kv_layout, int N2, int page_size, long long *page, long long *head,
+void pool_strides(int kv_layout, int N2, int page_size, int row, long long *page, long long *head,
                   long long *slot) {
-  *page = (long long)N2 * page_size * HEAD_DIM;
-  *head = kv_layout == BSA_KV_NHD ? HEAD_DIM : (long long)page_size * HEAD_DIM;
-  *slot = kv_layout == BSA_KV_NHD ? (long long)N2 * HEAD_DIM : HEAD_DIM;
+  *page = (long long)N2 * page_size * row;
+  *head = kv_layout == BSA_KV_NHD ? row : (long long)page_size * row;
+  *slot = kv_layout == BSA_KV_NHD ? (long long)N2 * row : row;
 }
 
-bsa_status_t validate_decode(const bsa_fp8_decode_dims_t *d) {
+bsa_status_t validate_decode(const bsa_fp8_decode_dims_t *d, bool fp4) {
   if (!d || d->D != HEAD_DIM || (d->page_size != 32 && d->page_size != 64))
     return BSA_ERR_INVALID_ARGUMENT;
   if (d->B < 0 || d->N1 < 1 || d->N2 < 1 || d->N1 % d->N2 != 0 || d->N1 / d->N2 > 16)
@@ -726,7 +730,8 @@ bsa_status_t validate_decode(const bsa_fp8_decode_dims_t *d) {
     return BSA_ERR_INVALID_ARGUMENT;
   if ((long long)d->max_pages_per_seq * d->page_size < d->max_kv_len)
     return BSA_ERR_INVALID_ARGUMENT;
-  if (d->k_scale_kind != BSA_SCALE_PER_TENSOR && d->k_scale_kind != BSA_SCALE_PER_TOKEN_HEAD)
+  if (d->k_scale_kind != BSA_SCALE_PER_TENSOR &&
+      d->k_scale_kind != (fp4 ? BSA_SCALE_PER_HEAD : BSA_SCALE_PER_TOKEN_HEAD))
     return BSA_ERR_INVALID_ARGUMENT;
   if (d->v_scale_kind != BSA_SCALE_PER_TENSOR && d->v_scale_kind != BSA_SCALE_PER_HEAD)
     return BSA_ERR_INVALID_ARGUMENT;
@@ -780,14 +785,20 @@ bsa_status_t enable_decode() {
   std::lock_guard<std::mutex> lock(g_devices_mu);
   DeviceInfo &di = g_devices[dev];  // check_device has bounded dev
   if (di.decode_attr) return BSA_OK;
-  const auto enable = [](const void *kernel) {
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                decode::SMEM_BYTES) == cudaSuccess;
+  const auto enable = [](const void *kernel, int bytes) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) ==
+           cudaSuccess;
   };
-  if (!enable((const void *)decode::decode_kernel<1, false>) ||
-      !enable((const void *)decode::decode_kernel<2, false>) ||
-      !enable((const void *)decode::decode_kernel<1, true>) ||
-      !enable((const void *)decode::decode_kernel<2, true>)) {
+  using decode::decode_kernel;
+  using decode::Format;
+  if (!enable((const void *)decode_kernel<1, false, false>, Format<false, 1>::SMEM) ||
+      !enable((const void *)decode_kernel<2, false, false>, Format<false, 2>::SMEM) ||
+      !enable((const void *)decode_kernel<1, true, false>, Format<false, 1>::SMEM) ||
+      !enable((const void *)decode_kernel<2, true, false>, Format<false, 2>::SMEM) ||
+      !enable((const void *)decode_kernel<1, false, true>, Format<true, 1>::SMEM) ||
+      !enable((const void *)decode_kernel<2, false, true>, Format<true, 2>::SMEM) ||
+      !enable((const void *)decode_kernel<1, true, true>, Format<true, 1>::SMEM) ||
+      !enable((const void *)decode_kernel<2, true, true>, Format<true, 2>::SMEM)) {
     (void)cudaGetLastError();  // leave no pending error behind
     return BSA_ERR_CUDA;
   }
@@ -817,23 +828,34 @@ bool launch_dependent(void (*kernel)(Args...), dim3 grid, int threads, size_t sm
 
 }  // namespace
 
-extern "C" size_t bsa_fp8_decode_workspace_size(const bsa_fp8_decode_dims_t *dims) {
-  if (validate_decode(dims) != BSA_OK) return 0;
+static size_t decode_workspace_size(const bsa_fp8_decode_dims_t *dims, bool fp4) {
+  if (validate_decode(dims, fp4) != BSA_OK) return 0;
   int num_sms = 0;
   if (check_device(0, &num_sms) != BSA_OK) return WORKSPACE_BYTES;
   return plan_decode(dims, num_sms).bytes;
 }
 
-extern "C" bsa_status_t bsa_fp8_decode(const bsa_fp8_decode_dims_t *d, const void *q,
-                                       const float *q_descale, const void *k_pages,
-                                       const void *v_pages, const float *k_descale,
-                                       const float *v_descale, const int *seqused_kv,
-                                       const int *block_table, const uint8_t *block_mask,
-                                       const int *sparse_indices, const int *sparse_seq_len,
-                                       float softmax_scale, void *out_bf16, float *lse_f32,
-                                       void *workspace, size_t workspace_bytes, int *dev_status,
-                                       void *stream) {
-  bsa_status_t st = validate_decode(d);
+extern "C" size_t bsa_fp8_decode_workspace_size(const bsa_fp8_decode_dims_t *dims) {
+  return decode_workspace_size(dims, false);
+}
+
+extern "C" size_t bsa_fp4_decode_workspace_size(const bsa_fp8_decode_dims_t *dims) {
+  return decode_workspace_size(dims, true);
+}
+
+// Both cache formats' decode; k_scales and v_scales are the block scales of 4-bit pages.
+template <bool FP4>
+static bsa_status_t decode_impl(const bsa_fp8_decode_dims_t *d, const void *q,
+                                const float *q_descale, const void *k_pages, const void *v_pages,
+                                const void *k_scales, const void *v_scales,
+                                const float *k_descale, const float *v_descale,
+                                const int *seqused_kv, const int *block_table,
+                                const uint8_t *block_mask, const int *sparse_indices,
+                                const int *sparse_seq_len, float softmax_scale, void *out_bf16,
+                                float *lse_f32, void *workspace, size_t workspace_bytes,
+                                int *dev_status, void *stream) {
+  using F = decode::Format<FP4, 1>;
+  bsa_status_t st = validate_decode(d, FP4);
   if (st != BSA_OK) return st;
   if (block_mask && sparse_indices) return BSA_ERR_INVALID_ARGUMENT;
   if (sparse_indices && !sparse_seq_len) return BSA_ERR_INVALID_ARGUMENT;
@@ -848,6 +870,8 @@ extern "C" bsa_status_t bsa_fp8_decode(const bsa_fp8_decode_dims_t *d, const voi
     return BSA_ERR_INVALID_ARGUMENT;
   if (!none && (!k_pages || !v_pages || !k_descale || !v_descale || !block_table ||
                 d->num_pages < 1))
+    return BSA_ERR_INVALID_ARGUMENT;
+  if (FP4 && ((!none && (!k_scales || !v_scales)) || !aligned16(k_scales) || !aligned16(v_scales)))
     return BSA_ERR_INVALID_ARGUMENT;
   if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) ||
       (k_tok && !aligned16(k_descale)) || !aligned16(out_bf16) ||
@@ -869,6 +893,8 @@ extern "C" bsa_status_t bsa_fp8_decode(const bsa_fp8_decode_dims_t *d, const voi
   p.q_descale = q_descale;
   p.k_pages = static_cast<const uint8_t *>(k_pages);
   p.v_pages = static_cast<const uint8_t *>(v_pages);
+  p.k_scales = static_cast<const uint8_t *>(k_scales);
+  p.v_scales = static_cast<const uint8_t *>(v_scales);
   p.k_descale = k_descale;
   p.v_descale = v_descale;
   p.seqused_kv = seqused_kv;
@@ -895,6 +921,7 @@ extern "C" bsa_status_t bsa_fp8_decode(const bsa_fp8_decode_dims_t *d, const voi
   p.max_kv_len = d->max_kv_len;
   p.q_e4m3 = e4m3;
   p.k_per_token = k_tok;
+  p.k_per_head = d->k_scale_kind == BSA_SCALE_PER_HEAD;
   p.v_per_head = d->v_scale_kind == BSA_SCALE_PER_HEAD;
   p.scale_log2 = (float)((double)softmax_scale * 1.4426950408889634);
   p.ps_shift = d->page_size == 64 ? 6 : 5;
@@ -904,7 +931,7 @@ extern "C" bsa_status_t bsa_fp8_decode(const bsa_fp8_decode_dims_t *d, const voi
   p.tiles = reinterpret_cast<uint32_t *>(ws + plan.off_tiles);
   const bool wide = p.G > 8;  // two blocks of eight query heads per KV head
   // Tensor maps of the pools: a box is a warp's 32 slots of one page and head, in shared memory
-  // consecutive 128-byte rows in either layout.  L2 fetches no more than those rows: in NHD pages
+  // consecutive rows (128 bytes, or 64 of 4-bit codes) in either layout.  L2 fetches no more than those rows: in NHD pages
   // the next 128 bytes are another head's, wanted at another time (16 sequences of 8K tokens x 8
   // heads: 65.9 us with 256-byte promotion, 50.3 without; HND 47.4 either way).
   CUtensorMap tk, tv;
@@ -913,13 +940,16 @@ extern "C" bsa_status_t bsa_fp8_decode(const bsa_fp8_decode_dims_t *d, const voi
   if (!none) {
     const cuuint64_t H = (cuuint64_t)d->N2, S = (cuuint64_t)d->page_size;
     const bool nhd = p.kv_nhd != 0;
-    const cuuint64_t gd[4] = {HEAD_DIM, nhd ? H : S, nhd ? S : H, (cuuint64_t)d->num_pages};
-    const cuuint64_t gs[3] = {HEAD_DIM, gd[1] * HEAD_DIM, H * S * HEAD_DIM};
-    const cuuint32_t box[4] = {HEAD_DIM, nhd ? 1u : (cuuint32_t)decode::TOK,
+    const cuuint64_t gd[4] = {F::ROW, nhd ? H : S, nhd ? S : H, (cuuint64_t)d->num_pages};
+    const cuuint64_t gs[3] = {F::ROW, gd[1] * F::ROW, H * S * F::ROW};
+    const cuuint32_t box[4] = {F::ROW, nhd ? 1u : (cuuint32_t)decode::TOK,
                                nhd ? (cuuint32_t)decode::TOK : 1u, 1};
-    const CUtensorMapL2promotion row = CU_TENSOR_MAP_L2_PROMOTION_L2_128B;
-    if (!encode_map(&tk, k_pages, 4, gd, gs, box, row) ||
-        !encode_map(&tv, v_pages, 4, gd, gs, box, row))
+    const CUtensorMapL2promotion row = FP4 && nhd ? CU_TENSOR_MAP_L2_PROMOTION_L2_64B
+                                                  : CU_TENSOR_MAP_L2_PROMOTION_L2_128B;
+    const CUtensorMapSwizzle swizzle =
+        FP4 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
+    if (!encode_map(&tk, k_pages, 4, gd, gs, box, row, swizzle) ||
+        !encode_map(&tv, v_pages, 4, gd, gs, box, row, swizzle))
       return BSA_ERR_CUDA;
   }
   const bool lists = d->sparse && !none;
@@ -928,11 +958,12 @@ extern "C" bsa_status_t bsa_fp8_decode(const bsa_fp8_decode_dims_t *d, const voi
                                  dim3((unsigned)(d->B * d->N2)),
                                  decode::PLAN_THREADS, (size_t)p.Kb * sizeof(uint32_t), stream, p))
     return BSA_ERR_CUDA;
-  const auto kernel = lists ? (wide ? decode::decode_kernel<2, true> : decode::decode_kernel<1, true>)
-                            : (wide ? decode::decode_kernel<2, false>
-                                    : decode::decode_kernel<1, false>);
-  if (!launch_dependent(kernel, dim3((unsigned)plan.grid), decode::THREADS, decode::SMEM_BYTES,
-                        stream, p, tk, tv))
+  const auto kernel = lists ? (wide ? decode::decode_kernel<2, true, FP4>
+                                    : decode::decode_kernel<1, true, FP4>)
+                            : (wide ? decode::decode_kernel<2, false, FP4>
+                                    : decode::decode_kernel<1, false, FP4>);
+  if (!launch_dependent(kernel, dim3((unsigned)plan.grid), decode::THREADS,
+                        (size_t)(wide ? decode::Format<FP4, 2>::SMEM : F::SMEM), stream, p, tk, tv))
     return BSA_ERR_CUDA;
   if (plan.whole || p.Kb <= 1) return BSA_OK;  // no task is cut
   // The join, 62 registers.  Beside two CTAs of the kernels for up to eight heads (220 registers,
@@ -949,16 +980,46 @@ extern "C" bsa_status_t bsa_fp8_decode(const bsa_fp8_decode_dims_t *d, const voi
   return BSA_OK;
 }
 
-extern "C" bsa_status_t bsa_fp8_gather_kv(const bsa_fp8_gather_dims_t *d, const void *k_pages,
-                                          const void *v_pages, const float *k_descale,
-                                          const float *v_descale, const int *cu_seqlens,
-                                          const int *cache_starts, const int *block_table,
-                                          void *k_out, void *v_out, int *dev_status,
-                                          void *stream) {
+extern "C" bsa_status_t bsa_fp8_decode(const bsa_fp8_decode_dims_t *d, const void *q,
+                                       const float *q_descale, const void *k_pages,
+                                       const void *v_pages, const float *k_descale,
+                                       const float *v_descale, const int *seqused_kv,
+                                       const int *block_table, const uint8_t *block_mask,
+                                       const int *sparse_indices, const int *sparse_seq_len,
+                                       float softmax_scale, void *out_bf16, float *lse_f32,
+                                       void *workspace, size_t workspace_bytes, int *dev_status,
+                                       void *stream) {
+  return decode_impl<false>(d, q, q_descale, k_pages, v_pages, nullptr, nullptr, k_descale,
+                            v_descale, seqused_kv, block_table, block_mask, sparse_indices,
+                            sparse_seq_len, softmax_scale, out_bf16, lse_f32, workspace,
+                            workspace_bytes, dev_status, stream);
+}
+
+extern "C" bsa_status_t bsa_fp4_decode(
+    const bsa_fp8_decode_dims_t *d, const void *q, const float *q_descale, const void *k_pages,
+    const void *v_pages, const void *k_scales, const void *v_scales, const float *k_descale,
+    const float *v_descale, const int *seqused_kv, const int *block_table,
+    const uint8_t *block_mask, const int *sparse_indices, const int *sparse_seq_len,
+    float softmax_scale, void *out_bf16, float *lse_f32, void *workspace, size_t workspace_bytes,
+    int *dev_status, void *stream) {
+  return decode_impl<true>(d, q, q_descale, k_pages, v_pages, k_scales, v_scales, k_descale,
+                           v_descale, seqused_kv, block_table, block_mask, sparse_indices,
+                           sparse_seq_len, softmax_scale, out_bf16, lse_f32, workspace,
+                           workspace_bytes, dev_status, stream);
+}
+
+template <bool FP4>
+static bsa_status_t gather_impl(const bsa_fp8_gather_dims_t *d, const void *k_pages,
+                                const void *v_pages, const void *k_scales, const void *v_scales,
+                                const float *k_descale, const float *v_descale,
+                                const int *cu_seqlens, const int *cache_starts,
+                                const int *block_table, void *k_out, void *v_out, int *dev_status,
+                                void *stream) {
   if (!d || d->D != HEAD_DIM || (d->page_size != 32 && d->page_size != 64) || d->B < 0 ||
       d->N2 < 1 || d->num_pages < 0 || d->max_pages_per_seq < 0 || d->total < 0)
     return BSA_ERR_INVALID_ARGUMENT;
-  if (d->k_scale_kind != BSA_SCALE_PER_TOKEN_HEAD && d->k_scale_kind != BSA_SCALE_PER_TENSOR)
+  if (d->k_scale_kind != (FP4 ? BSA_SCALE_PER_HEAD : BSA_SCALE_PER_TOKEN_HEAD) &&
+      d->k_scale_kind != BSA_SCALE_PER_TENSOR)
     return BSA_ERR_INVALID_ARGUMENT;
   if (d->v_scale_kind != BSA_SCALE_PER_HEAD && d->v_scale_kind != BSA_SCALE_PER_TENSOR)
     return BSA_ERR_INVALID_ARGUMENT;
@@ -968,6 +1029,7 @@ extern "C" bsa_status_t bsa_fp8_gather_kv(const bsa_fp8_gather_dims_t *d, const 
   if ((!k_out && !v_out) || !cu_seqlens || !block_table) return BSA_ERR_INVALID_ARGUMENT;
   if ((k_out && (!k_pages || !k_descale)) || (v_out && (!v_pages || !v_descale)))
     return BSA_ERR_INVALID_ARGUMENT;
+  if (FP4 && ((k_out && !k_scales) || (v_out && !v_scales))) return BSA_ERR_INVALID_ARGUMENT;
   if (!aligned16(k_out) || !aligned16(v_out) || !aligned16(k_pages) || !aligned16(v_pages))
     return BSA_ERR_INVALID_ARGUMENT;
   int num_sms = 0;
@@ -977,6 +1039,8 @@ extern "C" bsa_status_t bsa_fp8_gather_kv(const bsa_fp8_gather_dims_t *d, const 
   memset(&p, 0, sizeof(p));
   p.k_pages = static_cast<const uint8_t *>(k_pages);
   p.v_pages = static_cast<const uint8_t *>(v_pages);
+  p.k_scales = static_cast<const uint8_t *>(k_scales);
+  p.v_scales = static_cast<const uint8_t *>(v_scales);
   p.k_descale = k_descale;
   p.v_descale = v_descale;
   p.cu_seqlens = cu_seqlens;
@@ -985,7 +1049,8 @@ extern "C" bsa_status_t bsa_fp8_gather_kv(const bsa_fp8_gather_dims_t *d, const 
   p.k_out = k_out;
   p.v_out = v_out;
   p.dev_status = dev_status;
-  pool_strides(d->kv_layout, d->N2, d->page_size, &p.page_bytes, &p.head_bytes, &p.slot_bytes);
+  pool_strides(d->kv_layout, d->N2, d->page_size, FP4 ? fp4::ROW_BYTES : HEAD_DIM, &p.page_bytes,
+               &p.head_bytes, &p.slot_bytes);
   p.B = d->B;
   p.N2 = d->N2;
   p.ps = d->page_size;
@@ -993,6 +1058,7 @@ extern "C" bsa_status_t bsa_fp8_gather_kv(const bsa_fp8_gather_dims_t *d, const 
   p.L = d->max_pages_per_seq;
   p.total = d->total;
   p.k_per_token = d->k_scale_kind == BSA_SCALE_PER_TOKEN_HEAD;
+  p.k_per_head = d->k_scale_kind == BSA_SCALE_PER_HEAD;
   p.v_per_head = d->v_scale_kind == BSA_SCALE_PER_HEAD;
   // a block's tokens: as many as leave every SM four rounds of its four resident blocks, so that a
   // lookup serves many rows and the last round is short (8 sequences of 100 to 5000 tokens
@@ -1001,10 +1067,33 @@ extern "C" bsa_status_t bsa_fp8_gather_kv(const bsa_fp8_gather_dims_t *d, const 
   while (p.tokens > 1 && cdiv(d->total, p.tokens) < 16 * num_sms) p.tokens /= 2;
   const unsigned grid = (unsigned)cdiv(d->total, p.tokens);
   if (d->out_type == BSA_OUT_FP32)
-    gather::gather_kernel<true><<<grid, gather::THREADS, 0, (cudaStream_t)stream>>>(p);
+    gather::gather_kernel<true, FP4><<<grid, gather::THREADS, 0, (cudaStream_t)stream>>>(p);
   else
-    gather::gather_kernel<false><<<grid, gather::THREADS, 0, (cudaStream_t)stream>>>(p);
+    gather::gather_kernel<false, FP4><<<grid, gather::THREADS, 0, (cudaStream_t)stream>>>(p);
   return cudaGetLastError() == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
+}
+
+extern "C" bsa_status_t bsa_fp8_gather_kv(const bsa_fp8_gather_dims_t *d, const void *k_pages,
+                                          const void *v_pages, const float *k_descale,
+                                          const float *v_descale, const int *cu_seqlens,
+                                          const int *cache_starts, const int *block_table,
+                                          void *k_out, void *v_out, int *dev_status,
+                                          void *stream) {
+  return gather_impl<false>(d, k_pages, v_pages, nullptr, nullptr, k_descale, v_descale,
+                            cu_seqlens, cache_starts, block_table, k_out, v_out, dev_status,
+                            stream);
+}
+
+extern "C" bsa_status_t bsa_fp4_gather_kv(const bsa_fp8_gather_dims_t *d, const void *k_pages,
+                                          const void *v_pages, const void *k_scales,
+                                          const void *v_scales, const float *k_descale,
+                                          const float *v_descale, const int *cu_seqlens,
+                                          const int *cache_starts, const int *block_table,
+                                          void *k_out, void *v_out, int *dev_status,
+                                          void *stream) {
+  return gather_impl<true>(d, k_pages, v_pages, k_scales, v_scales, k_descale, v_descale,
+                           cu_seqlens, cache_starts, block_table, k_out, v_out, dev_status,
+                           stream);
 }
 
 static bool overlap(const void *a, size_t na, const void *b, size_t nb) {
@@ -1064,5 +1153,276 @@ extern "C" bsa_status_t bsa_fp8_merge_states(int count, const void *const *outs,
       merge::merge_kernel<4>, merge::merge_kernel<5>, merge::merge_kernel<6>,
       merge::merge_kernel<7>, merge::merge_kernel<8>};
   kernels[count - 1]<<<grid, merge::THREADS, 0, (cudaStream_t)stream>>>(p);
+  return cudaGetLastError() == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
+}
+
+// ------------------------------------------------------------------------------------------
+// around attention: rotary positions, pages, tokens into the 4-bit cache
+// ------------------------------------------------------------------------------------------
+
+extern "C" bsa_status_t bsa_rope_frequencies(int rotary_dim, int scaling, double base, double factor,
+                                             double context, double slow, double fast,
+                                             const double *inv_freq, uint64_t *freqs) {
+  if (rotary_dim < 16 || rotary_dim > HEAD_DIM || rotary_dim % 16 != 0 || !freqs)
+    return BSA_ERR_INVALID_ARGUMENT;
+  if (!inv_freq) {
+    if (scaling < BSA_ROPE_NONE || scaling > BSA_ROPE_PARTS || !std::isfinite(base) || base <= 0 ||
+        (scaling != BSA_ROPE_NONE && (!std::isfinite(factor) || factor <= 0)))
+      return BSA_ERR_INVALID_ARGUMENT;
+    if (scaling == BSA_ROPE_PARTS && (!std::isfinite(context) || context <= 0 ||
+                                      !std::isfinite(slow) || !std::isfinite(fast) || slow >= fast))
+      return BSA_ERR_INVALID_ARGUMENT;
+  }
+  const double R = rotary_dim, two_pi = 6.283185307179586476925;
+  if (!inv_freq && scaling == BSA_ROPE_BASE) base *= std::pow(factor, R / (R - 2));
+  for (int i = 0; i < rotary_dim / 2; ++i) {
+    double f;
+    if (inv_freq) {
+      f = inv_freq[i];
+      if (!std::isfinite(f)) return BSA_ERR_INVALID_ARGUMENT;
+    } else {
+      f = std::pow(base, -2.0 * i / R);
+      if (scaling == BSA_ROPE_LINEAR) f /= factor;
+      if (scaling == BSA_ROPE_PARTS) {
+        const double turns = context * f / two_pi;
+        const double w = std::min(1.0, std::max(0.0, (turns - slow) / (fast - slow)));
+        f = f * w + f / factor * (1 - w);
+      }
+    }
+    // turns a position, less whole ones: positions are whole numbers.  In (-1, 1), times 2^64; a
+    // negative one counts down from 2^64.
+    const double turns = std::fmod(f / two_pi, 1.0);
+    const double size = std::floor(std::fabs(turns) * 0x1p64 + 0.5);
+    const uint64_t u = size >= 0x1p64 ? 0u : (uint64_t)size;
+    freqs[i] = turns < 0 ? 0u - u : u;
+  }
+  return BSA_OK;
+}
+
+namespace {
+
+bool rope_dims_ok(const bsa_rope_dims_t *d) {
+  return d && d->D == HEAD_DIM && d->T >= 0 && d->N1 >= 1 && d->N2 >= 0 &&
+         d->N1 <= (1 << 20) && d->N2 <= (1 << 20) && d->rotary_dim >= 16 &&
+         d->rotary_dim <= HEAD_DIM && d->rotary_dim % 16 == 0 &&
+         (d->layout == BSA_ROPE_HALF || d->layout == BSA_ROPE_INTERLEAVED);
+}
+
+// from token to token: rows side by side at least, 16-byte vectors
+bool rope_stride_ok(long long stride, int heads) {
+  return stride >= (long long)heads * HEAD_DIM && stride % 8 == 0;
+}
+
+bsa_status_t rope_params(const bsa_rope_dims_t *d, const void *q, const void *k,
+                         const int *positions, const uint64_t *freqs, float amplitude,
+                         rope::Params *p, unsigned *grid) {
+  int num_sms = 0;
+  const bsa_status_t st = check_device(0, &num_sms);
+  if (st != BSA_OK) return st;
+  memset(p, 0, sizeof(*p));
+  p->q = static_cast<const __nv_bfloat16 *>(q);
+  p->k = static_cast<const __nv_bfloat16 *>(k);
+  p->positions = positions;
+  p->freqs = reinterpret_cast<const unsigned long long *>(freqs);
+  p->q_stride = d->q_stride;
+  p->k_stride = d->k_stride;
+  p->N1 = d->N1;
+  p->N2 = d->N2;
+  p->R = d->rotary_dim;
+  p->interleaved = d->layout == BSA_ROPE_INTERLEAVED;
+  p->amplitude = amplitude;
+  // heads that one thread serves with its sines and cosines: as many as leave every SM eight warps
+  const int heads = d->N1 + d->N2;
+  p->heads = 1;
+  while (p->heads < 8 && (long long)d->T * cdiv(heads, 2 * p->heads) * rope::LANES >=
+                             (long long)num_sms * 256)
+    p->heads *= 2;
+  p->groups = cdiv(heads, p->heads);
+  p->units = (long long)d->T * p->groups;
+  const long long blocks = (p->units + rope::THREADS / rope::LANES - 1) /
+                           (rope::THREADS / rope::LANES);
+  if (blocks > 0x7fffffffLL) return BSA_ERR_UNSUPPORTED;
+  *grid = (unsigned)blocks;
+  return BSA_OK;
+}
+
+}  // namespace
+
+extern "C" bsa_status_t bsa_rope(const bsa_rope_dims_t *d, const void *q, const void *k,
+                                 const int *positions, const uint64_t *freqs, float amplitude,
+                                 void *q_out, void *k_out, void *stream) {
+  if (!rope_dims_ok(d) || !std::isfinite(amplitude)) return BSA_ERR_INVALID_ARGUMENT;
+  if (!rope_stride_ok(d->q_stride, d->N1) || !rope_stride_ok(d->q_out_stride, d->N1) ||
+      (d->N2 && (!rope_stride_ok(d->k_stride, d->N2) || !rope_stride_ok(d->k_out_stride, d->N2))))
+    return BSA_ERR_INVALID_ARGUMENT;
+  if (d->T == 0) return BSA_OK;
+  if (!q || !q_out || !positions || !freqs || (d->N2 != 0) != (k != nullptr) ||
+      (d->N2 != 0) != (k_out != nullptr) || !aligned16(q) || !aligned16(k) || !aligned16(q_out) ||
+      !aligned16(k_out) || (reinterpret_cast<uintptr_t>(freqs) & 7u) != 0)
+    return BSA_ERR_INVALID_ARGUMENT;
+  // a tensor may be turned where it lies
+  if ((q_out == q && d->q_out_stride != d->q_stride) ||
+      (k && k_out == k && d->k_out_stride != d->k_stride))
+    return BSA_ERR_INVALID_ARGUMENT;
+  rope::Params p;
+  unsigned grid = 0;
+  const bsa_status_t st = rope_params(d, q, k, positions, freqs, amplitude, &p, &grid);
+  if (st != BSA_OK) return st;
+  p.q_out = static_cast<__nv_bfloat16 *>(q_out);
+  p.k_out = static_cast<__nv_bfloat16 *>(k_out);
+  p.q_out_stride = d->q_out_stride;
+  p.k_out_stride = d->k_out_stride;
+  rope::rope_kernel<false><<<grid, rope::THREADS, 0, (cudaStream_t)stream>>>(p);
+  return cudaGetLastError() == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
+}
+
+extern "C" bsa_status_t bsa_rope_quantize(const bsa_rope_dims_t *d, const void *q,
+                                          const int *positions, const uint64_t *freqs,
+                                          float amplitude, int descale_rule, void *codes_e4m3,
+                                          float *descale, void *stream) {
+  if (!rope_dims_ok(d) || d->N2 != 0 || !std::isfinite(amplitude) ||
+      !rope_stride_ok(d->q_stride, d->N1) ||
+      (descale_rule != BSA_DESCALE_AMAX && descale_rule != BSA_DESCALE_UE8M0))
+    return BSA_ERR_INVALID_ARGUMENT;
+  if (d->T == 0) return BSA_OK;
+  if (!q || !positions || !freqs || !codes_e4m3 || !descale || !aligned16(q) ||
+      !aligned16(codes_e4m3) || (reinterpret_cast<uintptr_t>(freqs) & 7u) != 0)
+    return BSA_ERR_INVALID_ARGUMENT;
+  rope::Params p;
+  unsigned grid = 0;
+  const bsa_status_t st = rope_params(d, q, nullptr, positions, freqs, amplitude, &p, &grid);
+  if (st != BSA_OK) return st;
+  p.codes = static_cast<uint2 *>(codes_e4m3);
+  p.descale = descale;
+  p.ue8m0 = descale_rule == BSA_DESCALE_UE8M0;
+  rope::rope_kernel<true><<<grid, rope::THREADS, 0, (cudaStream_t)stream>>>(p);
+  return cudaGetLastError() == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
+}
+
+namespace {
+
+bool pages_dims_ok(const bsa_pages_dims_t *d) {
+  return d && d->B >= 0 && (d->page_size == 32 || d->page_size == 64) && d->num_pages >= 0 &&
+         d->max_pages_per_seq >= 0 && d->total >= 0 &&
+         (long long)d->num_pages * d->page_size <= 0x7fffffffLL &&
+         (long long)d->max_pages_per_seq * d->page_size <= 0x7fffffffLL;
+}
+
+pages::Params pages_params(const bsa_pages_dims_t *d, int *block_table, int *free_pages,
+                           int *free_count, int *dev_status) {
+  pages::Params p;
+  memset(&p, 0, sizeof(p));
+  p.block_table = block_table;
+  p.free_pages = free_pages;
+  p.free_count = free_count;
+  p.dev_status = dev_status;
+  p.B = d->B;
+  p.ps_shift = d->page_size == 64 ? 6 : 5;
+  p.num_pages = d->num_pages;
+  p.L = d->max_pages_per_seq;
+  p.total = d->total;
+  return p;
+}
+
+}  // namespace
+
+extern "C" bsa_status_t bsa_assign_pages(const bsa_pages_dims_t *d, const int *new_lens,
+                                         const int *cache_seqlens, int *block_table,
+                                         int *free_pages, int *free_count, int *cu_seqlens,
+                                         int *seqused_kv, int *positions, int *slot_map,
+                                         int *dev_status, void *stream) {
+  if (!pages_dims_ok(d)) return BSA_ERR_INVALID_ARGUMENT;
+  if (d->B == 0 && d->total == 0) return BSA_OK;
+  if (!free_count || !cu_seqlens || (d->total && (!positions || !slot_map)) ||
+      (d->num_pages && !free_pages) || (d->B && (!new_lens || !cache_seqlens || !seqused_kv)) ||
+      (d->B && d->max_pages_per_seq && !block_table) || (d->B && seqused_kv == cache_seqlens))
+    return BSA_ERR_INVALID_ARGUMENT;
+  int num_sms = 0;
+  const bsa_status_t st = check_device(0, &num_sms);
+  if (st != BSA_OK) return st;
+  pages::Params p = pages_params(d, block_table, free_pages, free_count, dev_status);
+  p.new_lens = new_lens;
+  p.cache_seqlens = cache_seqlens;
+  p.cu_seqlens = cu_seqlens;
+  p.seqused_kv = seqused_kv;
+  p.positions = positions;
+  p.slot_map = slot_map;
+  p.fill = d->total <= 2 * pages::THREADS || d->B == 0;
+  if (!launch_dependent(pages::assign_kernel, dim3(1), pages::THREADS, 0, stream, p))
+    return BSA_ERR_CUDA;
+  if (p.fill) return BSA_OK;
+  return launch_dependent(pages::fill_kernel, dim3((unsigned)cdiv(d->total, pages::FILL_ROWS)),
+                          pages::FILL_THREADS, 0, stream, p)
+             ? BSA_OK
+             : BSA_ERR_CUDA;
+}
+
+extern "C" bsa_status_t bsa_release_pages(const bsa_pages_dims_t *d, const int *seq_lens,
+                                          const int *keep_lens, const int *block_table,
+                                          int *free_pages, int *free_count, int *lens_out,
+                                          int *dev_status, void *stream) {
+  if (!pages_dims_ok(d)) return BSA_ERR_INVALID_ARGUMENT;
+  if (d->B == 0) return BSA_OK;
+  if (!seq_lens || !keep_lens || !free_count || !lens_out || (d->num_pages && !free_pages) ||
+      (d->max_pages_per_seq && !block_table))
+    return BSA_ERR_INVALID_ARGUMENT;
+  int num_sms = 0;
+  const bsa_status_t st = check_device(0, &num_sms);
+  if (st != BSA_OK) return st;
+  pages::Params p =
+      pages_params(d, const_cast<int *>(block_table), free_pages, free_count, dev_status);
+  p.seq_lens = seq_lens;
+  p.keep_lens = keep_lens;
+  p.lens_out = lens_out;
+  return launch_dependent(pages::release_kernel, dim3(1), pages::THREADS, 0, stream, p)
+             ? BSA_OK
+             : BSA_ERR_CUDA;
+}
+
+extern "C" bsa_status_t bsa_fp4_append_kv(const bsa_fp4_append_dims_t *d, const void *k_new_bf16,
+                                          const void *v_new_bf16, const int *slot_map,
+                                          const float *k_descale, const float *v_descale,
+                                          void *k_pages, void *v_pages, void *k_scales,
+                                          void *v_scales, int *dev_status, void *stream) {
+  if (!d || d->D != HEAD_DIM || (d->page_size != 32 && d->page_size != 64) || d->N2 < 1 ||
+      d->N2 > (1 << 20) || d->num_pages < 0 || d->total_new < 0 ||
+      (d->k_scale_kind != BSA_SCALE_PER_TENSOR && d->k_scale_kind != BSA_SCALE_PER_HEAD) ||
+      (d->v_scale_kind != BSA_SCALE_PER_TENSOR && d->v_scale_kind != BSA_SCALE_PER_HEAD) ||
+      (d->kv_layout != BSA_KV_HND && d->kv_layout != BSA_KV_NHD) ||
+      !rope_stride_ok(d->k_stride, d->N2) || !rope_stride_ok(d->v_stride, d->N2))
+    return BSA_ERR_INVALID_ARGUMENT;
+  if (d->total_new == 0) return BSA_OK;
+  if (!k_new_bf16 || !v_new_bf16 || !slot_map || !k_descale || !v_descale || !k_pages ||
+      !v_pages || !k_scales || !v_scales || !aligned16(k_new_bf16) || !aligned16(v_new_bf16) ||
+      !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(k_scales) || !aligned16(v_scales))
+    return BSA_ERR_INVALID_ARGUMENT;
+  int num_sms = 0;
+  const bsa_status_t st = check_device(0, &num_sms);
+  if (st != BSA_OK) return st;
+  fp4::AppendParams p;
+  memset(&p, 0, sizeof(p));
+  p.k_new = static_cast<const __nv_bfloat16 *>(k_new_bf16);
+  p.v_new = static_cast<const __nv_bfloat16 *>(v_new_bf16);
+  p.k_stride = d->k_stride;
+  p.v_stride = d->v_stride;
+  p.slot_map = slot_map;
+  p.k_descale = k_descale;
+  p.v_descale = v_descale;
+  p.k_pages = static_cast<uint8_t *>(k_pages);
+  p.v_pages = static_cast<uint8_t *>(v_pages);
+  p.k_scales = static_cast<uint8_t *>(k_scales);
+  p.v_scales = static_cast<uint8_t *>(v_scales);
+  p.dev_status = dev_status;
+  p.rows = (long long)d->total_new * d->N2;
+  p.N2 = d->N2;
+  p.ps_shift = d->page_size == 64 ? 6 : 5;
+  p.num_pages = d->num_pages;
+  p.k_per_head = d->k_scale_kind == BSA_SCALE_PER_HEAD;
+  p.v_per_head = d->v_scale_kind == BSA_SCALE_PER_HEAD;
+  p.kv_nhd = d->kv_layout == BSA_KV_NHD;
+  const long long blocks =
+      (p.rows + fp4::THREADS / fp4::BLOCKS - 1) / (fp4::THREADS / fp4::BLOCKS);
+  if (blocks > 0x7fffffffLL) return BSA_ERR_UNSUPPORTED;
+  fp4::append_kernel<<<(unsigned)blocks, fp4::THREADS, 0, (cudaStream_t)stream>>>(p);
   return cudaGetLastError() == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
 }

@@ -1,7 +1,9 @@
-// The paged e4m3 cache read back into contiguous rows: value = code * descale, one fp32 product,
-// rounded once more for bf16.
+// The paged cache read back into contiguous rows: value = code * descale for e4m3 pages, (code * scale)
+// * descale for 4-bit ones (bsa_fp4.cuh; the first product is exact), one fp32 product rounded once
+// more for bf16.
 //
-// HBM-bound (a KV head's token: 256 bytes of codes and 4 of descale in, 512 or 1024 out).  A block
+// HBM-bound (a KV head's token: 256 bytes of codes and 4 of descale in, or 144 of codes and scales;
+// 512 or 1024 out).  A block
 // takes a run of tokens.  Its first threads look the tokens up -- the sequence by binary search over
 // cu_seqlens, then the block table -- and leave page and slot in shared memory, so that the
 // dependent reads are paid once a token and not once a row.  Then a row of 128 values belongs to
@@ -20,6 +22,7 @@
 #include <cstdint>
 
 #include "bsa_common.cuh"
+#include "bsa_fp4.cuh"
 
 namespace bsa {
 namespace gather {
@@ -30,13 +33,14 @@ constexpr int ROWS = 4;         // rows in flight per thread
 
 struct Params {
   const uint8_t *k_pages, *v_pages;
+  const uint8_t *k_scales, *v_scales;  // 4-bit pages
   const float *k_descale, *v_descale;
   const int *cu_seqlens, *cache_starts, *block_table;
   void *k_out, *v_out;
   int *dev_status;
   long long page_bytes, head_bytes, slot_bytes;
   int B, N2, ps, num_pages, L, total;
-  int k_per_token, v_per_head;
+  int k_per_token, k_per_head, v_per_head;
   int tokens;  // of a block, a power of two up to MAX_TOKENS
 };
 
@@ -63,18 +67,56 @@ __device__ __forceinline__ uint32_t bf16x2(float a, float b) {
 constexpr int LANES = 16;                // of a row
 constexpr int STEP = THREADS / LANES;    // rows of a block's pass
 
-// Lane li's 8 codes of the row at p.
-template <bool F32>
+// Two e2m1 codes (the low byte) as fp32.
+__device__ __forceinline__ float2 values2_e2m1(uint32_t codes) {
+  uint32_t h;
+  asm("{\n\t.reg .b8 a;\n\t"
+      "cvt.u8.u32 a, %1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\t}"
+      : "=r"(h)
+      : "r"(codes & 0xffu));
+  __half2 x;
+  memcpy(&x, &h, 4);
+  return __half22float2(x);
+}
+
+// Lane li's 8 codes of the row at p: eight neighbours, or four neighbours of each half.
+template <bool F32, bool FP4>
 __device__ __forceinline__ uint2 load_codes(const uint8_t *p, int li) {
+  if (FP4 && F32)
+    return make_uint2(reinterpret_cast<const uint16_t *>(p)[li],
+                      reinterpret_cast<const uint16_t *>(p)[li + 16]);
+  if (FP4) {
+    const uint32_t w = reinterpret_cast<const uint32_t *>(p)[li];
+    return make_uint2(w, w >> 16);
+  }
   if (!F32) return reinterpret_cast<const uint2 *>(p)[li];
   return make_uint2(reinterpret_cast<const uint32_t *>(p)[li],
                     reinterpret_cast<const uint32_t *>(p)[li + 16]);
 }
 
-// ... and their values, into the row at out.
+// The scales of the two halves of those codes, in the low byte of either half word.
 template <bool F32>
-__device__ __forceinline__ void store_values(void *out, size_t row, int li, uint2 c, float s) {
-  const float2 a = values2(c.x), b = values2(c.x >> 16), d = values2(c.y), e = values2(c.y >> 16);
+__device__ __forceinline__ uint32_t load_scales(const uint8_t *p, int li) {
+  if (F32) return p[li >> 2] | (uint32_t)p[4 + (li >> 2)] << 16;
+  const uint32_t s = p[li >> 1];
+  return s | s << 16;
+}
+
+// ... and their values, into the row at out.
+template <bool F32, bool FP4>
+__device__ __forceinline__ void store_values(void *out, size_t row, int li, uint2 c, uint32_t sc,
+                                             float s) {
+  float2 a, b, d, e;
+  if (FP4) {
+    const float f = fp4::value_of_e4m3(sc), g = fp4::value_of_e4m3(sc >> 16);
+    a = values2_e2m1(c.x), b = values2_e2m1(c.x >> 8);
+    d = values2_e2m1(c.y), e = values2_e2m1(c.y >> 8);
+    a.x *= f, a.y *= f, b.x *= f, b.y *= f;
+    d.x *= g, d.y *= g, e.x *= g, e.y *= g;
+  } else {
+    a = values2(c.x), b = values2(c.x >> 16), d = values2(c.y), e = values2(c.y >> 16);
+  }
   if (F32) {
     float4 *o = static_cast<float4 *>(out) + row * (HEAD_DIM / 4) + li;
     __stcs(o, make_float4(a.x * s, a.y * s, b.x * s, b.y * s));
@@ -86,7 +128,7 @@ __device__ __forceinline__ void store_values(void *out, size_t row, int li, uint
   }
 }
 
-template <bool F32>
+template <bool F32, bool FP4>
 __global__ void __launch_bounds__(THREADS) gather_kernel(const Params p) {
   __shared__ int s_page[MAX_TOKENS], s_slot[MAX_TOKENS];
   const int tid = threadIdx.x, t0 = blockIdx.x * p.tokens;
@@ -115,11 +157,12 @@ __global__ void __launch_bounds__(THREADS) gather_kernel(const Params p) {
   __syncthreads();
   // The block's rows (token, head), token-major: a thread's next row lies STEP rows on.
   const int li = tid % LANES, dt = STEP / p.N2, dg = STEP % p.N2;
-  const float k_all = p.k_per_token || !p.k_out ? 0.f : p.k_descale[0];
+  const float k_all = p.k_per_token || p.k_per_head || !p.k_out ? 0.f : p.k_descale[0];
   const float v_all = p.v_per_head || !p.v_out ? 0.f : p.v_descale[0];
   int t = tid / LANES / p.N2, g = tid / LANES - t * p.N2;
   while (t < p.tokens) {
     uint2 k[ROWS], v[ROWS];
+    uint32_t kb[ROWS], vb[ROWS];  // block scales
     float ks[ROWS], vs[ROWS];
     int page[ROWS];
     size_t row[ROWS];
@@ -128,17 +171,21 @@ __global__ void __launch_bounds__(THREADS) gather_kernel(const Params p) {
       page[i] = t < p.tokens ? s_page[t] : -2;
       row[i] = (size_t)(t0 + t) * p.N2 + g;
       k[i] = v[i] = make_uint2(0, 0);
+      kb[i] = vb[i] = 0u;
       ks[i] = k_all;
       vs[i] = v_all;
       if (page[i] >= 0) {
         const int slot = s_slot[t];
         const long long off = page[i] * p.page_bytes + g * p.head_bytes + slot * p.slot_bytes;
+        const size_t hnd = ((size_t)page[i] * p.N2 + g) * p.ps + slot;
         if (p.k_out) {
-          k[i] = load_codes<F32>(p.k_pages + off, li);
-          if (p.k_per_token) ks[i] = p.k_descale[((size_t)page[i] * p.N2 + g) * p.ps + slot];
+          k[i] = load_codes<F32, FP4>(p.k_pages + off, li);
+          if (FP4) kb[i] = load_scales<F32>(p.k_scales + hnd * fp4::BLOCKS, li);
+          if (FP4 ? p.k_per_head : p.k_per_token) ks[i] = p.k_descale[FP4 ? g : hnd];
         }
         if (p.v_out) {
-          v[i] = load_codes<F32>(p.v_pages + off, li);
+          v[i] = load_codes<F32, FP4>(p.v_pages + off, li);
+          if (FP4) vb[i] = load_scales<F32>(p.v_scales + hnd * fp4::BLOCKS, li);
           if (p.v_per_head) vs[i] = p.v_descale[g];
         }
       }
@@ -154,8 +201,8 @@ __global__ void __launch_bounds__(THREADS) gather_kernel(const Params p) {
       if (page[i] == -2) continue;
       // a missing page's codes are zero: so are its values, whatever the descale
       const bool none = page[i] < 0;
-      if (p.k_out) store_values<F32>(p.k_out, row[i], li, k[i], none ? 0.f : ks[i]);
-      if (p.v_out) store_values<F32>(p.v_out, row[i], li, v[i], none ? 0.f : vs[i]);
+      if (p.k_out) store_values<F32, FP4>(p.k_out, row[i], li, k[i], kb[i], none ? 0.f : ks[i]);
+      if (p.v_out) store_values<F32, FP4>(p.v_out, row[i], li, v[i], vb[i], none ? 0.f : vs[i]);
     }
   }
 }

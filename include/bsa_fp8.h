@@ -72,6 +72,7 @@ typedef enum {
 #define BSA_DEV_BAD_PAGE 2    /* block_table entry out of range for a needed page (reads 0) */
 #define BSA_DEV_BAD_SEQLEN 4  /* q_len / kv_len negative or above the declared maximum */
 #define BSA_DEV_TIMEOUT 8     /* a bounded wait inside a kernel ran out */
+#define BSA_DEV_NO_PAGES 16 /* fewer free pages than a sequence wants (it gets none) */
 
 /* Problem geometry (host struct).  Layouts follow the Quant Block Sparse Attention
  * parameter table with the page size made a parameter:
@@ -436,6 +437,164 @@ bsa_status_t bsa_fp8_gather_kv(const bsa_fp8_gather_dims_t *dims, const void *k_
  * (BSA_ERR_INVALID_ARGUMENT).  T * N1 <= 2^31 - 1. */
 bsa_status_t bsa_fp8_merge_states(int count, const void *const *outs, const float *const *lses,
                                   int T, int N1, void *out_bf16, float *lse_f32, void *stream);
+
+/* ------------------------------------------------------------------------------------------
+ * Around attention: rotary positions of Q and K, pages for new tokens, and a cache held in 4 bits.
+ * No counterpart in the pages.  A step of a serving loop is bsa_assign_pages, bsa_rope (or
+ * bsa_rope_quantize for Q), bsa_fp4_append_kv (or bsa_fp8_append_kv) and a decode.
+ * ------------------------------------------------------------------------------------------ */
+
+/* Pairs of a rotated head: value i with value i + rotary_dim/2, or value 2i with value 2i + 1. */
+#define BSA_ROPE_HALF 0
+#define BSA_ROPE_INTERLEAVED 1
+
+/* Frequencies f_i = base^(-2i/rotary_dim) radians a position, and their stretching by `factor`: */
+#define BSA_ROPE_NONE 0   /* as they are */
+#define BSA_ROPE_LINEAR 1 /* f_i / factor: positions interpolated */
+#define BSA_ROPE_BASE 2   /* base * factor^(R/(R-2)): the slowest is divided by factor, the fastest kept */
+#define BSA_ROPE_PARTS 3  /* by parts: kept where a dimension turns more than `fast` times within
+                             `context` positions, divided by factor where fewer than `slow` times,
+                             a blend, linear in the number of turns, between */
+
+/* Writes rotary_dim/2 frequencies to the HOST array `freqs`, in the fixed-point form that bsa_rope
+ * takes: turns per position times 2^64, modulo 2^64.  inv_freq (host, rotary_dim/2 radians a
+ * position) gives frequencies of the caller's own, the other arguments are then unused; or NULL.
+ * rotary_dim is a multiple of 16 up to 128.  Runs on the host alone. */
+bsa_status_t bsa_rope_frequencies(int rotary_dim, int scaling, double base, double factor,
+                                  double context, double slow, double fast,
+                                  const double *inv_freq, uint64_t *freqs);
+
+typedef struct {
+  int T;                  /* tokens, >= 0 */
+  int N1;                 /* heads of q, >= 1 */
+  int N2;                 /* heads of k, 0: none */
+  int D;                  /* head dim, must be 128 */
+  int rotary_dim;         /* the first values of a head that are rotated: a multiple of 16, <= 128 */
+  int layout;             /* BSA_ROPE_HALF or BSA_ROPE_INTERLEAVED */
+  long long q_stride;     /* elements from token to token, >= heads * 128 and a multiple of 8 (a */
+  long long k_stride;     /*   slice of a wider projection's output) */
+  long long q_out_stride;
+  long long k_out_stride;
+} bsa_rope_dims_t;
+
+/* Rotary positions: every pair (x, y) of the first rotary_dim values of a head becomes
+ *   amplitude * (x cos a - y sin a,  y cos a + x sin a),   a = 2 pi * frac(position * f_i),
+ * the rest of the head is copied.  q bf16 [T, N1, 128], k bf16 [T, N2, 128] or NULL, positions int32
+ * [T] (any values), freqs uint64 [rotary_dim/2] as bsa_rope_frequencies writes them; q_out and k_out
+ * bf16, either may be its input itself (with the same stride) and must not overlap an input
+ * otherwise.  Everything is 16-byte aligned but positions (4) and freqs (8).  The angle is exact to
+ * 2^-32 turns for any position; the rest is fp32, rounded once. */
+bsa_status_t bsa_rope(const bsa_rope_dims_t *dims, const void *q, const void *k,
+                      const int *positions, const uint64_t *freqs, float amplitude, void *q_out,
+                      void *k_out, void *stream);
+
+/* The same on q alone (dims->N2 = 0, the out strides unused), quantised as bsa_fp8_quantize_rows does
+ * it, without rounding to bf16 in between: codes_e4m3 [T, N1, 128] and descale fp32 [T, N1], under
+ * descale_rule BSA_DESCALE_AMAX or BSA_DESCALE_UE8M0.  Inputs must be finite. */
+bsa_status_t bsa_rope_quantize(const bsa_rope_dims_t *dims, const void *q, const int *positions,
+                               const uint64_t *freqs, float amplitude, int descale_rule,
+                               void *codes_e4m3, float *descale, void *stream);
+
+typedef struct {
+  int B;                 /* sequences, >= 0 */
+  int page_size;         /* 32 or 64 */
+  int num_pages;         /* physical pages, entries of free_pages; num_pages * page_size < 2^31 */
+  int max_pages_per_seq; /* L, columns of block_table; L * page_size < 2^31 */
+  int total;             /* bsa_assign_pages: rows of positions / slot_map */
+} bsa_pages_dims_t;
+
+/* Gives every sequence the pages for its new tokens, and says where those tokens go.
+ *   new_lens, cache_seqlens  int32 [B]: tokens to add, tokens held
+ *   block_table   int32 [B, L], updated: sequence b's new pages behind its ceil(cache_seqlens/page)
+ *                 held ones; every other entry is left as it was
+ *   free_pages    int32 [num_pages], a stack: its first *free_count entries are the free pages; read
+ *   free_count    int32 [1], updated
+ *   cu_seqlens    int32 [B + 1]: first rows of the sequences' new tokens
+ *   seqused_kv    int32 [B]: tokens held afterwards; not cache_seqlens itself
+ *   positions     int32 [total]: position of each new token in its sequence
+ *   slot_map      int32 [total]: its place in the cache, page * page_size + slot, or -1
+ * Rows from cu_seqlens[B] on get position 0 and slot -1, so that a step captured for `total` tokens
+ * can be replayed with fewer.  Pages are taken from the stack's top, in the sequences' order.  A
+ * sequence that wants pages is served if they and those that the sequences before it want are there;
+ * otherwise it gets none, its rows get slot -1, its seqused_kv stays, and BSA_DEV_NO_PAGES is set.  A
+ * negative length, one beyond L pages, or rows beyond `total` set BSA_DEV_BAD_SEQLEN, and the
+ * sequence is not served (a negative new length counts as none).  An entry of free_pages or
+ * block_table outside [0, num_pages) sets BSA_DEV_BAD_PAGE, its tokens get slot -1. */
+bsa_status_t bsa_assign_pages(const bsa_pages_dims_t *dims, const int *new_lens,
+                              const int *cache_seqlens, int *block_table, int *free_pages,
+                              int *free_count, int *cu_seqlens, int *seqused_kv, int *positions,
+                              int *slot_map, int *dev_status, void *stream);
+
+/* Cuts every sequence down to its first keep_lens[b] tokens (0: all of it goes; more than it holds:
+ * nothing does) and puts the pages that hold none of them on the stack, in an order that undoes
+ * bsa_assign_pages: pages that one call took and the next gives back lie where they were.
+ *   seq_lens, keep_lens  int32 [B];  lens_out  int32 [B]: tokens held afterwards (may be seq_lens)
+ *   block_table          int32 [B, L], read: the entries stay
+ * A page must be held by one sequence only (keep a shared prefix by keep_lens).  A length that is
+ * negative or beyond L pages sets BSA_DEV_BAD_SEQLEN and its sequence is left alone; an entry outside
+ * [0, num_pages) sets BSA_DEV_BAD_PAGE and goes on the stack as -1; more pages than the stack has room
+ * for set BSA_DEV_BAD_PAGE, the surplus is dropped. */
+bsa_status_t bsa_release_pages(const bsa_pages_dims_t *dims, const int *seq_lens,
+                               const int *keep_lens, const int *block_table, int *free_pages,
+                               int *free_count, int *lens_out, int *dev_status, void *stream);
+
+/* The 4-bit cache.  A row of 128 values is 64 bytes of e2m1 codes, two to a byte, the first in the low
+ * half, and eight e4m3 scales, one for each 16 values:  value = code * scale * descale.
+ *   k/v pages            uint8 [num_pages, N2, page_size, 64] (HND) or [num_pages, page_size, N2, 64]
+ *                        (NHD), 16-byte aligned
+ *   k_scales, v_scales   e4m3 [num_pages, N2, page_size, 8] in either layout, 16-byte aligned
+ *   k_descale, v_descale fp32 [1] (BSA_SCALE_PER_TENSOR) or [N2] (BSA_SCALE_PER_HEAD), positive and
+ *                        finite; the caller chooses them: the largest value expected / (6 * 448) uses
+ *                        the scales' whole range
+ * 144 bytes hold K and V of a token and KV head, 260 in the e4m3 cache. */
+typedef struct {
+  int N2;                /* KV heads */
+  int D;                 /* head dim, must be 128 */
+  int page_size;         /* 32 or 64 */
+  int num_pages;         /* physical pages */
+  int total_new;         /* rows of k_new / v_new and slot_map */
+  int k_scale_kind;      /* BSA_SCALE_PER_TENSOR or BSA_SCALE_PER_HEAD */
+  int v_scale_kind;      /* BSA_SCALE_PER_TENSOR or BSA_SCALE_PER_HEAD */
+  int kv_layout;         /* BSA_KV_HND (0) or BSA_KV_NHD (1) */
+  long long k_stride;    /* elements from token to token, >= N2 * 128 and a multiple of 8 */
+  long long v_stride;
+} bsa_fp4_append_dims_t;
+
+/* Writes new tokens into the 4-bit cache.  Row i of k_new / v_new (bf16 [total_new, N2, 128], 16-byte
+ * aligned) goes to slot slot_map[i] = page * page_size + slot, as bsa_assign_pages gives it; a
+ * negative one is skipped, one beyond the pool is reported (BSA_DEV_BAD_PAGE) and skipped.  No slot may
+ * be named twice in a call.  The scale of 16 values is the e4m3 number nearest to their largest
+ * magnitude / (6 * descale), a code the e2m1 number nearest to value / (scale * descale), ties to
+ * the even code, 448 and 6 the largest; both decided exactly (for blocks whose largest magnitude is
+ * at least 2^-100).  Inputs must be finite. */
+bsa_status_t bsa_fp4_append_kv(const bsa_fp4_append_dims_t *dims, const void *k_new_bf16,
+                               const void *v_new_bf16, const int *slot_map,
+                               const float *k_descale, const float *v_descale, void *k_pages,
+                               void *v_pages, void *k_scales, void *v_scales, int *dev_status,
+                               void *stream);
+
+/* bsa_fp8_gather_kv on the 4-bit cache (dims->k_scale_kind BSA_SCALE_PER_TENSOR or
+ * BSA_SCALE_PER_HEAD): code * scale is exact, the product with the descale is one fp32 product,
+ * rounded once more for bf16. */
+bsa_status_t bsa_fp4_gather_kv(const bsa_fp8_gather_dims_t *dims, const void *k_pages,
+                               const void *v_pages, const void *k_scales, const void *v_scales,
+                               const float *k_descale, const float *v_descale,
+                               const int *cu_seqlens, const int *cache_starts,
+                               const int *block_table, void *k_out, void *v_out, int *dev_status,
+                               void *stream);
+
+/* bsa_fp8_decode over the 4-bit cache (dims->k_scale_kind BSA_SCALE_PER_TENSOR or BSA_SCALE_PER_HEAD),
+ * with the same queries, selection, outputs, workspace rules and precision: code * scale is exact
+ * in the products' fp16. */
+size_t bsa_fp4_decode_workspace_size(const bsa_fp8_decode_dims_t *dims);
+bsa_status_t bsa_fp4_decode(const bsa_fp8_decode_dims_t *dims, const void *q,
+                            const float *q_descale, const void *k_pages, const void *v_pages,
+                            const void *k_scales, const void *v_scales, const float *k_descale,
+                            const float *v_descale, const int *seqused_kv,
+                            const int *block_table, const uint8_t *block_mask,
+                            const int *sparse_indices, const int *sparse_seq_len,
+                            float softmax_scale, void *out_bf16, float *lse_f32, void *workspace,
+                            size_t workspace_bytes, int *dev_status, void *stream);
 
 /* Sets the limit of every bounded wait inside the prefill and decode kernels for launches that
  * follow, in nanoseconds, for the whole process; 0 restores the default of 2 s.  A wait that runs out

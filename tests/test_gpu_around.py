@@ -1,0 +1,745 @@
+"""Rotary positions, page tables and the 4-bit cache on the GPU against references (bounds and their
+derivation: around_helpers.py, serving_helpers.py)."""
+import numpy as np
+import pytest
+import torch
+
+import around_helpers as A
+import serving_helpers as S
+from gpu_helpers import ensure_built
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    ensure_built()
+
+
+def _bf16(rng, shape, scale=1.0):
+    return torch.from_numpy((rng.standard_normal(shape) * scale).astype(np.float32)).to(
+        torch.bfloat16)
+
+
+def _slice_of(x, extra, at, fill=float("nan")):
+    """x [T, N, 128] as a slice of a wider tensor whose other columns hold NaN; (slice, whole)."""
+    T, N, D = x.shape
+    wide = torch.full((T, N + extra, D), fill, dtype=x.dtype, device="cuda")
+    wide[:, at:at + N] = x.cuda()
+    return wide[:, at:at + N], wide
+
+
+def _i32(a):
+    return torch.from_numpy(np.asarray(a, dtype=np.int32)).cuda()
+
+
+# ---------------------------------------------------------------------------------------------
+# rope
+# ---------------------------------------------------------------------------------------------
+
+FAR = [0, 1, -1, 7, 4095, 131071, 500000, 2 ** 31 - 1, -2 ** 31, 12345678]
+
+
+def _freqs(R, **kw):
+    import block_sparse_fp8_gb300 as bsa
+
+    f = bsa.rope_frequencies(R, **kw)
+    return f.cuda(), f.numpy().view(np.uint64)
+
+
+ROPE = [
+    # T, N1, N2, R, layout, amplitude
+    (1, 1, 0, 128, 0, 1.0),
+    (1, 8, 1, 128, 1, 1.0),
+    (3, 5, 2, 64, 0, 1.25),
+    (7, 9, 3, 96, 0, 1.0),
+    (10, 4, 4, 16, 1, 0.5),
+    (10, 1, 1, 16, 0, -1.0),
+    (33, 32, 8, 80, 1, 1.0),
+    (129, 12, 4, 112, 0, 1.0),
+    (1000, 64, 8, 128, 0, 1.1),
+    (2049, 7, 1, 32, 1, 1.0),
+    (6001, 32, 8, 128, 1, 1.0),
+]
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("T,N1,N2,R,layout,amplitude", ROPE)
+def test_rope(T, N1, N2, R, layout, amplitude, wide):
+    import block_sparse_fp8_gb300 as bsa
+
+    rng = np.random.default_rng(T + R)
+    q, k = _bf16(rng, (T, N1, 128)), _bf16(rng, (T, N2, 128)) if N2 else None
+    pos = np.resize(np.array(FAR), T).astype(np.int64)
+    pos[len(FAR):] = rng.integers(0, 1 << 20, max(0, T - len(FAR)))
+    fd, f = _freqs(R, base=10000.0)
+    if wide:
+        qd, _ = _slice_of(q, 3, 1)
+        kd = _slice_of(k, 2, 0)[0] if N2 else None
+        out, out_all = _slice_of(torch.zeros_like(q), 2, 2, fill=5.0)
+    else:
+        qd, kd, out = q.cuda(), k.cuda() if N2 else None, None
+    got = bsa.rope(qd, _i32(pos), fd, k=kd, layout=layout, amplitude=amplitude, out=out)
+    torch.cuda.synchronize()
+    for x, y in ((q, got[0]), (k, got[1])):
+        if x is None:
+            assert y is None
+            continue
+        ref, e = A.turned(x.double().numpy(), pos, f, layout, np.float64(np.float32(amplitude)))
+        S.within(y, ref, e + 2.0 ** -8 * np.abs(ref), "rope")
+        assert torch.equal(y[..., R:].cpu(), x[..., R:])         # the rest is copied
+    if wide:
+        assert (out_all[:, :2] == 5).all()
+    # where they lie: the same bits
+    again = bsa.rope(qd, _i32(pos), fd, k=kd, layout=layout, amplitude=amplitude, out=qd, k_out=kd)
+    assert torch.equal(again[0], got[0]) and (k is None or torch.equal(again[1], got[1]))
+
+
+@pytest.mark.parametrize("rule", [0, 1])
+@pytest.mark.parametrize("T,N1,N2,R,layout,amplitude", ROPE)
+def test_rope_quantize(T, N1, N2, R, layout, amplitude, rule):
+    import block_sparse_fp8_gb300 as bsa
+
+    rng = np.random.default_rng(T + R + 1)
+    x = _bf16(rng, (T, N1, 128), 3.0)
+    x[0, 0] = 0                                             # a zero row: descale 1, zero codes
+    pos = np.resize(np.array(FAR), T).astype(np.int64)
+    fd, f = _freqs(R, base=500000.0)
+    qd, _ = _slice_of(x, 1, 0)
+    codes, d = bsa.rope_quantize(qd, _i32(pos), fd, layout=layout, amplitude=amplitude, rule=rule)
+    codes, d = codes.cpu().numpy(), d.double().cpu().numpy()
+    ref, e = A.turned(x.double().numpy(), pos, f, layout, np.float64(np.float32(amplitude)))
+    top, err = np.abs(ref).max(-1) / 448, e.max(-1) / 448
+    assert d[0, 0] == 1 and (codes[0, 0] & 127 == 0).all()
+    top[0, 0], err[0, 0] = 1, 0
+    if rule:
+        assert (np.frexp(d)[0] == 0.5).all()
+        assert (d >= top - err).all() and (d < 2 * (top + err) * (1 + 2.0 ** -23)).all()
+    else:
+        assert (np.abs(d - top) <= err + 2.0 ** -23 * top).all()
+    y = ref / d[..., None]
+    v = np.abs(S.VAL[codes])
+    assert np.isfinite(v).all()
+    best = S.VAL[:127][A.nearest(np.minimum(np.abs(y), 448), S.VAL[:127])]
+    slack = e / d[..., None] + 2.0 ** -22 * np.abs(y)
+    assert (np.abs(np.abs(y) - v) <= np.abs(np.abs(y) - best) + 2 * slack).all()
+    assert (np.signbit(S.VAL[codes]) == np.signbit(y))[(v > 0) & (np.abs(y) > slack)].all()
+
+
+def test_rope_agrees_with_quantize_rows():
+    """rope_quantize at position 0 is quantize_rows, bit for bit."""
+    import block_sparse_fp8_gb300 as bsa
+
+    x = _bf16(np.random.default_rng(4), (70, 6, 128), 2.0).cuda()
+    fd, _ = _freqs(128)
+    for rule in (bsa.DESCALE_AMAX, bsa.DESCALE_UE8M0):
+        a = bsa.rope_quantize(x, torch.zeros(70, dtype=torch.int32, device="cuda"), fd, rule=rule)
+        b = bsa.quantize_rows(x, rule=rule)
+        assert torch.equal(a[1], b[1]) and torch.equal(a[0] & 127, b[0] & 127)
+
+
+def test_rope_does_not_spread_nan():
+    """A NaN or an infinity in one row leaves the others as they are."""
+    import block_sparse_fp8_gb300 as bsa
+
+    x = _bf16(np.random.default_rng(5), (40, 8, 128)).cuda()
+    bad = x.clone()
+    bad[3, 2, 5], bad[30, 7, 127] = float("nan"), float("inf")
+    pos, (fd, _) = _i32(np.arange(40)), _freqs(128)
+    a, b = bsa.rope(x, pos, fd)[0], bsa.rope(bad, pos, fd)[0]
+    hit = torch.zeros(40, 8, dtype=torch.bool, device="cuda")
+    hit[3, 2] = hit[30, 7] = True
+    assert torch.equal(a[~hit], b[~hit]) and not torch.isfinite(b[3, 2, 5])
+
+
+# ---------------------------------------------------------------------------------------------
+# pages
+# ---------------------------------------------------------------------------------------------
+
+def _pages_case(seed, B, ps, hi, old_hi, short=0, spare=5, L=None):
+    rng = np.random.default_rng(seed)
+    new = rng.integers(0, hi + 1, B)
+    old = rng.integers(0, old_hi + 1, B)
+    held, need = -(-old // ps), -(-(old + new) // ps)
+    L = L or max(int(need.max()) if B else 0, 1) + 1
+    P = int(need.sum()) + spare
+    perm = rng.permutation(P)
+    table = rng.integers(-5, 0, (B, L)).astype(np.int32)
+    at = 0
+    for b in range(B):
+        table[b, :held[b]] = perm[at:at + held[b]]
+        at += held[b]
+    count = P - at
+    free = np.full(P, -9, dtype=np.int32)
+    free[:count] = perm[at:]
+    return new, old, table, free, max(count - short, 0)
+
+
+def _assign(new, old, table, free, count, ps, total):
+    import block_sparse_fp8_gb300 as bsa
+
+    d = dict(table=_i32(table), free=_i32(free), count=_i32([count]))
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    outs = [torch.full((n,), 77, dtype=torch.int32, device="cuda")
+            for n in (len(new) + 1, len(new), total, total)]
+    bsa.assign_pages(_i32(new), _i32(old), d["table"], d["free"], d["count"], ps, total, *outs,
+                     dev_status=st)
+    torch.cuda.synchronize()
+    return outs, d, int(st.item())
+
+
+def _same(got, ref, what):
+    got = got.cpu().numpy()
+    bad = np.argwhere(got != ref)
+    assert got.shape == ref.shape and not len(bad), (what, len(bad), bad[:3], got[tuple(bad[0])],
+                                                     ref[tuple(bad[0])])
+
+
+PAGES = [
+    # B, ps, hi, old_hi, total padding
+    (1, 32, 1, 0, 0), (1, 64, 1, 64, 3), (1, 32, 5000, 31, 7), (5, 32, 33, 100, 0),
+    (17, 64, 0, 200, 4), (300, 32, 1, 500, 9), (1023, 32, 2, 70, 0), (1024, 64, 1, 64, 1),
+    (1025, 32, 3, 40, 2), (3000, 32, 1, 33, 5), (2500, 64, 200, 10, 100), (64, 64, 3000, 0, 3),
+    (40, 32, 2000, 3000, 0),
+]
+
+
+@pytest.mark.parametrize("B,ps,hi,old_hi,pad", PAGES)
+def test_assign_and_release(B, ps, hi, old_hi, pad):
+    import block_sparse_fp8_gb300 as bsa
+
+    new, old, table, free, count = _pages_case(B + hi, B, ps, hi, old_hi)
+    total = int(new.sum()) + pad
+    outs, d, st = _assign(new, old, table, free, count, ps, total)
+    cu, used, pos, slots, table2, left, status = A.assigned(new, old, table, free, count, ps, total)
+    assert st == status == 0
+    for got, ref, what in zip(outs, (cu, used, pos, slots), ("cu", "used", "positions", "slots")):
+        _same(got, ref, what)
+    _same(d["table"], table2, "table")
+    _same(d["free"], free, "free")
+    assert int(d["count"]) == left
+    # taken back at once: the stack as it was
+    left_lens = bsa.release_pages(outs[1], _i32(old), d["table"], d["free"], d["count"], ps)
+    _same(left_lens, old, "lens")
+    _same(d["free"], free, "free after")
+    assert int(d["count"]) == count
+    # some kept in part, in place
+    rng = np.random.default_rng(B)
+    keep = rng.integers(-3, old.max() + 10, B)
+    lens = _i32(old)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ref = A.released(old, keep, table2, free, count, ps)
+    bsa.release_pages(lens, _i32(keep), d["table"], d["free"], d["count"], ps, out=lens,
+                      dev_status=st)
+    _same(lens, ref[0], "lens kept")
+    _same(d["free"], ref[1], "free kept")
+    assert int(d["count"]) == ref[2] and int(st.item()) == ref[3] == 0
+
+
+@pytest.mark.parametrize("B,ps,hi,old_hi,short", [
+    (1, 32, 100, 10, 50), (8, 64, 500, 100, 20), (2000, 32, 40, 60, 700), (30, 32, 700, 0, 10 ** 6),
+    (1100, 32, 1, 64, 7)])
+def test_assign_with_too_few_pages(B, ps, hi, old_hi, short):
+    new, old, table, free, count = _pages_case(B, B, ps, hi, old_hi, short)
+    total = int(new.sum())
+    outs, d, st = _assign(new, old, table, free, count, ps, total)
+    cu, used, pos, slots, table2, left, status = A.assigned(new, old, table, free, count, ps, total)
+    assert st == status == 16
+    for got, ref, what in zip(outs, (cu, used, pos, slots), ("cu", "used", "positions", "slots")):
+        _same(got, ref, what)
+    _same(d["table"], table2, "table")
+    assert int(d["count"]) == left
+
+
+@pytest.mark.parametrize("total_off", [0, -100, 3000])
+def test_assign_with_bad_lengths(total_off):
+    """Negative lengths, one beyond the table, one at its very end, and too many rows."""
+    new, old, table, free, count = _pages_case(3, 40, 32, 60, 100, L=6)
+    new[3], old[7], new[11], old[20] = -4, -1, 2 ** 31 - 1, 2 ** 31 - 1
+    new[25], old[25] = 192, 0                          # exactly the table's room
+    new[26], old[26] = 193, 0
+    total = int(np.maximum(new, 0).astype(np.int64)[[i for i in range(40) if i != 11]].sum())
+    total = max(0, total + total_off)
+    ref = A.assigned(np.where(new > 10 ** 6, 10 ** 6, new), old, table, free, count, 32, total)
+    outs, d, st = _assign(new, old, table, free, count, 32, total)
+    assert st == ref[6] and st & 4
+    for got, r, what in zip(outs, ref, ("cu", "used", "positions", "slots")):
+        if what == "positions":                        # of sequences that have one
+            ok = ref[3] >= 0
+            got, r = got[torch.from_numpy(ok).cuda()], r[ok]
+        _same(got, r, what)
+    _same(d["table"], ref[4], "table")
+    assert int(d["count"]) == ref[5]
+
+
+def test_assign_and_release_bad_entries():
+    """Stack and table entries outside the pool are reported, and their tokens have no slot."""
+    import block_sparse_fp8_gb300 as bsa
+
+    new, old, table, free, count = _pages_case(9, 6, 32, 100, 50)
+    free[count - 2] = len(free)                        # one past the pool
+    held = np.flatnonzero((old % 32 != 0) & (new > 0))
+    table[held[0], old[held[0]] // 32] = -1            # a page in use that is none
+    total = int(new.sum())
+    ref = A.assigned(new, old, table, free, count, 32, total)
+    outs, d, st = _assign(new, old, table, free, count, 32, total)
+    assert st == ref[6] == 2
+    _same(outs[3], ref[3], "slots")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    zero = torch.zeros_like(outs[1])
+    ref2 = A.released(ref[1], np.zeros(6), ref[4], free, ref[5], 32)
+    bsa.release_pages(outs[1], zero, d["table"], d["free"], d["count"], 32, dev_status=st)
+    _same(d["free"], ref2[1], "free")
+    assert int(d["count"]) == ref2[2] and int(st.item()) == ref2[3] == 2
+    # given back twice: what the stack has no room for is dropped
+    before = d["free"].clone()
+    bsa.release_pages(outs[1], zero, d["table"], d["free"], d["count"], 32, dev_status=st)
+    assert int(d["count"]) == min(len(free), ref2[2] + (ref2[2] - ref[5]))
+    assert before.shape == d["free"].shape
+
+
+def test_assign_nothing():
+    """No sequences, or none that gets a token: the padding rows are marked all the same."""
+    import block_sparse_fp8_gb300 as bsa
+
+    e = torch.zeros(0, dtype=torch.int32, device="cuda")
+    for total in (0, 5, 5000):
+        cu, used, pos, slot = bsa.assign_pages(
+            e, e, torch.zeros(0, 4, dtype=torch.int32, device="cuda"), _i32([0, 1]), _i32([2]), 32,
+            total)
+        assert (slot == -1).all() and (pos == 0).all() and slot.numel() == total
+        if total:
+            assert cu.tolist() == [0]
+        count = _i32([2])
+        cu, used, pos, slot = bsa.assign_pages(
+            _i32([0, 0]), _i32([5, 0]), _i32([[1, -1], [-1, -1]]), _i32([0, 1]), count, 32, total)
+        assert cu.tolist() == [0, 0, 0] and used.tolist() == [5, 0] and int(count) == 2
+        assert (slot == -1).all() and (pos == 0).all()
+
+
+# ---------------------------------------------------------------------------------------------
+# the 4-bit cache: append and gather
+# ---------------------------------------------------------------------------------------------
+
+def _pool4(P, N2, ps, nhd, fill=0xA5):
+    shape = (P, ps, N2, 64) if nhd else (P, N2, ps, 64)
+    pages = [torch.full(shape, fill, dtype=torch.uint8, device="cuda") for _ in "kv"]
+    scales = [torch.full((P, N2, ps, 8), fill, dtype=torch.uint8, device="cuda") for _ in "kv"]
+    return pages, scales
+
+
+def _rows_of(pages, scales, nhd):
+    """[P, N2, ps, ...] on the host."""
+    p = [x.cpu().numpy() for x in pages]
+    return [x.transpose(0, 2, 1, 3) if nhd else x for x in p], [x.cpu().numpy() for x in scales]
+
+
+def _borders(rng, T, N2, g):
+    """bf16 rows whose quotients lie on, or next to, the borders between codes and between scales."""
+    x = rng.standard_normal((T, N2, 8, 16))
+    top = S.VAL[rng.integers(1, 127, (T, N2, 8, 1))]
+    mids = np.array([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 0.0, 6.0])
+    x = np.where(rng.random(x.shape) < 0.7, mids[rng.integers(0, 9, x.shape)] * np.sign(x), x)
+    x[..., 0] = 6
+    half = rng.random((T, N2, 8)) < 0.3                # a largest value between two scales
+    nxt = S.VAL[np.minimum(np.searchsorted(S.VAL[:127], top[..., 0]) + 1, 126)]
+    x = x * top * g.reshape(1, -1, 1, 1)
+    x[..., 0] = np.where(half, 3 * (top[..., 0] + nxt) * g.reshape(1, -1, 1), x[..., 0])
+    return x.reshape(T, N2, 128)
+
+
+APPEND = [
+    # T, N2, ps, nhd, head, kind of values
+    (1, 1, 32, False, True, "normal"), (1, 8, 64, True, True, "normal"),
+    (5, 3, 32, True, False, "normal"), (64, 8, 64, False, True, "normal"),
+    (77, 1, 64, False, False, "borders"), (100, 5, 32, True, True, "borders"),
+    (1000, 2, 32, False, True, "borders"), (40, 4, 64, False, True, "extremes"),
+    (513, 8, 32, True, True, "sevenths"), (4097, 8, 64, False, False, "sevenths"),
+]
+
+
+@pytest.mark.parametrize("T,N2,ps,nhd,head,kind", APPEND)
+def test_append_and_gather_fp4(T, N2, ps, nhd, head, kind):
+    import block_sparse_fp8_gb300 as bsa
+
+    rng = np.random.default_rng(T + N2)
+    gk = rng.uniform(0.001, 0.01, N2 if head else 1).astype(np.float32)
+    gv = rng.uniform(0.001, 0.01, N2 if head else 1).astype(np.float32)
+    if kind == "borders":
+        gk = np.exp2(rng.integers(-9, -4, gk.shape)).astype(np.float32)    # exact ties
+        x = torch.from_numpy(_borders(rng, T, N2, np.broadcast_to(gk.astype(float), N2)).astype(
+            np.float32)).to(torch.bfloat16)
+    else:
+        x = _bf16(rng, (T, N2, 128), 2.0)
+    v = _bf16(rng, (T, N2, 128), 1.5)
+    if kind == "sevenths":                              # descales as a largest value gives them
+        gk[:] = np.float32(np.float32(x.abs().max().item()) / np.float32(2688))
+        gv[:] = np.float32(np.float32(v.abs().max().item()) / np.float32(2688))
+    if kind == "extremes":
+        x[0] = 0                                        # nothing but zeros
+        x[1] *= 2.0 ** -40                              # below the smallest scale
+        x[2] *= 1000.0                                  # above the largest
+        x[3] = 2.0 ** -30
+        x[4], x[5] = torch.finfo(torch.bfloat16).max, -torch.finfo(torch.bfloat16).max
+        x[6, :, ::16] = 100.0                           # one of each block stands out
+        x[7] = -0.0
+        x[8] *= 2.0 ** -9
+    P = -(-T // ps) + 3
+    slots = rng.permutation(P * ps)[:T].astype(np.int32)
+    skip = np.zeros(T, dtype=bool)
+    if T > 4:
+        skip[[1, T // 2]] = True
+        slots[skip] = -1
+    pages, scales = _pool4(P, N2, ps, nhd)
+    kinds = dict(kv_layout=bsa.KV_NHD if nhd else bsa.KV_HND,
+                 k_scale_kind=bsa.SCALE_PER_HEAD if head else bsa.SCALE_PER_TENSOR,
+                 v_scale_kind=bsa.SCALE_PER_HEAD if head else bsa.SCALE_PER_TENSOR)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    t = lambda a: torch.from_numpy(a).cuda()
+    bsa.append_kv_fp4(x.cuda(), _slice_of(v, 3, 2)[0], _i32(slots), *pages, *scales, t(gk), t(gv),
+                      dev_status=st, **kinds)
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0
+    p, s = _rows_of(pages, scales, nhd)
+    untouched = np.ones(P * ps, dtype=bool)
+    untouched[slots[~skip]] = False
+    pg, sl = slots[~skip] // ps, slots[~skip] % ps
+    for rows, g, c, e in ((x, gk, p[0], s[0]), (v, gv, p[1], s[1])):
+        ref_c, ref_s = A.quantise4(rows.double().numpy()[~skip],
+                                   np.broadcast_to(g.astype(np.float64), N2)[:, None])
+        got_c, got_s = c[pg, :, sl], e[pg, :, sl]
+        assert np.array_equal(got_s, ref_s), np.argwhere(got_s != ref_s)[:3]
+        a, b = A.LEVEL[A.unpack4(got_c)], A.LEVEL[A.unpack4(ref_c)]
+        assert np.array_equal(a, b), (np.argwhere(a != b)[:3], a[a != b][:3], b[a != b][:3])
+        for arr in (c, e):
+            flat = arr.transpose(0, 2, 1, 3).reshape(P * ps, -1)
+            assert (flat[untouched] == 0xA5).all()
+    # and read back, sequence by sequence: runs of consecutive slots
+    table = rng.permutation(P).astype(np.int32).reshape(1, P)
+    n = P * ps - 5
+    cu = np.array([0, n], dtype=np.int32)
+    for dtype in (torch.bfloat16, torch.float32):
+        for which in ("both", "k", "v"):
+            a = [pages[0] if which != "v" else None, pages[1] if which != "k" else None]
+            rest = [scales[0] if which != "v" else None, scales[1] if which != "k" else None]
+            got = bsa.gather_kv_fp4(*a, *rest, t(gk), t(gv), _i32(cu), _i32(table), n + 2,
+                                    cache_starts=_i32([3]), out_dtype=dtype, dev_status=st, **kinds)
+            for out, c, e, g, off in ((got[0], p[0], s[0], gk, which == "v"),
+                                      (got[1], p[1], s[1], gv, which == "k")):
+                if off:
+                    assert out is None
+                    continue
+                at = np.arange(3, 3 + n)
+                val = A.values4(c, e)[table[0, at // ps], :, at % ps].astype(np.float32)
+                ref = torch.from_numpy(val * np.broadcast_to(g, N2)[:, None]).to(dtype)
+                out = out[:n].cpu()
+                same = (out == ref) | (torch.isnan(out) & torch.isnan(ref))
+                assert same.all()
+    assert int(st.item()) == 0
+
+
+def test_append_fp4_bad_slots():
+    """A slot beyond the pool is reported, and nothing is written for it."""
+    import block_sparse_fp8_gb300 as bsa
+
+    pages, scales = _pool4(2, 2, 32, False)
+    x = _bf16(np.random.default_rng(0), (4, 2, 128)).cuda()
+    g = torch.full((1,), 0.001, device="cuda")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    bsa.append_kv_fp4(x, x, _i32([64, 2 ** 31 - 1, -1, -2 ** 31]), *pages, *scales, g, g,
+                      dev_status=st)
+    assert int(st.item()) == bsa.DEV_BAD_PAGE
+    assert all((t == 0xA5).all() for t in pages + scales)
+    bsa.append_kv_fp4(x, x, _i32([64, 3, -1, 63]), *pages, *scales, g, g)
+    assert (pages[0][0, :, 3] != 0xA5).any() and (pages[1][1, :, 31] != 0xA5).any()
+
+
+def test_gather_fp4_bad_pages_and_rows_behind():
+    import block_sparse_fp8_gb300 as bsa
+
+    pages, scales = _pool4(3, 2, 32, False, fill=0x33)
+    g = torch.full((2,), 2.0, device="cuda")
+    k = torch.full((40, 2, 128), 9.0, device="cuda")
+    v = torch.full((40, 2, 128), 9.0, device="cuda")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    bsa.gather_kv_fp4(*pages, *scales, g, g, _i32([0, 33]), _i32([[1, 3]]), 40, k_out=k, v_out=v,
+                      dev_status=st)
+    assert int(st.item()) == bsa.DEV_BAD_PAGE
+    want = 1.5 * S.VAL[0x33] * 2
+    assert (k[:32] == want).all() and (k[32] == 0).all() and (k[33:] == 9).all()
+    assert (v[:32] == want).all() and (v[32] == 0).all() and (v[33:] == 9).all()
+
+
+# ---------------------------------------------------------------------------------------------
+# decode over it
+# ---------------------------------------------------------------------------------------------
+
+def _decode4(cache, q, qd, enabled=None, form="mask", scale=None, dev=None, **kw):
+    import block_sparse_fp8_gb300 as bsa
+
+    d = dev or cache.device()
+    q, qd = q.cuda(), None if qd is None else qd.cuda()
+    B, N1, _ = q.shape
+    max_kv = kw.pop("max_kv_len", max(cache.lens + [0]))
+    if enabled is not None:
+        if form == "mask":
+            kw["block_mask"] = torch.from_numpy(enabled.astype(np.uint8) * 3).cuda()
+        else:
+            idx, cnt = S.index_lists(enabled, np.random.default_rng(3))
+            kw["sparse_indices"] = torch.from_numpy(idx).cuda()
+            kw["sparse_seq_len"] = torch.from_numpy(cnt).cuda()
+    dims = bsa.make_decode_dims(q, d["k_pages"], d["block_table"], max_kv,
+                                d["kinds"]["k_scale_kind"], d["kinds"]["v_scale_kind"],
+                                d["kinds"]["kv_layout"], sparse=enabled is not None)
+    ws = torch.full((bsa.decode_fp4_workspace_size(dims),), 0xff, dtype=torch.uint8, device="cuda")
+    out = torch.full((B, N1, 128), float("nan"), dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((N1, B), float("nan"), device="cuda")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    expect = kw.pop("status", 0)
+    got = bsa.decode_fp4(q, d["k_pages"], d["v_pages"], d["k_scales"], d["v_scales"],
+                         d["k_descale"], d["v_descale"], d["seqused_kv"], d["block_table"], max_kv,
+                         q_descale=qd, softmax_scale=scale, out=out, lse=lse, dev_status=st,
+                         workspace=ws, **d["kinds"], **kw)
+    torch.cuda.synchronize()
+    assert got[0] is out and got[1] is lse
+    assert int(st.item()) == expect
+    return out, lse
+
+
+def _compare(cache, q64, got, enabled=None, what="", scale=None):
+    O, Z, E, F = A.reference4(cache, q64, enabled, **({} if scale is None else {"scale": scale}))
+    S.within(got[0], O, E, what + " O")
+    S.within(got[1], Z, F, what + " LSE")
+
+
+DENSE = [
+    # lens, N1, N2, ps, q8, head, nhd
+    ([1], 1, 1, 32, False, True, False),
+    ([2, 31], 2, 2, 32, True, True, True),
+    ([32, 33, 63, 64, 65], 8, 2, 32, False, True, False),
+    ([127, 128, 129], 8, 1, 64, False, False, False),
+    ([255, 0, 256, 257, 0], 12, 4, 64, True, False, True),
+    ([1000, 1, 517], 7, 1, 32, False, True, True),
+    ([300] * 3, 9, 1, 64, False, True, False),
+    ([640, 5, 1290], 32, 2, 64, True, True, False),
+    ([77], 48, 3, 32, False, True, True),
+    ([2048], 5, 5, 64, False, True, False),
+    ([200] * 80, 8, 4, 64, True, True, False),
+    ([9001, 130], 10, 2, 32, False, True, False),
+    ([20000], 16, 1, 64, True, True, True),
+]
+
+
+@pytest.mark.parametrize("lens,N1,N2,ps,q8,head,nhd", DENSE)
+def test_decode_fp4_dense(lens, N1, N2, ps, q8, head, nhd):
+    cache = A.Cache4(sum(lens) + N1, lens, N2, ps, head, nhd)
+    q, qd, q64 = S.queries(N1, len(lens), N1, q8)
+    got = _decode4(cache, q, qd)
+    _compare(cache, q64, got, what="dense")
+    again = _decode4(cache, q, qd)
+    assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
+
+
+@pytest.mark.parametrize("form", ["mask", "index"])
+@pytest.mark.parametrize("lens,N1,N2,ps,q8,head,nhd", [
+    ([700, 130, 0, 1], 8, 2, 32, False, True, False), ([5000, 4000], 16, 1, 64, True, False, True),
+    ([1290] * 5, 12, 4, 64, False, True, True), ([9000], 7, 1, 32, True, True, False)])
+def test_decode_fp4_sparse(lens, N1, N2, ps, q8, head, nhd, form):
+    cache = A.Cache4(sum(lens), lens, N2, ps, head, nhd)
+    Kb = -(-max(lens) // 128)
+    rng = np.random.default_rng(N1)
+    on = rng.random((len(lens), N1, Kb)) < 0.3
+    on[0, 0] = False                                   # a head with nothing enabled
+    on[-1, :, :] |= rng.random((1, Kb)) < 0.2          # tiles that all heads share
+    q, qd, q64 = S.queries(N1, len(lens), N1, q8)
+    _compare(cache, q64, _decode4(cache, q, qd, on, form), on, form)
+
+
+def test_decode_fp4_many_short_sequences():
+    rng = np.random.default_rng(5)
+    lens = [int(x) for x in rng.integers(0, 300, 301)]
+    cache = A.Cache4(11, lens, 2, 32)
+    q, qd, q64 = S.queries(12, len(lens), 4, False)
+    _compare(cache, q64, _decode4(cache, q, qd), what="many")
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.05, 1.0, 30.0])
+def test_decode_fp4_scales(scale):
+    """No weight but equal ones, a negative scale, and scores beyond any probability's range."""
+    cache = A.Cache4(21, [500, 64, 3], 2, 64)
+    q, qd, q64 = S.queries(22, 3, 8, False)
+    _compare(cache, q64, _decode4(cache, q, qd, scale=scale), scale=np.float64(np.float32(scale)))
+
+
+def test_decode_fp4_strided_queries_and_in_place():
+    import block_sparse_fp8_gb300 as bsa
+
+    cache = A.Cache4(31, [300, 90, 1], 2, 32)
+    q, _, q64 = S.queries(32, 3, 8, False)
+    d = cache.device()
+    view, _ = _slice_of(q, 5, 2)
+    args = (d["k_pages"], d["v_pages"], d["k_scales"], d["v_scales"], d["k_descale"],
+            d["v_descale"], d["seqused_kv"], d["block_table"], 300)
+    a, la = bsa.decode_fp4(view, *args, **d["kinds"])
+    _compare(cache, q64, (a, la))
+    own = q.cuda()
+    b, none = bsa.decode_fp4(own, *args, out=own, return_lse=False, **d["kinds"])
+    assert b is own and none is None and torch.equal(a, b)
+
+
+def test_decode_fp4_bad_data():
+    """Bad pages read as zeros, bad lengths as none; both are reported, nothing else changes."""
+    import block_sparse_fp8_gb300 as bsa
+
+    lens = [400, 200, 129]
+    cache = A.Cache4(41, lens, 2, 32)
+    q, qd, q64 = S.queries(42, 3, 8, False)
+    cache.table[0, 2] = cache.P
+    cache.table[1, 0] = -1
+    for w in "kv":
+        cache.codes[w][0][:, 64:96] = 0
+        cache.codes[w][1][:, :32] = 0
+    _compare(cache, q64, _decode4(cache, q, qd, status=bsa.DEV_BAD_PAGE))
+    d = cache.device()
+    d["seqused_kv"][0] = 401
+    d["seqused_kv"][1] = -1
+    got = _decode4(cache, q, qd, dev=d, status=bsa.DEV_BAD_SEQLEN)
+    cache.lens = [0, 0, 129]
+    _compare(cache, q64, got)
+
+
+def test_decode_fp4_nan_scale_stays_in_its_heads():
+    """A NaN scale of V reaches the heads that enable its tile, and no other."""
+    lens = [600]
+    cache = A.Cache4(51, lens, 1, 64)
+    q, qd, q64 = S.queries(52, 1, 4, False)
+    on = np.ones((1, 4, 5), dtype=bool)
+    on[0, 1:3, 2] = False
+    clean = _decode4(cache, q, qd, on)
+    page, slot = cache.table[0, 300 // 64], 300 % 64
+    cache.v_scales[page, 0, slot, 3] = 0x7f
+    got = _decode4(cache, q, qd, on)
+    bad = torch.isnan(got[0]).cpu().numpy()
+    assert bad[0, [0, 3]][:, 48:64].all() and bad.sum() == 2 * 16
+    assert torch.equal(got[0][:, 1:3], clean[0][:, 1:3]) and torch.equal(got[1], clean[1])
+
+
+# ---------------------------------------------------------------------------------------------
+# together
+# ---------------------------------------------------------------------------------------------
+
+def test_serving_steps_captured():
+    """Prompts admitted, then steps of one token each from one captured graph: pages, rotation,
+    append, decode.  Every step against the fp64 attention over what four bits hold."""
+    import block_sparse_fp8_gb300 as bsa
+
+    B, N1, N2, ps, L = 5, 8, 2, 32, 12
+    P = B * L
+    rng = np.random.default_rng(61)
+    prompts = np.array([70, 0, 33, 1, 200])
+    fd, f = _freqs(128, base=10000.0)
+    pages, scales = _pool4(P, N2, ps, False, fill=0x7f)
+    g = torch.full((N2,), 5.0 / 2688, device="cuda")
+    table = torch.full((B, L), -1, dtype=torch.int32, device="cuda")
+    free, count = _i32(rng.permutation(P)), _i32([P])
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    lens = torch.zeros(B, dtype=torch.int32, device="cuda")
+    history = [[[], []] for _ in range(B)]             # rotated k and v rows as appended
+
+    def place(new, cap, rows):
+        """rows [cap, N1 + 2 N2, 128]; returns (rotated q, lengths afterwards)."""
+        cu, used, pos, slots = bsa.assign_pages(new, lens, table, free, count, ps, cap,
+                                                dev_status=st)
+        q, k = bsa.rope(rows[:, :N1], pos, fd, k=rows[:, N1:N1 + N2])
+        bsa.append_kv_fp4(k, rows[:, N1 + N2:], slots, *pages, *scales, g, g, dev_status=st)
+        lens.copy_(used)
+        return q, k, cu, pos
+
+    def remember(k, rows, cu):
+        cu = cu.tolist()
+        for b in range(B):
+            history[b][0].append(k[cu[b]:cu[b + 1]].double().cpu().numpy())
+            history[b][1].append(rows[cu[b]:cu[b + 1], N1 + N2:].double().cpu().numpy())
+
+    cap = int(prompts.sum()) + 6
+    rows = _bf16(rng, (cap, N1 + 2 * N2, 128)).cuda()
+    _, k, cu, pos = place(_i32(prompts), cap, rows)
+    remember(k, rows, cu)
+    assert pos.tolist()[:70] == list(range(70)) and int(st.item()) == 0
+
+    one = torch.ones(B, dtype=torch.int32, device="cuda")
+    step_rows = torch.zeros(B, N1 + 2 * N2, 128, dtype=torch.bfloat16, device="cuda")
+    keep = {}
+
+    def step():
+        q, k, cu, pos = place(one, B, step_rows)
+        # a sequence may sit a step out, so rows are not sequences: the step's own are its first
+        out, lse = bsa.decode_fp4(q, *pages, *scales, g, g, lens, table, L * ps, dev_status=st)
+        keep.update(q=q, k=k, cu=cu, out=out, lse=lse, pos=pos)
+
+    state = [t.clone() for t in (lens, table, free, count)] + [t.clone() for t in pages + scales]
+    step()                                             # warm-up, taken back
+    for t, was in zip((lens, table, free, count, *pages, *scales), state):
+        t.copy_(was)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for t, was in zip((lens, table, free, count, *pages, *scales), state):
+        t.copy_(was)
+    for i in range(35):                                # across a page's end for every sequence
+        new = _bf16(rng, (B, N1 + 2 * N2, 128)).cuda()
+        step_rows.copy_(new)
+        graph.replay()
+        torch.cuda.synchronize()
+        remember(keep["k"], new, keep["cu"])
+        if i % 17 and i != 34:
+            continue
+        cache = A.Cache4(1, [0] * B, N2, ps)           # only its reference is used
+        cache.kd = cache.vd = g.cpu().numpy()
+        cache.lens = [int(x) for x in lens.tolist()]
+        assert cache.lens == [int(p) + i + 1 for p in prompts]
+        for w in range(2):
+            rows_w = [np.concatenate(h[w]) for h in history]
+            both = [A.quantise4(r.transpose(1, 0, 2), cache.kd.astype(np.float64)[:, None, None])
+                    for r in rows_w]
+            cache.codes["kv"[w]] = [c for c, _ in both]
+            cache.scales["kv"[w]] = [s for _, s in both]
+        _compare(cache, keep["q"].double().cpu().numpy(), (keep["out"], keep["lse"]), what=f"step {i}")
+        # the queries as they were turned
+        ref, e = A.turned(new[:, :N1].double().cpu().numpy(),
+                          np.array(cache.lens) - 1, f, 0, 1.0)
+        S.within(keep["q"], ref, e + 2.0 ** -8 * np.abs(ref), "q")
+    assert int(st.item()) == 0
+    # everything given back: every page is free again, once
+    bsa.release_pages(lens, torch.zeros_like(lens), table, free, count, ps, out=lens)
+    assert int(count) == P and sorted(free.tolist()) == list(range(P)) and lens.tolist() == [0] * B
+
+
+def test_fp4_cache_into_a_prefill():
+    """What follows a prompt held in 4 bits: read back, appended to an e4m3 pool, and prefilled over."""
+    import block_sparse_fp8_gb300 as bsa
+
+    lens, N2, ps = [150, 64], 2, 32
+    cache = A.Cache4(71, lens, N2, ps)
+    d = cache.device()
+    total, cu = sum(lens), _i32([0, 150, 214])
+    k, v = bsa.gather_kv_fp4(d["k_pages"], d["v_pages"], d["k_scales"], d["v_scales"],
+                             d["k_descale"], d["v_descale"], cu, d["block_table"], total,
+                             **d["kinds"])
+    table = _i32(np.arange(10).reshape(2, 5))
+    k8 = torch.zeros(10, N2, ps, 128, dtype=torch.uint8, device="cuda")
+    v8, kd = torch.zeros_like(k8), torch.zeros(10, N2, ps, device="cuda")
+    vs = torch.full((N2,), float(v.abs().max()) / 448, device="cuda")
+    bsa.append_kv(k, v, cu, _i32([0, 0]), table, k8, v8, k_descale=kd, v_scale=vs)
+    q = _bf16(np.random.default_rng(72), (2, 4, 128)).cuda()
+    fd, _ = _freqs(128)
+    q8, qd = bsa.rope_quantize(q, _i32([149, 63]), fd)
+    out, lse = bsa.prefill(q8, k8, v8, qd, kd, vs, _i32([0, 1, 2]), _i32(lens), table, 1, 150)
+    a, la = bsa.decode(q8, k8, v8, kd, vs, _i32(lens), table, 150, q_descale=qd)
+    torch.cuda.synchronize()
+    # the same rows and queries: the prefill's probabilities are e4m3
+    assert torch.allclose(lse, la, rtol=1e-3, atol=1e-3)
+    assert (out.float() - a.float()).abs().max() <= 2.0 ** -4 * float(v.abs().max())
