@@ -53,7 +53,6 @@
 #include <cstdint>
 
 #include "bsa_common.cuh"
-#include "bsa_fp4.cuh"
 #include "ptx_sm103.cuh"
 
 namespace bsa {
@@ -62,24 +61,13 @@ namespace decode {
 constexpr int WARPS = 4;
 constexpr int THREADS = WARPS * 32;
 constexpr int TOK = TILE / WARPS;  // tokens of a tile that one warp owns: one mma row block pair
+constexpr int STAGES = 2;
 constexpr int CTAS_PER_SM = 2;
+// one warp's stage: K rows, V rows (1024-byte aligned, as the swizzle wants)
+constexpr int OFF_V = TOK * HEAD_DIM;
+constexpr int STAGE_BYTES = 2 * TOK * HEAD_DIM;
 constexpr int SMEM_ALIGN = 1024;
-
-// What depends on the cache's format: a row's bytes of codes, and one warp's stage: K rows, V rows
-// (1024- or 512-byte aligned, as the swizzle wants), 4-bit pages' block scales of K and V.
-template <bool FP4, int NT>  // NT: blocks of eight query heads per KV head
-struct Format {
-  static constexpr int STAGES = FP4 ? 4 : 2;
-  static constexpr int ROW = FP4 ? fp4::ROW_BYTES : HEAD_DIM;
-  static constexpr int OFF_V = TOK * ROW;
-  static constexpr int OFF_SCALES = 2 * TOK * ROW;
-  static constexpr int SCALE_BYTES = TOK * fp4::BLOCKS;  // of K or V
-  static constexpr int STAGE_BYTES = OFF_SCALES + (FP4 ? 2 * SCALE_BYTES : 0);
-  // where a warp leaves its sums at the end of a segment: the stage just consumed, or a place behind
-  // the ring where a stage has no room for them
-  static constexpr int SUMS = FP4 ? NT * 8 * HEAD_DIM * 4 : 0;
-  static constexpr int SMEM = WARPS * (STAGES * STAGE_BYTES + SUMS) + SMEM_ALIGN;
-};
+constexpr int SMEM_BYTES = WARPS * STAGES * STAGE_BYTES + SMEM_ALIGN;
 // fp16 probabilities are kept as 2^(s - m + P_SHIFT): the largest, 2^15, fits, and weights down to
 // 2^-29 of it are normal numbers
 constexpr float P_SHIFT = 15.f;
@@ -90,7 +78,7 @@ struct Params {
   const void *q;
   const float *q_descale;
   const uint8_t *k_pages, *v_pages;
-  const uint8_t *k_scales, *v_scales;  // 4-bit pages
+  const uint8_t *k_scales, *v_scales;  // 4-bit pages (bsa_decode_fp4.cuh)
   const float *k_descale, *v_descale;
   const int *seqused_kv, *block_table;
   const uint8_t *block_mask;
@@ -165,22 +153,6 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
   return v;
 }
 
-__device__ __forceinline__ uint2 lds64(uint32_t a) {
-  uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
-  return v;
-}
-__device__ __forceinline__ uint32_t lds16(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.u16 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-  return v;
-}
-__device__ __forceinline__ uint32_t lds8(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-  return v;
-}
-
 __device__ __forceinline__ void prefetch_l2(const void *a) {
   asm volatile("prefetch.global.L2 [%0];" ::"l"(a));
 }
@@ -196,35 +168,6 @@ __device__ __forceinline__ void f16_of_e4m3x4(uint32_t w, uint32_t &lo, uint32_t
       "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
       : "=r"(lo), "=r"(hi)
       : "r"(w));
-}
-
-// Two e4m3 codes (the low half word) -> an f16 pair.
-__device__ __forceinline__ uint32_t f16_of_e4m3x2(uint32_t w) {
-  uint32_t r;
-  asm("{\n\t.reg .b16 a, b;\n\t"
-      "mov.b32 {a, b}, %1;\n\t"
-      "cvt.rn.f16x2.e4m3x2 %0, a;\n\t}"
-      : "=r"(r)
-      : "r"(w));
-  return r;
-}
-
-// Eight e2m1 codes -> four f16 pairs, exactly.
-__device__ __forceinline__ void f16_of_e2m1x8(uint32_t w, uint32_t (&h)[4]) {
-  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
-      "mov.b32 {a, b, c, d}, %4;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
-      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
-      : "r"(w));
-}
-
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
 }
 
 __device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
@@ -483,15 +426,13 @@ struct Cursor {
   }
 };
 
-template <int NT, bool SPARSE, bool FP4>
+template <int NT, bool SPARSE>  // NT: blocks of eight query heads per KV head
 __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
     decode_kernel(const Params p, const __grid_constant__ CUtensorMap tk,
                   const __grid_constant__ CUtensorMap tv) {
-  using F = Format<FP4, NT>;
-  constexpr int STAGES = F::STAGES, STAGE_BYTES = F::STAGE_BYTES, OFF_V = F::OFF_V;
   extern __shared__ uint8_t smem_raw[];
   __shared__ float2 s_ml[WARPS][MAX_G];
-  __shared__ __align__(16) float s_kd[WARPS][STAGES][FP4 ? 4 : TOK];
+  __shared__ __align__(16) float s_kd[WARPS][STAGES][TOK];
   // {heads, tokens left, last tile of its task (1) and of the run (2), page bad}
   __shared__ __align__(16) int4 s_meta[WARPS][STAGES];
   __shared__ uint64_t s_full[WARPS][STAGES];
@@ -551,9 +492,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
   uint32_t qf[NT][16];
   float fac[NT][2];  // score factors of the thread's columns 2 q4, 2 q4 + 1
   float qd[NT];
-  float kd_head = 1.f;  // 4-bit pages: K's descale
   const auto fetch_q = [&](int qb, int qh) {
-    if (FP4 && p.k_descale) kd_head = p.k_descale[p.k_per_head ? qh : 0];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int g = nt * 8 + r;
@@ -581,7 +520,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
   const auto convert_q = [&]() {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      float f = FP4 ? p.scale_log2 * kd_head : p.scale_log2;
+      float f = p.scale_log2;
       if (p.q_e4m3) {
         uint32_t w[8];
 #pragma unroll
@@ -636,19 +575,12 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
         if (bad) report(p, BSA_DEV_BAD_PAGE);
         const int page = bad ? p.num_pages : cur.page, slot = cur.pos & (p.ps - 1);
         const int c1 = p.kv_nhd ? cur.kvh : slot, c2 = p.kv_nhd ? slot : cur.kvh;
-        const bool kd = !FP4 && p.k_per_token && !bad, scales = FP4 && !bad;
+        const bool kd = p.k_per_token && !bad;
         uint64_t *bar = &s_full[warp][stage];
         uint8_t *dst = smem + (warp * STAGES + stage) * STAGE_BYTES;
-        ptx::mbar_arrive_expect_tx(bar, F::OFF_SCALES + (kd ? TOK * 4 : 0) +
-                                            (scales ? 2 * F::SCALE_BYTES : 0));
+        ptx::mbar_arrive_expect_tx(bar, STAGE_BYTES + (kd ? TOK * 4 : 0));
         ptx::tma_load_4d(dst, &tk, bar, 0, c1, c2, page);
         ptx::tma_load_4d(dst + OFF_V, &tv, bar, 0, c1, c2, page);
-        if (scales) {
-          const size_t at = (((size_t)page * p.N2 + cur.kvh) * p.ps + slot) * fp4::BLOCKS;
-          ptx::bulk_load(dst + F::OFF_SCALES, p.k_scales + at, F::SCALE_BYTES, bar);
-          ptx::bulk_load(dst + F::OFF_SCALES + F::SCALE_BYTES, p.v_scales + at, F::SCALE_BYTES,
-                         bar);
-        }
         if (kd)
           ptx::bulk_load(s_kd[warp][stage],
                          p.k_descale + ((size_t)page * p.N2 + cur.kvh) * p.ps + slot, TOK * 4,
@@ -679,15 +611,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
   };
 
   // ---- one warp's 32 tokens of a tile
-  const float kd_all = FP4 || p.k_per_token || !p.k_descale ? 1.f : p.k_descale[0];
-  // A product's row i is token i of 16, but for 4-bit rows, 64 bytes each: there the eight tokens of
-  // a half are taken in the order 0 3 1 2 4 7 5 6, so that whatever rows a phase of the
-  // fragment reads touches, of K (two) or of V (four), they lie in different banks under the
-  // 64-byte swizzle (a row's 16-byte chunks XORed with half the row's number).
-  constexpr uint32_t ORDER = 0x65742130u;
-  const int tok_k = FP4 ? (ORDER >> (4 * r)) & 7 : r;
-  const int tok_v[2] = {FP4 ? (int)((ORDER >> (8 * q4)) & 7) : 2 * q4,
-                        FP4 ? (int)((ORDER >> (8 * q4 + 4)) & 7) : 2 * q4 + 1};
+  const float kd_all = p.k_per_token || !p.k_descale ? 1.f : p.k_descale[0];
   const int group = (1 << p.G) - 1;
   const auto compute = [&](uint32_t st, const float *kds, int heads, int left, bool bad) {
     float s[NT][2][4];  // [head block][16 tokens][token r | r + 8, head 2 q4 | + 1]
@@ -697,36 +621,6 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int c = 0; c < 4; ++c) s[nt][mt][c] = 0.f;
-      if constexpr (FP4) {
-        // a thread's 32 dimensions of a token: 16 bytes of codes, two scales
-        const int t = mt * 16 + tok_k;
-        const uint32_t row = st + t * F::ROW + ((q4 ^ (tok_k >> 1)) << 4);
-        const uint32_t sc = st + F::OFF_SCALES + t * fp4::BLOCKS + 2 * q4;
-        const uint4 a = lds128(row), c = lds128(row + 8 * F::ROW);
-        const uint32_t sa = f16_of_e4m3x2(lds16(sc)),
-                       sb = f16_of_e4m3x2(lds16(sc + 8 * fp4::BLOCKS));
-        const uint32_t wa[4] = {a.x, a.y, a.z, a.w}, wc[4] = {c.x, c.y, c.z, c.w};
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          const uint32_t pick = w < 2 ? 0x1010 : 0x3232;
-          const uint32_t fa = __byte_perm(sa, 0, pick), fb = __byte_perm(sb, 0, pick);
-          uint32_t ha[4], hc[4];
-          f16_of_e2m1x8(wa[w], ha);
-          f16_of_e2m1x8(wc[w], hc);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            ha[k] = mul_f16x2(ha[k], fa);
-            hc[k] = mul_f16x2(hc[k], fb);
-          }
-#pragma unroll
-          for (int k = 0; k < 2; ++k)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              mma16816(s[nt][mt], ha[2 * k], hc[2 * k], ha[2 * k + 1], hc[2 * k + 1],
-                       qf[nt][2 * (2 * w + k)], qf[nt][2 * (2 * w + k) + 1]);
-        }
-        continue;
-      }
       const uint32_t row = st + (mt * 16 + r) * HEAD_DIM;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -751,14 +645,14 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
     for (int mt = 0; mt < 2; ++mt) {
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        const int t = mt * 16 + half * 8 + tok_k;
-        const float kd = !FP4 && p.k_per_token ? kds[t] : kd_all;
+        const int t = mt * 16 + half * 8 + r;
+        const float kd = p.k_per_token ? kds[t] : kd_all;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             float &x = s[nt][mt][2 * half + c];
-            x *= FP4 ? fac[nt][c] : kd * fac[nt][c];
+            x *= kd * fac[nt][c];
             if (!whole) {
               if (bad) x = 0.f;  // no descale was fetched
               if (t >= left || (SPARSE && !((heads >> (nt * 8 + 2 * q4 + c)) & 1))) x = -INFINITY;
@@ -808,71 +702,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
     }
     // With `masked` the columns of heads that mask the tile keep their sums: their weights are zero,
     // but zero times a NaN of the tile's V would reach them through the shared product.
-    const auto pv4 = [&](const bool masked) {
-      uint2 v[2][4];         // as below
-      uint32_t f[2][2] = {};  // scales of tokens 2 q4, 2 q4 + 1 | those + 8, block r
-#pragma unroll
-      for (int mt = 0; mt < 2; ++mt) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int t = mt * 16 + tok_v[j];
-          const uint32_t at =
-              st + OFF_V + t * F::ROW + (((r >> 1) ^ (tok_v[j] >> 1)) << 4) + (r & 1) * 8;
-          v[mt][j] = lds64(at);
-          v[mt][2 + j] = lds64(at + 8 * F::ROW);
-        }
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint32_t c[2];
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const int t = mt * 16 + half * 8 + tok_v[j];
-            c[j] = lds8(st + F::OFF_SCALES + F::SCALE_BYTES + t * fp4::BLOCKS + r);
-            // whatever lies past the end counts as zero (a code is a number, a scale may be a NaN)
-            if (t >= left || bad) c[j] = 0u;
-          }
-          f[mt][half] = f16_of_e4m3x2(c[0] | c[1] << 8);
-        }
-      }
-#pragma unroll
-      for (int w = 0; w < 2; ++w) {
-        uint32_t h[2][4][4];  // [16 tokens][dimensions 8 w + 0 2 4 6 | + 1 of tokens, of those + 8]
-#pragma unroll
-        for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            // the codes of two tokens interleaved: a fragment pairs tokens within a dimension
-            const uint32_t x = w == 0 ? v[mt][2 * half].x : v[mt][2 * half].y;
-            const uint32_t y = w == 0 ? v[mt][2 * half + 1].x : v[mt][2 * half + 1].y;
-            f16_of_e2m1x8((x & 0x0f0f0f0fu) | ((y << 4) & 0xf0f0f0f0u), h[mt][2 * half]);
-            f16_of_e2m1x8(((x >> 4) & 0x0f0f0f0fu) | (y & 0xf0f0f0f0u), h[mt][2 * half + 1]);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              h[mt][2 * half][k] = mul_f16x2(h[mt][2 * half][k], f[mt][half]);
-              h[mt][2 * half + 1][k] = mul_f16x2(h[mt][2 * half + 1][k], f[mt][half]);
-            }
-          }
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          float o[NT][4] = {};
-#pragma unroll
-          for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-            for (int part = 1; part >= 0; --part)
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-                mma16816(o[nt], h[mt][0][k], h[mt][1][k], h[mt][2][k], h[mt][3][k],
-                         pf[nt][mt][part][0], pf[nt][mt][part][1]);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-              if (!masked || ((heads >> (nt * 8 + 2 * q4 + (c & 1))) & 1))
-                acc[nt][4 * w + k][c] = fmaf(acc[nt][4 * w + k][c], alpha[nt][c & 1], o[nt][c]);
-        }
-      }
-    };
-    const auto pv8 = [&](const bool masked) {
+    const auto pv = [&](const bool masked) {
       uint4 v[2][4];  // [16 tokens][tokens 2 q4, 2 q4 + 1 and those + 8], dimensions 16 r .. 16 r + 15
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt) {
@@ -925,9 +755,6 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
                 acc[nt][2 * w + i][c] = fmaf(acc[nt][2 * w + i][c], alpha[nt][c & 1], o[i][nt][c]);
       }
     };
-    const auto pv = [&](const bool masked) {
-      if constexpr (FP4) pv4(masked); else pv8(masked);
-    };
     if (!SPARSE || heads == group)
       pv(false);
     else
@@ -936,11 +763,10 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
 
   // ---- the end of a segment: the four warps' states combined; written out when the segment is
   // its whole task, left as a partial otherwise.  O goes through the stage just consumed, the one
-  // that the next copy will overwrite (4-bit pages: through room of its own).
+  // that the next copy will overwrite.
   bool first_segment = true;
   const auto flush = [&](int stage, bool to_end) {
-    const uint32_t buf = FP4 ? ptx::smem_u32(smem) + WARPS * STAGES * STAGE_BYTES + warp * F::SUMS
-                             : ring + stage * STAGE_BYTES;
+    const uint32_t buf = ring + stage * STAGE_BYTES;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -962,8 +788,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
     __syncthreads();
     const bool complete = from_start && to_end;
     const size_t slot = 2 * (size_t)cta + (first_segment ? 0 : 1);
-    const uint8_t *o0 = smem + (FP4 ? WARPS * STAGES : stage) * STAGE_BYTES;
-    constexpr int o_step = FP4 ? F::SUMS : STAGES * STAGE_BYTES;
+    const uint8_t *o0 = smem + stage * STAGE_BYTES;
 #pragma unroll 2
     for (int g = warp; g < p.G; g += WARPS) {  // a head a warp, four dimensions a lane
       float mm = -INFINITY, ll = 0.f;
@@ -971,7 +796,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
 #pragma unroll
       for (int w = 0; w < WARPS; ++w)
         add_part(mm, ll, o, s_ml[w][g],
-                 *reinterpret_cast<const float4 *>(o0 + w * o_step +
+                 *reinterpret_cast<const float4 *>(o0 + w * STAGES * STAGE_BYTES +
                                                    g * (HEAD_DIM * 4) +
                                                    ((lane ^ ((g >> 1) & 3)) << 4)));
       if (complete) {
@@ -982,7 +807,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
       }
     }
     // the stage's next contents come through the async proxy
-    if (!FP4) ptx::fence_proxy_async_smem();
+    ptx::fence_proxy_async_smem();
     __syncthreads();
   };
 

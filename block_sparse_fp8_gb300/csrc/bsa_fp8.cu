@@ -25,6 +25,7 @@
 #include "bsa_attention_wide.cuh"
 #include "bsa_common.cuh"
 #include "bsa_decode.cuh"
+#include "bsa_decode_fp4.cuh"
 #include "bsa_fp4.cuh"
 #include "bsa_fp8.h"
 #include "bsa_gather.cuh"
@@ -202,14 +203,13 @@ static Params make_params(const bsa_fp8_dims_t *d) {
 
 static bool encode_map(CUtensorMap *map, const void *base, int rank, const cuuint64_t *dims,
                        const cuuint64_t *strides, const cuuint32_t *box,
-                       CUtensorMapL2promotion promotion = CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                       CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
+                       CUtensorMapL2promotion promotion = CU_TENSOR_MAP_L2_PROMOTION_L2_256B) {
   auto fn = encode_fn();
   if (!fn) return false;
   cuuint32_t estr[4] = {1, 1, 1, 1};
   CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, (cuuint32_t)rank, const_cast<void *>(base),
                   dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  swizzle, promotion,
+                  CU_TENSOR_MAP_SWIZZLE_128B, promotion,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
@@ -743,6 +743,9 @@ bsa_status_t validate_decode(const bsa_fp8_decode_dims_t *d, bool fp4) {
   if (d->sparse != 0 && d->sparse != 1) return BSA_ERR_INVALID_ARGUMENT;
   const long long kb = cdiv(d->max_kv_len, TILE);
   if (kb > KB_MAX) return BSA_ERR_UNSUPPORTED;
+  // rows of a 4-bit pool are counted in 32 bits
+  if (fp4 && (long long)d->num_pages * d->N2 * d->page_size > 0xffffffffLL)
+    return BSA_ERR_UNSUPPORTED;
   // tile counts and grid sizes are int
   if ((long long)d->B * d->N1 > (1LL << 30) || (long long)d->B * d->N2 * (kb + 1) > (1LL << 30))
     return BSA_ERR_UNSUPPORTED;
@@ -757,10 +760,11 @@ struct DecodePlan {
   size_t off_o = 0, off_counts = 0, off_tiles = 0, bytes = 0;
 };
 
-DecodePlan plan_decode(const bsa_fp8_decode_dims_t *d, int num_sms) {
+DecodePlan plan_decode(const bsa_fp8_decode_dims_t *d, int num_sms, bool fp4) {
   DecodePlan plan;
+  const int ctas = fp4 ? decode4::CTAS_PER_SM : decode::CTAS_PER_SM;
   const long long tasks = (long long)d->B * d->N2, kb = cdiv(d->max_kv_len, TILE);
-  const long long resident = (long long)decode::CTAS_PER_SM * std::max(num_sms, 1);
+  const long long resident = (long long)ctas * std::max(num_sms, 1);
   // One CTA goes through up to four tiles about as fast as a cut task's are joined (one sequence of
   // 300 tokens 5.2 us against 5.8, 16 of 512 6.2 against 8.9); with eight, or with more
   // tasks than CTAs, an even cut is faster (64 of 300 11.9 us against 12.4).
@@ -789,16 +793,14 @@ bsa_status_t enable_decode() {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) ==
            cudaSuccess;
   };
-  using decode::decode_kernel;
-  using decode::Format;
-  if (!enable((const void *)decode_kernel<1, false, false>, Format<false, 1>::SMEM) ||
-      !enable((const void *)decode_kernel<2, false, false>, Format<false, 2>::SMEM) ||
-      !enable((const void *)decode_kernel<1, true, false>, Format<false, 1>::SMEM) ||
-      !enable((const void *)decode_kernel<2, true, false>, Format<false, 2>::SMEM) ||
-      !enable((const void *)decode_kernel<1, false, true>, Format<true, 1>::SMEM) ||
-      !enable((const void *)decode_kernel<2, false, true>, Format<true, 2>::SMEM) ||
-      !enable((const void *)decode_kernel<1, true, true>, Format<true, 1>::SMEM) ||
-      !enable((const void *)decode_kernel<2, true, true>, Format<true, 2>::SMEM)) {
+  if (!enable((const void *)decode::decode_kernel<1, false>, decode::SMEM_BYTES) ||
+      !enable((const void *)decode::decode_kernel<2, false>, decode::SMEM_BYTES) ||
+      !enable((const void *)decode::decode_kernel<1, true>, decode::SMEM_BYTES) ||
+      !enable((const void *)decode::decode_kernel<2, true>, decode::SMEM_BYTES) ||
+      !enable((const void *)decode4::decode_kernel<1, false>, decode4::SMEM_BYTES) ||
+      !enable((const void *)decode4::decode_kernel<2, false>, decode4::SMEM_BYTES) ||
+      !enable((const void *)decode4::decode_kernel<1, true>, decode4::SMEM_BYTES) ||
+      !enable((const void *)decode4::decode_kernel<2, true>, decode4::SMEM_BYTES)) {
     (void)cudaGetLastError();  // leave no pending error behind
     return BSA_ERR_CUDA;
   }
@@ -832,7 +834,7 @@ static size_t decode_workspace_size(const bsa_fp8_decode_dims_t *dims, bool fp4)
   if (validate_decode(dims, fp4) != BSA_OK) return 0;
   int num_sms = 0;
   if (check_device(0, &num_sms) != BSA_OK) return WORKSPACE_BYTES;
-  return plan_decode(dims, num_sms).bytes;
+  return plan_decode(dims, num_sms, fp4).bytes;
 }
 
 extern "C" size_t bsa_fp8_decode_workspace_size(const bsa_fp8_decode_dims_t *dims) {
@@ -854,7 +856,6 @@ static bsa_status_t decode_impl(const bsa_fp8_decode_dims_t *d, const void *q,
                                 const int *sparse_seq_len, float softmax_scale, void *out_bf16,
                                 float *lse_f32, void *workspace, size_t workspace_bytes,
                                 int *dev_status, void *stream) {
-  using F = decode::Format<FP4, 1>;
   bsa_status_t st = validate_decode(d, FP4);
   if (st != BSA_OK) return st;
   if (block_mask && sparse_indices) return BSA_ERR_INVALID_ARGUMENT;
@@ -882,7 +883,7 @@ static bsa_status_t decode_impl(const bsa_fp8_decode_dims_t *d, const void *q,
   int num_sms = 0;
   st = check_device(0, &num_sms);
   if (st != BSA_OK) return st;
-  const DecodePlan plan = plan_decode(d, num_sms);
+  const DecodePlan plan = plan_decode(d, num_sms, FP4);
   if (workspace_bytes < plan.bytes) return BSA_ERR_WORKSPACE;
   st = enable_decode();
   if (st != BSA_OK) return st;
@@ -930,41 +931,46 @@ static bsa_status_t decode_impl(const bsa_fp8_decode_dims_t *d, const void *q,
   p.counts = reinterpret_cast<int2 *>(ws + plan.off_counts);
   p.tiles = reinterpret_cast<uint32_t *>(ws + plan.off_tiles);
   const bool wide = p.G > 8;  // two blocks of eight query heads per KV head
-  // Tensor maps of the pools: a box is a warp's 32 slots of one page and head, in shared memory
-  // consecutive rows (128 bytes, or 64 of 4-bit codes) in either layout.  L2 fetches no more than those rows: in NHD pages
-  // the next 128 bytes are another head's, wanted at another time (16 sequences of 8K tokens x 8
-  // heads: 65.9 us with 256-byte promotion, 50.3 without; HND 47.4 either way).
-  CUtensorMap tk, tv;
-  memset(&tk, 0, sizeof(tk));
-  memset(&tv, 0, sizeof(tv));
-  if (!none) {
-    const cuuint64_t H = (cuuint64_t)d->N2, S = (cuuint64_t)d->page_size;
-    const bool nhd = p.kv_nhd != 0;
-    const cuuint64_t gd[4] = {F::ROW, nhd ? H : S, nhd ? S : H, (cuuint64_t)d->num_pages};
-    const cuuint64_t gs[3] = {F::ROW, gd[1] * F::ROW, H * S * F::ROW};
-    const cuuint32_t box[4] = {F::ROW, nhd ? 1u : (cuuint32_t)decode::TOK,
-                               nhd ? (cuuint32_t)decode::TOK : 1u, 1};
-    const CUtensorMapL2promotion row = FP4 && nhd ? CU_TENSOR_MAP_L2_PROMOTION_L2_64B
-                                                  : CU_TENSOR_MAP_L2_PROMOTION_L2_128B;
-    const CUtensorMapSwizzle swizzle =
-        FP4 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
-    if (!encode_map(&tk, k_pages, 4, gd, gs, box, row, swizzle) ||
-        !encode_map(&tv, v_pages, 4, gd, gs, box, row, swizzle))
-      return BSA_ERR_CUDA;
-  }
   const bool lists = d->sparse && !none;
   if (lists && !launch_dependent(block_mask ? decode::plan_kernel<true>
                                             : decode::plan_kernel<false>,
                                  dim3((unsigned)(d->B * d->N2)),
                                  decode::PLAN_THREADS, (size_t)p.Kb * sizeof(uint32_t), stream, p))
     return BSA_ERR_CUDA;
-  const auto kernel = lists ? (wide ? decode::decode_kernel<2, true, FP4>
-                                    : decode::decode_kernel<1, true, FP4>)
-                            : (wide ? decode::decode_kernel<2, false, FP4>
-                                    : decode::decode_kernel<1, false, FP4>);
-  if (!launch_dependent(kernel, dim3((unsigned)plan.grid), decode::THREADS,
-                        (size_t)(wide ? decode::Format<FP4, 2>::SMEM : F::SMEM), stream, p, tk, tv))
-    return BSA_ERR_CUDA;
+  if constexpr (FP4) {
+    const auto kernel =
+        lists ? (wide ? decode4::decode_kernel<2, true> : decode4::decode_kernel<1, true>)
+              : (wide ? decode4::decode_kernel<2, false> : decode4::decode_kernel<1, false>);
+    if (!launch_dependent(kernel, dim3((unsigned)plan.grid), decode4::THREADS,
+                          decode4::SMEM_BYTES, stream, p))
+      return BSA_ERR_CUDA;
+  } else {
+    // Tensor maps of the pools: a box is a warp's 32 slots of one page and head, in shared memory
+    // consecutive 128-byte rows in either layout.  L2 fetches no more than those rows: in NHD pages
+    // the next 128 bytes are another head's, wanted at another time (16 sequences of 8K tokens x 8
+    // heads: 65.9 us with 256-byte promotion, 50.3 without; HND 47.4 either way).
+    CUtensorMap tk, tv;
+    memset(&tk, 0, sizeof(tk));
+    memset(&tv, 0, sizeof(tv));
+    if (!none) {
+      const cuuint64_t H = (cuuint64_t)d->N2, S = (cuuint64_t)d->page_size;
+      const bool nhd = p.kv_nhd != 0;
+      const cuuint64_t gd[4] = {HEAD_DIM, nhd ? H : S, nhd ? S : H, (cuuint64_t)d->num_pages};
+      const cuuint64_t gs[3] = {HEAD_DIM, gd[1] * HEAD_DIM, H * S * HEAD_DIM};
+      const cuuint32_t box[4] = {HEAD_DIM, nhd ? 1u : (cuuint32_t)decode::TOK,
+                                 nhd ? (cuuint32_t)decode::TOK : 1u, 1};
+      const CUtensorMapL2promotion row = CU_TENSOR_MAP_L2_PROMOTION_L2_128B;
+      if (!encode_map(&tk, k_pages, 4, gd, gs, box, row) ||
+          !encode_map(&tv, v_pages, 4, gd, gs, box, row))
+        return BSA_ERR_CUDA;
+    }
+    const auto kernel =
+        lists ? (wide ? decode::decode_kernel<2, true> : decode::decode_kernel<1, true>)
+              : (wide ? decode::decode_kernel<2, false> : decode::decode_kernel<1, false>);
+    if (!launch_dependent(kernel, dim3((unsigned)plan.grid), decode::THREADS, decode::SMEM_BYTES,
+                          stream, p, tk, tv))
+      return BSA_ERR_CUDA;
+  }
   if (plan.whole || p.Kb <= 1) return BSA_OK;  // no task is cut
   // The join, 62 registers.  Beside two CTAs of the kernels for up to eight heads (220 registers,
   // with lists 214) an SM has room for one block of four warps or two of two; the kernels for more

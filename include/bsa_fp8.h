@@ -584,8 +584,9 @@ bsa_status_t bsa_fp4_gather_kv(const bsa_fp8_gather_dims_t *dims, const void *k_
                                void *stream);
 
 /* bsa_fp8_decode over the 4-bit cache (dims->k_scale_kind BSA_SCALE_PER_TENSOR or BSA_SCALE_PER_HEAD),
- * with the same queries, selection, outputs, workspace rules and precision: code * scale is exact
- * in the products' fp16. */
+ * with the same queries, selection, outputs and workspace rules, for pools of at most 2^32 - 1 rows
+ * (num_pages * N2 * page_size).  code * scale is exact in the products' fp16; scores, softmax
+ * statistics and sums are fp32, the probabilities go into the product with V as one fp16 number. */
 size_t bsa_fp4_decode_workspace_size(const bsa_fp8_decode_dims_t *dims);
 bsa_status_t bsa_fp4_decode(const bsa_fp8_decode_dims_t *dims, const void *q,
                             const float *q_descale, const void *k_pages, const void *v_pages,

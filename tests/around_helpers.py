@@ -8,11 +8,11 @@ cache.  Bounds:
 * rope_quantize.  descale: the largest turned value is off by that bound, the division rounds.  A code
   is the nearest e4m3 value to the quotient, but for quotients nearer to a border than the bound.
 * append_kv_fp4 is exact: codes and scales equal.  gather_kv_fp4 is exact: one fp32 product, rounded.
-* decode_fp4: the bounds of serving_helpers.reference (the 4-bit values are exact in fp16), and what a
-  block of zeros lets one see: a weight goes into its product as two fp16 terms of 2^15 times itself,
-  the second rounded at half the smallest fp16 number, 2^-25, so that each weight may be off by 2^-40
-  of its warp's largest whatever its own size, 2^-40 sum_j |v_j| / l in all, with l >= 1 in
-  units of the largest.  (Where a dimension's largest weights meet zeros, that is what remains.)
+* decode_fp4: the bounds of serving_helpers.reference (the 4-bit values are exact in fp16, a weight is
+  rounded to fp16 once), and what a block of zeros lets one see: a weight goes into its product as
+  2^15 times itself, where fp16's smallest step is 2^-24, so that each weight may be off by 2^-40 of
+  its warp's largest whatever its own size, 2^-40 sum_j |v_j| / l in all, with l >= 1 in units of the
+  largest.  (Where a dimension's largest weights meet zeros, that is what remains.)
 """
 from __future__ import annotations
 
