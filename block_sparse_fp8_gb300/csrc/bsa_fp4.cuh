@@ -23,6 +23,7 @@
 
 #include "bsa_common.cuh"
 #include "bsa_quant.cuh"
+#include "ptx_sm103.cuh"
 
 namespace bsa {
 namespace fp4 {
@@ -64,14 +65,20 @@ __device__ __forceinline__ float value_of_e4m3(uint32_t c) {
   return __half2float(__ushort_as_half((unsigned short)(h & 0xffffu)));
 }
 
-// e2m1 codes of two values, the first in the low half of the byte.
-__device__ __forceinline__ uint32_t e2m1x2(float lo, float hi) {
+// e2m1 codes of eight values (as pairs), the first in the lowest half byte.
+__device__ __forceinline__ uint32_t e2m1x8(const uint64_t (&v)[4]) {
+  float x[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) ptx::upk(v[i], x[2 * i], x[2 * i + 1]);
   uint32_t r;
-  asm("{\n\t.reg .b8 c;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 c, %2, %1;\n\t"
-      "cvt.u32.u8 %0, c;\n\t}"
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+      "mov.b32 %0, {a, b, c, d};\n\t}"
       : "=r"(r)
-      : "f"(lo), "f"(hi));
+      : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
   return r;
 }
 
@@ -98,45 +105,54 @@ __device__ __forceinline__ uint32_t scale_of(float amax, float descale, float in
   return settle(down, fmaf(-6.f * border, descale, amax));
 }
 
-// The codes of a block's 16 values under its scale.
-__device__ __forceinline__ uint2 codes_of(const float (&x)[16], float scale, float descale) {
-  const float d = scale * descale, r = d > 0.f ? __frcp_rn(d) : 0.f;
-  uint32_t w[2] = {0u, 0u}, other[2] = {0u, 0u};
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float a = x[2 * i] * r, b = x[2 * i + 1] * r;
-    w[i >> 2] |= e2m1x2(a * NUDGE_UP, b * NUDGE_UP) << (8 * (i & 3));
-    other[i >> 2] |= e2m1x2(a * NUDGE_DOWN, b * NUDGE_DOWN) << (8 * (i & 3));
+// Where the nudged codes of eight values differ: the exact decision, a value at a time (read again
+// from where it came: a register cannot be picked by number).
+__device__ __noinline__ uint32_t settled(uint32_t up, uint32_t down, const __nv_bfloat16 *x,
+                                         float scale, float descale) {
+  uint32_t differ = (up ^ down) & 0x77777777u;
+  while (differ) {
+    const int i = (__ffs((int)differ) - 1) >> 2, at = 4 * i;
+    const uint32_t u = (up >> at) & 7u, d = (down >> at) & 7u;
+    // the border is (twice one + twice the other) / 4, exact with the scale
+    const float border = 0.25f * (float)(twice_e2m1(u) + twice_e2m1(d)) * scale;
+    const float size = fabsf(__bfloat162float(x[i]));
+    up = (up & ~(7u << at)) | settle(d, fmaf(-border, descale, size)) << at;
+    differ &= ~(0xfu << at);
   }
-  if (w[0] != other[0] || w[1] != other[1]) {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int at = 4 * (i & 7);
-      const uint32_t up = (w[i >> 3] >> at) & 7u, down = (other[i >> 3] >> at) & 7u;
-      if (up == down) continue;
-      // the border is (twice one + twice the other) / 4, exact with the scale
-      const float border = 0.25f * (float)(twice_e2m1(up) + twice_e2m1(down)) * scale;
-      const uint32_t c = settle(down, fmaf(-border, descale, fabsf(x[i])));
-      w[i >> 3] = (w[i >> 3] & ~(7u << at)) | c << at;
-    }
-  }
-  return make_uint2(w[0], w[1]);
+  return up;
 }
 
-__device__ __forceinline__ void store_block(const uint4 &a, const uint4 &b, float descale,
-                                            float inv6, uint8_t *codes, uint8_t *scale_at) {
-  float lo[8], hi[8], x[16];
-  quant::unpack8(a, lo);
-  quant::unpack8(b, hi);
-  float amax = 0.f;
+// One block of 16 values, at x: their codes and scale.
+__device__ __forceinline__ void store_block(const uint4 &a, const uint4 &b,
+                                            const __nv_bfloat16 *from, float descale, float inv6,
+                                            uint8_t *codes, uint8_t *scale_at) {
+  const uint32_t word[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  float lo[8], hi[8], amax = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    x[i] = lo[i];
-    x[8 + i] = hi[i];
+    lo[i] = __uint_as_float(word[i] << 16);
+    hi[i] = __uint_as_float(word[i] & 0xffff0000u);
     amax = fmaxf(amax, fmaxf(fabsf(lo[i]), fabsf(hi[i])));
   }
   const uint32_t s = scale_of(amax, descale, inv6);
-  *reinterpret_cast<uint2 *>(codes) = codes_of(x, value_of_e4m3(s), descale);
+  const float scale = value_of_e4m3(s), d = scale * descale, r = d > 0.f ? __frcp_rn(d) : 0.f;
+  const uint64_t up = ptx::pk(r * NUDGE_UP, r * NUDGE_UP),
+                 down = ptx::pk(r * NUDGE_DOWN, r * NUDGE_DOWN);
+  uint32_t w[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint64_t u[4], v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint64_t x = ptx::pk(lo[4 * h + i], hi[4 * h + i]);
+      u[i] = ptx::mul2(x, up);
+      v[i] = ptx::mul2(x, down);
+    }
+    w[h] = e2m1x8(u);
+    const uint32_t other = e2m1x8(v);
+    if (w[h] != other) w[h] = settled(w[h], other, from + 8 * h, scale, descale);
+  }
+  *reinterpret_cast<uint2 *>(codes) = make_uint2(w[0], w[1]);
   *scale_at = (uint8_t)s;
 }
 
@@ -160,10 +176,10 @@ __global__ void __launch_bounds__(THREADS) append_kernel(const AppendParams p) {
   }
   const long long hnd = (((long long)page * p.N2 + g) << p.ps_shift) + in;
   const long long dst = p.kv_nhd ? (((long long)page << p.ps_shift) + in) * p.N2 + g : hnd;
-  store_block(k0, k1, kg, __frcp_rn(6.f * kg), p.k_pages + dst * ROW_BYTES + block * (BLOCK / 2),
-              p.k_scales + hnd * BLOCKS + block);
-  store_block(v0, v1, vg, __frcp_rn(6.f * vg), p.v_pages + dst * ROW_BYTES + block * (BLOCK / 2),
-              p.v_scales + hnd * BLOCKS + block);
+  store_block(k0, k1, p.k_new + tok * p.k_stride + at, kg, __frcp_rn(6.f * kg),
+              p.k_pages + dst * ROW_BYTES + block * (BLOCK / 2), p.k_scales + hnd * BLOCKS + block);
+  store_block(v0, v1, p.v_new + tok * p.v_stride + at, vg, __frcp_rn(6.f * vg),
+              p.v_pages + dst * ROW_BYTES + block * (BLOCK / 2), p.v_scales + hnd * BLOCKS + block);
 }
 
 }  // namespace fp4

@@ -1072,10 +1072,10 @@ static bsa_status_t gather_impl(const bsa_fp8_gather_dims_t *d, const void *k_pa
   p.tokens = gather::MAX_TOKENS;
   while (p.tokens > 1 && cdiv(d->total, p.tokens) < 16 * num_sms) p.tokens /= 2;
   const unsigned grid = (unsigned)cdiv(d->total, p.tokens);
-  if (d->out_type == BSA_OUT_FP32)
-    gather::gather_kernel<true, FP4><<<grid, gather::THREADS, 0, (cudaStream_t)stream>>>(p);
-  else
-    gather::gather_kernel<false, FP4><<<grid, gather::THREADS, 0, (cudaStream_t)stream>>>(p);
+  const bool f32 = d->out_type == BSA_OUT_FP32;
+  const auto kernel = FP4 ? (f32 ? gather::gather_fp4_kernel<true> : gather::gather_fp4_kernel<false>)
+                          : (f32 ? gather::gather_kernel<true> : gather::gather_kernel<false>);
+  kernel<<<grid, gather::THREADS, 0, (cudaStream_t)stream>>>(p);
   return cudaGetLastError() == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
 }
 

@@ -19,11 +19,12 @@
 
 #include "bsa_common.cuh"
 #include "bsa_quant.cuh"
+#include "ptx_sm103.cuh"
 
 namespace bsa {
 namespace rope {
 
-constexpr int THREADS = 256;
+constexpr int THREADS = 128;
 constexpr int LANES = 8;    // threads of a row
 constexpr int VEC = 8;      // values of a 16-byte vector
 constexpr int VECS = HEAD_DIM / VEC;
@@ -43,16 +44,47 @@ struct Params {
   float amplitude;
 };
 
-__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+// Two bf16 values as a pair of fp32, and back.
+__device__ __forceinline__ uint64_t pair_of(uint32_t w) {
+  return ptx::pk(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+__device__ __forceinline__ uint32_t bf16_of(uint64_t v) {
+  float lo, hi;
+  ptx::upk(v, lo, hi);
   const __nv_bfloat162 x = __floats2bfloat162_rn(lo, hi);
   uint32_t r;
   memcpy(&r, &x, 4);
   return r;
 }
+__device__ __forceinline__ uint4 pack8(const uint64_t (&v)[4]) {
+  return make_uint4(bf16_of(v[0]), bf16_of(v[1]), bf16_of(v[2]), bf16_of(v[3]));
+}
+__device__ __forceinline__ uint64_t swapped(uint64_t v) {
+  float lo, hi;
+  ptx::upk(v, lo, hi);
+  return ptx::pk(hi, lo);
+}
 
-__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
-  return make_uint4(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]), bf16x2(v[4], v[5]),
-                    bf16x2(v[6], v[7]));
+// The codes of eight values, as quant::codes8 makes them: rounded quotients (Markstein's correction of
+// the product with the rounded reciprocal).
+__device__ __forceinline__ uint2 codes8(const uint64_t (&v)[4], float scale, uint64_t inv,
+                                        uint64_t neg) {
+  float q[8];
+  if (scale >= 0x1p-90f && scale <= 0x1p90f) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint64_t q0 = ptx::mul2(v[i], inv);
+      ptx::upk(ptx::fma2(ptx::fma2(q0, neg, v[i]), inv, q0), q[2 * i], q[2 * i + 1]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      ptx::upk(v[i], q[2 * i], q[2 * i + 1]);
+      q[2 * i] = __fdiv_rn(q[2 * i], scale);
+      q[2 * i + 1] = __fdiv_rn(q[2 * i + 1], scale);
+    }
+  }
+  return make_uint2(ptx::cvt_e4m3x4(q[0], q[1], q[2], q[3]), ptx::cvt_e4m3x4(q[4], q[5], q[6], q[7]));
 }
 
 constexpr int AHEAD = 4;  // heads in flight per thread
@@ -118,41 +150,47 @@ __global__ void __launch_bounds__(THREADS) rope_kernel(const Params p) {
     const int h = h0 + step * AHEAD;
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i) {
-      float x[8], y[8];
-      quant::unpack8(a[i], x);
-      quant::unpack8(b[i], y);
+      const uint32_t wa[4] = {a[i].x, a[i].y, a[i].z, a[i].w},
+                     wb[4] = {b[i].x, b[i].y, b[i].z, b[i].w};
+      uint64_t x[4], y[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        x[j] = pair_of(wa[j]);
+        y[j] = pair_of(wb[j]);
+      }
       if (p.interleaved) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const float x0 = x[2 * j], x1 = x[2 * j + 1], y0 = y[2 * j], y1 = y[2 * j + 1];
-          if (turn0) {
-            x[2 * j] = x0 * c[j] - x1 * s[j];
-            x[2 * j + 1] = x1 * c[j] + x0 * s[j];
-          }
-          if (turn1) {
-            y[2 * j] = y0 * c[4 + j] - y1 * s[4 + j];
-            y[2 * j + 1] = y1 * c[4 + j] + y0 * s[4 + j];
-          }
+          // (x0, x1) (c, c) + (x1, x0) (-s, s)
+          x[j] = ptx::fma2(swapped(x[j]), ptx::pk(-s[j], s[j]), ptx::mul2(x[j], ptx::pk(c[j], c[j])));
+          y[j] = ptx::fma2(swapped(y[j]), ptx::pk(-s[4 + j], s[4 + j]),
+                           ptx::mul2(y[j], ptx::pk(c[4 + j], c[4 + j])));
         }
-      } else if (turn0) {
+      } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float u = x[j], v = y[j];
-          x[j] = u * c[j] - v * s[j];
-          y[j] = v * c[j] + u * s[j];
+        for (int j = 0; j < 4; ++j) {
+          const uint64_t u = x[j], v = y[j], cc = ptx::pk(c[2 * j], c[2 * j + 1]);
+          x[j] = ptx::fma2(v, ptx::pk(-s[2 * j], -s[2 * j + 1]), ptx::mul2(u, cc));
+          y[j] = ptx::fma2(u, ptx::pk(s[2 * j], s[2 * j + 1]), ptx::mul2(v, cc));
         }
       }
       if constexpr (QUANT) {
         float m = 0.f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) m = fmaxf(m, fmaxf(fabsf(x[j]), fabsf(y[j])));
+        for (int j = 0; j < 4; ++j) {
+          float x0, x1, y0, y1;
+          ptx::upk(x[j], x0, x1);
+          ptx::upk(y[j], y0, y1);
+          m = fmaxf(fmaxf(m, fmaxf(fabsf(x0), fabsf(x1))), fmaxf(fabsf(y0), fabsf(y1)));
+        }
 #pragma unroll
         for (int o = LANES / 2; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
         if (h + i < h1) {
-          const float d = quant::descale_of(m, p.ue8m0);
+          const float d = quant::descale_of(m, p.ue8m0), r = __frcp_rn(d);
+          const uint64_t inv = ptx::pk(r, r), neg = ptx::pk(-d, -d);
           const long long row = t * p.N1 + h + i;
-          p.codes[row * VECS + v0] = quant::codes8(x, d);
-          p.codes[row * VECS + v1] = quant::codes8(y, d);
+          p.codes[row * VECS + v0] = codes8(x, d, inv, neg);
+          p.codes[row * VECS + v1] = codes8(y, d, inv, neg);
           if (lane == 0) p.descale[row] = d;
         }
       } else if (h + i < h1) {
