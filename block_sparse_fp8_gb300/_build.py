@@ -14,7 +14,7 @@ SOURCES = [os.path.join(CSRC, "bsa_fp8.cu")]
 HEADERS = [os.path.join(CSRC, f) for f in ("ptx_sm103.cuh", "bsa_common.cuh", "bsa_attention.cuh",
                                            "bsa_attention_wide.cuh", "bsa_quant.cuh",
                                            "bsa_decode.cuh", "bsa_gather.cuh", "bsa_merge.cuh",
-                                           "bsa_decode_fp4.cuh", "bsa_fp4.cuh", "bsa_pages.cuh", "bsa_rope.cuh")] + [
+                                           "bsa_decode_fp4.cuh", "bsa_div.cuh", "bsa_fp4.cuh", "bsa_pages.cuh", "bsa_rope.cuh")] + [
     os.path.join(INCLUDE, "bsa_fp8.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

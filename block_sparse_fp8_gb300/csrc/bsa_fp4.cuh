@@ -22,6 +22,7 @@
 #include <cstdint>
 
 #include "bsa_common.cuh"
+#include "bsa_div.cuh"
 #include "bsa_quant.cuh"
 #include "ptx_sm103.cuh"
 
@@ -40,7 +41,8 @@ struct AppendParams {
   const float *k_descale, *v_descale;
   uint8_t *k_pages, *v_pages, *k_scales, *v_scales;
   int *dev_status;
-  long long rows;  // tokens x KV heads
+  uint32_t rows;  // tokens x KV heads, below 2^31
+  Divisor heads;
   int N2, ps_shift, num_pages;
   int k_per_head, v_per_head, kv_nhd;
 };
@@ -88,6 +90,13 @@ __device__ __forceinline__ int twice_e2m1(uint32_t c) {
   return e == 0 ? m : (2 + m) << (e - 1);
 }
 
+// 1 / x to 2^-22, 0 for an x of zero or next to it.
+__device__ __forceinline__ float inverse(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return x > 0x1p-120f ? r : 0.f;
+}
+
 constexpr float NUDGE_UP = 1.f + 0x1p-20f, NUDGE_DOWN = 1.f - 0x1p-20f;
 
 // Which of two neighbouring codes (`down`, `down` + 1) is nearer: the sign of the value less the border
@@ -105,21 +114,25 @@ __device__ __forceinline__ uint32_t scale_of(float amax, float descale, float in
   return settle(down, fmaf(-6.f * border, descale, amax));
 }
 
-// Where the nudged codes of eight values differ: the exact decision, a value at a time (read again
-// from where it came: a register cannot be picked by number).
-__device__ __noinline__ uint32_t settled(uint32_t up, uint32_t down, const __nv_bfloat16 *x,
-                                         float scale, float descale) {
-  uint32_t differ = (up ^ down) & 0x77777777u;
+// Where the nudged codes of a block differ: the exact decision, a value at a time (read again from
+// where it came: a register cannot be picked by number).
+__device__ __forceinline__ void settle_codes(uint32_t (&up)[2], const uint32_t (&down)[2],
+                                             const __nv_bfloat16 *x, float scale, float descale) {
+  uint64_t w = (uint64_t)up[1] << 32 | up[0];
+  const uint64_t other = (uint64_t)down[1] << 32 | down[0];
+  uint64_t differ = (w ^ other) & 0x7777777777777777ull;
+#pragma unroll 1
   while (differ) {
-    const int i = (__ffs((int)differ) - 1) >> 2, at = 4 * i;
-    const uint32_t u = (up >> at) & 7u, d = (down >> at) & 7u;
+    const int i = (__ffsll((long long)differ) - 1) >> 2, at = 4 * i;
+    const uint32_t u = (uint32_t)(w >> at) & 7u, d = (uint32_t)(other >> at) & 7u;
     // the border is (twice one + twice the other) / 4, exact with the scale
     const float border = 0.25f * (float)(twice_e2m1(u) + twice_e2m1(d)) * scale;
     const float size = fabsf(__bfloat162float(x[i]));
-    up = (up & ~(7u << at)) | settle(d, fmaf(-border, descale, size)) << at;
-    differ &= ~(0xfu << at);
+    w = (w & ~(7ull << at)) | (uint64_t)settle(d, fmaf(-border, descale, size)) << at;
+    differ &= ~(0xfull << at);
   }
-  return up;
+  up[0] = (uint32_t)w;
+  up[1] = (uint32_t)(w >> 32);
 }
 
 // One block of 16 values, at x: their codes and scale.
@@ -135,10 +148,10 @@ __device__ __forceinline__ void store_block(const uint4 &a, const uint4 &b,
     amax = fmaxf(amax, fmaxf(fabsf(lo[i]), fabsf(hi[i])));
   }
   const uint32_t s = scale_of(amax, descale, inv6);
-  const float scale = value_of_e4m3(s), d = scale * descale, r = d > 0.f ? __frcp_rn(d) : 0.f;
+  const float scale = value_of_e4m3(s), d = scale * descale, r = inverse(d);
   const uint64_t up = ptx::pk(r * NUDGE_UP, r * NUDGE_UP),
                  down = ptx::pk(r * NUDGE_DOWN, r * NUDGE_DOWN);
-  uint32_t w[2];
+  uint32_t w[2], other[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     uint64_t u[4], v[4];
@@ -149,20 +162,20 @@ __device__ __forceinline__ void store_block(const uint4 &a, const uint4 &b,
       v[i] = ptx::mul2(x, down);
     }
     w[h] = e2m1x8(u);
-    const uint32_t other = e2m1x8(v);
-    if (w[h] != other) w[h] = settled(w[h], other, from + 8 * h, scale, descale);
+    other[h] = e2m1x8(v);
   }
+  if (w[0] != other[0] || w[1] != other[1]) settle_codes(w, other, from, scale, descale);
   *reinterpret_cast<uint2 *>(codes) = make_uint2(w[0], w[1]);
   *scale_at = (uint8_t)s;
 }
 
 __global__ void __launch_bounds__(THREADS) append_kernel(const AppendParams p) {
   const int block = threadIdx.x & (BLOCKS - 1);
-  const long long row = (long long)blockIdx.x * (THREADS / BLOCKS) + threadIdx.x / BLOCKS;
+  const uint32_t row = blockIdx.x * (THREADS / BLOCKS) + threadIdx.x / BLOCKS;
   if (row >= p.rows) return;
-  const long long tok = row / p.N2;
-  const int g = (int)(row % p.N2);
-  const long long at = (long long)g * HEAD_DIM + block * BLOCK;
+  const uint32_t tok = p.heads.quotient(row);
+  const int g = (int)(row - tok * p.N2);
+  const int at = g * HEAD_DIM + block * BLOCK;
   const uint4 *k = reinterpret_cast<const uint4 *>(p.k_new + tok * p.k_stride + at);
   const uint4 *v = reinterpret_cast<const uint4 *>(p.v_new + tok * p.v_stride + at);
   const uint4 k0 = k[0], k1 = k[1], v0 = v[0], v1 = v[1];
@@ -176,9 +189,9 @@ __global__ void __launch_bounds__(THREADS) append_kernel(const AppendParams p) {
   }
   const long long hnd = (((long long)page * p.N2 + g) << p.ps_shift) + in;
   const long long dst = p.kv_nhd ? (((long long)page << p.ps_shift) + in) * p.N2 + g : hnd;
-  store_block(k0, k1, p.k_new + tok * p.k_stride + at, kg, __frcp_rn(6.f * kg),
+  store_block(k0, k1, p.k_new + tok * p.k_stride + at, kg, inverse(6.f * kg),
               p.k_pages + dst * ROW_BYTES + block * (BLOCK / 2), p.k_scales + hnd * BLOCKS + block);
-  store_block(v0, v1, p.v_new + tok * p.v_stride + at, vg, __frcp_rn(6.f * vg),
+  store_block(v0, v1, p.v_new + tok * p.v_stride + at, vg, inverse(6.f * vg),
               p.v_pages + dst * ROW_BYTES + block * (BLOCK / 2), p.v_scales + hnd * BLOCKS + block);
 }
 

@@ -1244,11 +1244,11 @@ bsa_status_t rope_params(const bsa_rope_dims_t *d, const void *q, const void *k,
                              (long long)num_sms * 256)
     p->heads *= 2;
   p->groups = cdiv(heads, p->heads);
-  p->units = (long long)d->T * p->groups;
-  const long long blocks = (p->units + rope::THREADS / rope::LANES - 1) /
-                           (rope::THREADS / rope::LANES);
-  if (blocks > 0x7fffffffLL) return BSA_ERR_UNSUPPORTED;
-  *grid = (unsigned)blocks;
+  const long long units = (long long)d->T * p->groups;
+  if (units > 0x7ffffff0LL) return BSA_ERR_UNSUPPORTED;  // (more rows than any memory holds)
+  p->units = (uint32_t)units;
+  p->by_groups = Divisor::of((uint32_t)p->groups);
+  *grid = (unsigned)cdiv(units, rope::THREADS / rope::LANES);
   return BSA_OK;
 }
 
@@ -1419,16 +1419,16 @@ extern "C" bsa_status_t bsa_fp4_append_kv(const bsa_fp4_append_dims_t *d, const 
   p.k_scales = static_cast<uint8_t *>(k_scales);
   p.v_scales = static_cast<uint8_t *>(v_scales);
   p.dev_status = dev_status;
-  p.rows = (long long)d->total_new * d->N2;
+  const long long rows = (long long)d->total_new * d->N2;
+  if (rows > 0x7ffffff0LL) return BSA_ERR_UNSUPPORTED;  // (more rows than any memory holds)
+  p.rows = (uint32_t)rows;
+  p.heads = Divisor::of((uint32_t)d->N2);
   p.N2 = d->N2;
   p.ps_shift = d->page_size == 64 ? 6 : 5;
   p.num_pages = d->num_pages;
   p.k_per_head = d->k_scale_kind == BSA_SCALE_PER_HEAD;
   p.v_per_head = d->v_scale_kind == BSA_SCALE_PER_HEAD;
   p.kv_nhd = d->kv_layout == BSA_KV_NHD;
-  const long long blocks =
-      (p.rows + fp4::THREADS / fp4::BLOCKS - 1) / (fp4::THREADS / fp4::BLOCKS);
-  if (blocks > 0x7fffffffLL) return BSA_ERR_UNSUPPORTED;
-  fp4::append_kernel<<<(unsigned)blocks, fp4::THREADS, 0, (cudaStream_t)stream>>>(p);
+  fp4::append_kernel<<<(unsigned)cdiv(rows, fp4::THREADS / fp4::BLOCKS), fp4::THREADS, 0, (cudaStream_t)stream>>>(p);
   return cudaGetLastError() == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
 }

@@ -21,6 +21,7 @@ namespace pages {
 
 constexpr int THREADS = 1024;
 constexpr int WARPS = THREADS / 32;
+constexpr int AT_ONCE = 4;  // pages in flight per thread
 constexpr int FILL_THREADS = 256;
 constexpr int FILL_ROWS = 4 * FILL_THREADS;  // of a CTA
 
@@ -152,16 +153,25 @@ __global__ void __launch_bounds__(THREADS) assign_kernel(const Params p) {
     }
     const int here = min(p.B - b0, THREADS);
     __syncthreads();
-    // the pages of these sequences, a thread a page
-    const long long first = taken, last = min(taken + all_pages, (long long)count);
-    for (long long j = first + tid; j < last; j += THREADS) {
-      const int i = last_at_most(s_page, 0, here - 1, j);
-      const int k = (int)(j - s_page[i]);
-      if (k >= s_take[i]) continue;  // not served after all
-      const int page = p.free_pages[count - 1 - (int)j];
-      const long long col = (((long long)s_old[i] + ps_mask) >> p.ps_shift) + k;
-      if (page < 0 || page >= p.num_pages) report(p, BSA_DEV_BAD_PAGE);
-      p.block_table[(size_t)(b0 + i) * p.L + col] = page;
+    // the pages of these sequences, a thread a page, some of them at once
+    const long long last = min(taken + all_pages, (long long)count);
+    for (long long j0 = taken + tid; j0 < last; j0 += THREADS * AT_ONCE) {
+      int page[AT_ONCE], at[AT_ONCE];
+#pragma unroll
+      for (int u = 0; u < AT_ONCE; ++u) {
+        const long long j = j0 + u * THREADS;
+        page[u] = j < last ? p.free_pages[count - 1 - (int)j] : 0;
+        at[u] = j < last ? last_at_most(s_page, 0, here - 1, j) : -1;
+      }
+#pragma unroll
+      for (int u = 0; u < AT_ONCE; ++u) {
+        if (at[u] < 0) continue;
+        const int k = (int)(j0 + u * THREADS - s_page[at[u]]);
+        if (k >= s_take[at[u]]) continue;  // not served after all
+        if (page[u] < 0 || page[u] >= p.num_pages) report(p, BSA_DEV_BAD_PAGE);
+        const long long col = (((long long)s_old[at[u]] + ps_mask) >> p.ps_shift) + k;
+        p.block_table[(size_t)(b0 + at[u]) * p.L + col] = page[u];
+      }
     }
     __syncthreads();
     if (p.fill) {
@@ -221,9 +231,10 @@ __global__ void __launch_bounds__(THREADS) release_kernel(const Params p) {
   decode::pdl_wait();
   decode::pdl_launch_dependents();
   const int count = min(max(*p.free_count, 0), p.num_pages);
-  // the pages' places on the stack count down from the last one: how many there are comes first
+  // the pages' places on the stack count down from the last one: how many there are comes first, in a
+  // pass of its own if one sum does not take in all sequences
   long long total = 0, none = 0;
-  for (int pass = 0; pass < 2; ++pass) {
+  for (int pass = p.B <= THREADS ? 1 : 0; pass < 2; ++pass) {
     long long given = 0;
     for (int b0 = 0; b0 < p.B; b0 += THREADS) {
       const int b = b0 + tid;
@@ -233,7 +244,7 @@ __global__ void __launch_bounds__(THREADS) release_kernel(const Params p) {
         len = p.seq_lens[b];
         keep = min(max(p.keep_lens[b], 0), max(len, 0));
         const bool good = len >= 0 && len <= room;
-        if (!good && pass == 0) report(p, BSA_DEV_BAD_SEQLEN);
+        if (!good && pass == 1) report(p, BSA_DEV_BAD_SEQLEN);
         if (!good) keep = len;  // left as it is
         else
           back = (((long long)len + ps_mask) >> p.ps_shift) -
@@ -246,16 +257,28 @@ __global__ void __launch_bounds__(THREADS) release_kernel(const Params p) {
         s_col[tid] = (int)(((long long)keep + ps_mask) >> p.ps_shift);
         __syncthreads();
         const int here = min(p.B - b0, THREADS);
-        for (long long j = given + tid; j < given + all; j += THREADS) {
-          const int i = last_at_most(s_page, 0, here - 1, j);
-          const long long col = s_col[i] + (j - s_page[i]);
-          int page = p.block_table[(size_t)(b0 + i) * p.L + col];
-          if (page < 0 || page >= p.num_pages) {
-            report(p, BSA_DEV_BAD_PAGE);
-            page = -1;
+        if (p.B <= THREADS) total = all;
+        for (long long j0 = given + tid; j0 < given + all; j0 += THREADS * AT_ONCE) {
+          int page[AT_ONCE];
+#pragma unroll
+          for (int u = 0; u < AT_ONCE; ++u) {
+            const long long j = j0 + u * THREADS;
+            page[u] = 0;
+            if (j < given + all) {
+              const int i = last_at_most(s_page, 0, here - 1, j);
+              page[u] = p.block_table[(size_t)(b0 + i) * p.L + s_col[i] + (j - s_page[i])];
+            }
           }
-          const long long at = count + total - 1 - j;
-          if (at < p.num_pages) p.free_pages[at] = page;
+#pragma unroll
+          for (int u = 0; u < AT_ONCE; ++u) {
+            const long long j = j0 + u * THREADS, at = count + total - 1 - j;
+            if (j >= given + all) continue;
+            if (page[u] < 0 || page[u] >= p.num_pages) {
+              report(p, BSA_DEV_BAD_PAGE);
+              page[u] = -1;
+            }
+            if (at < p.num_pages) p.free_pages[at] = page[u];
+          }
         }
         if (b < p.B) p.lens_out[b] = keep;
       }
@@ -263,11 +286,9 @@ __global__ void __launch_bounds__(THREADS) release_kernel(const Params p) {
       given += all;
     }
     total = given;
-    if (pass == 0 && count + total > p.num_pages) {
-      // more pages than there are: some are held twice
-      if (tid == 0) report(p, BSA_DEV_BAD_PAGE);
-    }
   }
+  // more pages than there are: some are held twice
+  if (tid == 0 && count + total > p.num_pages) report(p, BSA_DEV_BAD_PAGE);
   if (tid == 0) *p.free_count = (int)min(count + total, (long long)p.num_pages);
 }
 

@@ -18,6 +18,7 @@
 #include <cstdint>
 
 #include "bsa_common.cuh"
+#include "bsa_div.cuh"
 #include "bsa_quant.cuh"
 #include "ptx_sm103.cuh"
 
@@ -37,7 +38,8 @@ struct Params {
   const int *positions;
   const unsigned long long *freqs;
   long long q_stride, k_stride, q_out_stride, k_out_stride;  // elements from token to token
-  long long units;  // tokens x groups of heads
+  uint32_t units;  // tokens x groups of heads, below 2^31
+  Divisor by_groups;
   int N1, N2, R;
   int groups, heads;  // groups of `heads` heads that one thread serves
   int interleaved, ue8m0;
@@ -93,10 +95,10 @@ template <bool QUANT>
 __global__ void __launch_bounds__(THREADS) rope_kernel(const Params p) {
   const int lane = threadIdx.x & (LANES - 1);
   // whole warps stay to the end: the rows' maxima go by shuffles
-  const long long unit = (long long)blockIdx.x * (THREADS / LANES) + threadIdx.x / LANES;
+  const uint32_t unit = blockIdx.x * (THREADS / LANES) + threadIdx.x / LANES;
   const bool live = unit < p.units;
-  const int group = live ? (int)(unit % p.groups) : 0;
-  const long long t = live ? unit / p.groups : 0;
+  const long long t = live ? p.by_groups.quotient(unit) : 0;
+  const int group = live ? (int)(unit - (uint32_t)t * p.groups) : 0;
   const int heads = p.N1 + p.N2, h0 = group * p.heads,
             h1 = live ? min(h0 + p.heads, heads) : h0;
 
