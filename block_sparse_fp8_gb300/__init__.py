@@ -774,20 +774,19 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: int = ROPE
 
 
 def _rows(name, t, T, dev):
-    """The strides from token to token of a bf16 tensor [T, heads, 128] whose tokens are each in one
+    """The stride from token to token of a bf16 tensor [T, heads, 128] whose tokens are each in one
     piece."""
-    shape = t.shape
+    shape, stride = t.shape, t.stride()
+    if (t.dtype is _torch_names()[1] and len(shape) == 3 and shape[2] == 128 and shape[0] == T
+            and stride[2] == 1 and (stride[1] == 128 or shape[1] == 1) and t.get_device() == dev):
+        return stride[0] if T > 1 else shape[1] * 128
     if t.dtype is not _torch_names()[1]:
         raise ValueError(f"{name} has dtype {t.dtype}, expected bf16")
     if len(shape) != 3 or shape[2] != 128 or shape[0] != T:
         raise ValueError(f"{name} has shape {tuple(shape)}, expected [{T}, heads, 128]")
     if t.get_device() != dev:
         raise ValueError(f"{name} is on {t.device}, the others on another device")
-    if t.is_contiguous():
-        return shape[1] * 128
-    if t.stride(2) != 1 or (shape[1] > 1 and t.stride(1) != 128):
-        raise ValueError(f"{name} must be contiguous within a token")
-    return t.stride(0) if T > 1 else shape[1] * 128
+    raise ValueError(f"{name} must be contiguous within a token")
 
 
 def _rope_common(q, positions, freqs):

@@ -810,19 +810,22 @@ bsa_status_t enable_decode() {
 
 // A launch that may begin while the kernel before it on the stream runs; it waits for that
 // kernel's writes itself (griddepcontrol.wait).
-template <typename... Args>
+template <bool CLUSTER = false, typename... Args>  // CLUSTER: the grid is one cluster
 bool launch_dependent(void (*kernel)(Args...), dim3 grid, int threads, size_t smem, void *stream,
                       const Args &...args) {
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = grid.x;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3((unsigned)threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = (cudaStream_t)stream;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = CLUSTER && grid.x > 1 ? 2 : 1;
   if (cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess) return true;
   (void)cudaGetLastError();  // leave no pending error behind
   return false;
@@ -1353,8 +1356,10 @@ extern "C" bsa_status_t bsa_assign_pages(const bsa_pages_dims_t *d, const int *n
   p.seqused_kv = seqused_kv;
   p.positions = positions;
   p.slot_map = slot_map;
-  p.fill = d->total <= 2 * pages::THREADS || d->B == 0;
-  if (!launch_dependent(pages::assign_kernel, dim3(1), pages::THREADS, 0, stream, p))
+  p.fill = d->total <= pages::FEW_ROWS || d->B == 0;
+  if (!launch_dependent<true>(pages::assign_kernel,
+                              dim3(p.fill ? 1u : pages::CLUSTER), pages::THREADS, 0,
+                              stream, p))
     return BSA_ERR_CUDA;
   if (p.fill) return BSA_OK;
   return launch_dependent(pages::fill_kernel, dim3((unsigned)cdiv(d->total, pages::FILL_ROWS)),
@@ -1380,7 +1385,9 @@ extern "C" bsa_status_t bsa_release_pages(const bsa_pages_dims_t *d, const int *
   p.seq_lens = seq_lens;
   p.keep_lens = keep_lens;
   p.lens_out = lens_out;
-  return launch_dependent(pages::release_kernel, dim3(1), pages::THREADS, 0, stream, p)
+  return launch_dependent<true>(pages::release_kernel,
+                                dim3(d->num_pages <= pages::FEW_PAGES ? 1u : pages::CLUSTER),
+                                pages::THREADS, 0, stream, p)
              ? BSA_OK
              : BSA_ERR_CUDA;
 }

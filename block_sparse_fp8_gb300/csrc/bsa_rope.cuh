@@ -25,7 +25,7 @@
 namespace bsa {
 namespace rope {
 
-constexpr int THREADS = 128;
+constexpr int THREADS = 64;
 constexpr int LANES = 8;    // threads of a row
 constexpr int VEC = 8;      // values of a 16-byte vector
 constexpr int VECS = HEAD_DIM / VEC;
@@ -113,18 +113,16 @@ __global__ void __launch_bounds__(THREADS) rope_kernel(const Params p) {
     v1 = turn0 ? lane + half : turned + rest + LANES - half;
   }
 
-  const auto in = [&](int h) {
-    return reinterpret_cast<const uint4 *>(
-        h < p.N1 ? p.q + t * p.q_stride + (long long)h * HEAD_DIM
-                 : p.k + t * p.k_stride + (long long)(h - p.N1) * HEAD_DIM);
-  };
+  const uint4 *const q_row = reinterpret_cast<const uint4 *>(p.q + t * p.q_stride);
+  const uint4 *const k_row =
+      QUANT ? nullptr : reinterpret_cast<const uint4 *>(p.k + t * p.k_stride) - p.N1 * VECS;
   uint4 a[AHEAD], b[AHEAD];
   const auto load = [&](int h) {
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i) {
       a[i] = b[i] = make_uint4(0, 0, 0, 0);
       if (h + i < h1) {
-        const uint4 *x = in(h + i);
+        const uint4 *x = (QUANT || h + i < p.N1 ? q_row : k_row) + (h + i) * VECS;
         a[i] = x[v0];
         b[i] = x[v1];
       }
@@ -146,6 +144,8 @@ __global__ void __launch_bounds__(THREADS) rope_kernel(const Params p) {
     s[j] = on ? s[j] * p.amplitude : 0.f;
   }
 
+  uint2 *const codes = QUANT ? p.codes + t * p.N1 * VECS : nullptr;
+  float *const descale = QUANT ? p.descale + t * p.N1 : nullptr;
   // (with codes to make, whole warps walk the same heads: groups may be short, rows not)
   const int steps = (p.heads + AHEAD - 1) / AHEAD;
   for (int step = 0; step < steps; ++step) {
@@ -190,10 +190,10 @@ __global__ void __launch_bounds__(THREADS) rope_kernel(const Params p) {
         if (h + i < h1) {
           const float d = quant::descale_of(m, p.ue8m0), r = __frcp_rn(d);
           const uint64_t inv = ptx::pk(r, r), neg = ptx::pk(-d, -d);
-          const long long row = t * p.N1 + h + i;
-          p.codes[row * VECS + v0] = codes8(x, d, inv, neg);
-          p.codes[row * VECS + v1] = codes8(y, d, inv, neg);
-          if (lane == 0) p.descale[row] = d;
+          uint2 *o = codes + (h + i) * VECS;
+          o[v0] = codes8(x, d, inv, neg);
+          o[v1] = codes8(y, d, inv, neg);
+          if (lane == 0) descale[h + i] = d;
         }
       } else if (h + i < h1) {
         uint4 *o = reinterpret_cast<uint4 *>(
