@@ -10,22 +10,26 @@
 // issue as four other instructions.  What is here to spend fewer:
 //
 //   * A warp owns 64 tokens of a tile (32 in the e4m3 kernel), so that the softmax's reductions, the
-//     rescaling of O and the loop are paid half as often: 259 -> 220 us (all figures: 64 sequences of
-//     8-16K tokens, 64/8 heads, 917 MB, 137 us at the copy rate; mean of back-to-back calls).
+//     rescaling of O and the loop are paid half as often (all figures: 64 sequences of 8-16K tokens,
+//     64/8 heads, 917 MB, 137 us at the copy rate; mean of back-to-back calls): 259 -> 220 us.
 //   * Copies are 16-byte cp.async by all lanes, their places looked up for sixteen tiles at once, a lane
 //     a box of 32 tokens: 18 instructions a tile and no barrier to wait at.  TMA by one lane takes
-//     fewer copies, but their operands go through uniform registers: 211 us against 189.
+//     fewer copies, but their operands go through uniform registers: 211 -> 189.  They go through
+//     L1: past it (.cg) every 32-byte sector is fetched once for either half (303 MB for 151), 174
+//     against 164.  L2 is asked for no more than a row's 64 bytes, beside which NHD pages have other
+//     heads' rows (2 x 128K tokens, 32/4 heads: 43.8 -> 40.6; HND 35.5 either way).
 //   * The score factor is kept above zero (its sign goes into the queries), so that the maximum is
 //     taken of the bare products and the factor goes into the exponent's fma.
 //   * P goes in as one fp16 number, 2^-12 of it off (bf16's own rounding of the result is 2^-9): the
-//     rest as a second term, as over e4m3 pages, costs 15 us more (190 against 175) for what four bits
+//     rest as a second term, as over e4m3 pages, costs 19 us more (183 against 164) for what four bits
 //     have long lost; 6% of the results then lie a bf16 step from the rounded fp64 value.
 //
-// What did not help: twelve or sixteen warps an SM in place of eight (177 and more: the pipes are
-// shared), three stages (177), two products of K side by side, codes converted by shifts and masks
-// (305 against 259), 128- or 256-byte L2 prefetch of the copies.
+// What did not help: twelve warps an SM in place of eight (64 tokens a warp: no room for L1, 233; 32
+// tokens: 175), sixteen (201), six (207), three stages (220: no room for L1), products of K side by
+// side, fp32 arithmetic in pairs (no change), codes converted by shifts and masks (305 against 259).
 //
-// Measured: the case above 175 us, 78% of the copy rate.
+// Measured: the case above 164 us, 84% of the copy rate; 2 x 128K tokens, 32/4 heads (151 MB) 35.5 us,
+// 40.6 in NHD pages; a quarter of the tiles of 8 x 50-64K tokens (118 MB) 37.4 us.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -73,7 +77,7 @@ constexpr int SMEM_BYTES = WARPS * STAGES * STAGE_BYTES;
 static_assert(STAGE_BYTES >= MAX_G * HEAD_DIM * 4, "a segment's sums pass through a stage");
 
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src, uint32_t bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+  asm volatile("cp.async.ca.shared.global.L2::64B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
                : "memory");
 }
 __device__ __forceinline__ void copies_close() { asm volatile("cp.async.commit_group;" ::: "memory"); }
