@@ -470,15 +470,22 @@ def _check_status(dev_status, dev):
         raise ValueError("dev_status must be an int32 tensor on the device of the others")
 
 
+def _check_codes(name, t, shape, dev, codes):
+    """_check() of a tensor that holds e4m3 codes as bytes or as such."""
+    if (t.dtype in codes and t.shape == shape and t.get_device() == dev and t.is_contiguous()):
+        return
+    _check(name, t, t.dtype if t.dtype in codes else codes, shape, dev)
+
+
 def _check_fp4(k_pages, v_pages, k_scales, v_scales, pool, scales, dev):
     """The pages and block scales of a 4-bit cache; a side whose pages are None is not looked at."""
-    torch, codes = _torch_names()[0], _torch_names()[4]
+    codes = _torch_names()[4]
     for name, t, sc in (("k", k_pages, k_scales), ("v", v_pages, v_scales)):
         if t is not None:
             if sc is None:
                 raise ValueError(f"{name}_pages given without {name}_scales")
-            _check(name + "_pages", t, torch.uint8, pool, dev)
-            _check(name + "_scales", sc, sc.dtype if sc.dtype in codes else codes, scales, dev)
+            _check(name + "_pages", t, codes[0], pool, dev)
+            _check_codes(name + "_scales", sc, scales, dev, codes)
 
 
 def _pool(pages, kv_layout):
@@ -546,8 +553,8 @@ def _decode(fn, what, size, fp4, q, k_pages, v_pages, k_scales, v_scales, k_desc
     if fp4:
         _check_fp4(k_pages, v_pages, k_scales, v_scales, pool, (P, N2, ps, 8), dev)
     else:
-        _check("k_pages", k_pages, k_pages.dtype if k_pages.dtype in codes else codes, pool, dev)
-        _check("v_pages", v_pages, v_pages.dtype if v_pages.dtype in codes else codes, pool, dev)
+        _check_codes("k_pages", k_pages, pool, dev, codes)
+        _check_codes("v_pages", v_pages, pool, dev, codes)
     _check("k_descale", k_descale, f32,
            (P, N2, ps) if k_kind == SCALE_PER_TOKEN_HEAD else
            (N2,) if k_kind == SCALE_PER_HEAD else (1,), dev)
@@ -665,8 +672,7 @@ def _gather(fn, what, fp4, k_pages, v_pages, k_scales, v_scales, k_descale, v_de
         else:
             k_kind = SCALE_PER_TOKEN_HEAD if k_descale.dim() == 3 else SCALE_PER_TENSOR
         if not fp4:
-            _check("k_pages", k_pages, k_pages.dtype if k_pages.dtype in codes else codes,
-                   pages.shape, dev)
+            _check_codes("k_pages", k_pages, pages.shape, dev, codes)
         _check("k_descale", k_descale, f32,
                (P, N2, ps) if k_kind == SCALE_PER_TOKEN_HEAD else
                (N2,) if k_kind == SCALE_PER_HEAD else (1,), dev)
@@ -677,8 +683,7 @@ def _gather(fn, what, fp4, k_pages, v_pages, k_scales, v_scales, k_descale, v_de
         v_kind = v_scale_kind if v_scale_kind is not None else (
             SCALE_PER_HEAD if v_descale.numel() == N2 else SCALE_PER_TENSOR)
         if not fp4:
-            _check("v_pages", v_pages, v_pages.dtype if v_pages.dtype in codes else codes,
-                   pages.shape, dev)
+            _check_codes("v_pages", v_pages, pages.shape, dev, codes)
         _check("v_descale", v_descale, f32, (N2,) if v_kind == SCALE_PER_HEAD else (1,), dev)
         v_out = _gather_rows("v_out", v_out, out_dtype, shape, pages, stream)
     elif v_out is not None:

@@ -1222,6 +1222,25 @@ bool rope_stride_ok(long long stride, int heads) {
   return stride >= (long long)heads * HEAD_DIM && stride % 8 == 0;
 }
 
+// T rows of `bytes` each, `stride` bytes apart, at `at`
+struct Rows {
+  const void *at;
+  long long stride;
+  size_t bytes;
+  size_t span(int T) const { return (size_t)(T - 1) * (size_t)stride + bytes; }
+};
+
+// Whether two sets of rows share a byte.  Rows that lie between one another are told apart by their
+// places modulo the stride, which has to be the same; otherwise they count as overlapping.
+bool rows_overlap(const Rows &a, const Rows &b, int T) {
+  if (!overlap(a.at, a.span(T), b.at, b.span(T))) return false;
+  if (T == 1 || a.stride != b.stride) return true;
+  const uintptr_t s = (uintptr_t)a.stride;
+  const uintptr_t d = (reinterpret_cast<uintptr_t>(b.at) % s + s -
+                       reinterpret_cast<uintptr_t>(a.at) % s) % s;  // from a's row up to b's
+  return d < a.bytes || s - d < b.bytes;
+}
+
 bsa_status_t rope_params(const bsa_rope_dims_t *d, const void *q, const void *k,
                          const int *positions, const uint64_t *freqs, float amplitude,
                          rope::Params *p, unsigned *grid) {
@@ -1269,9 +1288,14 @@ extern "C" bsa_status_t bsa_rope(const bsa_rope_dims_t *d, const void *q, const 
       (d->N2 != 0) != (k_out != nullptr) || !aligned16(q) || !aligned16(k) || !aligned16(q_out) ||
       !aligned16(k_out) || (reinterpret_cast<uintptr_t>(freqs) & 7u) != 0)
     return BSA_ERR_INVALID_ARGUMENT;
-  // a tensor may be turned where it lies
-  if ((q_out == q && d->q_out_stride != d->q_stride) ||
-      (k && k_out == k && d->k_out_stride != d->k_stride))
+  // a tensor may be turned where it lies; any other overlap would read what is written
+  const size_t q_bytes = (size_t)d->N1 * HEAD_DIM * 2, k_bytes = (size_t)d->N2 * HEAD_DIM * 2;
+  const Rows qi = {q, d->q_stride * 2, q_bytes}, qo = {q_out, d->q_out_stride * 2, q_bytes},
+             ki = {k, d->k_stride * 2, k_bytes}, ko = {k_out, d->k_out_stride * 2, k_bytes};
+  const auto same = [](const Rows &a, const Rows &b) { return a.at == b.at && a.stride == b.stride; };
+  if (!same(qo, qi) && rows_overlap(qo, qi, d->T)) return BSA_ERR_INVALID_ARGUMENT;
+  if (k && ((!same(ko, ki) && rows_overlap(ko, ki, d->T)) || rows_overlap(qo, ki, d->T) ||
+            rows_overlap(ko, qi, d->T) || rows_overlap(qo, ko, d->T)))
     return BSA_ERR_INVALID_ARGUMENT;
   rope::Params p;
   unsigned grid = 0;
@@ -1296,6 +1320,9 @@ extern "C" bsa_status_t bsa_rope_quantize(const bsa_rope_dims_t *d, const void *
   if (d->T == 0) return BSA_OK;
   if (!q || !positions || !freqs || !codes_e4m3 || !descale || !aligned16(q) ||
       !aligned16(codes_e4m3) || (reinterpret_cast<uintptr_t>(freqs) & 7u) != 0)
+    return BSA_ERR_INVALID_ARGUMENT;
+  const Rows in = {q, d->q_stride * 2, (size_t)d->N1 * HEAD_DIM * 2};
+  if (overlap(codes_e4m3, (size_t)d->T * d->N1 * HEAD_DIM, q, in.span(d->T)))
     return BSA_ERR_INVALID_ARGUMENT;
   rope::Params p;
   unsigned grid = 0;
@@ -1344,7 +1371,13 @@ extern "C" bsa_status_t bsa_assign_pages(const bsa_pages_dims_t *d, const int *n
   if (d->B == 0 && d->total == 0) return BSA_OK;
   if (!free_count || !cu_seqlens || (d->total && (!positions || !slot_map)) ||
       (d->num_pages && !free_pages) || (d->B && (!new_lens || !cache_seqlens || !seqused_kv)) ||
-      (d->B && d->max_pages_per_seq && !block_table) || (d->B && seqused_kv == cache_seqlens))
+      (d->B && d->max_pages_per_seq && !block_table))
+    return BSA_ERR_INVALID_ARGUMENT;
+  // the lengths are read to the end of the call
+  const size_t nb = (size_t)d->B * sizeof(int);
+  if (d->B && (overlap(seqused_kv, nb, cache_seqlens, nb) || overlap(seqused_kv, nb, new_lens, nb) ||
+               overlap(cu_seqlens, nb + sizeof(int), cache_seqlens, nb) ||
+               overlap(cu_seqlens, nb + sizeof(int), new_lens, nb)))
     return BSA_ERR_INVALID_ARGUMENT;
   int num_sms = 0;
   const bsa_status_t st = check_device(0, &num_sms);

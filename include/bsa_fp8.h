@@ -481,16 +481,16 @@ typedef struct {
  *   amplitude * (x cos a - y sin a,  y cos a + x sin a),   a = 2 pi * frac(position * f_i),
  * the rest of the head is copied.  q bf16 [T, N1, 128], k bf16 [T, N2, 128] or NULL, positions int32
  * [T] (any values), freqs uint64 [rotary_dim/2] as bsa_rope_frequencies writes them; q_out and k_out
- * bf16, either may be its input itself (with the same stride) and must not overlap an input
- * otherwise.  Everything is 16-byte aligned but positions (4) and freqs (8).  The angle is exact to
+ * bf16, either may be its input itself (with the same stride); any other overlap with an input or with
+ * each other is refused, and so is a span shared by rows of different strides.  Everything is 16-byte aligned but positions (4) and freqs (8).  The angle is exact to
  * 2^-32 turns for any position; the rest is fp32, rounded once. */
 bsa_status_t bsa_rope(const bsa_rope_dims_t *dims, const void *q, const void *k,
                       const int *positions, const uint64_t *freqs, float amplitude, void *q_out,
                       void *k_out, void *stream);
 
 /* The same on q alone (dims->N2 = 0, the out strides unused), quantised as bsa_fp8_quantize_rows does
- * it, without rounding to bf16 in between: codes_e4m3 [T, N1, 128] and descale fp32 [T, N1], under
- * descale_rule BSA_DESCALE_AMAX or BSA_DESCALE_UE8M0.  Inputs must be finite. */
+ * it, without rounding to bf16 in between: codes_e4m3 [T, N1, 128], apart from q, and descale fp32
+ * [T, N1], under descale_rule BSA_DESCALE_AMAX or BSA_DESCALE_UE8M0.  Inputs must be finite. */
 bsa_status_t bsa_rope_quantize(const bsa_rope_dims_t *dims, const void *q, const int *positions,
                                const uint64_t *freqs, float amplitude, int descale_rule,
                                void *codes_e4m3, float *descale, void *stream);
@@ -510,7 +510,7 @@ typedef struct {
  *   free_pages    int32 [num_pages], a stack: its first *free_count entries are the free pages; read
  *   free_count    int32 [1], updated
  *   cu_seqlens    int32 [B + 1]: first rows of the sequences' new tokens
- *   seqused_kv    int32 [B]: tokens held afterwards; not cache_seqlens itself
+ *   seqused_kv    int32 [B]: tokens held afterwards; neither overlaps the lengths read
  *   positions     int32 [total]: position of each new token in its sequence
  *   slot_map      int32 [total]: its place in the cache, page * page_size + slot, or -1
  * Rows from cu_seqlens[B] on get position 0 and slot -1, so that a step captured for `total` tokens

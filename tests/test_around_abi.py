@@ -98,7 +98,7 @@ def _rope(L, dims, **kw):
 
 
 def _ropeq(L, dims, **kw):
-    a = dict(q=FAKE, pos=FAKE, f=FAKE, amp=1.0, rule=0, c=FAKE, d=FAKE)
+    a = dict(q=FAKE, pos=FAKE, f=FAKE, amp=1.0, rule=0, c=8 * FAKE, d=FAKE)
     a.update(kw)
     return L.bsa_rope_quantize(ctypes.byref(dims), a["q"], a["pos"], a["f"], a["amp"], a["rule"],
                                a["c"], a["d"], None)
@@ -128,11 +128,22 @@ def test_rope_pointers(L):
     assert _rope(L, _rdims(k_out_stride=512), ko=2 * FAKE) == INVALID
     assert _rope(L, _rdims(T=0), q=None, k=None, pos=None, f=None, qo=None, ko=None) == OK
     assert L.bsa_rope(None, *([FAKE] * 4), 1.0, FAKE, FAKE, None) == INVALID
+    # memory that overlaps in part: rows of 2048 bytes, k's of 512, four of them
+    far = 1 << 30
+    for a in (dict(qo=FAKE + 16), dict(qo=FAKE + 2032), dict(qo=FAKE - 2032), dict(ko=2 * FAKE + 16),
+              dict(qo=2 * FAKE - 64), dict(ko=FAKE + 4 * 2048 - 16), dict(qo=far, ko=far + 2032),
+              dict(qo=far, ko=far), dict(ko=FAKE), dict(qo=2 * FAKE)):
+        assert _rope(L, d, **a) == INVALID, a
+    wide = _rdims(q_stride=4096, k_stride=4096, q_out_stride=4096, k_out_stride=4096)
+    for a in (dict(k=FAKE + 2048, qo=FAKE + 2048 + 512 - 16), dict(k=FAKE + 2048, ko=FAKE + 16),
+              dict(k=FAKE + 2048, qo=FAKE + 8192 - 16)):
+        assert _rope(L, wide, **a) == INVALID, a
     q = _rdims(N2=0)
+    assert _ropeq(L, q, c=FAKE + 16) == INVALID and _ropeq(L, q, c=FAKE + 4 * 2048 - 16) == INVALID
     for name in ("q", "pos", "f", "c", "d"):
         assert _ropeq(L, q, **{name: None}) == INVALID, name
     for name in ("q", "c"):
-        assert _ropeq(L, q, **{name: FAKE + 8}) == INVALID, name
+        assert _ropeq(L, q, **{name: 9 * FAKE + 8}) == INVALID, name
     assert _ropeq(L, q, rule=2) == INVALID
     assert _ropeq(L, d) == INVALID                                  # q alone
     assert _ropeq(L, _rdims(T=0, N2=0), q=None) == OK
@@ -149,7 +160,7 @@ def _pdims(**kw):
 
 
 def _assign(L, dims, **kw):
-    a = dict(new=FAKE, old=2 * FAKE, bt=FAKE, fp=FAKE, fc=FAKE, cu=FAKE, used=FAKE, pos=FAKE,
+    a = dict(new=FAKE, old=2 * FAKE, bt=FAKE, fp=FAKE, fc=FAKE, cu=3 * FAKE, used=4 * FAKE, pos=FAKE,
              slot=FAKE)
     a.update(kw)
     return L.bsa_assign_pages(ctypes.byref(dims), a["new"], a["old"], a["bt"], a["fp"], a["fc"],
@@ -171,7 +182,8 @@ def test_pages_refused(L):
         assert _release(L, _pdims(**bad)) == INVALID, bad
     for name in ("new", "old", "bt", "fp", "fc", "cu", "used", "pos", "slot"):
         assert _assign(L, _pdims(), **{name: None}) == INVALID, name
-    assert _assign(L, _pdims(), used=2 * FAKE) == INVALID            # the lengths themselves
+    for a in (dict(used=2 * FAKE), dict(used=FAKE + 8), dict(cu=FAKE - 12), dict(cu=2 * FAKE)):
+        assert _assign(L, _pdims(), **a) == INVALID, a                # the lengths themselves
     for name in ("lens", "keep", "bt", "fp", "fc", "out"):
         assert _release(L, _pdims(), **{name: None}) == INVALID, name
     assert _assign(L, _pdims(B=0, total=0), fc=None, cu=None) == OK
@@ -315,3 +327,57 @@ def test_bindings_refuse_shapes_and_types(L):
         with pytest.raises(ValueError):
             call()
             pytest.fail(f"call {i} was not refused")
+
+
+class _Library:
+    """Stands in for the compiled library: every call succeeds, every workspace has 512 bytes."""
+
+    def __getattr__(self, name):
+        return lambda *args: 512 if name.endswith("_size") else 0
+
+
+class _Stream:
+    cuda_stream = 0
+    device = torch.device("cuda", 0)
+
+
+@pytest.mark.parametrize("name,count", [("rope", 2), ("rope_quantize", 2), ("assign_pages", 4),
+                                        ("release_pages", 1), ("gather_kv_fp4", 2),
+                                        ("decode_fp4", 2)])
+def test_tensors_come_from_the_stream_of_the_call(name, count, monkeypatch):
+    """Whatever a call on a named stream makes for itself is allocated with that stream current."""
+    c = _cpu()
+    x, i4 = c["x"], c["i4"]
+    call = {
+        "rope": lambda **k: bsa.rope(x, c["pos"], c["f"], k=x, **k),
+        "rope_quantize": lambda **k: bsa.rope_quantize(x, c["pos"], c["f"], **k),
+        "assign_pages": lambda **k: bsa.assign_pages(i4, i4, c["bt"], c["fp"], c["fc"], 32, 5, **k),
+        "release_pages": lambda **k: bsa.release_pages(i4, i4, c["bt"], c["fp"], c["fc"], 32, **k),
+        "gather_kv_fp4": lambda **k: bsa.gather_kv_fp4(c["p"], c["p"], c["s"], c["s"], c["g"], c["g"],
+                                                       i4[:3], c["bt"][:2], 5, **k),
+        "decode_fp4": lambda **k: bsa.decode_fp4(x, c["p"], c["p"], c["s"], c["s"], c["g"], c["g"], i4,
+                                                 c["bt"], 90, **k),
+    }[name]
+    state, seen, empty = [None], [], torch.empty
+
+    class on:
+        def __init__(self, stream):
+            self.stream = stream
+
+        def __enter__(self):
+            self.before, state[0] = state[0], self.stream
+
+        def __exit__(self, *_):
+            state[0] = self.before
+
+    def made(*args, **kw):
+        seen.append(state[0])
+        return empty(*args, **kw)
+
+    monkeypatch.setattr(torch.cuda, "stream", on)
+    monkeypatch.setattr(torch, "empty", made)
+    monkeypatch.setattr(bsa, "lib", lambda: _Library())
+    side = _Stream()
+    with pytest.raises(ValueError):       # for their CPU tensors, after the outputs were made
+        call(stream=side)
+    assert seen == [side] * count

@@ -154,6 +154,40 @@ def test_rope_does_not_spread_nan():
     assert torch.equal(a[~hit], b[~hit]) and not torch.isfinite(b[3, 2, 5])
 
 
+def test_rope_side_by_side():
+    """Outputs between the rows of the inputs, in the same wide tensor, are no overlap."""
+    import block_sparse_fp8_gb300 as bsa
+
+    x = _bf16(np.random.default_rng(6), (20, 3, 128))
+    wide = torch.zeros(20, 9, 128, dtype=torch.bfloat16, device="cuda")
+    wide[:, 1:4] = x.cuda()
+    pos, (fd, _) = _i32(np.arange(20) * 77), _freqs(64)
+    a, ka = bsa.rope(x.cuda(), pos, fd, k=x[:, :2].contiguous().cuda())
+    b, kb = bsa.rope(wide[:, 1:4], pos, fd, k=wide[:, 1:3], out=wide[:, 4:7], k_out=wide[:, 7:])
+    assert torch.equal(a, b) and torch.equal(ka, kb) and torch.equal(wide[:, 1:4].cpu(), x)
+    for bad in (dict(out=wide[:, 3:6]), dict(out=wide[:, :3])):
+        with pytest.raises(bsa.BsaError):
+            bsa.rope(wide[:, 1:4], pos, fd, **bad)
+
+
+def test_rope_far_apart_rows():
+    """Rows whose places pass 32 bits."""
+    import block_sparse_fp8_gb300 as bsa
+
+    T, far = 3, (1 << 31) - 8
+    x = _bf16(np.random.default_rng(7), (T, 2, 128)).cuda()
+    store = torch.empty((T - 1) * far + 256, dtype=torch.bfloat16, device="cuda")
+    q = store.as_strided((T, 2, 128), (far, 128, 1))
+    q.copy_(x)
+    pos, (fd, _) = _i32([5, 6, 700]), _freqs(128)
+    a, _ = bsa.rope(x, pos, fd)
+    c = bsa.rope_quantize(q, pos, fd)
+    bsa.rope(q, pos, fd, out=q)
+    assert torch.equal(q, a)
+    d = bsa.rope_quantize(x, pos, fd)
+    assert torch.equal(c[0], d[0]) and torch.equal(c[1], d[1])
+
+
 # ---------------------------------------------------------------------------------------------
 # pages
 # ---------------------------------------------------------------------------------------------
@@ -298,6 +332,46 @@ def test_assign_and_release_bad_entries():
     bsa.release_pages(outs[1], zero, d["table"], d["free"], d["count"], 32, dev_status=st)
     assert int(d["count"]) == min(len(free), ref2[2] + (ref2[2] - ref[5]))
     assert before.shape == d["free"].shape
+
+
+def test_assign_and_release_captured():
+    """Prompts of many rows, captured: replayed with other lengths, fewer rows and other stacks."""
+    import block_sparse_fp8_gb300 as bsa
+
+    B, ps, L, total = 37, 32, 200, 40000
+    P = B * L
+    rng = np.random.default_rng(17)
+    new, old, keep = (torch.zeros(B, dtype=torch.int32, device="cuda") for _ in range(3))
+    table = torch.full((B, L), -1, dtype=torch.int32, device="cuda")
+    free, count = torch.zeros(P, dtype=torch.int32, device="cuda"), _i32([0])
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    outs = [torch.zeros(n, dtype=torch.int32, device="cuda") for n in (B + 1, B, total, total)]
+    left = torch.zeros(B, dtype=torch.int32, device="cuda")
+
+    def both():
+        bsa.assign_pages(new, old, table, free, count, ps, total, *outs, dev_status=st)
+        bsa.release_pages(outs[1], keep, table, free, count, ps, out=left, dev_status=st)
+
+    both()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        both()
+    for hi in (1000, 3, 0, 700):
+        n = rng.integers(0, hi + 1, B)
+        k = rng.integers(0, n.max() + 2, B)
+        stack = rng.permutation(P).astype(np.int32)
+        new.copy_(_i32(n)), old.zero_(), keep.copy_(_i32(k)), free.copy_(_i32(stack))
+        count.fill_(P)
+        graph.replay()
+        torch.cuda.synchronize()
+        ref = A.assigned(n, np.zeros(B, int), np.full((B, L), -1), stack, P, ps, total)
+        for got, want, what in zip(outs, ref, ("cu", "used", "positions", "slots")):
+            _same(got, want, what)
+        lens, stack2, c2, status = A.released(ref[1], k, ref[4], stack, ref[5], ps)
+        _same(left, lens, "left")
+        assert int(count) == c2 and int(st.item()) == status == 0
+        _same(free[:c2], stack2[:c2], "stack")
 
 
 def test_assign_nothing():
@@ -626,9 +700,122 @@ def test_decode_fp4_nan_scale_stays_in_its_heads():
     assert torch.equal(got[0][:, 1:3], clean[0][:, 1:3]) and torch.equal(got[1], clean[1])
 
 
+@pytest.mark.parametrize("form", [None, "mask", "index"])
+def test_decode_fp4_longest_capacity(form):
+    """max_kv_len at the supported limit, as a graph for any length would be captured."""
+    cap = 4096 * 128
+    lens = [70, 0, 4000]
+    cache = A.Cache4(14, lens, 1, 64, spare_cols=0)
+    full = np.full((len(lens), cap // 64), 0x7fffffff, dtype=np.int32)
+    full[:, :cache.L] = cache.table
+    cache.table, cache.L = full, cap // 64
+    on = np.random.default_rng(2).random((len(lens), 3, 4096)) < 0.05 if form else None
+    q, qd, q64 = S.queries(15, len(lens), 3, False)
+    _compare(cache, q64, _decode4(cache, q, qd, on, form, max_kv_len=cap), on, str(form))
+
+
+def test_decode_fp4_idle_batch():
+    """Sequences without a token only, with and without a capacity."""
+    cache = A.Cache4(16, [0, 0, 0], 2, 32)
+    q, qd, q64 = S.queries(17, 3, 20, True)
+    for cap in (0, 32):
+        out, lse = _decode4(cache, q, qd, max_kv_len=cap)
+        assert (out == 0).all() and (lse == S.NEG_FLT_MAX).all()
+
+
+def test_fp4_pool_beyond_32_bits():
+    """Slots whose bytes lie past 2^32 in the pool, written, read back and decoded over."""
+    import block_sparse_fp8_gb300 as bsa
+
+    N2, ps = 8, 64
+    P = (1 << 32) // (N2 * ps * 64) + 40
+    pages = [torch.empty(P, N2, ps, 64, dtype=torch.uint8, device="cuda") for _ in "kv"]
+    scales = [torch.empty(P, N2, ps, 8, dtype=torch.uint8, device="cuda") for _ in "kv"]
+    rng = np.random.default_rng(18)
+    n = 300
+    k, v = _bf16(rng, (n, N2, 128)), _bf16(rng, (n, N2, 128))
+    table = (P - 1 - rng.permutation(5)).astype(np.int32).reshape(1, 5)
+    at = np.arange(n)
+    slots = table[0, at // ps] * ps + at % ps
+    g = np.full(N2, 5.0 / 2688, dtype=np.float32)
+    gd = torch.from_numpy(g).cuda()
+    bsa.append_kv_fp4(k.cuda(), v.cuda(), _i32(slots), *pages, *scales, gd, gd)
+    got = bsa.gather_kv_fp4(*pages, *scales, gd, gd, _i32([0, n]), _i32(table), n,
+                            out_dtype=torch.float32)
+    cache = A.Cache4(1, [0], N2, ps)
+    cache.kd = cache.vd = g
+    cache.lens = [n]
+    for w, x, y in (("k", k, got[0]), ("v", v, got[1])):
+        c, e = A.quantise4(x.double().numpy().transpose(1, 0, 2), g.astype(np.float64)[:, None, None])
+        cache.codes[w], cache.scales[w] = [c], [e]
+        ref = A.values4(c, e).astype(np.float32) * g[:, None, None]
+        assert np.array_equal(y.cpu().numpy(), ref.transpose(1, 0, 2))
+    q, _, q64 = S.queries(19, 1, 16, False)
+    _compare(cache, q64, bsa.decode_fp4(q.cuda(), *pages, *scales, gd, gd, _i32([n]), _i32(table), n))
+
+
 # ---------------------------------------------------------------------------------------------
 # together
 # ---------------------------------------------------------------------------------------------
+
+def test_calls_on_two_streams_at_once():
+    """Every call on a side stream beside the same call on other data on the current one, again and
+    again: both come out as they do alone."""
+    import block_sparse_fp8_gb300 as bsa
+
+    fd, _ = _freqs(128)
+    side = torch.cuda.Stream()
+
+    def data(seed):
+        rng = np.random.default_rng(seed)
+        lens = [int(x) for x in rng.integers(1, 3000, 6)]
+        cache = A.Cache4(seed, lens, 2, 32)
+        d = cache.device()
+        q, _, _ = S.queries(seed, 6, 16, False)
+        n = 500
+        x = _bf16(rng, (n, 6, 128)).cuda()
+        pages, scales = _pool4(20, 2, 32, False)
+        slots = _i32(rng.permutation(20 * 32)[:n])
+        new = _i32(rng.integers(0, 900, 6))
+        return dict(d=d, q=q.cuda(), x=x, pool=pages + scales, slots=slots, new=new, top=max(lens),
+                    pos=_i32(rng.integers(0, 9000, n)), total=int(new.sum()))
+
+    def calls(s, stream):
+        d = s["d"]
+        o, lse = bsa.decode_fp4(s["q"], d["k_pages"], d["v_pages"], d["k_scales"], d["v_scales"],
+                                d["k_descale"], d["v_descale"], d["seqused_kv"], d["block_table"],
+                                s["top"], stream=stream, **d["kinds"])
+        qr, kr = bsa.rope(s["x"][:, :4], s["pos"], fd, k=s["x"][:, 4:], stream=stream)
+        c, e = bsa.rope_quantize(s["x"], s["pos"], fd, stream=stream)
+        bsa.append_kv_fp4(kr, s["x"][:, 2:4], s["slots"], *s["pool"], d["k_descale"],
+                          d["v_descale"], stream=stream)
+        k, v = bsa.gather_kv_fp4(*s["pool"], d["k_descale"], d["v_descale"], s["cu"], s["row"], 640,
+                                 stream=stream)
+        table, free, count = s["table"].clone(), s["free"].clone(), s["count"].clone()
+        outs = bsa.assign_pages(s["new"], s["zero"], table, free, count, 32, s["total"],
+                                stream=stream)
+        return [o, lse, qr, kr, c, e, k, v, *outs]
+
+    sets = []
+    for seed in (81, 82):
+        s = data(seed)
+        s.update(cu=_i32([0, 640]), row=_i32(np.arange(20).reshape(1, 20)),
+                 table=torch.zeros(6, 40, dtype=torch.int32, device="cuda"),
+                 free=_i32(np.arange(240)), count=_i32([240]),
+                 zero=torch.zeros(6, dtype=torch.int32, device="cuda"))
+        sets.append(s)
+    alone = [[t.clone() for t in calls(s, None)] for s in sets]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        # what the calls make beside the library's work (clones) is made before the streams part
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            b = calls(sets[1], side)
+        a = calls(sets[0], None)
+        torch.cuda.current_stream().wait_stream(side)
+        for got, want in zip(a + b, alone[0] + alone[1]):
+            assert torch.equal(got, want)
+
 
 def test_serving_steps_captured():
     """Prompts admitted, then steps of one token each from one captured graph: pages, rotation,
