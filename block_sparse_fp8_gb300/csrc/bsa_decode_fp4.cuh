@@ -22,7 +22,8 @@
 //     taken of the bare products and the factor goes into the exponent's fma.
 //   * P goes in as one fp16 number, 2^-12 of it off (bf16's own rounding of the result is 2^-9): the
 //     rest as a second term, as over e4m3 pages, costs 19 us more (183 against 164) for what four bits
-//     have long lost; 6% of the results then lie a bf16 step from the rounded fp64 value.
+//     have long lost; 6 to 8% of the results then lie a bf16 step from the rounded fp64 value (0.1% in
+//     plain fp32), 1.7e-3 off in norm like those.
 //
 // What did not help: twelve warps an SM in place of eight (64 tokens a warp: no room for L1, 233; 32
 // tokens: 175), sixteen (201), six (207), three stages (220: no room for L1), products of K side by

@@ -12,8 +12,11 @@
 // them, times scale and descale, is compared with the value itself by the sign of one fma, which rounds
 // but never crosses zero.
 //
-// HBM-bound: 256 bytes of a row read, 72 written.  A thread has one block of 16 values of K and the
-// same of V, eight threads a row.
+// 256 bytes of a row read, 72 written.  A thread has one block of 16 values of K and the same of V,
+// eight threads a row.  Bound by the integer pipe, which converts and compares (71% busy; HBM 50%).
+//
+// Measured: 64K tokens x 8 heads, NHD pages (344 MB) 74 us, 70% of the measured copy rate (with
+// 64-bit divisions and the rare borders settled in four places 95).
 #pragma once
 
 #include <cuda_bf16.h>

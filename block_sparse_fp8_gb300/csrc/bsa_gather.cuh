@@ -14,7 +14,8 @@
 // 22K tokens x 8 heads to fp32 (224 MB) 35 us, 94%.
 //
 // 4-bit pages (bsa_fp4.cuh) have a kernel of their own over the same blocks of tokens: there a thread
-// has 16 codes of K or of V and their scale, and writes 32 bytes at once.
+// has 16 codes of K or of V and their scale, and writes 32 bytes at once.  64K tokens x 8 heads to bf16
+// (344 MB) 59 us, 87% (eight rows in flight a thread 89, two 63, blocks of 32 tokens 61).
 #pragma once
 
 #include <cuda_bf16.h>

@@ -10,7 +10,15 @@
 //
 // HBM-bound (a row of 128 values: 256 bytes in, 256 or 132 out).  Eight threads have a row, two
 // 16-byte vectors each, chosen so that a thread's vectors hold whole pairs and eight threads' loads
-// lie side by side; eight frequencies serve a thread's sixteen values in either layout.
+// lie side by side; eight frequencies serve a thread's sixteen values in either layout.  A thread works
+// its sines and cosines out once for the heads that it serves, up to eight, its first loads in
+// flight meanwhile; the arithmetic runs on pairs (fma.f32x2).
+//
+// Measured (mean of back-to-back calls): 8192 tokens x 40 heads in bf16, half of each head turned (168
+// MB) 29 us, 86% of the measured copy rate, 26.7 in a graph (94%); 16K tokens x 64 heads to e4m3 (407
+// MB) 81 us, 75%: latency at 95 registers, 18 warps an SM (of it the sines 4 us; blocks of 128
+// threads 83, two parts of two heads in turn 91, 80 registers 104, fp32 in single values 116); 16
+// tokens x 40 heads 2.2 us.
 #pragma once
 
 #include <cuda_bf16.h>
