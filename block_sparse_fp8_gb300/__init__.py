@@ -470,6 +470,14 @@ def _check_status(dev_status, dev):
         raise ValueError("dev_status must be an int32 tensor on the device of the others")
 
 
+def _check_all(dev, *items):
+    """_check() of several (name, tensor, dtype, shape); a call less for each that is in order."""
+    for name, t, dtype, shape in items:
+        if not (t.dtype is dtype and t.shape == shape and t.get_device() == dev
+                and t.is_contiguous()):
+            _check(name, t, dtype, shape, dev)
+
+
 def _check_codes(name, t, shape, dev, codes):
     """_check() of a tensor that holds e4m3 codes as bytes or as such."""
     if (t.dtype in codes and t.shape == shape and t.get_device() == dev and t.is_contiguous()):
@@ -481,10 +489,15 @@ def _check_fp4(k_pages, v_pages, k_scales, v_scales, pool, scales, dev):
     """The pages and block scales of a 4-bit cache; a side whose pages are None is not looked at."""
     codes = _torch_names()[4]
     for name, t, sc in (("k", k_pages, k_scales), ("v", v_pages, v_scales)):
-        if t is not None:
-            if sc is None:
-                raise ValueError(f"{name}_pages given without {name}_scales")
+        if t is None:
+            continue
+        if sc is None:
+            raise ValueError(f"{name}_pages given without {name}_scales")
+        if not (t.dtype is codes[0] and t.shape == pool and t.get_device() == dev
+                and t.is_contiguous()):
             _check(name + "_pages", t, codes[0], pool, dev)
+        if not (sc.dtype in codes and sc.shape == scales and sc.get_device() == dev
+                and sc.is_contiguous()):
             _check_codes(name + "_scales", sc, scales, dev, codes)
 
 
@@ -798,11 +811,10 @@ def _rope_common(q, positions, freqs):
     torch, _, _, i32, _ = _torch_names()
     if q.dim() != 3:
         raise ValueError(f"q has shape {tuple(q.shape)}, expected [T, N1, 128]")
-    T, dev = q.shape[0], q.get_device()
-    _check("positions", positions, i32, (T,), dev)
-    if freqs.dim() != 1:
-        raise ValueError(f"freqs has shape {tuple(freqs.shape)}, expected [rotary_dim / 2]")
-    _check("freqs", freqs, torch.int64, freqs.shape, dev)
+    T, dev, n = q.shape[0], q.get_device(), freqs.shape
+    if len(n) != 1:
+        raise ValueError(f"freqs has shape {tuple(n)}, expected [rotary_dim / 2]")
+    _check_all(dev, ("positions", positions, i32, (T,)), ("freqs", freqs, torch.int64, n))
     return T, dev, _rows("q", q, T, dev)
 
 
@@ -872,9 +884,9 @@ def _check_pages(block_table, free_pages, free_count, B, dev):
     if free_pages.dim() != 1:
         raise ValueError(f"free_pages has shape {tuple(free_pages.shape)}, expected [num_pages]")
     L = block_table.shape[1]
-    _check("block_table", block_table, i32, (B, L), dev)
-    _check("free_pages", free_pages, i32, free_pages.shape, dev)
-    _check("free_count", free_count, i32, (1,), dev)
+    _check_all(dev, ("block_table", block_table, i32, (B, L)),
+               ("free_pages", free_pages, i32, free_pages.shape),
+               ("free_count", free_count, i32, (1,)))
     return L
 
 
@@ -894,18 +906,17 @@ def assign_pages(new_lens, cache_seqlens, block_table, free_pages, free_count, p
     if new_lens.dim() != 1:
         raise ValueError(f"new_lens has shape {tuple(new_lens.shape)}, expected [B]")
     B, dev, total = new_lens.shape[0], new_lens.get_device(), int(total)
-    _check("new_lens", new_lens, i32, (B,), dev)
-    _check("cache_seqlens", cache_seqlens, i32, (B,), dev)
+    _check_all(dev, ("new_lens", new_lens, i32, (B,)), ("cache_seqlens", cache_seqlens, i32, (B,)))
     L = _check_pages(block_table, free_pages, free_count, B, dev)
     if dev_status is not None:
         _check_status(dev_status, dev)
-    device = new_lens.device
     outs = []
     for name, t, n in (("cu_seqlens", cu_seqlens, B + 1), ("seqused_kv", seqused_kv, B),
                        ("positions", positions, total), ("slot_map", slot_map, total)):
         if t is None:
-            t = _empty((n,), i32, device, stream)
-        else:
+            t = _empty((n,), i32, new_lens.device, stream)
+        elif not (t.dtype is i32 and t.shape == (n,) and t.get_device() == dev
+                  and t.is_contiguous()):
             _check(name, t, i32, (n,), dev)
         outs.append(t)
     dims = PagesDims(B, int(page_size), free_pages.shape[0], L, total)
@@ -927,8 +938,7 @@ def release_pages(seq_lens, keep_lens, block_table, free_pages, free_count, page
     if seq_lens.dim() != 1:
         raise ValueError(f"seq_lens has shape {tuple(seq_lens.shape)}, expected [B]")
     B, dev = seq_lens.shape[0], seq_lens.get_device()
-    _check("seq_lens", seq_lens, i32, (B,), dev)
-    _check("keep_lens", keep_lens, i32, (B,), dev)
+    _check_all(dev, ("seq_lens", seq_lens, i32, (B,)), ("keep_lens", keep_lens, i32, (B,)))
     L = _check_pages(block_table, free_pages, free_count, B, dev)
     if dev_status is not None:
         _check_status(dev_status, dev)
@@ -968,9 +978,9 @@ def append_kv_fp4(k_new, v_new, slot_map, k_pages, v_pages, k_scales, v_scales, 
                          f"{tuple(k_new.shape)} and {tuple(v_new.shape)} in 4 bits")
     _check_fp4(k_pages, v_pages, k_scales, v_scales, k_pages.shape, (P, N2, ps, 8), dev)
     k_kind, v_kind = _fp4_kind(k_scale_kind, k_descale, N2), _fp4_kind(v_scale_kind, v_descale, N2)
-    _check("k_descale", k_descale, f32, (N2,) if k_kind == SCALE_PER_HEAD else (1,), dev)
-    _check("v_descale", v_descale, f32, (N2,) if v_kind == SCALE_PER_HEAD else (1,), dev)
-    _check("slot_map", slot_map, i32, (T,), dev)
+    _check_all(dev, ("k_descale", k_descale, f32, (N2,) if k_kind == SCALE_PER_HEAD else (1,)),
+               ("v_descale", v_descale, f32, (N2,) if v_kind == SCALE_PER_HEAD else (1,)),
+               ("slot_map", slot_map, i32, (T,)))
     if dev_status is not None:
         _check_status(dev_status, dev)
     dims = Fp4AppendDims(N2, 128, ps, P, T, k_kind, v_kind, int(kv_layout), k_stride, v_stride)
