@@ -19,7 +19,10 @@
 //     against 164.  L2 is asked for no more than a row's 64 bytes, beside which NHD pages have other
 //     heads' rows (2 x 128K tokens, 32/4 heads: 43.8 -> 40.6; HND 35.5 either way).
 //   * The score factor is kept above zero (its sign goes into the queries), so that the maximum is
-//     taken of the bare products and the factor goes into the exponent's fma.
+//     taken of the bare products.  A weight is 2^((s - max) * factor + 15): the difference comes before
+//     the product, so that the largest score's weight is 2^15 whatever its size (of rounded products
+//     beyond 2^24 it is not: the exponent loses the 15, or the score itself lies below its maximum).
+//     Differences in pairs, products singly: 164 us, as with one fma for both; both in pairs 166.
 //   * P goes in as one fp16 number, 2^-12 of it off (bf16's own rounding of the result is 2^-9): the
 //     rest as a second term, as over e4m3 pages, costs 19 us more (183 against 164) for what four bits
 //     have long lost; 6 to 8% of the results then lie a bf16 step from the rounded fp64 value (0.1% in
@@ -378,7 +381,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) decode_kernel(const Para
 #pragma unroll
   for (int s = 0; s < STAGES - 1; ++s) issue(s);
 
-  float m[NT][2], l[NT][2], acc[NT][8][4];
+  float m[NT][2], l[NT][2], acc[NT][8][4];  // m: of the bare products
   const auto reset = [&]() {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -456,7 +459,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) decode_kernel(const Para
     float alpha[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      float ref[2];
+      float base[2];
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         float mx = fmaxf(s[nt][0][c], s[nt][0][2 + c]);
@@ -465,21 +468,24 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) decode_kernel(const Para
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-        const float mn = fmaxf(m[nt][c], __fmul_ru(mx, fac[nt][c]));  // no score is above it
-        const float base = mn == -INFINITY ? 0.f : mn;
-        alpha[nt][c] = ptx::ex2_approx(m[nt][c] - base);
+        const float mn = fmaxf(m[nt][c], mx);
+        base[c] = mn == -INFINITY ? 0.f : mn;
+        alpha[nt][c] = ptx::ex2_approx((m[nt][c] - base[c]) * fac[nt][c]);
         m[nt][c] = mn;
-        // rounded up: beyond 2^24 the nearest number may lie 16 below, where the largest weight,
-        // 2^16, is no fp16 number (the shift is then less than 15, scores are whole numbers)
-        ref[c] = __fadd_ru(base, -P_SHIFT);
       }
+      const uint64_t below = ptx::pk(-base[0], -base[1]);
       float sum0 = 0.f, sum1 = 0.f;
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
         float e[4];
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-          e[c] = ptx::ex2_approx(fmaf(s[nt][mt][c], fac[nt][c & 1], -ref[c & 1]));
+        for (int half = 0; half < 2; ++half) {
+          const uint64_t x = ptx::pk(s[nt][mt][2 * half], s[nt][mt][2 * half + 1]);
+          float x0, x1;
+          ptx::upk(ptx::add2(x, below), x0, x1);
+          e[2 * half] = ptx::ex2_approx(fmaf(x0, fac[nt][0], P_SHIFT));
+          e[2 * half + 1] = ptx::ex2_approx(fmaf(x1, fac[nt][1], P_SHIFT));
+        }
         sum0 += e[0] + e[2];
         sum1 += e[1] + e[3];
 #pragma unroll
@@ -578,7 +584,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) decode_kernel(const Para
         t += __shfl_xor_sync(0xffffffffu, t, 8);
         t += __shfl_xor_sync(0xffffffffu, t, 16);
         const int g = nt * 8 + 2 * q4 + c;
-        if (r == 0) s_ml[warp][g] = make_float2(m[nt][c], t);
+        if (r == 0) s_ml[warp][g] = make_float2(m[nt][c] * fac[nt][c], t);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
           asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(

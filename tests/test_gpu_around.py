@@ -930,3 +930,70 @@ def test_fp4_cache_into_a_prefill():
     # the same rows and queries: the prefill's probabilities are e4m3
     assert torch.allclose(lse, la, rtol=1e-3, atol=1e-3)
     assert (out.float() - a.float()).abs().max() <= 2.0 ** -4 * float(v.abs().max())
+
+
+# ---------------------------------------------------------------------------------------------
+# ends of ranges
+# ---------------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("N1,N2,q8,form", [(8, 2, False, None), (12, 1, False, None),
+                                           (4, 1, True, None), (6, 2, False, "mask"),
+                                           (16, 1, True, "index")])
+@pytest.mark.parametrize("power", [20, 25, 28, 29, 31, 33, 60])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_decode_fp4_scores_of_any_size(N1, N2, q8, form, power, sign):
+    """log2-scores up to 2^power, all above or all below zero: the largest keep their weight.
+
+    Queries are small whole numbers and K's values halves, so the products are exact and two tokens'
+    scores are equal or far apart: O is the mean of V over the tokens of the largest score, LSE that
+    score plus the logarithm of their number.  O is off by a weight's rounding to fp16, 2^-11, and the
+    exponentials', 2^-20, before its own, 2^-8; the LSE by the roundings of the factor (the scale, its
+    product with two descales), of the largest score, of two sums and of the product with ln 2 (a
+    constant rounded too): 8, 2^-24 each.  What a token t nats below the largest weighs, t >= 14, is off
+    by 8 t 2^-24 of it (the factor's roundings), t e^-t 2^-21 < 2^-37.4, and by fp16's smallest step,
+    2^-40 of the largest weight: 2^-37 sum_j |v_j| for them all."""
+    lens = [500, 64, 3, 1300]
+    cache = A.Cache4(power + N1, lens, N2, 32)
+    rng = np.random.default_rng(power)
+    for b in range(len(lens)):
+        cache.codes["k"][b] = rng.integers(0, 256, cache.codes["k"][b].shape, dtype=np.uint8) & 0x77
+        cache.scales["k"][b][:] = 0x38                  # one
+        for i in range(-(-lens[b] // 32)):
+            m = min(32, lens[b] - 32 * i)
+            cache.k_pages[cache.table[b, i], :, :m] = cache.codes["k"][b][:, 32 * i:32 * i + m]
+            cache.k_scales[cache.table[b, i], :, :m] = 0x38
+    q64 = rng.integers(1, 9, (len(lens), N1, 128)).astype(np.float64)
+    q, qd = torch.from_numpy(q64).to(torch.bfloat16), None
+    if q8:
+        qd = torch.from_numpy(rng.uniform(0.5, 2, (len(lens), N1)).astype(np.float32))
+        q = torch.from_numpy(q64.astype(np.float32)).to(torch.float8_e4m3fn).view(torch.uint8)
+        q64 = q64 * qd.double().numpy()[..., None]
+    scale = float(np.float32(sign * 2.0 ** power / (128 * 8 * 6 * 0.03 * 2)))
+    Kb = -(-max(lens) // 128)
+    on = np.ones((len(lens), N1, Kb), dtype=bool)
+    if form:
+        on &= rng.random(on.shape) < 0.6
+    got = _decode4(cache, q, qd, on if form else None, form, scale=scale)
+    O, Z = np.zeros(q64.shape), np.full((N1, len(lens)), S.NEG_FLT_MAX)
+    E, F = np.zeros(q64.shape), np.zeros(Z.shape)
+    for b, n in enumerate(lens):
+        k, v = cache.rows(b)
+        for h in range(N1):
+            seen = np.flatnonzero(np.repeat(on[b, h], 128)[:n])
+            if not len(seen):
+                continue
+            # whole halves first: ties are exact
+            s = np.rint(2 * (A.values4(cache.codes["k"][b], cache.scales["k"][b])[h * N2 // N1, seen]
+                             @ np.rint(q64[b, h] / (1 if qd is None else float(qd[b, h])))))
+            unit = 0.5 * float(cache.kd[h * N2 // N1]) * (1 if qd is None else float(qd[b, h])) * scale
+            top = (sign * s).max() * sign
+            assert abs(unit) > 14
+            w = np.exp((s - top) * unit)
+            vs = v[h * N2 // N1, seen]
+            O[b, h] = (w @ vs) / w.sum()
+            E[b, h] = 2.0 ** -8 * np.abs(O[b, h]) + 2.0 ** -37 * np.abs(vs).sum(0) + (
+                2.0 ** -11 + 2.0 ** -20) * (w @ np.abs(vs)) / w.sum()
+            Z[h, b] = top * unit + np.log(w.sum())
+            F[h, b] = 8 * 2.0 ** -24 * abs(Z[h, b]) + 2.0 ** -20
+    S.within(got[0], O, E, "O")
+    S.within(got[1], Z, F, "LSE")
