@@ -48,7 +48,8 @@ DEV_NO_PAGES = 16
 
 EXPORTED = ("bsa_fp8_prefill", "bsa_fp8_prefill_workspace_size", "bsa_fp8_compact_tiles",
             "bsa_fp8_prefill_noalloc", "bsa_fp8_prefill_host", "bsa_fp8_quantize_rows",
-            "bsa_fp8_quantize_rows_ue8m0", "bsa_fp8_append_kv", "bsa_fp8_set_wait_limit_ns",
+            "bsa_fp8_quantize_rows_ue8m0", "bsa_fp8_append_kv", "bsa_fp8_append_kv_slots",
+            "bsa_fp8_set_wait_limit_ns",
             "bsa_fp8_decode", "bsa_fp8_decode_workspace_size", "bsa_fp8_gather_kv",
             "bsa_fp8_merge_states", "bsa_rope_frequencies", "bsa_rope", "bsa_rope_quantize",
             "bsa_assign_pages", "bsa_release_pages", "bsa_fp4_append_kv", "bsa_fp4_gather_kv",
@@ -162,6 +163,8 @@ def lib():
         L.bsa_fp8_quantize_rows_ue8m0.argtypes = [vp, ctypes.c_longlong, vp, vp, vp]
         L.bsa_fp8_append_kv.restype = i32
         L.bsa_fp8_append_kv.argtypes = [ctypes.POINTER(AppendDims)] + [vp] * 12
+        L.bsa_fp8_append_kv_slots.restype = i32
+        L.bsa_fp8_append_kv_slots.argtypes = [ctypes.POINTER(AppendDims)] + [vp] * 10
         L.bsa_fp8_set_wait_limit_ns.restype = i32
         L.bsa_fp8_set_wait_limit_ns.argtypes = [ctypes.c_ulonglong]
         L.bsa_fp8_decode.restype = i32
@@ -384,19 +387,40 @@ def quantize_rows(x, codes=None, descale=None, stream=None, rule: int = DESCALE_
 def append_kv(k_new, v_new, cu_seqlens_new, cache_seqlens, block_table, k_pages, v_pages,
               k_descale=None, k_scale=None, v_scale=None, k_scale_kind=SCALE_PER_TOKEN_HEAD,
               v_scale_kind=SCALE_PER_HEAD, dev_status=None, stream=None, kv_layout=KV_HND,
-              k_descale_rule: int = DESCALE_AMAX):
+              k_descale_rule: int = DESCALE_AMAX, slot_map=None):
     """Writes bf16 K/V tokens [T_new, N2, 128] into the paged cache (k_pages / v_pages
     [P, N2, page_size, 128] (KV_HND) or [P, page_size, N2, 128] (KV_NHD) uint8 e4m3,
     k_descale [P, N2, page_size] for per-token K, computed under k_descale_rule) at positions
-    cache_seqlens[b] + i through block_table [B, L]; in place."""
+    cache_seqlens[b] + i through block_table [B, L]; in place.  Behind assign_pages() give its
+    slot_map i32 [T_new] (page * page_size + slot; negative: skipped) and None for cu_seqlens_new,
+    cache_seqlens and block_table: rows that got no place are then skipped, where the table may still
+    name pages that were given back and belong to another sequence by now."""
+    if slot_map is not None:
+        if cu_seqlens_new is not None or cache_seqlens is not None or block_table is not None:
+            raise ValueError("slot_map takes the place of cu_seqlens_new, cache_seqlens and block_table")
     if kv_layout == KV_NHD:
         P, ps, N2, D = k_pages.shape
     else:
         P, N2, ps, D = k_pages.shape
-    dims = AppendDims(B=cu_seqlens_new.numel() - 1, N2=N2, D=D, page_size=ps, num_pages=P,
-                      max_pages_per_seq=block_table.shape[1], total_new=k_new.shape[0],
+    named = slot_map is not None
+    if named:
+        _, bf16, _, i32, codes = _torch_names()
+        T, dev = k_new.shape[0], k_pages.get_device()
+        _check_all(dev, ("k_new", k_new, bf16, (T, N2, D)), ("v_new", v_new, bf16, (T, N2, D)),
+                   ("slot_map", slot_map, i32, (T,)))
+        _check_codes("k_pages", k_pages, k_pages.shape, dev, codes)
+        _check_codes("v_pages", v_pages, k_pages.shape, dev, codes)
+    dims = AppendDims(B=0 if named else cu_seqlens_new.numel() - 1, N2=N2, D=D, page_size=ps,
+                      num_pages=P, max_pages_per_seq=0 if named else block_table.shape[1],
+                      total_new=k_new.shape[0],
                       k_scale_kind=k_scale_kind, v_scale_kind=v_scale_kind,
                       kv_layout=int(kv_layout), k_descale_rule=int(k_descale_rule))
+    if named:
+        _call(lib().bsa_fp8_append_kv_slots,
+              (ctypes.byref(dims), _p(k_new), _p(v_new), _p(slot_map), _p(k_scale), _p(v_scale),
+               _p(k_pages), _p(v_pages), _p(k_descale), _p(dev_status)), dev, stream,
+              "bsa_fp8_append_kv_slots")
+        return k_pages, v_pages, k_descale
     st = lib().bsa_fp8_append_kv(ctypes.byref(dims), _p(k_new), _p(v_new), _p(cu_seqlens_new),
                                  _p(cache_seqlens), _p(block_table), _p(k_scale), _p(v_scale),
                                  _p(k_pages), _p(v_pages), _p(k_descale), _p(dev_status),
@@ -899,9 +923,10 @@ def assign_pages(new_lens, cache_seqlens, block_table, free_pages, free_count, p
     taken from its top in the sequences' order.  Returns (cu_seqlens i32 [B + 1], seqused_kv i32
     [B], positions i32 [total], slot_map i32 [total]): the new tokens' first rows, the lengths
     afterwards, and each new token's position in its sequence and its slot (page * page_size +
-    slot), as prefill(), append_kv(), rope() and append_kv_fp4() take them; rows from
+    slot), as prefill(), rope(), append_kv() and append_kv_fp4() take them; rows from
     cu_seqlens[B] on get position 0 and slot -1.  A sequence whose pages are not there gets none:
-    slots -1, its length unchanged, DEV_NO_PAGES.  seqused_kv must not be cache_seqlens."""
+    slots -1, its length unchanged, DEV_NO_PAGES (the table keeps whatever it named before, so both
+    appends take the slots).  seqused_kv must not be cache_seqlens."""
     i32 = _torch_names()[3]
     if new_lens.dim() != 1:
         raise ValueError(f"new_lens has shape {tuple(new_lens.shape)}, expected [B]")

@@ -639,12 +639,13 @@ extern "C" bsa_status_t bsa_fp8_quantize_rows_ue8m0(const void *x_bf16, long lon
   return quantize_rows_impl(x_bf16, rows, codes_e4m3, descale, stream, true);
 }
 
-extern "C" bsa_status_t bsa_fp8_append_kv(const bsa_fp8_append_dims_t *d, const void *k_new_bf16,
-                                          const void *v_new_bf16, const int *cu_seqlens_new,
-                                          const int *cache_seqlens, const int *block_table,
-                                          const float *k_scale, const float *v_scale,
-                                          void *k_pages, void *v_pages, float *k_descale,
-                                          int *dev_status, void *stream) {
+// The tokens' places come from the table or, with `slots`, from slot_map.
+static bsa_status_t append_impl(const bsa_fp8_append_dims_t *d, bool slots, const void *k_new_bf16,
+                                const void *v_new_bf16, const int *cu_seqlens_new,
+                                const int *cache_seqlens, const int *block_table,
+                                const int *slot_map, const float *k_scale, const float *v_scale,
+                                void *k_pages, void *v_pages, float *k_descale, int *dev_status,
+                                void *stream) {
   if (!d || d->D != HEAD_DIM || (d->page_size != 32 && d->page_size != 64) || d->B < 0 ||
       d->N2 < 1 || d->num_pages < 0 || d->max_pages_per_seq < 0 || d->total_new < 0)
     return BSA_ERR_INVALID_ARGUMENT;
@@ -656,10 +657,12 @@ extern "C" bsa_status_t bsa_fp8_append_kv(const bsa_fp8_append_dims_t *d, const 
   if (d->k_descale_rule != BSA_DESCALE_AMAX && d->k_descale_rule != BSA_DESCALE_UE8M0)
     return BSA_ERR_INVALID_ARGUMENT;
   const long long rows = (long long)d->total_new * d->N2;
-  if (rows == 0 || d->B == 0) return BSA_OK;
+  if (rows == 0 || (!slots && d->B == 0)) return BSA_OK;
   const bool k_tok = d->k_scale_kind == BSA_SCALE_PER_TOKEN_HEAD;
-  if (!k_new_bf16 || !v_new_bf16 || !cu_seqlens_new || !cache_seqlens || !block_table ||
-      !v_scale || !k_pages || !v_pages || (k_tok ? !k_descale : !k_scale))
+  if (slots ? !slot_map : !cu_seqlens_new || !cache_seqlens || !block_table)
+    return BSA_ERR_INVALID_ARGUMENT;
+  if (!k_new_bf16 || !v_new_bf16 || !v_scale || !k_pages || !v_pages ||
+      (k_tok ? !k_descale : !k_scale))
     return BSA_ERR_INVALID_ARGUMENT;
   if (!aligned16(k_new_bf16) || !aligned16(v_new_bf16) || !aligned16(k_pages) ||
       !aligned16(v_pages))
@@ -673,6 +676,7 @@ extern "C" bsa_status_t bsa_fp8_append_kv(const bsa_fp8_append_dims_t *d, const 
   p.cu_new = cu_seqlens_new;
   p.cache_len = cache_seqlens;
   p.block_table = block_table;
+  p.slot_map = slot_map;
   p.k_scale = k_scale;
   p.v_scale = v_scale;
   p.k_pages = static_cast<uint2 *>(k_pages);
@@ -691,6 +695,26 @@ extern "C" bsa_status_t bsa_fp8_append_kv(const bsa_fp8_append_dims_t *d, const 
   p.k_ue8m0 = d->k_descale_rule == BSA_DESCALE_UE8M0 ? 1 : 0;
   quant::append_kv_kernel<<<grid, quant::THREADS, 0, (cudaStream_t)stream>>>(p);
   return cudaGetLastError() == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
+}
+
+extern "C" bsa_status_t bsa_fp8_append_kv(const bsa_fp8_append_dims_t *d, const void *k_new_bf16,
+                                          const void *v_new_bf16, const int *cu_seqlens_new,
+                                          const int *cache_seqlens, const int *block_table,
+                                          const float *k_scale, const float *v_scale,
+                                          void *k_pages, void *v_pages, float *k_descale,
+                                          int *dev_status, void *stream) {
+  return append_impl(d, false, k_new_bf16, v_new_bf16, cu_seqlens_new, cache_seqlens, block_table,
+                     nullptr, k_scale, v_scale, k_pages, v_pages, k_descale, dev_status, stream);
+}
+
+extern "C" bsa_status_t bsa_fp8_append_kv_slots(const bsa_fp8_append_dims_t *d,
+                                                const void *k_new_bf16, const void *v_new_bf16,
+                                                const int *slot_map, const float *k_scale,
+                                                const float *v_scale, void *k_pages,
+                                                void *v_pages, float *k_descale, int *dev_status,
+                                                void *stream) {
+  return append_impl(d, true, k_new_bf16, v_new_bf16, nullptr, nullptr, nullptr, slot_map, k_scale,
+                     v_scale, k_pages, v_pages, k_descale, dev_status, stream);
 }
 
 extern "C" bsa_status_t bsa_fp8_prefill_noalloc(

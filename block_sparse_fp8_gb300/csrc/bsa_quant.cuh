@@ -134,6 +134,7 @@ __global__ void __launch_bounds__(THREADS) quantize_rows_kernel(const uint4 *__r
 struct AppendParams {
   const uint4 *k_new, *v_new;
   const int *cu_new, *cache_len, *block_table;
+  const int *slot_map;  // the tokens' places, in place of those three; or null
   const float *k_scale, *v_scale;
   uint2 *k_pages, *v_pages;
   float *k_descale;
@@ -143,7 +144,7 @@ struct AppendParams {
   int k_ue8m0;  // per-token K descales rounded up to a power of two
 };
 
-// One warp per new token.  The token's first four heads of K and V are loaded before its
+// One warp per new token, whose place is named (slot_map) or looked up.  The token's first four heads of K and V are loaded before its
 // page is looked up, so that the lookup's dependent reads (the sequence by binary search over
 // cu_new, then the block table) overlap those loads; the two half-warps then take two heads at
 // a time, four heads per batch of loads (deeper batches cost occupancy and measured slower).
@@ -167,7 +168,17 @@ __global__ void __launch_bounds__(THREADS) append_kv_kernel(const AppendParams p
     load(0);
     long long slot = 0;
     int pg = -1;
-    if (lane == 0) {
+    if (lane == 0 && p.slot_map) {
+      const int s = p.slot_map[tok];
+      if (s >= 0) {  // (a row without a place otherwise)
+        pg = s / p.ps;
+        slot = s % p.ps;
+        if (pg >= p.num_pages) {
+          report_status(p.dev_status, BSA_DEV_BAD_PAGE);
+          pg = -1;
+        }
+      }
+    } else if (lane == 0) {
       // sequence of the token: the last b with cu_new[b] <= tok
       int lo = 0, hi = p.B - 1;
       while (lo < hi) {

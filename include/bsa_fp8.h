@@ -323,6 +323,18 @@ bsa_status_t bsa_fp8_append_kv(const bsa_fp8_append_dims_t *dims, const void *k_
                                const float *k_scale, const float *v_scale, void *k_pages,
                                void *v_pages, float *k_descale, int *dev_status, void *stream);
 
+/* The same with the tokens' places named: row i goes to slot slot_map[i] = page * page_size + slot
+ * (device int32 [total_new]), as bsa_assign_pages gives it; a negative one is skipped, one beyond the
+ * pool is reported (BSA_DEV_BAD_PAGE) and skipped.  No slot may be named twice in a call.
+ * dims->B and max_pages_per_seq are not used.  This is the call behind bsa_assign_pages: rows that got
+ * no place (too few pages, rows behind the last sequence) are skipped, whereas the table may still
+ * name pages at their positions that were given back and belong to another sequence by now. */
+bsa_status_t bsa_fp8_append_kv_slots(const bsa_fp8_append_dims_t *dims, const void *k_new_bf16,
+                                     const void *v_new_bf16, const int *slot_map,
+                                     const float *k_scale, const float *v_scale, void *k_pages,
+                                     void *v_pages, float *k_descale, int *dev_status,
+                                     void *stream);
+
 /* ------------------------------------------------------------------------------------------
  * Serving beside the prefill: the next token's attention over the cache, the cache read back,
  * and the join of attention results over parts of a cache.  No counterpart in the pages; the
@@ -441,7 +453,7 @@ bsa_status_t bsa_fp8_merge_states(int count, const void *const *outs, const floa
 /* ------------------------------------------------------------------------------------------
  * Around attention: rotary positions of Q and K, pages for new tokens, and a cache held in 4 bits.
  * No counterpart in the pages.  A step of a serving loop is bsa_assign_pages, bsa_rope (or
- * bsa_rope_quantize for Q), bsa_fp4_append_kv (or bsa_fp8_append_kv) and a decode.
+ * bsa_rope_quantize for Q), bsa_fp4_append_kv (or bsa_fp8_append_kv_slots) and a decode.
  * ------------------------------------------------------------------------------------------ */
 
 /* Pairs of a rotated head: value i with value i + rotary_dim/2, or value 2i with value 2i + 1. */

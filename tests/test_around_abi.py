@@ -381,3 +381,48 @@ def test_tensors_come_from_the_stream_of_the_call(name, count, monkeypatch):
     with pytest.raises(ValueError):       # for their CPU tensors, after the outputs were made
         call(stream=side)
     assert seen == [side] * count
+
+
+# ---------------------------------------------------------------------------------------------
+# the e4m3 cache behind assign_pages
+# ---------------------------------------------------------------------------------------------
+
+def test_append_slots_refused(L):
+    def call(dims, **kw):
+        a = dict(k=FAKE, v=FAKE, slot=FAKE, ks=None, vs=FAKE, kp=FAKE, vp=FAKE, kd=FAKE)
+        a.update(kw)
+        return L.bsa_fp8_append_kv_slots(ctypes.byref(dims), a["k"], a["v"], a["slot"], a["ks"],
+                                         a["vs"], a["kp"], a["vp"], a["kd"], None, None)
+
+    def dims(**kw):
+        return bsa.AppendDims(**dict(dict(B=0, N2=2, D=128, page_size=64, num_pages=4,
+                                          max_pages_per_seq=0, total_new=8, k_scale_kind=1,
+                                          v_scale_kind=2, kv_layout=0, k_descale_rule=0), **kw))
+
+    for bad in (dict(N2=0), dict(D=64), dict(page_size=16), dict(num_pages=-1), dict(total_new=-1),
+                dict(k_scale_kind=2), dict(v_scale_kind=1), dict(kv_layout=2), dict(k_descale_rule=2)):
+        assert call(dims(**bad)) == INVALID, bad
+    for name in ("k", "v", "slot", "vs", "kp", "vp", "kd"):
+        assert call(dims(), **{name: None}) == INVALID, name
+    for name in ("k", "v", "kp", "vp"):
+        assert call(dims(), **{name: FAKE + 8}) == INVALID, name
+    assert call(dims(k_scale_kind=0), kd=None) == INVALID           # a descale per tensor is given
+    assert call(dims(total_new=0), k=None, slot=None) == OK
+
+
+def test_append_slots_binding_refuses(L):
+    x, i4 = torch.zeros(4, 2, 128, dtype=torch.bfloat16), torch.zeros(4, dtype=torch.int32)
+    p, kd, vs = torch.zeros(6, 2, 32, 128, dtype=torch.uint8), torch.zeros(6, 2, 32), torch.ones(2)
+    none = (None, None, None)
+    wide = torch.zeros(4, 6, 128, dtype=torch.bfloat16)
+    for call in (lambda: bsa.append_kv(x, x, i4, i4, i4[None], p, p, kd, v_scale=vs, slot_map=i4),
+                 lambda: bsa.append_kv(x, x, None, None, i4[None], p, p, kd, v_scale=vs, slot_map=i4),
+                 lambda: bsa.append_kv(x, x, *none, p, p, kd, v_scale=vs, slot_map=i4[:3]),
+                 lambda: bsa.append_kv(x, x, *none, p, p, kd, v_scale=vs, slot_map=i4.long()),
+                 lambda: bsa.append_kv(wide[:, :2], x, *none, p, p, kd, v_scale=vs, slot_map=i4),
+                 lambda: bsa.append_kv(x, wide[:, 4:], *none, p, p, kd, v_scale=vs, slot_map=i4),
+                 lambda: bsa.append_kv(x, x[:3], *none, p, p, kd, v_scale=vs, slot_map=i4),
+                 lambda: bsa.append_kv(x, x, *none, p, p[:5], kd, v_scale=vs, slot_map=i4),
+                 lambda: bsa.append_kv(x, x, *none, p, p, kd, v_scale=vs, slot_map=i4)):  # no GPU
+        with pytest.raises(ValueError):
+            call()

@@ -997,3 +997,124 @@ def test_decode_fp4_scores_of_any_size(N1, N2, q8, form, power, sign):
             F[h, b] = 8 * 2.0 ** -24 * abs(Z[h, b]) + 2.0 ** -20
     S.within(got[0], O, E, "O")
     S.within(got[1], Z, F, "LSE")
+
+
+# ---------------------------------------------------------------------------------------------
+# the e4m3 cache behind assign_pages
+# ---------------------------------------------------------------------------------------------
+
+class _Pool8:
+    """An e4m3 pool, and the bytes that it has to hold."""
+
+    def __init__(self, P, N2, ps, nhd, k_tok=True):
+        import block_sparse_fp8_gb300 as bsa
+
+        self.ps, self.nhd, self.k_tok = ps, nhd, k_tok
+        shape = (P, ps, N2, 128) if nhd else (P, N2, ps, 128)
+        self.k, self.v = (torch.full(shape, 0x55, dtype=torch.uint8, device="cuda") for _ in "kv")
+        self.kd = torch.full((P, N2, ps), -7.0, device="cuda")
+        self.ks, self.vs = torch.full((1,), 0.02, device="cuda"), torch.linspace(0.02, 0.03, N2).cuda()
+        self.kinds = dict(k_scale_kind=bsa.SCALE_PER_TOKEN_HEAD if k_tok else bsa.SCALE_PER_TENSOR,
+                          v_scale_kind=bsa.SCALE_PER_HEAD,
+                          kv_layout=bsa.KV_NHD if nhd else bsa.KV_HND)
+        self.want = [t.clone() for t in (self.k, self.v, self.kd)]
+
+    def append(self, k, v, *where, **kw):
+        import block_sparse_fp8_gb300 as bsa
+
+        bsa.append_kv(k, v, *(where or (None,) * 3), self.k, self.v, self.kd, k_scale=self.ks,
+                      v_scale=self.vs, **self.kinds, **kw)
+
+    def expect(self, k, v, slots):
+        """The rows whose slot is not below zero, by the quantise step's rule."""
+        import block_sparse_fp8_gb300 as bsa
+
+        on = torch.from_numpy(np.flatnonzero(slots >= 0)).cuda()
+        at = torch.from_numpy(slots[slots >= 0]).cuda()
+        pg, sl = at // self.ps, at % self.ps
+        e4m3 = lambda x: x.to(torch.float8_e4m3fn).view(torch.uint8)
+        codes, d = bsa.quantize_rows(k) if self.k_tok else (e4m3(k.float() / self.ks), None)
+        for t, rows in zip(self.want, (codes, e4m3(v.float() / self.vs[:, None]))):
+            (t.transpose(1, 2) if self.nhd else t)[pg, :, sl] = rows[on]
+        if self.k_tok:
+            self.want[2][pg, :, sl] = d[on]
+
+    def check(self, what):
+        for got, want, name in zip((self.k, self.v, self.kd), self.want, ("K", "V", "K descales")):
+            assert torch.equal(got, want), (what, name, int((got != want).sum()))
+
+
+@pytest.mark.parametrize("T,N2,ps,nhd,k_tok", [(1, 1, 32, False, True), (77, 5, 32, True, True),
+                                               (300, 8, 64, False, False), (1000, 3, 64, True, True)])
+def test_append_kv_slots(T, N2, ps, nhd, k_tok):
+    """Rows into slots in any order; negative ones skipped, those beyond the pool reported too."""
+    import block_sparse_fp8_gb300 as bsa
+
+    rng = np.random.default_rng(T)
+    P = -(-T // ps) + 3
+    pool = _Pool8(P, N2, ps, nhd, k_tok)
+    slots = rng.permutation(P * ps)[:T].astype(np.int32)
+    k, v = _bf16(rng, (T, N2, 128)).cuda(), _bf16(rng, (T, N2, 128)).cuda()
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    skip = slots.copy()
+    if T > 4:
+        skip[[1, T // 2]] = -1, -2 ** 31
+    pool.append(k, v, slot_map=_i32(skip), dev_status=st)
+    pool.expect(k, v, skip)
+    pool.check("slots")
+    assert int(st.item()) == 0
+    skip[0] = P * ps
+    skip[-1] = 2 ** 31 - 1
+    pool.append(v, k, slot_map=_i32(skip), dev_status=st)
+    skip[[0, -1]] = -1
+    pool.expect(v, k, skip)
+    pool.check("beyond the pool")
+    assert int(st.item()) == bsa.DEV_BAD_PAGE
+
+
+@pytest.mark.parametrize("ps,nhd", [(32, False), (64, True)])
+def test_pages_for_the_e4m3_cache_captured(ps, nhd):
+    """Steps of assign_pages and append_kv from one captured graph, pages given back and assigned to
+    others between them: sequences that get no pages, rows behind the last one, sequences that sit out.
+    No byte of the pool changes but the served rows'."""
+    import block_sparse_fp8_gb300 as bsa
+
+    B, N2, L, P, cap = 6, 2, 8, 14, 200
+    rng = np.random.default_rng(ps)
+    pool = _Pool8(P, N2, ps, nhd)
+    zeros = lambda *s: torch.zeros(*s, dtype=torch.int32, device="cuda")
+    new, lens, st = zeros(B), zeros(B), zeros(1)
+    table, free, count = zeros(B, L) - 1, _i32(rng.permutation(P)), _i32([P])
+    outs = [zeros(n) for n in (B + 1, B, cap, cap)]
+    k, v = (torch.zeros(cap, N2, 128, dtype=torch.bfloat16, device="cuda") for _ in "kv")
+
+    def step():
+        bsa.assign_pages(new, lens, table, free, count, ps, cap, *outs, dev_status=st)
+        pool.append(k, v, slot_map=outs[3], dev_status=st)
+        lens.copy_(outs[1])
+
+    step()                                              # nothing to assign: nothing changes
+    torch.cuda.synchronize()
+    pool.check("warm-up")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    short = 0
+    for i in range(40):
+        n = rng.integers(0, (40, 2, 90)[i % 3], B) * (rng.random(B) < 0.7)
+        state = [t.cpu().numpy() for t in (lens, table, free, count)]
+        ref = A.assigned(n, state[0], state[1], state[2], int(state[3][0]), ps, cap)
+        new.copy_(_i32(n))
+        k.copy_(_bf16(rng, (cap, N2, 128)).cuda())
+        v.copy_(_bf16(rng, (cap, N2, 128)).cuda())
+        st.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        _same(outs[3], ref[3], "slots")
+        assert int(st.item()) == ref[6] and ref[6] in (0, 4, 16, 20)
+        short += ref[6] >= 16
+        pool.expect(k, v, ref[3])
+        pool.check(f"step {i}")
+        keep = np.where(rng.random(B) < 0.4, rng.integers(0, 60, B), 10 ** 6)
+        bsa.release_pages(lens, _i32(keep), table, free, count, ps, out=lens)
+    assert short
