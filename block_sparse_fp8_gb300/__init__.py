@@ -391,7 +391,8 @@ def append_kv(k_new, v_new, cu_seqlens_new, cache_seqlens, block_table, k_pages,
     """Writes bf16 K/V tokens [T_new, N2, 128] into the paged cache (k_pages / v_pages
     [P, N2, page_size, 128] (KV_HND) or [P, page_size, N2, 128] (KV_NHD) uint8 e4m3,
     k_descale [P, N2, page_size] for per-token K, computed under k_descale_rule) at positions
-    cache_seqlens[b] + i through block_table [B, L]; in place.  Behind assign_pages() give its
+    cache_seqlens[b] + i through block_table [B, L]; in place; rows from cu_seqlens_new[B] on are
+    skipped.  Behind assign_pages() give its
     slot_map i32 [T_new] (page * page_size + slot; negative: skipped) and None for cu_seqlens_new,
     cache_seqlens and block_table: rows that got no place are then skipped, where the table may still
     name pages that were given back and belong to another sequence by now."""

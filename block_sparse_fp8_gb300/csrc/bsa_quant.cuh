@@ -179,7 +179,8 @@ __global__ void __launch_bounds__(THREADS) append_kv_kernel(const AppendParams p
         }
       }
     } else if (lane == 0) {
-      // sequence of the token: the last b with cu_new[b] <= tok
+      // sequence of the token: the last b with cu_new[b] <= tok (none of a row behind the last one)
+      const int rows = p.cu_new[p.B];
       int lo = 0, hi = p.B - 1;
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
@@ -187,8 +188,10 @@ __global__ void __launch_bounds__(THREADS) append_kv_kernel(const AppendParams p
       }
       const long long pos = (long long)p.cache_len[lo] + (tok - p.cu_new[lo]);
       const long long lp = pos / p.ps;
-      pg = (pos >= 0 && lp < p.L) ? p.block_table[(size_t)lo * p.L + lp] : -1;
-      if (pg < 0 || pg >= p.num_pages) {
+      pg = pos >= 0 && lp < p.L ? p.block_table[(size_t)lo * p.L + lp] : -1;
+      if (tok >= rows) {
+        pg = -1;
+      } else if (pg < 0 || pg >= p.num_pages) {
         report_status(p.dev_status, BSA_DEV_BAD_PAGE);
         pg = -1;
       } else {

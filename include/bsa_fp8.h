@@ -293,7 +293,8 @@ typedef struct {
   int page_size;         /* 32 or 64 */
   int num_pages;         /* P */
   int max_pages_per_seq; /* L, columns of block_table */
-  int total_new;         /* T_new = cu_seqlens_new[B], rows of k_new / v_new */
+  int total_new;         /* T_new >= cu_seqlens_new[B], rows of k_new / v_new; those from
+                            cu_seqlens_new[B] on are skipped */
   bsa_scale_kind_t k_scale_kind; /* BSA_SCALE_PER_TOKEN_HEAD (computed) or BSA_SCALE_PER_TENSOR */
   bsa_scale_kind_t v_scale_kind; /* BSA_SCALE_PER_HEAD or BSA_SCALE_PER_TENSOR (given) */
   int kv_layout;         /* BSA_KV_HND (0): pages [P, N2, page_size, 128]; BSA_KV_NHD (1):

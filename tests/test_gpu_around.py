@@ -1118,3 +1118,23 @@ def test_pages_for_the_e4m3_cache_captured(ps, nhd):
         keep = np.where(rng.random(B) < 0.4, rng.integers(0, 60, B), 10 ** 6)
         bsa.release_pages(lens, _i32(keep), table, free, count, ps, out=lens)
     assert short
+
+
+def test_append_kv_rows_behind_the_last_sequence():
+    """Rows from cu_seqlens_new[B] on belong to nobody, whatever the last sequence's table names."""
+    rng = np.random.default_rng(7)
+    T, B, ps = 120, 2, 32
+    pool = _Pool8(8, 2, ps, False)
+    k, v = _bf16(rng, (T, 2, 128)).cuda(), _bf16(rng, (T, 2, 128)).cuda()
+    table = np.array([[0, 1, 2, 3], [4, 5, 6, 7]])
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for cu, cached in (([0, 40, 70], [0, 10]), ([0, 0, 0], [5, 0]), ([0, 33, 33], [40, 128])):
+        slots = np.full(T, -1)
+        for b in range(B):
+            at = cached[b] + np.arange(cu[b + 1] - cu[b])
+            slots[cu[b]:cu[b + 1]] = table[b, at // ps] * ps + at % ps
+        pool.append(k, v, _i32(cu), _i32(cached), _i32(table), dev_status=st)
+        pool.expect(k, v, slots)
+        pool.check(str(cu))
+        k, v = v, k
+    assert int(st.item()) == 0
