@@ -50,10 +50,10 @@ EXPORTED = ("bsa_fp8_prefill", "bsa_fp8_prefill_workspace_size", "bsa_fp8_compac
             "bsa_fp8_prefill_noalloc", "bsa_fp8_prefill_host", "bsa_fp8_quantize_rows",
             "bsa_fp8_quantize_rows_ue8m0", "bsa_fp8_append_kv", "bsa_fp8_append_kv_slots",
             "bsa_fp8_set_wait_limit_ns",
-            "bsa_fp8_decode", "bsa_fp8_decode_workspace_size", "bsa_fp8_gather_kv",
+            "bsa_fp8_decode", "bsa_fp8_decode_rows", "bsa_fp8_decode_workspace_size", "bsa_fp8_gather_kv",
             "bsa_fp8_merge_states", "bsa_rope_frequencies", "bsa_rope", "bsa_rope_quantize",
             "bsa_assign_pages", "bsa_release_pages", "bsa_fp4_append_kv", "bsa_fp4_gather_kv",
-            "bsa_fp4_decode", "bsa_fp4_decode_workspace_size", "bsa_status_string")
+            "bsa_fp4_decode", "bsa_fp4_decode_rows", "bsa_fp4_decode_workspace_size", "bsa_status_string")
 
 # descale rules of the quantise step
 DESCALE_AMAX = 0    # amax / 448
@@ -194,6 +194,10 @@ def lib():
         L.bsa_fp4_decode.restype = i32
         L.bsa_fp4_decode.argtypes = [ctypes.POINTER(DecodeDims)] + [vp] * 13 + [f32, vp, vp, vp,
                                                                                 sz, vp, vp]
+        for rows, fn in ((L.bsa_fp8_decode_rows, L.bsa_fp8_decode),
+                         (L.bsa_fp4_decode_rows, L.bsa_fp4_decode)):
+            rows.restype = i32
+            rows.argtypes = [fn.argtypes[0], i32, vp] + fn.argtypes[1:]
         L.bsa_fp4_decode_workspace_size.restype = sz
         L.bsa_fp4_decode_workspace_size.argtypes = [ctypes.POINTER(DecodeDims)]
         L.bsa_status_string.restype = ctypes.c_char_p
@@ -537,13 +541,13 @@ def _pool(pages, kv_layout):
 
 def make_decode_dims(q, k_pages, block_table, max_kv_len, k_scale_kind, v_scale_kind,
                      kv_layout=KV_HND, sparse=False) -> DecodeDims:
-    B, N1, D = q.shape
+    T, N1, D = q.shape
     P, N2, ps, _ = _pool(k_pages, kv_layout)
     # in the order of DecodeDims' fields
-    return DecodeDims(B, N1, N2, D, ps, max_kv_len, P, block_table.shape[1], k_scale_kind,
-                      v_scale_kind, kv_layout,
+    return DecodeDims(block_table.shape[0], N1, N2, D, ps, max_kv_len, P, block_table.shape[1],
+                      k_scale_kind, v_scale_kind, kv_layout,
                       QTYPE_E4M3 if q.element_size() == 1 else QTYPE_BF16,
-                      q.stride(0) if B > 1 else N1 * D, 1 if sparse else 0)
+                      q.stride(0) if T > 1 else N1 * D, 1 if sparse else 0)
 
 
 def decode_workspace_size(dims: DecodeDims) -> int:
@@ -551,7 +555,7 @@ def decode_workspace_size(dims: DecodeDims) -> int:
     return int(lib().bsa_fp8_decode_workspace_size(ctypes.byref(dims)))
 
 
-def _decode(fn, what, size, fp4, q, k_pages, v_pages, k_scales, v_scales, k_descale,
+def _decode(what, size, fp4, cu_seqlens_q, q, k_pages, v_pages, k_scales, v_scales, k_descale,
             v_descale, seqused_kv, block_table, max_kv_len, q_descale, block_mask, sparse_indices,
             sparse_seq_len, softmax_scale, out, lse, return_lse, dev_status, workspace, stream,
             k_scale_kind, v_scale_kind, kv_layout):
@@ -561,7 +565,14 @@ def _decode(fn, what, size, fp4, q, k_pages, v_pages, k_scales, v_scales, k_desc
     shape = q.shape
     if len(shape) != 3:
         raise ValueError(f"q has shape {tuple(shape)}, expected [B, N1, 128]")
-    B, N1, D = shape
+    T, N1, D = shape
+    B, packed = T, ()
+    if cu_seqlens_q is not None:
+        if cu_seqlens_q.dim() != 1 or cu_seqlens_q.shape[0] < 1:
+            raise ValueError(f"cu_seqlens_q has shape {tuple(cu_seqlens_q.shape)}, expected [B + 1]")
+        B = cu_seqlens_q.shape[0] - 1
+        _check("cu_seqlens_q", cu_seqlens_q, i32, (B + 1,), dev)
+        what, packed = what + "_rows", (T, cu_seqlens_q.data_ptr())
     is_bf16 = q.dtype is bf16
     if not is_bf16 and q.dtype not in codes:
         raise ValueError(f"q has dtype {q.dtype}, expected bf16 or e4m3 codes")
@@ -569,7 +580,7 @@ def _decode(fn, what, size, fp4, q, k_pages, v_pages, k_scales, v_scales, k_desc
     if not q.is_contiguous():
         if q.stride(2) != 1 or (N1 > 1 and q.stride(1) != D):
             raise ValueError("q must be contiguous within a sequence's row")
-        if B > 1:
+        if T > 1:
             q_stride = q.stride(0)
             if q_stride >= 1 << 31:
                 raise ValueError(f"q's rows lie {q_stride} elements apart: 2^31 - 1 at most")
@@ -601,7 +612,7 @@ def _decode(fn, what, size, fp4, q, k_pages, v_pages, k_scales, v_scales, k_desc
     L = table[1]
     _check("block_table", block_table, i32, (B, L), dev)
     if q_descale is not None:
-        _check("q_descale", q_descale, f32, (B, N1), dev)
+        _check("q_descale", q_descale, f32, (T, N1), dev)
     sparse = block_mask is not None or sparse_indices is not None
     if sparse:
         Kb = -(-int(max_kv_len) // 128)
@@ -613,13 +624,13 @@ def _decode(fn, what, size, fp4, q, k_pages, v_pages, k_scales, v_scales, k_desc
         if sparse_seq_len is not None:
             _check("sparse_seq_len", sparse_seq_len, i32, (B, N1), dev)
     if out is None:
-        out = _empty((B, N1, D), bf16, q.device, stream)
+        out = _empty((T, N1, D), bf16, q.device, stream)
     else:
         _check("out", out, bf16, shape, dev)
     if lse is not None:
-        _check("lse", lse, f32, (N1, B), dev)
+        _check("lse", lse, f32, (N1, T), dev)
     elif return_lse:
-        lse = _empty((N1, B), f32, q.device, stream)
+        lse = _empty((N1, T), f32, q.device, stream)
     if dev_status is not None:
         _check_status(dev_status, dev)
     # in the order of DecodeDims' fields, as make_decode_dims
@@ -636,8 +647,8 @@ def _decode(fn, what, size, fp4, q, k_pages, v_pages, k_scales, v_scales, k_desc
     if softmax_scale is None:
         softmax_scale = 1.0 / math.sqrt(D)
     scales = (k_scales.data_ptr(), v_scales.data_ptr()) if fp4 else ()
-    _call(fn,
-          (ctypes.byref(dims), q.data_ptr(), _p(q_descale), k_pages.data_ptr(),
+    _call(getattr(lib(), what),
+          (ctypes.byref(dims), *packed, q.data_ptr(), _p(q_descale), k_pages.data_ptr(),
            v_pages.data_ptr(), *scales, k_descale.data_ptr(), v_descale.data_ptr(), seqused_kv.data_ptr(),
            block_table.data_ptr(), _p(block_mask), _p(sparse_indices), _p(sparse_seq_len),
            float(softmax_scale), out.data_ptr(), _p(lse), workspace.data_ptr(), workspace.nbytes,
@@ -649,7 +660,7 @@ def decode(q, k_pages, v_pages, k_descale, v_descale, seqused_kv, block_table, m
            q_descale=None, block_mask=None, sparse_indices=None, sparse_seq_len=None,
            softmax_scale: float | None = None, out=None, lse=None, return_lse: bool = True,
            dev_status=None, workspace=None, stream=None, k_scale_kind: int | None = None,
-           v_scale_kind: int | None = None, kv_layout: int = KV_HND):
+           v_scale_kind: int | None = None, kv_layout: int = KV_HND, cu_seqlens_q=None):
     """Attention of one new token per sequence over the paged cache (whose seqused_kv counts the
     new token, appended beforehand).  q bf16 [B, N1, 128], or uint8/float8_e4m3fn with q_descale
     f32 [B, N1]; its rows may lie further apart than N1 * 128 (a slice of a wider projection).
@@ -658,9 +669,13 @@ def decode(q, k_pages, v_pages, k_descale, v_descale, seqused_kv, block_table, m
     select 128-token tiles for each query head, Kb = ceil(max_kv_len / 128).
     Returns (out bf16 [B, N1, 128], lse f32 [N1, B] or None); a sequence without tokens, or a head
     without an enabled tile, gives 0 and -FLT_MAX.  `out` may be q itself.  `workspace`
-    (decode_workspace_size bytes) must not be shared by calls in flight at once."""
-    return _decode(lib().bsa_fp8_decode, "bsa_fp8_decode", decode_workspace_size, False, q, k_pages,
-                   v_pages, None, None, k_descale, v_descale, seqused_kv, block_table, max_kv_len, q_descale,
+    (decode_workspace_size bytes) must not be shared by calls in flight at once.
+    With cu_seqlens_q i32 [B + 1], as assign_pages() gives it, q, q_descale, out and lse have a row
+    for each sequence that has a new token, [T, N1, 128] and so on, row cu_seqlens_q[b] being
+    sequence b's, and a sequence without one takes no part; rows behind the last sequence's get 0
+    and -FLT_MAX, and so do those of a sequence with several (DEV_BAD_SEQLEN)."""
+    return _decode("bsa_fp8_decode", decode_workspace_size, False, cu_seqlens_q, q, k_pages, v_pages,
+                   None, None, k_descale, v_descale, seqused_kv, block_table, max_kv_len, q_descale,
                    block_mask, sparse_indices, sparse_seq_len, softmax_scale, out, lse, return_lse,
                    dev_status, workspace, stream, k_scale_kind, v_scale_kind, kv_layout)
 
@@ -1039,10 +1054,10 @@ def decode_fp4(q, k_pages, v_pages, k_scales, v_scales, k_descale, v_descale, se
                sparse_seq_len=None, softmax_scale: float | None = None, out=None, lse=None,
                return_lse: bool = True, dev_status=None, workspace=None, stream=None,
                k_scale_kind: int | None = None, v_scale_kind: int | None = None,
-               kv_layout: int = KV_HND):
-    """decode() over a 4-bit cache (append_kv_fp4() says how it lies): the same queries, selection of
-    tiles, outputs and rules; `workspace` has decode_fp4_workspace_size bytes."""
-    return _decode(lib().bsa_fp4_decode, "bsa_fp4_decode", decode_fp4_workspace_size, True, q, k_pages,
+               kv_layout: int = KV_HND, cu_seqlens_q=None):
+    """decode() over a 4-bit cache (append_kv_fp4() says how it lies): the same queries, packed ones
+    too, selection of tiles, outputs and rules; `workspace` has decode_fp4_workspace_size bytes."""
+    return _decode("bsa_fp4_decode", decode_fp4_workspace_size, True, cu_seqlens_q, q, k_pages,
                    v_pages, k_scales, v_scales, k_descale, v_descale, seqused_kv, block_table,
                    max_kv_len, q_descale, block_mask, sparse_indices, sparse_seq_len, softmax_scale,
                    out, lse, return_lse, dev_status, workspace, stream, k_scale_kind, v_scale_kind,

@@ -75,6 +75,7 @@ constexpr int MAX_G = 16;
 constexpr int WHOLE_TILES = 4;
 
 struct Params {
+  static constexpr bool PACKED = false;
   const void *q;
   const float *q_descale;
   const uint8_t *k_pages, *v_pages;
@@ -102,17 +103,54 @@ struct Params {
   unsigned long long wait_limit_ns;
 };
 
+// Packed query rows: sequence b's is cu_q[b], none if that is cu_q[b + 1].  Kernels of their own: as a
+// branch in the others they cost 1 to 6% there (64 sequences of 8-16K tokens, 64/8 heads: 246.5 us
+// packed and not, over 4-bit pages 166 against 164).
+struct PackedParams : Params {
+  static constexpr bool PACKED = true;
+  const int *cu_q;
+  int rows;  // of q, out and lse
+};
+
+// Rows of q, out and lse.
+template <typename P>
+__device__ __forceinline__ int rows_of(const P &p) {
+  if constexpr (P::PACKED)
+    return p.rows;
+  else
+    return p.B;
+}
+
 __device__ __forceinline__ void report(const Params &p, int bits) {
   if (p.dev_status) atomicOr(p.dev_status, bits);
 }
 
-// Tokens of sequence b; a bad length counts as none.  Read past L1: the join looks before it has
-// waited for the kernel that it joins.
-__device__ __forceinline__ int seq_len(const Params &p, int b) {
+// Tokens of sequence b; a bad length counts as none, and so do those of a sequence without a query
+// row (or with a bad one, or several).  Read past L1: the join looks before it has waited for the
+// kernel that it joins.
+template <typename P>
+__device__ __forceinline__ int seq_len(const P &p, int b) {
   const int kv = __ldcg(p.seqused_kv + b);
+  if constexpr (P::PACKED) {
+    const int first = __ldcg(p.cu_q + b), end = __ldcg(p.cu_q + b + 1);
+    if (first == end) return 0;
+    if (first < 0 || first >= p.rows || end != first + 1) {
+      report(p, BSA_DEV_BAD_SEQLEN);
+      return 0;
+    }
+  }
   if (kv >= 0 && kv <= p.max_kv_len) return kv;  // max_kv_len <= L * ps is checked on the host
   report(p, BSA_DEV_BAD_SEQLEN);
   return 0;
+}
+
+// The query row of sequence b.  One without any reads some row, for nothing.
+template <typename P>
+__device__ __forceinline__ int row_of(const P &p, int b) {
+  if constexpr (P::PACKED)
+    return min(max(p.cu_q[b], 0), p.rows - 1);
+  else
+    return b;
 }
 
 // Tiles of a task that takes no part still number one, so that a CTA comes by and writes its
@@ -198,8 +236,26 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// Packed rows behind the last sequence's count as empty ones, the CTAs sharing them out.
+__device__ __forceinline__ void clear_rows(const PackedParams &p) {
+  for (int row = max(p.cu_q[p.B], 0) + (int)blockIdx.x; row < p.rows; row += gridDim.x) {
+    uint4 *const out = reinterpret_cast<uint4 *>(p.out) + (size_t)row * p.N1 * (HEAD_DIM / 8);
+    for (int i = threadIdx.x; i < p.N1 * (HEAD_DIM / 8); i += blockDim.x)
+      out[i] = make_uint4(0, 0, 0, 0);
+    if (p.lse)
+      for (int h = threadIdx.x; h < p.N1; h += blockDim.x) p.lse[(size_t)h * p.rows + row] = -FLT_MAX;
+  }
+}
+
+// ... when there is no sequence at all.
+__global__ void clear_kernel(const PackedParams p) {
+  pdl_wait();
+  clear_rows(p);
+}
+
 // Head g of (b, kvh)'s result from a warp's (m, l, O), four dimensions a lane, and its LSE.
-__device__ __forceinline__ void write_row(const Params &p, int b, int kvh, int g, int lane, float m,
+template <typename P>
+__device__ __forceinline__ void write_row(const P &p, int b, int kvh, int g, int lane, float m,
                                           float l, float4 o) {
   const int h = kvh * p.G + g;
   const bool some = l != 0.f;  // a NaN sum is a result, not an empty row
@@ -212,10 +268,17 @@ __device__ __forceinline__ void write_row(const Params &p, int b, int kvh, int g
   uint2 w;
   memcpy(&w.x, &lo, 4);
   memcpy(&w.y, &hi, 4);
-  reinterpret_cast<uint2 *>(p.out)[((size_t)b * p.N1 + h) * 32 + lane] = w;
-  if (lane == 0 && p.lse)
-    p.lse[(size_t)h * p.B + b] =
-        some ? (m + log2f(l) - P_SHIFT) * 0.6931471805599453f : -FLT_MAX;
+  const float lse = some ? (m + log2f(l) - P_SHIFT) * 0.6931471805599453f : -FLT_MAX;
+  int row = b, end = b + 1;
+  if constexpr (P::PACKED) {  // (several rows only where the sequence counts as empty)
+    row = max(p.cu_q[b], 0);
+    end = min(p.cu_q[b + 1], p.rows);
+  }
+#pragma unroll 1
+  for (; row < end; ++row) {
+    reinterpret_cast<uint2 *>(p.out)[((size_t)row * p.N1 + h) * 32 + lane] = w;
+    if (lane == 0 && p.lse) p.lse[(size_t)h * rows_of(p) + row] = lse;
+  }
 }
 
 // (m, l, O) += a partial of its own maximum.
@@ -237,8 +300,8 @@ constexpr int PLAN_WARPS = 16;  // a warp per query head of the group
 constexpr int PLAN_THREADS = PLAN_WARPS * 32;
 constexpr int PLAN_AHEAD = 8;   // list entries in flight per lane
 
-template <bool MASK>  // block_mask, or sparse_indices
-__global__ void __launch_bounds__(PLAN_THREADS, 2) plan_kernel(const Params p) {
+template <bool MASK, typename P>  // block_mask, or sparse_indices
+__global__ void __launch_bounds__(PLAN_THREADS, 2) plan_kernel(const P p) {
   extern __shared__ uint32_t heads[];  // [Kb]
   __shared__ int warp_n[PLAN_WARPS];
   pdl_wait();
@@ -340,8 +403,8 @@ struct Found {
 
 constexpr int MAX_WARPS = 8;
 
-template <bool SPARSE, typename Want>
-__device__ __forceinline__ Found find_tile(const Params &p, int grid, int threads, Cut &cut,
+template <bool SPARSE, typename P, typename Want>
+__device__ __forceinline__ Found find_tile(const P &p, int grid, int threads, Cut &cut,
                                            bool by_item, Want &&want) {
   __shared__ int s_sum[MAX_WARPS], s_item, s_off, s_kv;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -400,7 +463,8 @@ struct Cursor {
   int pos, heads, page;    // of the current tile: the warp's first token, heads, physical page
 
   // The current tile's entry and page (the page still unchecked; -1: nothing to read).
-  __device__ __forceinline__ void look(const Params &p, int warp) {
+  template <typename P>
+  __device__ __forceinline__ void look(const P &p, int warp) {
     int tile = idx;
     heads = 0xffff;
     if (SPARSE) {
@@ -412,7 +476,8 @@ struct Cursor {
     pos = tile * TILE + warp * TOK;
     page = pos < kv && heads != 0 ? p.block_table[(size_t)b * p.L + (pos >> p.ps_shift)] : -1;
   }
-  __device__ __forceinline__ void next(const Params &p, int warp) {
+  template <typename P>
+  __device__ __forceinline__ void next(const P &p, int warp) {
     if (++idx == n) {
       idx = 0;
       if (++kvh == p.N2) {
@@ -426,9 +491,9 @@ struct Cursor {
   }
 };
 
-template <int NT, bool SPARSE>  // NT: blocks of eight query heads per KV head
+template <int NT, bool SPARSE, typename P>  // NT: blocks of eight query heads per KV head
 __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
-    decode_kernel(const Params p, const __grid_constant__ CUtensorMap tk,
+    decode_kernel(const P p, const __grid_constant__ CUtensorMap tk,
                   const __grid_constant__ CUtensorMap tv) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ float2 s_ml[WARPS][MAX_G];
@@ -451,7 +516,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
   if (SPARSE) {
     // while the lists are being made: the queries and the block table into L2, a line a thread
     const size_t line = ((size_t)blockIdx.x * THREADS + tid) * 128;
-    const size_t q_end = (size_t)(p.B - 1) * p.q_stride + (size_t)p.N1 * HEAD_DIM;  // elements
+    const size_t q_end = (size_t)(rows_of(p) - 1) * p.q_stride + (size_t)p.N1 * HEAD_DIM;  // elements
     if (line < q_end * (p.q_e4m3 ? 1 : 2)) prefetch_l2(static_cast<const uint8_t *>(p.q) + line);
     if (line < (size_t)p.B * p.L * 4)
       prefetch_l2(reinterpret_cast<const uint8_t *>(p.block_table) + line);
@@ -475,7 +540,10 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
     const Found at = find_tile<SPARSE>(p, (int)gridDim.x, THREADS, cut, false, [&](const Cut &c) {
       return cta < c.runs ? c.begin(cta) : -1;
     });
-    if (at.item < 0) return;
+    if (at.item < 0) {
+      if constexpr (P::PACKED) clear_rows(p);
+      return;
+    }
     tiles_left = cut.begin(cta + 1) - cut.begin(cta);
     cur.b = SPARSE ? at.item / p.N2 : at.item;
     cur.kv = at.kv;
@@ -493,6 +561,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
   float fac[NT][2];  // score factors of the thread's columns 2 q4, 2 q4 + 1
   float qd[NT];
   const auto fetch_q = [&](int qb, int qh) {
+    const size_t row = row_of(p, qb);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int g = nt * 8 + r;
@@ -500,7 +569,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
 #pragma unroll
       for (int i = 0; i < 16; ++i) qf[nt][i] = 0u;
       if (g >= p.G) continue;
-      const size_t at = (size_t)qb * p.q_stride + (size_t)(qh * p.G + g) * HEAD_DIM + q4 * 32;
+      const size_t at = row * p.q_stride + (size_t)(qh * p.G + g) * HEAD_DIM + q4 * 32;
       const uint4 *src = p.q_e4m3 ? reinterpret_cast<const uint4 *>(
                                         static_cast<const uint8_t *>(p.q) + at)
                                   : reinterpret_cast<const uint4 *>(
@@ -514,7 +583,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
         qf[nt][4 * i + 2] = v.z;
         qf[nt][4 * i + 3] = v.w;
       }
-      if (p.q_e4m3) qd[nt] = p.q_descale[(size_t)qb * p.N1 + qh * p.G + g];
+      if (p.q_e4m3) qd[nt] = p.q_descale[row * p.N1 + qh * p.G + g];
     }
   };
   const auto convert_q = [&]() {
@@ -551,8 +620,9 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
     }
   };
 
-  fetch_q(b, kvh);
+  if constexpr (!P::PACKED) fetch_q(b, kvh);
   cur.look(p, warp);
+  if constexpr (P::PACKED) fetch_q(b, kvh);  // (a read more in the chain: not in front of the pages')
 
   const uint32_t ring = ptx::smem_u32(smem) + warp * STAGES * STAGE_BYTES;
   uint32_t phases = 0, in_flight = 0;  // a bit a stage
@@ -560,7 +630,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
   const int q_size = p.q_e4m3 ? 1 : 2, q_lines = p.G * q_size;  // 128-byte lines of a group
   const auto q_row = [&](int qb, int qh) {
     return static_cast<const uint8_t *>(p.q) +
-           ((size_t)qb * p.q_stride + (size_t)qh * p.G * HEAD_DIM) * q_size;
+           ((size_t)row_of(p, qb) * p.q_stride + (size_t)qh * p.G * HEAD_DIM) * q_size;
   };
 
   const auto issue = [&](int stage) {
@@ -596,6 +666,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
 
 #pragma unroll
   for (int s = 0; s < STAGES - 1; ++s) issue(s);
+  if constexpr (P::PACKED) clear_rows(p);
 
   float m[NT][2], l[NT][2], acc[NT][8][4];
   const auto reset = [&]() {
@@ -869,9 +940,8 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
 // ------------------------------------------------------------------------------------------
 constexpr int JOIN_AHEAD = 5;  // partials in flight per warp
 
-template <bool SPARSE>
-__global__ void __launch_bounds__(MAX_WARPS * 32) join_kernel(const Params p, bool by_task,
-                                                              int grid) {
+template <bool SPARSE, typename P>
+__global__ void __launch_bounds__(MAX_WARPS * 32) join_kernel(const P p, bool by_task, int grid) {
   __shared__ float2 s_ml[MAX_WARPS];
   __shared__ float4 s_o[MAX_WARPS][32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;

@@ -58,7 +58,6 @@ using decode::lds128;
 using decode::mma16816;
 using decode::MAX_G;
 using decode::P_SHIFT;
-using decode::Params;
 using decode::transpose8x8;
 
 constexpr int WARPS = 2;
@@ -144,8 +143,8 @@ __device__ __forceinline__ void mma16816_new(float (&d)[4], uint32_t a0, uint32_
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
-template <int NT, bool SPARSE>  // NT: blocks of eight query heads per KV head
-__global__ void __launch_bounds__(THREADS, CTAS_PER_SM) decode_kernel(const Params p) {
+template <int NT, bool SPARSE, typename P>  // NT: blocks of eight query heads per KV head
+__global__ void __launch_bounds__(THREADS, CTAS_PER_SM) decode_kernel(const P p) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ float2 s_ml[WARPS][MAX_G];
   // {heads, tokens left, last tile of its task (1) and of the run (2), -}
@@ -155,7 +154,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) decode_kernel(const Para
   if (SPARSE) {
     // while the lists are being made: the queries and the block table into L2, a line a thread
     const size_t line = ((size_t)blockIdx.x * THREADS + tid) * 128;
-    const size_t q_end = (size_t)(p.B - 1) * p.q_stride + (size_t)p.N1 * HEAD_DIM;  // elements
+    const size_t q_end = (size_t)(decode::rows_of(p) - 1) * p.q_stride + (size_t)p.N1 * HEAD_DIM;  // elements
     if (line < q_end * (p.q_e4m3 ? 1 : 2))
       decode::prefetch_l2(static_cast<const uint8_t *>(p.q) + line);
     if (line < (size_t)p.B * p.L * 4)
@@ -181,7 +180,10 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) decode_kernel(const Para
         decode::find_tile<SPARSE>(p, (int)gridDim.x, THREADS, cut, false, [&](const Cut &c) {
           return cta < c.runs ? c.begin(cta) : -1;
         });
-    if (at.item < 0) return;
+    if (at.item < 0) {
+      if constexpr (P::PACKED) decode::clear_rows(p);
+      return;
+    }
     tiles_left = cut.begin(cta + 1) - cut.begin(cta);
     c_b = SPARSE ? at.item / p.N2 : at.item;
     c_kv = at.kv;
@@ -200,6 +202,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) decode_kernel(const Para
   float qd[NT], kd = 1.f;
   const auto fetch_q = [&](int qb, int qh) {
     if (p.k_descale) kd = p.k_descale[p.k_per_head ? qh : 0];
+    const size_t row = decode::row_of(p, qb);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int g = nt * 8 + r;
@@ -207,7 +210,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) decode_kernel(const Para
 #pragma unroll
       for (int i = 0; i < 16; ++i) qf[nt][i] = 0u;
       if (g >= p.G) continue;
-      const size_t at = (size_t)qb * p.q_stride + (size_t)(qh * p.G + g) * HEAD_DIM + q4 * 32;
+      const size_t at = row * p.q_stride + (size_t)(qh * p.G + g) * HEAD_DIM + q4 * 32;
       const uint4 *src = p.q_e4m3 ? reinterpret_cast<const uint4 *>(
                                         static_cast<const uint8_t *>(p.q) + at)
                                   : reinterpret_cast<const uint4 *>(
@@ -221,7 +224,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) decode_kernel(const Para
         qf[nt][4 * i + 2] = v.z;
         qf[nt][4 * i + 3] = v.w;
       }
-      if (p.q_e4m3) qd[nt] = p.q_descale[(size_t)qb * p.N1 + qh * p.G + g];
+      if (p.q_e4m3) qd[nt] = p.q_descale[row * p.N1 + qh * p.G + g];
     }
   };
   const auto convert_q = [&]() {
@@ -265,13 +268,14 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) decode_kernel(const Para
     }
   };
 
-  fetch_q(b, kvh);
+  if constexpr (!P::PACKED) fetch_q(b, kvh);
 
   const int q_size = p.q_e4m3 ? 1 : 2, q_lines = p.G * q_size;  // 128-byte lines of a group
   const auto prefetch_q = [&](int qb, int qh) {
     if (lane < q_lines)
       decode::prefetch_l1(static_cast<const uint8_t *>(p.q) +
-                          ((size_t)qb * p.q_stride + (size_t)qh * p.G * HEAD_DIM) * q_size +
+                          ((size_t)decode::row_of(p, qb) * p.q_stride + (size_t)qh * p.G * HEAD_DIM) *
+                              q_size +
                           lane * 128);
   };
 
@@ -378,8 +382,10 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) decode_kernel(const Para
   };
 
   look();
+  if constexpr (P::PACKED) fetch_q(b, kvh);  // (a read more in the chain: not in front of the pages')
 #pragma unroll
   for (int s = 0; s < STAGES - 1; ++s) issue(s);
+  if constexpr (P::PACKED) decode::clear_rows(p);
 
   float m[NT][2], l[NT][2], acc[NT][8][4];  // m: of the bare products
   const auto reset = [&]() {

@@ -817,14 +817,18 @@ bsa_status_t enable_decode() {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) ==
            cudaSuccess;
   };
-  if (!enable((const void *)decode::decode_kernel<1, false>, decode::SMEM_BYTES) ||
-      !enable((const void *)decode::decode_kernel<2, false>, decode::SMEM_BYTES) ||
-      !enable((const void *)decode::decode_kernel<1, true>, decode::SMEM_BYTES) ||
-      !enable((const void *)decode::decode_kernel<2, true>, decode::SMEM_BYTES) ||
-      !enable((const void *)decode4::decode_kernel<1, false>, decode4::SMEM_BYTES) ||
-      !enable((const void *)decode4::decode_kernel<2, false>, decode4::SMEM_BYTES) ||
-      !enable((const void *)decode4::decode_kernel<1, true>, decode4::SMEM_BYTES) ||
-      !enable((const void *)decode4::decode_kernel<2, true>, decode4::SMEM_BYTES)) {
+  const auto enable_all = [&](auto params) {  // the kernels that take such parameters
+    using P = decltype(params);
+    return enable((const void *)decode::decode_kernel<1, false, P>, decode::SMEM_BYTES) &&
+           enable((const void *)decode::decode_kernel<2, false, P>, decode::SMEM_BYTES) &&
+           enable((const void *)decode::decode_kernel<1, true, P>, decode::SMEM_BYTES) &&
+           enable((const void *)decode::decode_kernel<2, true, P>, decode::SMEM_BYTES) &&
+           enable((const void *)decode4::decode_kernel<1, false, P>, decode4::SMEM_BYTES) &&
+           enable((const void *)decode4::decode_kernel<2, false, P>, decode4::SMEM_BYTES) &&
+           enable((const void *)decode4::decode_kernel<1, true, P>, decode4::SMEM_BYTES) &&
+           enable((const void *)decode4::decode_kernel<2, true, P>, decode4::SMEM_BYTES);
+  };
+  if (!enable_all(decode::Params()) || !enable_all(decode::PackedParams())) {
     (void)cudaGetLastError();  // leave no pending error behind
     return BSA_ERR_CUDA;
   }
@@ -872,11 +876,72 @@ extern "C" size_t bsa_fp4_decode_workspace_size(const bsa_fp8_decode_dims_t *dim
   return decode_workspace_size(dims, true);
 }
 
-// Both cache formats' decode; k_scales and v_scales are the block scales of 4-bit pages.
+// The launches of a decode: the tile lists where there are some, the attention, the join.
+template <bool FP4, typename P>
+static bsa_status_t launch_decode(const P &p, const DecodePlan &plan, bool lists, int num_sms,
+                                  void *stream) {
+  const bool wide = p.G > 8;  // two blocks of eight query heads per KV head
+  if (lists && !launch_dependent(p.block_mask ? decode::plan_kernel<true, P>
+                                              : decode::plan_kernel<false, P>,
+                                 dim3((unsigned)(p.B * p.N2)),
+                                 decode::PLAN_THREADS, (size_t)p.Kb * sizeof(uint32_t), stream, p))
+    return BSA_ERR_CUDA;
+  if constexpr (FP4) {
+    const auto kernel =
+        lists ? (wide ? decode4::decode_kernel<2, true, P> : decode4::decode_kernel<1, true, P>)
+              : (wide ? decode4::decode_kernel<2, false, P> : decode4::decode_kernel<1, false, P>);
+    if (!launch_dependent(kernel, dim3((unsigned)plan.grid), decode4::THREADS,
+                          decode4::SMEM_BYTES, stream, p))
+      return BSA_ERR_CUDA;
+  } else {
+    // Tensor maps of the pools: a box is a warp's 32 slots of one page and head, in shared memory
+    // consecutive 128-byte rows in either layout.  L2 fetches no more than those rows: in NHD pages
+    // the next 128 bytes are another head's, wanted at another time (16 sequences of 8K tokens x 8
+    // heads: 65.9 us with 256-byte promotion, 50.3 without; HND 47.4 either way).
+    CUtensorMap tk, tv;
+    memset(&tk, 0, sizeof(tk));
+    memset(&tv, 0, sizeof(tv));
+    if (p.Kb > 0) {
+      const cuuint64_t H = (cuuint64_t)p.N2, S = (cuuint64_t)p.ps;
+      const bool nhd = p.kv_nhd != 0;
+      const cuuint64_t gd[4] = {HEAD_DIM, nhd ? H : S, nhd ? S : H, (cuuint64_t)p.num_pages};
+      const cuuint64_t gs[3] = {HEAD_DIM, gd[1] * HEAD_DIM, H * S * HEAD_DIM};
+      const cuuint32_t box[4] = {HEAD_DIM, nhd ? 1u : (cuuint32_t)decode::TOK,
+                                 nhd ? (cuuint32_t)decode::TOK : 1u, 1};
+      const CUtensorMapL2promotion row = CU_TENSOR_MAP_L2_PROMOTION_L2_128B;
+      if (!encode_map(&tk, p.k_pages, 4, gd, gs, box, row) ||
+          !encode_map(&tv, p.v_pages, 4, gd, gs, box, row))
+        return BSA_ERR_CUDA;
+    }
+    const auto kernel =
+        lists ? (wide ? decode::decode_kernel<2, true, P> : decode::decode_kernel<1, true, P>)
+              : (wide ? decode::decode_kernel<2, false, P> : decode::decode_kernel<1, false, P>);
+    if (!launch_dependent(kernel, dim3((unsigned)plan.grid), decode::THREADS, decode::SMEM_BYTES,
+                          stream, p, tk, tv))
+      return BSA_ERR_CUDA;
+  }
+  if (plan.whole || p.Kb <= 1) return BSA_OK;  // no task is cut
+  // The join, 62 registers.  Beside two CTAs of the kernels for up to eight heads (220 registers,
+  // with lists 214) an SM has room for one block of four warps or two of two; the kernels for more
+  // heads (255) leave none.  Blocks that find no room start as attention CTAs end.  The more heads and
+  // tasks there are, the fewer warps a block has.
+  const long long tasks = (long long)p.B * p.N2;
+  const bool by_task = tasks < plan.grid;
+  const int warps = !by_task ? 4 : tasks * p.G <= num_sms ? 8 : tasks * p.G <= 2 * num_sms ? 4 : 2;
+  if (!launch_dependent(lists ? decode::join_kernel<true, P> : decode::join_kernel<false, P>,
+                        by_task ? dim3((unsigned)tasks, (unsigned)p.G) : dim3((unsigned)plan.grid),
+                        warps * 32, 0, stream, p, by_task, plan.grid))
+    return BSA_ERR_CUDA;
+  return BSA_OK;
+}
+
+// Both cache formats' decode; k_scales and v_scales are the block scales of 4-bit pages.  With
+// `packed` the queries are total_q rows, found by cu_seqlens_q; without, a row a sequence.
 template <bool FP4>
-static bsa_status_t decode_impl(const bsa_fp8_decode_dims_t *d, const void *q,
-                                const float *q_descale, const void *k_pages, const void *v_pages,
-                                const void *k_scales, const void *v_scales,
+static bsa_status_t decode_impl(const bsa_fp8_decode_dims_t *d, bool packed, int total_q,
+                                const int *cu_seqlens_q, const void *q, const float *q_descale,
+                                const void *k_pages, const void *v_pages, const void *k_scales,
+                                const void *v_scales,
                                 const float *k_descale, const float *v_descale,
                                 const int *seqused_kv, const int *block_table,
                                 const uint8_t *block_mask, const int *sparse_indices,
@@ -888,13 +953,15 @@ static bsa_status_t decode_impl(const bsa_fp8_decode_dims_t *d, const void *q,
   if (block_mask && sparse_indices) return BSA_ERR_INVALID_ARGUMENT;
   if (sparse_indices && !sparse_seq_len) return BSA_ERR_INVALID_ARGUMENT;
   if (!std::isfinite(softmax_scale)) return BSA_ERR_INVALID_ARGUMENT;
-  if (d->B == 0) return BSA_OK;
+  if (packed && total_q < 0) return BSA_ERR_INVALID_ARGUMENT;
+  if (packed ? total_q == 0 : d->B == 0) return BSA_OK;
+  if (packed && !cu_seqlens_q) return BSA_ERR_INVALID_ARGUMENT;
   // a batch of empty sequences only (max_kv_len = 0) has no cache and no tiles to name
-  const bool none = d->max_kv_len == 0;
+  const bool none = d->max_kv_len == 0 || d->B == 0;
   if (!none && (d->sparse != 0) != (block_mask || sparse_indices)) return BSA_ERR_INVALID_ARGUMENT;
   const bool k_tok = d->k_scale_kind == BSA_SCALE_PER_TOKEN_HEAD;
   const bool e4m3 = d->q_type == BSA_QTYPE_E4M3;
-  if (!q || !seqused_kv || !out_bf16 || e4m3 != (q_descale != nullptr))
+  if (!q || (d->B && !seqused_kv) || !out_bf16 || e4m3 != (q_descale != nullptr))
     return BSA_ERR_INVALID_ARGUMENT;
   if (!none && (!k_pages || !v_pages || !k_descale || !v_descale || !block_table ||
                 d->num_pages < 1))
@@ -915,7 +982,7 @@ static bsa_status_t decode_impl(const bsa_fp8_decode_dims_t *d, const void *q,
   st = enable_decode();
   if (st != BSA_OK) return st;
   uint8_t *ws = static_cast<uint8_t *>(workspace);
-  decode::Params p;
+  decode::PackedParams p;
   memset(&p, 0, sizeof(p));
   p.q = q;
   p.q_descale = q_descale;
@@ -933,6 +1000,8 @@ static bsa_status_t decode_impl(const bsa_fp8_decode_dims_t *d, const void *q,
   p.out = static_cast<__nv_bfloat16 *>(out_bf16);
   p.lse = lse_f32;
   p.dev_status = dev_status;
+  p.cu_q = cu_seqlens_q;
+  p.rows = total_q;
   p.q_stride = d->q_stride;
   p.kv_nhd = d->kv_layout == BSA_KV_NHD;
   p.whole = plan.whole;
@@ -957,60 +1026,15 @@ static bsa_status_t decode_impl(const bsa_fp8_decode_dims_t *d, const void *q,
   p.part_o = reinterpret_cast<float *>(ws + plan.off_o);
   p.counts = reinterpret_cast<int2 *>(ws + plan.off_counts);
   p.tiles = reinterpret_cast<uint32_t *>(ws + plan.off_tiles);
-  const bool wide = p.G > 8;  // two blocks of eight query heads per KV head
+  if (d->B == 0)
+    return launch_dependent(decode::clear_kernel, dim3((unsigned)std::min(total_q, num_sms)),
+                            decode::THREADS, 0, stream, p)
+               ? BSA_OK
+               : BSA_ERR_CUDA;
   const bool lists = d->sparse && !none;
-  if (lists && !launch_dependent(block_mask ? decode::plan_kernel<true>
-                                            : decode::plan_kernel<false>,
-                                 dim3((unsigned)(d->B * d->N2)),
-                                 decode::PLAN_THREADS, (size_t)p.Kb * sizeof(uint32_t), stream, p))
-    return BSA_ERR_CUDA;
-  if constexpr (FP4) {
-    const auto kernel =
-        lists ? (wide ? decode4::decode_kernel<2, true> : decode4::decode_kernel<1, true>)
-              : (wide ? decode4::decode_kernel<2, false> : decode4::decode_kernel<1, false>);
-    if (!launch_dependent(kernel, dim3((unsigned)plan.grid), decode4::THREADS,
-                          decode4::SMEM_BYTES, stream, p))
-      return BSA_ERR_CUDA;
-  } else {
-    // Tensor maps of the pools: a box is a warp's 32 slots of one page and head, in shared memory
-    // consecutive 128-byte rows in either layout.  L2 fetches no more than those rows: in NHD pages
-    // the next 128 bytes are another head's, wanted at another time (16 sequences of 8K tokens x 8
-    // heads: 65.9 us with 256-byte promotion, 50.3 without; HND 47.4 either way).
-    CUtensorMap tk, tv;
-    memset(&tk, 0, sizeof(tk));
-    memset(&tv, 0, sizeof(tv));
-    if (!none) {
-      const cuuint64_t H = (cuuint64_t)d->N2, S = (cuuint64_t)d->page_size;
-      const bool nhd = p.kv_nhd != 0;
-      const cuuint64_t gd[4] = {HEAD_DIM, nhd ? H : S, nhd ? S : H, (cuuint64_t)d->num_pages};
-      const cuuint64_t gs[3] = {HEAD_DIM, gd[1] * HEAD_DIM, H * S * HEAD_DIM};
-      const cuuint32_t box[4] = {HEAD_DIM, nhd ? 1u : (cuuint32_t)decode::TOK,
-                                 nhd ? (cuuint32_t)decode::TOK : 1u, 1};
-      const CUtensorMapL2promotion row = CU_TENSOR_MAP_L2_PROMOTION_L2_128B;
-      if (!encode_map(&tk, k_pages, 4, gd, gs, box, row) ||
-          !encode_map(&tv, v_pages, 4, gd, gs, box, row))
-        return BSA_ERR_CUDA;
-    }
-    const auto kernel =
-        lists ? (wide ? decode::decode_kernel<2, true> : decode::decode_kernel<1, true>)
-              : (wide ? decode::decode_kernel<2, false> : decode::decode_kernel<1, false>);
-    if (!launch_dependent(kernel, dim3((unsigned)plan.grid), decode::THREADS, decode::SMEM_BYTES,
-                          stream, p, tk, tv))
-      return BSA_ERR_CUDA;
-  }
-  if (plan.whole || p.Kb <= 1) return BSA_OK;  // no task is cut
-  // The join, 62 registers.  Beside two CTAs of the kernels for up to eight heads (220 registers,
-  // with lists 214) an SM has room for one block of four warps or two of two; the kernels for more
-  // heads (255) leave none.  Blocks that find no room start as attention CTAs end.  The more heads and
-  // tasks there are, the fewer warps a block has.
-  const long long tasks = (long long)d->B * d->N2;
-  const bool by_task = tasks < plan.grid;
-  const int warps = !by_task ? 4 : tasks * p.G <= num_sms ? 8 : tasks * p.G <= 2 * num_sms ? 4 : 2;
-  if (!launch_dependent(lists ? decode::join_kernel<true> : decode::join_kernel<false>,
-                        by_task ? dim3((unsigned)tasks, (unsigned)p.G) : dim3((unsigned)plan.grid),
-                        warps * 32, 0, stream, p, by_task, plan.grid))
-    return BSA_ERR_CUDA;
-  return BSA_OK;
+  return packed ? launch_decode<FP4>(p, plan, lists, num_sms, stream)
+                : launch_decode<FP4>(static_cast<const decode::Params &>(p), plan, lists,
+                                     num_sms, stream);
 }
 
 extern "C" bsa_status_t bsa_fp8_decode(const bsa_fp8_decode_dims_t *d, const void *q,
@@ -1022,10 +1046,23 @@ extern "C" bsa_status_t bsa_fp8_decode(const bsa_fp8_decode_dims_t *d, const voi
                                        float softmax_scale, void *out_bf16, float *lse_f32,
                                        void *workspace, size_t workspace_bytes, int *dev_status,
                                        void *stream) {
-  return decode_impl<false>(d, q, q_descale, k_pages, v_pages, nullptr, nullptr, k_descale,
-                            v_descale, seqused_kv, block_table, block_mask, sparse_indices,
-                            sparse_seq_len, softmax_scale, out_bf16, lse_f32, workspace,
-                            workspace_bytes, dev_status, stream);
+  return decode_impl<false>(d, false, 0, nullptr, q, q_descale, k_pages, v_pages, nullptr, nullptr,
+                            k_descale, v_descale, seqused_kv, block_table, block_mask,
+                            sparse_indices, sparse_seq_len, softmax_scale, out_bf16, lse_f32,
+                            workspace, workspace_bytes, dev_status, stream);
+}
+
+extern "C" bsa_status_t bsa_fp8_decode_rows(
+    const bsa_fp8_decode_dims_t *d, int total_q, const int *cu_seqlens_q, const void *q,
+    const float *q_descale, const void *k_pages, const void *v_pages, const float *k_descale,
+    const float *v_descale, const int *seqused_kv, const int *block_table,
+    const uint8_t *block_mask, const int *sparse_indices, const int *sparse_seq_len,
+    float softmax_scale, void *out_bf16, float *lse_f32, void *workspace, size_t workspace_bytes,
+    int *dev_status, void *stream) {
+  return decode_impl<false>(d, true, total_q, cu_seqlens_q, q, q_descale, k_pages, v_pages, nullptr,
+                            nullptr, k_descale, v_descale, seqused_kv, block_table, block_mask,
+                            sparse_indices, sparse_seq_len, softmax_scale, out_bf16, lse_f32,
+                            workspace, workspace_bytes, dev_status, stream);
 }
 
 extern "C" bsa_status_t bsa_fp4_decode(
@@ -1035,10 +1072,23 @@ extern "C" bsa_status_t bsa_fp4_decode(
     const uint8_t *block_mask, const int *sparse_indices, const int *sparse_seq_len,
     float softmax_scale, void *out_bf16, float *lse_f32, void *workspace, size_t workspace_bytes,
     int *dev_status, void *stream) {
-  return decode_impl<true>(d, q, q_descale, k_pages, v_pages, k_scales, v_scales, k_descale,
-                           v_descale, seqused_kv, block_table, block_mask, sparse_indices,
-                           sparse_seq_len, softmax_scale, out_bf16, lse_f32, workspace,
-                           workspace_bytes, dev_status, stream);
+  return decode_impl<true>(d, false, 0, nullptr, q, q_descale, k_pages, v_pages, k_scales, v_scales,
+                           k_descale, v_descale, seqused_kv, block_table, block_mask,
+                           sparse_indices, sparse_seq_len, softmax_scale, out_bf16, lse_f32,
+                           workspace, workspace_bytes, dev_status, stream);
+}
+
+extern "C" bsa_status_t bsa_fp4_decode_rows(
+    const bsa_fp8_decode_dims_t *d, int total_q, const int *cu_seqlens_q, const void *q,
+    const float *q_descale, const void *k_pages, const void *v_pages, const void *k_scales,
+    const void *v_scales, const float *k_descale, const float *v_descale, const int *seqused_kv,
+    const int *block_table, const uint8_t *block_mask, const int *sparse_indices,
+    const int *sparse_seq_len, float softmax_scale, void *out_bf16, float *lse_f32, void *workspace,
+    size_t workspace_bytes, int *dev_status, void *stream) {
+  return decode_impl<true>(d, true, total_q, cu_seqlens_q, q, q_descale, k_pages, v_pages, k_scales,
+                           v_scales, k_descale, v_descale, seqused_kv, block_table, block_mask,
+                           sparse_indices, sparse_seq_len, softmax_scale, out_bf16, lse_f32,
+                           workspace, workspace_bytes, dev_status, stream);
 }
 
 template <bool FP4>

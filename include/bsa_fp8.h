@@ -358,7 +358,7 @@ typedef struct {
   int v_scale_kind;      /* BSA_SCALE_PER_TENSOR or BSA_SCALE_PER_HEAD */
   int kv_layout;         /* BSA_KV_HND (0) or BSA_KV_NHD (1) */
   int q_type;            /* BSA_QTYPE_BF16 (0) or BSA_QTYPE_E4M3 (1) */
-  int q_stride;          /* elements from one sequence's query row to the next's, >= N1 * 128 and
+  int q_stride;          /* elements from one query row to the next, >= N1 * 128 and
                             a multiple of 16 bytes (a slice of a wider projection's output) */
   int sparse;            /* 1: block_mask or sparse_indices is given; 0: neither (dense) */
 } bsa_fp8_decode_dims_t;
@@ -403,6 +403,22 @@ bsa_status_t bsa_fp8_decode(const bsa_fp8_decode_dims_t *dims, const void *q,
                             const int *sparse_seq_len, float softmax_scale, void *out_bf16,
                             float *lse_f32, void *workspace, size_t workspace_bytes,
                             int *dev_status, void *stream);
+
+/* The same with the queries packed, as a step leaves them in which some sequences get no token
+ * (bsa_assign_pages): q, q_descale, out_bf16 and lse_f32 have total_q rows (>= 0) in place of B, and
+ * sequence b's is row cu_seqlens_q[b] (device int32 [B + 1]) if cu_seqlens_q[b + 1] is one more, none
+ * if that is the same.  seqused_kv, block_table and the masks and lists stay a row a sequence.  A
+ * sequence with several rows, or with one outside [0, total_q), sets BSA_DEV_BAD_SEQLEN and counts
+ * as empty; its rows, and those from cu_seqlens_q[B] on, get O = 0 and LSE = -FLT_MAX. */
+bsa_status_t bsa_fp8_decode_rows(const bsa_fp8_decode_dims_t *dims, int total_q,
+                                 const int *cu_seqlens_q, const void *q, const float *q_descale,
+                                 const void *k_pages, const void *v_pages, const float *k_descale,
+                                 const float *v_descale, const int *seqused_kv,
+                                 const int *block_table, const uint8_t *block_mask,
+                                 const int *sparse_indices, const int *sparse_seq_len,
+                                 float softmax_scale, void *out_bf16, float *lse_f32,
+                                 void *workspace, size_t workspace_bytes, int *dev_status,
+                                 void *stream);
 
 #define BSA_OUT_BF16 0
 #define BSA_OUT_FP32 1
@@ -454,7 +470,8 @@ bsa_status_t bsa_fp8_merge_states(int count, const void *const *outs, const floa
 /* ------------------------------------------------------------------------------------------
  * Around attention: rotary positions of Q and K, pages for new tokens, and a cache held in 4 bits.
  * No counterpart in the pages.  A step of a serving loop is bsa_assign_pages, bsa_rope (or
- * bsa_rope_quantize for Q), bsa_fp4_append_kv (or bsa_fp8_append_kv_slots) and a decode.
+ * bsa_rope_quantize for Q), bsa_fp4_append_kv (or bsa_fp8_append_kv_slots) and bsa_fp4_decode_rows
+ * (or bsa_fp8_decode_rows): a sequence without a new token has no row.
  * ------------------------------------------------------------------------------------------ */
 
 /* Pairs of a rotated head: value i with value i + rotary_dim/2, or value 2i with value 2i + 1. */
@@ -609,6 +626,18 @@ bsa_status_t bsa_fp4_decode(const bsa_fp8_decode_dims_t *dims, const void *q,
                             const int *sparse_indices, const int *sparse_seq_len,
                             float softmax_scale, void *out_bf16, float *lse_f32, void *workspace,
                             size_t workspace_bytes, int *dev_status, void *stream);
+
+/* ... with packed queries, as bsa_fp8_decode_rows takes them. */
+bsa_status_t bsa_fp4_decode_rows(const bsa_fp8_decode_dims_t *dims, int total_q,
+                                 const int *cu_seqlens_q, const void *q, const float *q_descale,
+                                 const void *k_pages, const void *v_pages, const void *k_scales,
+                                 const void *v_scales, const float *k_descale,
+                                 const float *v_descale, const int *seqused_kv,
+                                 const int *block_table, const uint8_t *block_mask,
+                                 const int *sparse_indices, const int *sparse_seq_len,
+                                 float softmax_scale, void *out_bf16, float *lse_f32,
+                                 void *workspace, size_t workspace_bytes, int *dev_status,
+                                 void *stream);
 
 /* Sets the limit of every bounded wait inside the prefill and decode kernels for launches that
  * follow, in nanoseconds, for the whole process; 0 restores the default of 2 s.  A wait that runs out

@@ -426,3 +426,55 @@ def test_append_slots_binding_refuses(L):
                  lambda: bsa.append_kv(x, x, *none, p, p, kd, v_scale=vs, slot_map=i4)):  # no GPU
         with pytest.raises(ValueError):
             call()
+
+
+# ---------------------------------------------------------------------------------------------
+# packed queries
+# ---------------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("fp4", [False, True])
+def test_decode_rows_refused(L, fp4):
+    def dims(**kw):
+        return bsa.DecodeDims(**dict(dict(B=2, N1=8, N2=2, D=128, page_size=64, max_kv_len=1024,
+                                          num_pages=40, max_pages_per_seq=16,
+                                          k_scale_kind=2 if fp4 else 1, v_scale_kind=0, kv_layout=0,
+                                          q_type=0, q_stride=1024, sparse=0), **kw))
+
+    def call(d, **kw):
+        a = dict(T=3, cu=FAKE, q=FAKE, k=FAKE, v=FAKE, sc=FAKE, kd=FAKE, vd=FAKE, used=FAKE, bt=FAKE,
+                 out=FAKE, lse=FAKE)
+        a.update(kw)
+        fn = L.bsa_fp4_decode_rows if fp4 else L.bsa_fp8_decode_rows
+        return fn(ctypes.byref(d), a["T"], a["cu"], a["q"], None, a["k"], a["v"],
+                  *([a["sc"]] * 2 if fp4 else []), a["kd"], a["vd"], a["used"], a["bt"], None, None,
+                  None, 0.088, a["out"], a["lse"], None, 0, None, None)
+
+    assert call(dims()) == WORKSPACE
+    assert call(dims(), T=-1) == INVALID
+    for name in ("cu", "q", "k", "v", "kd", "vd", "used", "bt", "out"):
+        assert call(dims(), **{name: None}) == INVALID, name
+    assert call(dims(N1=9)) == INVALID and call(dims(B=-1)) == INVALID
+    assert call(dims(), T=0, cu=None, q=None, out=None) == OK
+    # no sequences: the rows are written all the same
+    assert call(dims(B=0), k=None, v=None, used=None, bt=None) == WORKSPACE
+    assert call(dims(B=0), out=None) == INVALID and call(dims(B=0), cu=None) == INVALID
+
+
+def test_decode_rows_binding_refuses(L):
+    x, i4 = torch.zeros(3, 8, 128, dtype=torch.bfloat16), torch.zeros(4, dtype=torch.int32)
+    p4, s4 = torch.zeros(6, 2, 32, 64, dtype=torch.uint8), torch.zeros(6, 2, 32, 8, dtype=torch.uint8)
+    p8, kd, g = torch.zeros(6, 2, 32, 128, dtype=torch.uint8), torch.zeros(6, 2, 32), torch.ones(2)
+    bt, cu = torch.zeros(4, 3, dtype=torch.int32), torch.zeros(5, dtype=torch.int32)
+    good = dict(q=x, seqused_kv=i4, block_table=bt, max_kv_len=90, cu_seqlens_q=cu)
+    for bad, match in ((dict(cu_seqlens_q=cu[:3]), "shape"), (dict(cu_seqlens_q=cu.long()), "dtype"),
+                       (dict(cu_seqlens_q=cu[:0]), "shape"), (dict(cu_seqlens_q=cu[None]), "shape"),
+                       (dict(seqused_kv=i4[:3]), "shape"), (dict(block_table=bt[:3]), "shape"),
+                       (dict(out=torch.zeros(4, 8, 128, dtype=torch.bfloat16)), "shape"),
+                       (dict(lse=torch.zeros(8, 4)), "shape"),
+                       (dict(block_mask=torch.zeros(3, 8, 1, dtype=torch.uint8)), "shape"),
+                       ({}, "CUDA")):
+        a = dict(good, **bad)
+        with pytest.raises(ValueError, match=match):
+            bsa.decode(k_pages=p8, v_pages=p8, k_descale=kd, v_descale=g, **a)
+        with pytest.raises(ValueError, match=match):
+            bsa.decode_fp4(k_pages=p4, v_pages=p4, k_scales=s4, v_scales=s4, k_descale=g, v_descale=g, **a)

@@ -1138,3 +1138,229 @@ def test_append_kv_rows_behind_the_last_sequence():
         pool.check(str(cu))
         k, v = v, k
     assert int(st.item()) == 0
+
+
+# ---------------------------------------------------------------------------------------------
+# packed queries: a step in which some sequences get no token
+# ---------------------------------------------------------------------------------------------
+
+def _decode_any(fp4, d, q, max_kv, **kw):
+    """decode() or decode_fp4() over a helper cache's tensors, outputs filled with NaN beforehand."""
+    import block_sparse_fp8_gb300 as bsa
+
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    if kw.get("out") is None:
+        kw["out"] = torch.full(q.shape, float("nan"), dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((q.shape[1], q.shape[0]), float("nan"), device="cuda")
+    kw.update(d["kinds"], lse=lse, dev_status=st)
+    if fp4:
+        got = bsa.decode_fp4(q, d["k_pages"], d["v_pages"], d["k_scales"], d["v_scales"],
+                             d["k_descale"], d["v_descale"], d["seqused_kv"], d["block_table"], max_kv,
+                             **kw)
+    else:
+        got = bsa.decode(q, d["k_pages"], d["v_pages"], d["k_descale"], d["v_descale"],
+                         d["seqused_kv"], d["block_table"], max_kv, **kw)
+    torch.cuda.synchronize()
+    return got[0], got[1], int(st.item())
+
+
+PACKED = [
+    # lens, which have a row, rows behind, N1, N2, q8, form
+    ([300], [1], 0, 8, 2, False, None),
+    ([300], [0], 2, 8, 2, False, None),
+    ([300, 7, 40], [1, 0, 1], 0, 8, 2, False, None),
+    ([300, 7, 40], [0, 1, 0], 3, 12, 1, True, None),
+    ([5000, 0, 129, 2000, 64], [1, 1, 0, 1, 0], 4, 16, 2, True, None),
+    ([9000, 1], [0, 1], 1, 6, 2, False, None),
+    ([200] * 90, [1, 0, 0] * 30, 50, 8, 4, False, None),
+    ([1290, 700, 130, 1], [0, 1, 1, 0], 1, 8, 2, False, "mask"),
+    ([1290, 700, 4000, 1], [1, 0, 1, 1], 0, 16, 1, True, "index"),
+    ([700, 130, 90], [0, 0, 0], 2, 4, 2, False, "mask"),
+]
+
+
+@pytest.mark.parametrize("fp4", [False, True])
+@pytest.mark.parametrize("lens,has,behind,N1,N2,q8,form", PACKED)
+def test_decode_packed_queries(lens, has, behind, N1, N2, q8, form, fp4):
+    """Row for row what decode gives for a row a sequence, those without one counted as empty; the rows
+    behind the last sequence's are empty."""
+    cache = (A.Cache4 if fp4 else S.Cache)(len(lens) + N1, lens, N2, 32)
+    d = cache.device()
+    B, max_kv = len(lens), max(lens)
+    has = np.array(has)
+    cu = np.concatenate([[0], np.cumsum(has)])
+    T = int(cu[-1]) + behind
+    q, qd, q64 = S.queries(B, max(T, 1), N1, q8)
+    q, qd = q[:T].cuda(), None if qd is None else qd[:T].cuda()
+    kw = {}
+    on = None
+    if form:
+        on = np.random.default_rng(N1).random((B, N1, -(-max_kv // 128))) < 0.4
+        if form == "mask":
+            kw["block_mask"] = torch.from_numpy(on.astype(np.uint8)).cuda()
+        else:
+            idx, cnt = S.index_lists(on, np.random.default_rng(3))
+            kw["sparse_indices"], kw["sparse_seq_len"] = (torch.from_numpy(a).cuda() for a in (idx, cnt))
+    wide, _ = _slice_of(q, 3, 1) if not q8 else (q, None)
+    out, lse, st = _decode_any(fp4, d, wide, max_kv, q_descale=qd, cu_seqlens_q=_i32(cu), **kw)
+    assert st == 0
+    # a row a sequence
+    rows = torch.from_numpy(np.flatnonzero(has)).cuda()
+    full = torch.zeros(B, N1, 128, dtype=q.dtype, device="cuda")
+    full[rows] = q[:cu[-1]]
+    fd = None
+    if q8:
+        fd = torch.ones(B, N1, device="cuda")
+        fd[rows] = qd[:cu[-1]]
+    plain = dict(d, seqused_kv=_i32(np.where(has, lens, 0)))
+    want, wlse, st = _decode_any(fp4, plain, full, max_kv, q_descale=fd, **kw)
+    assert st == 0
+    assert torch.equal(out[:cu[-1]], want[rows]) and torch.equal(lse[:, :cu[-1]], wlse[:, rows])
+    assert (out[cu[-1]:] == 0).all() and (lse[:, cu[-1]:] == S.NEG_FLT_MAX).all()
+    # against the definition
+    cache.lens = [n if h else 0 for n, h in zip(lens, has)]
+    f64 = np.zeros((B, N1, 128))
+    f64[has > 0] = q64[:cu[-1]]
+    O, Z, E, F = (A.reference4 if fp4 else S.reference)(cache, f64, on)
+    S.within(out[:cu[-1]], O[has > 0], E[has > 0], "O")
+    S.within(lse[:, :cu[-1]], Z[:, has > 0], F[:, has > 0], "LSE")
+    if not q8:                                          # in place
+        own = q.clone()
+        again, alse, st = _decode_any(fp4, d, own, max_kv, cu_seqlens_q=_i32(cu), out=own, **kw)
+        assert again is own and torch.equal(own, out) and torch.equal(alse, lse) and st == 0
+
+
+@pytest.mark.parametrize("fp4", [False, True])
+def test_decode_packed_bad_rows(fp4):
+    """Several rows of a sequence, rows that go back, before the first or beyond the last: reported, empty,
+    and the others as they are."""
+    import block_sparse_fp8_gb300 as bsa
+
+    lens, N1 = [300, 40, 129, 64], 8
+    cache = (A.Cache4 if fp4 else S.Cache)(3, lens, 2, 32)
+    d = cache.device()
+    q, _, _ = S.queries(4, 6, N1, False)
+    q = q.cuda()
+    # (rows: whose each is; one that two sequences name is left out)
+    for cu, rows in (([0, 1, 3, 4, 5], {0: 0, 3: 2, 4: 3}), ([0, 1, 0, 1, 2], {1: 3}),
+                     ([5, 6, 7, 7, 7], {5: 0}), ([-1, 0, 1, 2, 3], {0: 1, 1: 2, 2: 3}),
+                     ([2 ** 31 - 1, -2 ** 31, 0, 1, 1], {0: 2})):
+        out, lse, st = _decode_any(fp4, d, q, 300, cu_seqlens_q=_i32(cu))
+        assert st == bsa.DEV_BAD_SEQLEN, cu
+        for row, b in rows.items():
+            one = torch.zeros(4, N1, 128, dtype=torch.bfloat16, device="cuda")
+            one[b] = q[row]
+            only = dict(d, seqused_kv=_i32([n if i == b else 0 for i, n in enumerate(lens)]))
+            want, wlse, _ = _decode_any(fp4, only, one, 300)
+            assert torch.equal(out[row], want[b]) and torch.equal(lse[:, row], wlse[:, b]), cu
+        for row in range(max(cu[-1], 0), 6):
+            if row not in rows:
+                assert (out[row] == 0).all() and (lse[:, row] == S.NEG_FLT_MAX).all(), (cu, row)
+    out, lse, st = _decode_any(fp4, d, q, 300, cu_seqlens_q=_i32([0, 1, 3, 4, 5]))
+    assert (out[1:3] == 0).all() and (lse[:, 1:3] == S.NEG_FLT_MAX).all()
+
+
+@pytest.mark.parametrize("fp4", [False, True])
+def test_decode_packed_nothing(fp4):
+    """No sequences: every row is empty; no rows: nothing happens."""
+    cache = (A.Cache4 if fp4 else S.Cache)(3, [64], 2, 32)
+    d = cache.device()
+    q = torch.ones(5, 8, 128, dtype=torch.bfloat16, device="cuda")
+    none = dict(d, seqused_kv=d["seqused_kv"][:0], block_table=d["block_table"][:0])
+    for T in (5, 1, 0):
+        out, lse, st = _decode_any(fp4, none, q[:T], 64, cu_seqlens_q=_i32([0]))
+        assert st == 0 and (out == 0).all() and (lse == S.NEG_FLT_MAX).all()
+    out, lse, st = _decode_any(fp4, d, q[:0], 64, cu_seqlens_q=_i32([0, 0]))
+    assert st == 0 and out.numel() == 0
+
+
+class _Held:
+    """What a cache holds, for the reference: fp64 K and V [N2, n, 128] of each sequence."""
+
+    def __init__(self, N2, rows):
+        self.N2, self.held = N2, rows
+        self.lens = [r[0].shape[1] for r in rows]
+
+    def rows(self, b):
+        return self.held[b]
+
+
+def test_serving_steps_with_idle_sequences_captured():
+    """Steps of a token or none each, whichever sequences sit out, from one captured graph, over the
+    4-bit and the e4m3 cache: pages, rotation, append, decode by packed rows.  Every step against the
+    fp64 attention over what the caches hold (read back by gather)."""
+    import block_sparse_fp8_gb300 as bsa
+
+    B, N1, N2, ps, L = 7, 8, 2, 32, 6
+    P = B * L
+    rng = np.random.default_rng(91)
+    prompts = np.array([70, 0, 33, 1, 150, 64, 5])
+    fd, f = _freqs(128)
+    pages, scales = _pool4(P, N2, ps, False, fill=0x7f)
+    pool = _Pool8(P, N2, ps, True)
+    g = torch.full((N2,), 5.0 / 2688, device="cuda")
+    zeros = lambda *s: torch.zeros(*s, dtype=torch.int32, device="cuda")
+    table, free, count = zeros(B, L) - 1, _i32(rng.permutation(P)), _i32([P])
+    lens, new, st = zeros(B), zeros(B), zeros(1)
+
+    def place(cap, rows):
+        cu, used, pos, slots = bsa.assign_pages(new, lens, table, free, count, ps, cap, dev_status=st)
+        q, k = bsa.rope(rows[:, :N1], pos, fd, k=rows[:, N1:N1 + N2])
+        v = rows[:, N1 + N2:]
+        bsa.append_kv_fp4(k, v, slots, *pages, *scales, g, g, dev_status=st)
+        pool.append(k, v.contiguous(), slot_map=slots, dev_status=st)
+        lens.copy_(used)
+        return q, cu, pos
+
+    rows = torch.zeros(B, N1 + 2 * N2, 128, dtype=torch.bfloat16, device="cuda")
+    keep = {}
+
+    def step():
+        q, cu, pos = place(B, rows)
+        a = bsa.decode_fp4(q, *pages, *scales, g, g, lens, table, L * ps, dev_status=st,
+                           cu_seqlens_q=cu)
+        b = bsa.decode(q, pool.k, pool.v, pool.kd, pool.vs, lens, table, L * ps, dev_status=st,
+                       kv_layout=bsa.KV_NHD, cu_seqlens_q=cu)
+        keep.update(q=q, cu=cu, pos=pos, fp4=a, e4m3=b)
+
+    new.copy_(_i32(prompts))
+    place(int(prompts.sum()) + 3, _bf16(rng, (int(prompts.sum()) + 3, N1 + 2 * N2, 128)).cuda())
+    new.zero_()
+    step()                                              # nobody gets a token
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    want = prompts.copy()
+    for i in range(12):
+        n = (rng.random(B) < (0.5, 0.9, 0.2)[i % 3]).astype(int)
+        if i == 5:
+            n[:] = 0
+        want += n
+        x = _bf16(rng, (B, N1 + 2 * N2, 128)).cuda()
+        rows.copy_(x)
+        new.copy_(_i32(n))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert int(st.item()) == 0 and lens.tolist() == want.tolist()
+        who, T = np.flatnonzero(n), int(n.sum())
+        assert keep["cu"].tolist() == [0] + np.cumsum(n).tolist()
+        # row r belongs to the r-th sequence with a token, turned at its last position
+        ref, e = A.turned(x[:T, :N1].double().cpu().numpy(), want[who] - 1, f, 0, 1.0)
+        S.within(keep["q"][:T], ref, e + 2.0 ** -8 * np.abs(ref), "q")
+        full = np.zeros((B, N1, 128))
+        full[who] = keep["q"][:T].double().cpu().numpy()
+        cu = _i32(np.concatenate([[0], np.cumsum(want)]))
+        total = int(want.sum())
+        for name, kv in (("fp4", bsa.gather_kv_fp4(*pages, *scales, g, g, cu, table, total,
+                                                   out_dtype=torch.float32)),
+                         ("e4m3", bsa.gather_kv(pool.k, pool.v, pool.kd, pool.vs, cu, table, total,
+                                                out_dtype=torch.float32, kv_layout=bsa.KV_NHD))):
+            c = cu.tolist()
+            kv = [t.double().cpu().numpy().transpose(1, 0, 2) for t in kv]
+            held = _Held(N2, [[t[:, c[b]:c[b + 1] if n[b] else c[b]] for t in kv] for b in range(B)])
+            O, Z, E, F = (A.reference4 if name == "fp4" else S.reference)(held, full)
+            out, lse = keep[name]
+            S.within(out[:T], O[who], E[who], f"{name} O {i}")
+            S.within(lse[:, :T], Z[:, who], F[:, who], f"{name} LSE {i}")
+            assert (out[T:] == 0).all() and (lse[:, T:] == S.NEG_FLT_MAX).all()
