@@ -108,6 +108,13 @@ __device__ __forceinline__ uint32_t settle(uint32_t down, float above) {
   return above > 0.f || (above == 0.f && (down & 1u)) ? down + 1 : down;
 }
 
+// A power of two that brings a descale to where neither its reciprocal nor a product leaves fp32's
+// normal numbers.  Values are multiplied by it too: exactly, but for those beyond fp32, which are
+// beyond 448 * 6 descales, and those below 2^-149, which are below a code's first border.
+__device__ __forceinline__ float lift_of(float descale) {
+  return descale < 0x1p-60f ? 0x1p64f : descale > 0x1p60f ? 0x1p-64f : 1.f;
+}
+
 // The scale of a block whose largest magnitude is amax, as a code.
 __device__ __forceinline__ uint32_t scale_of(float amax, float descale, float inv6) {
   const float t = amax * inv6;
@@ -120,7 +127,8 @@ __device__ __forceinline__ uint32_t scale_of(float amax, float descale, float in
 // Where the nudged codes of a block differ: the exact decision, a value at a time (read again from
 // where it came: a register cannot be picked by number).
 __device__ __forceinline__ void settle_codes(uint32_t (&up)[2], const uint32_t (&down)[2],
-                                             const __nv_bfloat16 *x, float scale, float descale) {
+                                             const __nv_bfloat16 *x, float scale, float descale,
+                                             float lift) {
   uint64_t w = (uint64_t)up[1] << 32 | up[0];
   const uint64_t other = (uint64_t)down[1] << 32 | down[0];
   uint64_t differ = (w ^ other) & 0x7777777777777777ull;
@@ -130,7 +138,7 @@ __device__ __forceinline__ void settle_codes(uint32_t (&up)[2], const uint32_t (
     const uint32_t u = (uint32_t)(w >> at) & 7u, d = (uint32_t)(other >> at) & 7u;
     // the border is (twice one + twice the other) / 4, exact with the scale
     const float border = 0.25f * (float)(twice_e2m1(u) + twice_e2m1(d)) * scale;
-    const float size = fabsf(__bfloat162float(x[i]));
+    const float size = fabsf(__bfloat162float(x[i])) * lift;
     w = (w & ~(7ull << at)) | (uint64_t)settle(d, fmaf(-border, descale, size)) << at;
     differ &= ~(0xfull << at);
   }
@@ -140,8 +148,10 @@ __device__ __forceinline__ void settle_codes(uint32_t (&up)[2], const uint32_t (
 
 // One block of 16 values, at x: their codes and scale.
 __device__ __forceinline__ void store_block(const uint4 &a, const uint4 &b,
-                                            const __nv_bfloat16 *from, float descale, float inv6,
+                                            const __nv_bfloat16 *from, float descale,
                                             uint8_t *codes, uint8_t *scale_at) {
+  const float lift = lift_of(descale);
+  descale *= lift;
   const uint32_t word[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
   float lo[8], hi[8], amax = 0.f;
 #pragma unroll
@@ -150,7 +160,15 @@ __device__ __forceinline__ void store_block(const uint4 &a, const uint4 &b,
     hi[i] = __uint_as_float(word[i] & 0xffff0000u);
     amax = fmaxf(amax, fmaxf(fabsf(lo[i]), fabsf(hi[i])));
   }
-  const uint32_t s = scale_of(amax, descale, inv6);
+  if (lift != 1.f) {
+    amax *= lift;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      lo[i] *= lift;
+      hi[i] *= lift;
+    }
+  }
+  const uint32_t s = scale_of(amax, descale, inverse(6.f * descale));
   const float scale = value_of_e4m3(s), d = scale * descale, r = inverse(d);
   const uint64_t up = ptx::pk(r * NUDGE_UP, r * NUDGE_UP),
                  down = ptx::pk(r * NUDGE_DOWN, r * NUDGE_DOWN);
@@ -167,7 +185,7 @@ __device__ __forceinline__ void store_block(const uint4 &a, const uint4 &b,
     w[h] = e2m1x8(u);
     other[h] = e2m1x8(v);
   }
-  if (w[0] != other[0] || w[1] != other[1]) settle_codes(w, other, from, scale, descale);
+  if (w[0] != other[0] || w[1] != other[1]) settle_codes(w, other, from, scale, descale, lift);
   *reinterpret_cast<uint2 *>(codes) = make_uint2(w[0], w[1]);
   *scale_at = (uint8_t)s;
 }
@@ -192,9 +210,9 @@ __global__ void __launch_bounds__(THREADS) append_kernel(const AppendParams p) {
   }
   const long long hnd = (((long long)page * p.N2 + g) << p.ps_shift) + in;
   const long long dst = p.kv_nhd ? (((long long)page << p.ps_shift) + in) * p.N2 + g : hnd;
-  store_block(k0, k1, p.k_new + tok * p.k_stride + at, kg, inverse(6.f * kg),
+  store_block(k0, k1, p.k_new + tok * p.k_stride + at, kg,
               p.k_pages + dst * ROW_BYTES + block * (BLOCK / 2), p.k_scales + hnd * BLOCKS + block);
-  store_block(v0, v1, p.v_new + tok * p.v_stride + at, vg, inverse(6.f * vg),
+  store_block(v0, v1, p.v_new + tok * p.v_stride + at, vg,
               p.v_pages + dst * ROW_BYTES + block * (BLOCK / 2), p.v_scales + hnd * BLOCKS + block);
 }
 

@@ -595,8 +595,7 @@ typedef struct {
  * negative one is skipped, one beyond the pool is reported (BSA_DEV_BAD_PAGE) and skipped.  No slot may
  * be named twice in a call.  The scale of 16 values is the e4m3 number nearest to their largest
  * magnitude / (6 * descale), a code the e2m1 number nearest to value / (scale * descale), ties to
- * the even code, 448 and 6 the largest; both decided exactly (for blocks whose largest magnitude is
- * at least 2^-100).  Inputs must be finite. */
+ * the even code, 448 and 6 the largest; both decided exactly.  Inputs must be finite. */
 bsa_status_t bsa_fp4_append_kv(const bsa_fp4_append_dims_t *dims, const void *k_new_bf16,
                                const void *v_new_bf16, const int *slot_map,
                                const float *k_descale, const float *v_descale, void *k_pages,

@@ -999,6 +999,46 @@ def test_decode_fp4_scores_of_any_size(N1, N2, q8, form, power, sign):
     S.within(got[1], Z, F, "LSE")
 
 
+@pytest.mark.parametrize("g", [2.0 ** -149, 3e-44, 2.0 ** -126, 1e-37, 2.0 ** -122, 1e-36, 7e-32, 3e-20,
+                               2.0 ** -60, 0.01, 2.0 ** 60, 4e19, 1e30, 2e37, 1e38, 3.4e38])
+def test_append_fp4_with_any_descale(g):
+    """Descales from the smallest fp32 number to the largest, blocks below the smallest scale, in the
+    middle and above the largest: every code and scale by the definition, and read back exactly."""
+    import block_sparse_fp8_gb300 as bsa
+
+    T, N2, ps = 300, 2, 32
+    rng = np.random.default_rng(5)
+    gg = np.array([g, g], dtype=np.float32)
+    gg[1] = np.nextafter(gg[1], np.float32(1))
+    top = 2.0 ** rng.uniform(-12, 13, (T, N2, 8, 1)) * 6 * float(gg[0])
+    x = rng.uniform(-1, 1, (T, N2, 8, 16)) * top
+    x[..., 3] = top[..., 0]
+    big = float(torch.finfo(torch.bfloat16).max)
+    x = torch.from_numpy(np.clip(x, -big, big).reshape(T, N2, 128)).to(torch.bfloat16)
+    x[0], x[1], x[2], x[3] = 1.0, 1e38, -big, 2.0 ** -133
+    v = x.flip(0).contiguous()
+    P = -(-T // ps)
+    pages, scales = _pool4(P, N2, ps, False)
+    gd = torch.from_numpy(gg).cuda()
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    bsa.append_kv_fp4(x.cuda(), v.cuda(), _i32(np.arange(T)), *pages, *scales, gd, gd, dev_status=st)
+    p, s = _rows_of(pages, scales, False)
+    at = np.arange(T)
+    for rows, c, e in ((x, p[0], s[0]), (v, p[1], s[1])):
+        ref_c, ref_s = A.quantise4(rows.double().numpy(), gg.astype(np.float64)[:, None])
+        got_c, got_s = c[at // ps, :, at % ps], e[at // ps, :, at % ps]
+        assert np.array_equal(got_s, ref_s), np.argwhere(got_s != ref_s)[:3]
+        a, b = A.LEVEL[A.unpack4(got_c)], A.LEVEL[A.unpack4(ref_c)]
+        assert np.array_equal(a, b), np.argwhere(a != b)[:3]
+    got = bsa.gather_kv_fp4(*pages, *scales, gd, gd, _i32([0, T]), _i32(np.arange(P).reshape(1, P)), T,
+                            out_dtype=torch.float32, dev_status=st)
+    for out, c, e in zip(got, p, s):
+        with np.errstate(over="ignore"):
+            ref = A.values4(c, e).astype(np.float32)[at // ps, :, at % ps] * gg[:, None]
+        assert np.array_equal(out.cpu().numpy(), ref)
+    assert int(st.item()) == 0
+
+
 # ---------------------------------------------------------------------------------------------
 # the e4m3 cache behind assign_pages
 # ---------------------------------------------------------------------------------------------
