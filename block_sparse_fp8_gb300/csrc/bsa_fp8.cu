@@ -1442,7 +1442,16 @@ extern "C" bsa_status_t bsa_assign_pages(const bsa_pages_dims_t *d, const int *n
                                          int *seqused_kv, int *positions, int *slot_map,
                                          int *dev_status, void *stream) {
   if (!pages_dims_ok(d)) return BSA_ERR_INVALID_ARGUMENT;
-  if (d->B == 0 && d->total == 0) return BSA_OK;
+  if (d->B == 0 && d->total == 0) {  // nothing but the one offset
+    if (!cu_seqlens) return BSA_OK;
+    int num_sms = 0;
+    const bsa_status_t st = check_device(0, &num_sms);
+    if (st != BSA_OK) return st;
+    if (cudaMemsetAsync(cu_seqlens, 0, sizeof(int), (cudaStream_t)stream) == cudaSuccess)
+      return BSA_OK;
+    (void)cudaGetLastError();  // leave no pending error behind
+    return BSA_ERR_CUDA;
+  }
   if (!free_count || !cu_seqlens || (d->total && (!positions || !slot_map)) ||
       (d->num_pages && !free_pages) || (d->B && (!new_lens || !cache_seqlens || !seqused_kv)) ||
       (d->B && d->max_pages_per_seq && !block_table))

@@ -1039,6 +1039,25 @@ def test_append_fp4_with_any_descale(g):
     assert int(st.item()) == 0
 
 
+def test_assign_pages_without_sequences_writes_the_offset():
+    """cu_seqlens has an entry for no sequences too, whatever `total` is, and in a captured call."""
+    import block_sparse_fp8_gb300 as bsa
+
+    e, table = torch.zeros(0, dtype=torch.int32, device="cuda"), _i32(np.zeros((0, 4)))
+    free, count = _i32([0, 1]), _i32([2])
+    for total in (0, 5, 5000):
+        cu = _i32([77])
+        call = lambda: bsa.assign_pages(e, e, table, free, count, 32, total, cu_seqlens=cu)
+        assert call()[0] is cu and cu.tolist() == [0] and count.tolist() == [2]
+        graph = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph):
+            call()
+        cu.fill_(77)
+        graph.replay()
+        assert cu.tolist() == [0]
+
+
 # ---------------------------------------------------------------------------------------------
 # the e4m3 cache behind assign_pages
 # ---------------------------------------------------------------------------------------------
