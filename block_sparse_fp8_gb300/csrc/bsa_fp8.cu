@@ -1493,6 +1493,11 @@ extern "C" bsa_status_t bsa_release_pages(const bsa_pages_dims_t *d, const int *
   if (!seq_lens || !keep_lens || !free_count || !lens_out || (d->num_pages && !free_pages) ||
       (d->max_pages_per_seq && !block_table))
     return BSA_ERR_INVALID_ARGUMENT;
+  // a length is written where it was read from or where none is read
+  const size_t nb = (size_t)d->B * sizeof(int);
+  if ((lens_out != seq_lens && overlap(lens_out, nb, seq_lens, nb)) ||
+      (lens_out != keep_lens && overlap(lens_out, nb, keep_lens, nb)))
+    return BSA_ERR_INVALID_ARGUMENT;
   int num_sms = 0;
   const bsa_status_t st = check_device(0, &num_sms);
   if (st != BSA_OK) return st;

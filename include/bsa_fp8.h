@@ -558,7 +558,8 @@ bsa_status_t bsa_assign_pages(const bsa_pages_dims_t *dims, const int *new_lens,
 /* Cuts every sequence down to its first keep_lens[b] tokens (0: all of it goes; more than it holds:
  * nothing does) and puts the pages that hold none of them on the stack, in an order that undoes
  * bsa_assign_pages: pages that one call took and the next gives back lie where they were.
- *   seq_lens, keep_lens  int32 [B];  lens_out  int32 [B]: tokens held afterwards (may be seq_lens)
+ *   seq_lens, keep_lens  int32 [B];  lens_out  int32 [B]: tokens held afterwards (may be either of
+ *                        them itself; an overlap in part is refused)
  *   block_table          int32 [B, L], read: the entries stay
  * A page must be held by one sequence only (keep a shared prefix by keep_lens).  A length that is
  * negative or beyond L pages sets BSA_DEV_BAD_SEQLEN and its sequence is left alone; an entry outside

@@ -383,6 +383,23 @@ def test_tensors_come_from_the_stream_of_the_call(name, count, monkeypatch):
     assert seen == [side] * count
 
 
+def test_release_refuses_lengths_that_overlap_in_part(L):
+    """lens_out may be either of the lengths read, not lie across them: those of the first 1024 sequences
+    would be written before the others' are read."""
+    far = 64 * FAKE
+    for B in (3, 2000):
+        d = _pdims(B=B)
+        for name in ("lens", "keep"):
+            other = dict(lens=far, keep=2 * far)
+            for off in (4, -4, 4 * B - 4, 4 - 4 * B):
+                a = dict(other, out=other[name] + off)
+                assert _release(L, d, **a) == INVALID, (B, name, off)
+            # itself, or beside it: refused for nothing but the missing GPU
+            for off in (0, 4 * B, -4 * B):
+                if not torch.cuda.is_available():
+                    assert _release(L, d, **dict(other, out=other[name] + off)) not in (OK, INVALID)
+
+
 # ---------------------------------------------------------------------------------------------
 # the e4m3 cache behind assign_pages
 # ---------------------------------------------------------------------------------------------
