@@ -1257,12 +1257,14 @@ extern "C" bsa_status_t bsa_rope_frequencies(int rotary_dim, int scaling, double
       return BSA_ERR_INVALID_ARGUMENT;
   }
   const double R = rotary_dim, two_pi = 6.283185307179586476925;
-  if (!inv_freq && scaling == BSA_ROPE_BASE) base *= std::pow(factor, R / (R - 2));
+  if (!inv_freq && scaling == BSA_ROPE_BASE) {
+    base *= std::pow(factor, R / (R - 2));
+    if (!std::isfinite(base) || base <= 0) return BSA_ERR_INVALID_ARGUMENT;
+  }
   for (int i = 0; i < rotary_dim / 2; ++i) {
     double f;
     if (inv_freq) {
       f = inv_freq[i];
-      if (!std::isfinite(f)) return BSA_ERR_INVALID_ARGUMENT;
     } else {
       f = std::pow(base, -2.0 * i / R);
       if (scaling == BSA_ROPE_LINEAR) f /= factor;
@@ -1272,6 +1274,7 @@ extern "C" bsa_status_t bsa_rope_frequencies(int rotary_dim, int scaling, double
         f = f * w + f / factor * (1 - w);
       }
     }
+    if (!std::isfinite(f)) return BSA_ERR_INVALID_ARGUMENT;
     // turns a position, less whole ones: positions are whole numbers.  In (-1, 1), times 2^64; a
     // negative one counts down from 2^64.
     const double turns = std::fmod(f / two_pi, 1.0);

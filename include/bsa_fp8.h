@@ -489,7 +489,8 @@ bsa_status_t bsa_fp8_merge_states(int count, const void *const *outs, const floa
 /* Writes rotary_dim/2 frequencies to the HOST array `freqs`, in the fixed-point form that bsa_rope
  * takes: turns per position times 2^64, modulo 2^64.  inv_freq (host, rotary_dim/2 radians a
  * position) gives frequencies of the caller's own, the other arguments are then unused; or NULL.
- * rotary_dim is a multiple of 16 up to 128.  Runs on the host alone. */
+ * rotary_dim is a multiple of 16 up to 128.  Frequencies and a stretched base beyond a double's range
+ * are refused (BSA_ERR_INVALID_ARGUMENT).  Runs on the host alone. */
 bsa_status_t bsa_rope_frequencies(int rotary_dim, int scaling, double base, double factor,
                                   double context, double slow, double fast,
                                   const double *inv_freq, uint64_t *freqs);

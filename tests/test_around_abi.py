@@ -79,6 +79,16 @@ def test_frequencies_refused(L, kw):
         bsa.rope_frequencies(**dict(dict(rotary_dim=128), **kw))
 
 
+@pytest.mark.parametrize("kw", [
+    dict(base=1e-320), dict(base=5e-324),                           # fast ones beyond any double
+    dict(scaling=1, factor=1e-320), dict(scaling=3, factor=1e-320, context=4096),
+    dict(scaling=2, base=1e300, factor=1e300), dict(scaling=2, base=1e-300, factor=1e-300)])
+def test_frequencies_that_overflow_are_refused(L, kw):
+    """A stretched base or a frequency that no double holds."""
+    with pytest.raises(bsa.BsaError):
+        bsa.rope_frequencies(**dict(dict(rotary_dim=128), **kw))
+
+
 # ---------------------------------------------------------------------------------------------
 # rope
 # ---------------------------------------------------------------------------------------------
