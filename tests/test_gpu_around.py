@@ -1058,6 +1058,35 @@ def test_assign_pages_without_sequences_writes_the_offset():
         assert cu.tolist() == [0]
 
 
+@pytest.mark.parametrize("B,ps,hi,spare", [(6, 32, 100, 5), (40, 64, 9000, 3), (1500, 32, 70, 9),
+                                           (3000, 32, 60, 0), (1, 32, 100000, 2)])
+def test_release_of_more_pages_than_the_stack_holds(B, ps, hi, spare):
+    """Pages given back twice: the stack is filled to its end, what it has no room for is dropped, and the
+    call says so.  Few pages (one CTA) and many (a cluster), lengths out in place of either input."""
+    import block_sparse_fp8_gb300 as bsa
+
+    new, old, table, free, count = _pages_case(B + hi, B, ps, hi, 0, spare=spare)
+    outs, d, st = _assign(new, old, table, free, count, ps, int(new.sum()))
+    ref = A.assigned(new, old, table, free, count, ps, int(new.sum()))
+    assert st == 0
+    rng = np.random.default_rng(B)
+    keep = rng.integers(0, 40, B) * (rng.random(B) < 0.3)
+    first = A.released(ref[1], keep, ref[4], free, ref[5], ps)
+    again = A.released(ref[1], keep, ref[4], first[1], first[2], ps)
+    assert first[3] == 0 and again[3] == bsa.DEV_BAD_PAGE and again[2] == len(free)
+    assert (len(free) > 2048) == (B > 6)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    k = _i32(keep)
+    for want, lens, out in ((first, outs[1].clone(), None), (again, outs[1].clone(), k)):
+        left = bsa.release_pages(lens, k, d["table"], d["free"], d["count"], ps, out=out,
+                                 dev_status=status)
+        assert int(status.item()) == want[3] and int(d["count"]) == want[2]
+        _same(d["free"], want[1], "free")
+        _same(left, want[0], "lens")
+        _same(d["table"], ref[4], "table")
+        status.zero_()
+
+
 # ---------------------------------------------------------------------------------------------
 # the e4m3 cache behind assign_pages
 # ---------------------------------------------------------------------------------------------
