@@ -238,7 +238,7 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
 
 // Packed rows behind the last sequence's count as empty ones, the CTAs sharing them out.
 __device__ __forceinline__ void clear_rows(const PackedParams &p) {
-  for (int row = max(p.cu_q[p.B], 0) + (int)blockIdx.x; row < p.rows; row += gridDim.x) {
+  for (long long row = (long long)max(p.cu_q[p.B], 0) + blockIdx.x; row < p.rows; row += gridDim.x) {
     uint4 *const out = reinterpret_cast<uint4 *>(p.out) + (size_t)row * p.N1 * (HEAD_DIM / 8);
     for (int i = threadIdx.x; i < p.N1 * (HEAD_DIM / 8); i += blockDim.x)
       out[i] = make_uint4(0, 0, 0, 0);

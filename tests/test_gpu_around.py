@@ -1332,7 +1332,7 @@ def test_decode_packed_bad_rows(fp4):
     # (rows: whose each is; one that two sequences name is left out)
     for cu, rows in (([0, 1, 3, 4, 5], {0: 0, 3: 2, 4: 3}), ([0, 1, 0, 1, 2], {1: 3}),
                      ([5, 6, 7, 7, 7], {5: 0}), ([-1, 0, 1, 2, 3], {0: 1, 1: 2, 2: 3}),
-                     ([2 ** 31 - 1, -2 ** 31, 0, 1, 1], {0: 2})):
+                     ([2 ** 31 - 1, -2 ** 31, 0, 1, 1], {0: 2}), ([0, 1, 1, 1, 2 ** 31 - 1], {0: 0})):
         out, lse, st = _decode_any(fp4, d, q, 300, cu_seqlens_q=_i32(cu))
         assert st == bsa.DEV_BAD_SEQLEN, cu
         for row, b in rows.items():
@@ -1344,8 +1344,9 @@ def test_decode_packed_bad_rows(fp4):
         for row in range(max(cu[-1], 0), 6):
             if row not in rows:
                 assert (out[row] == 0).all() and (lse[:, row] == S.NEG_FLT_MAX).all(), (cu, row)
-    out, lse, st = _decode_any(fp4, d, q, 300, cu_seqlens_q=_i32([0, 1, 3, 4, 5]))
-    assert (out[1:3] == 0).all() and (lse[:, 1:3] == S.NEG_FLT_MAX).all()
+    for cu, end in (([0, 1, 3, 4, 5], 3), ([0, 1, 1, 1, 2 ** 31 - 1], 6)):
+        out, lse, st = _decode_any(fp4, d, q, 300, cu_seqlens_q=_i32(cu))
+        assert (out[1:end] == 0).all() and (lse[:, 1:end] == S.NEG_FLT_MAX).all()
 
 
 @pytest.mark.parametrize("fp4", [False, True])
