@@ -811,7 +811,8 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: int = ROPE
     2^64, modulo 2^64.  f_i = base^(-2i / rotary_dim) radians a position, stretched by `factor`:
     ROPE_LINEAR f_i / factor; ROPE_BASE base * factor^(R / (R - 2)); ROPE_PARTS f_i where a dimension
     turns more than `fast` times within `context` positions, f_i / factor where fewer than `slow`
-    times, a blend between.  inv_freq (rotary_dim / 2 numbers, radians a position) gives frequencies
+    times, a blend, linear in the number of turns, between (a model whose blend is linear in the number
+    of the dimension needs inv_freq).  inv_freq (rotary_dim / 2 numbers, radians a position) gives frequencies
     of the caller's own instead.  Made on the host, once for a model."""
     import torch
 
@@ -939,7 +940,8 @@ def assign_pages(new_lens, cache_seqlens, block_table, free_pages, free_count, p
     taken from its top in the sequences' order.  Returns (cu_seqlens i32 [B + 1], seqused_kv i32
     [B], positions i32 [total], slot_map i32 [total]): the new tokens' first rows, the lengths
     afterwards, and each new token's position in its sequence and its slot (page * page_size +
-    slot), as prefill(), rope(), append_kv() and append_kv_fp4() take them; rows from
+    slot), as prefill(), both decodes (cu_seqlens_q), rope(), append_kv() and append_kv_fp4() take
+    them; rows from
     cu_seqlens[B] on get position 0 and slot -1.  A sequence whose pages are not there gets none:
     slots -1, its length unchanged, DEV_NO_PAGES (the table keeps whatever it named before, so both
     appends take the slots).  seqused_kv must not be cache_seqlens."""
@@ -973,7 +975,7 @@ def release_pages(seq_lens, keep_lens, block_table, free_pages, free_count, page
                   out=None, dev_status=None, stream=None):
     """Cuts every sequence down to its first keep_lens i32 [B] tokens (0: all of it goes) and puts the
     pages that hold none of them back on the stack, so that a release undoes the assign_pages()
-    before it.  Returns the lengths afterwards (`out`, which may be seq_lens itself).  A page must be
+    before it.  Returns the lengths afterwards (`out`, which may be either length itself).  A page must be
     held by one sequence only."""
     i32 = _torch_names()[3]
     if seq_lens.dim() != 1:

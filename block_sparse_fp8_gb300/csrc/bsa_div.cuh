@@ -1,5 +1,6 @@
 // Division of an index by a number that the host knows: q = floor(n / d) for n < 2^31, from a product's
-// upper half.  With s = ceil(log2 d) and m = ceil(2^(32 + s) / d) - 2^32, n (2^32 + m) / 2^(32 + s) lies
+// upper half (T. Granlund, P. L. Montgomery, "Division by invariant integers using multiplication", PLDI
+// 1994).  With s = ceil(log2 d) and m = ceil(2^(32 + s) / d) - 2^32, n (2^32 + m) / 2^(32 + s) lies
 // above n / d by less than n / 2^32 / d, less than the distance to the next whole number.
 #pragma once
 

@@ -13,7 +13,9 @@
 // but never crosses zero.
 //
 // 256 bytes of a row read, 72 written.  A thread has one block of 16 values of K and the same of V,
-// eight threads a row.  Bound by the integer pipe, which converts and compares (71% busy; HBM 50%).
+// eight threads a row.  The integer pipe is what is busiest (71%; HBM 50%), much of it with this form's
+// own work and not the operator's: two conversions of every value to find the rare ones next to a
+// border, maxima of unpacked values.
 //
 // Measured: 64K tokens x 8 heads, NHD pages (344 MB) 74 us, 70% of the measured copy rate (with
 // 64-bit divisions and the rare borders settled in four places 95).

@@ -5,8 +5,10 @@
 // turned values, which are not rounded to bf16 in between).
 //
 // A frequency is a 64-bit fixed-point fraction of a turn, and the product with the position is taken
-// modulo a turn by the integers' own overflow: exact to 2^-33 turns for any 32-bit position, where an
-// fp32 product at position 500,000 is off by up to 0.03 radians.
+// modulo a turn by the integers' own overflow, exactly for any 32-bit position, where an fp32 product at
+// position 500,000 is off by up to 0.03 radians.  Of the product the upper 32 bits go on (2^-32 turns)
+// and are rounded to fp32 (2^-26 turns at most, next to half a turn).  The frequencies come from double
+// arithmetic, within 2^-55 turns a position of their formulas (2^-24 turns at position 2^31).
 //
 // HBM-bound (a row of 128 values: 256 bytes in, 256 or 132 out).  Eight threads have a row, two
 // 16-byte vectors each, chosen so that a thread's vectors hold whole pairs and eight threads' loads

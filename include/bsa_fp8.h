@@ -484,10 +484,13 @@ bsa_status_t bsa_fp8_merge_states(int count, const void *const *outs, const floa
 #define BSA_ROPE_BASE 2   /* base * factor^(R/(R-2)): the slowest is divided by factor, the fastest kept */
 #define BSA_ROPE_PARTS 3  /* by parts: kept where a dimension turns more than `fast` times within
                              `context` positions, divided by factor where fewer than `slow` times,
-                             a blend, linear in the number of turns, between */
+                             a blend, linear in the number of turns, between (a model whose blend is
+                             linear in the number of the dimension, between two rounded ones, has
+                             other frequencies: give them as inv_freq) */
 
 /* Writes rotary_dim/2 frequencies to the HOST array `freqs`, in the fixed-point form that bsa_rope
- * takes: turns per position times 2^64, modulo 2^64.  inv_freq (host, rotary_dim/2 radians a
+ * takes: turns per position times 2^64, modulo 2^64 (worked out in double: within 2^-55 turns a position
+ * for frequencies up to a radian a position).  inv_freq (host, rotary_dim/2 radians a
  * position) gives frequencies of the caller's own, the other arguments are then unused; or NULL.
  * rotary_dim is a multiple of 16 up to 128.  Frequencies and a stretched base beyond a double's range
  * are refused (BSA_ERR_INVALID_ARGUMENT).  Runs on the host alone. */
@@ -513,8 +516,10 @@ typedef struct {
  * the rest of the head is copied.  q bf16 [T, N1, 128], k bf16 [T, N2, 128] or NULL, positions int32
  * [T] (any values), freqs uint64 [rotary_dim/2] as bsa_rope_frequencies writes them; q_out and k_out
  * bf16, either may be its input itself (with the same stride); any other overlap with an input or with
- * each other is refused, and so is a span shared by rows of different strides.  Everything is 16-byte aligned but positions (4) and freqs (8).  The angle is exact to
- * 2^-32 turns for any position; the rest is fp32, rounded once. */
+ * each other is refused, and so is a span shared by rows of different strides.  Everything is 16-byte
+ * aligned but positions (4) and freqs (8).  The product of position and freqs is exact modulo a turn for
+ * any position; its fraction is rounded to fp32 (within 2^-25 turns in all), and so is the rest of the
+ * arithmetic; the result is rounded once. */
 bsa_status_t bsa_rope(const bsa_rope_dims_t *dims, const void *q, const void *k,
                       const int *positions, const uint64_t *freqs, float amplitude, void *q_out,
                       void *k_out, void *stream);
